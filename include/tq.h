@@ -360,6 +360,157 @@ tq_status tq_prefill_attention(const tq_context* ctx, const void* q, int q_is_fp
                                const int32_t* block_table, int max_blocks, int start, float softmax_scale,
                                void* workspace, size_t workspace_bytes, float* out, tq_stream_t stream);
 
+/* ---- one serving step over the compressed cache: rotate, append, attend a ragged batch ---- */
+
+/* Element type of the activations that the calls below read and write. */
+typedef enum tq_dtype { TQ_DTYPE_F32 = 0, TQ_DTYPE_F16 = 1, TQ_DTYPE_BF16 = 2 } tq_dtype;
+
+/* Rotary positions: which coordinates form a pair. */
+typedef enum tq_rope_layout {
+  TQ_ROPE_HALF = 0,        /* pair i = coordinates (i, i + rotary_dim / 2) */
+  TQ_ROPE_INTERLEAVED = 1  /* pair i = coordinates (2 i, 2 i + 1) */
+} tq_rope_layout;
+
+/* How the angles f_i = base^(-2 i / rotary_dim) per position are changed for contexts `factor` times longer. */
+typedef enum tq_rope_scaling {
+  TQ_ROPE_NONE = 0,
+  TQ_ROPE_LINEAR = 1,      /* f_i / factor */
+  TQ_ROPE_NTK = 2,         /* base * factor^(r / (r - 2)) in place of base, r = rotary_dim > 2 */
+  TQ_ROPE_WAVELENGTH = 3,  /* s f_i + (1 - s) f_i / factor, s = clamp((original_ctx f_i / 2 pi - low) / (high - low), 0, 1):
+                              pairs that turn more than `high` times within original_ctx keep their angle, pairs
+                              that turn less than `low` times are stretched (defaults low 1, high 4) */
+  TQ_ROPE_YARN = 4         /* g_i f_i / factor + (1 - g_i) f_i, g_i = clamp((i - a) / max(b - a, 0.001), 0, 1),
+                              a = max(floor(dim(high)), 0), b = min(ceil(dim(low)), r - 1),
+                              dim(t) = r ln(original_ctx / (2 pi t)) / (2 ln base) (defaults low 1, high 32);
+                              the rotated coordinates are multiplied by 0.1 ln factor + 1 */
+} tq_rope_scaling;
+
+typedef struct tq_rope_params {
+  int32_t head_dim;     /* 64, 128 or 256 */
+  int32_t rotary_dim;   /* even, 2 .. head_dim: coordinates [rotary_dim, head_dim) are not rotated */
+  int32_t layout;       /* tq_rope_layout */
+  int32_t scaling;      /* tq_rope_scaling */
+  double base;          /* > 1 */
+  double factor;        /* > 0 (ignored by TQ_ROPE_NONE) */
+  double original_ctx;  /* > 0 (TQ_ROPE_WAVELENGTH, TQ_ROPE_YARN) */
+  double low, high;     /* 0: the scaling's default; low < high */
+  double attn_factor;   /* factor on the rotated coordinates; 0: the scaling's default (1; see TQ_ROPE_YARN) */
+} tq_rope_params;
+
+/*
+ * The rotation in the form the kernels take: turns[i] is pair i's angle per position as a fraction of a turn in
+ * units of 2^-64.  position * turns[i] modulo 2^64 is the angle at any position, negative ones included, without
+ * the loss that a product in fp32 has at far positions.  Filled by tq_rope_build, passed by value to the kernels
+ * (no device memory); the caller owns it and may change it after a call returns.
+ */
+typedef struct tq_rope_table {
+  int32_t head_dim, rotary_dim, layout;
+  float attn_factor;
+  uint64_t turns[128];
+} tq_rope_table;
+
+/* Host; TQ_ERR_INVALID_ARG for values outside those noted above, TQ_ERR_UNSUPPORTED for another head_dim. */
+tq_status tq_rope_build(const tq_rope_params* params, tq_rope_table* table);
+
+/*
+ * Rotates n_tokens x n_heads vectors: element (t, h, i) is x[t * x_token_stride + h * d + i], the result goes to
+ * out[t * out_token_stride + h * d + i] in the same type (strides in elements, >= n_heads * d).  Token t turns by
+ * positions[t] (device int32 [n_tokens]) times the table's angles, in the other direction with inverse = 1, which is
+ * the gradient of the rotation (its transpose, attn_factor included).  Computed in fp32, rounded once.  out may be x
+ * with the same stride (in place); other overlaps are not allowed.  x and out 16-byte aligned, strides multiples of
+ * 16 bytes, else TQ_ERR_INVALID_ARG.  The context's device must be current (TQ_ERR_INVALID_ARG otherwise, here and in
+ * the calls below); the table's head_dim must be the context's.
+ */
+tq_status tq_rope(const tq_context* ctx, const tq_rope_table* table, const void* x, tq_dtype dtype, int n_tokens,
+                  int n_heads, int64_t x_token_stride, const int32_t* positions, int inverse, void* out,
+                  int64_t out_token_stride, tq_stream_t stream);
+
+/*
+ * A ragged batch of new tokens.  Sequence b has the tokens [cu_tokens[b], cu_tokens[b + 1]) of the call's n_tokens
+ * rows (device int32 [n_seqs + 1], from 0 on, not decreasing; rows behind cu_tokens[n_seqs] are padding: not read,
+ * and left as they are in every output) and seq_lens[b] tokens in all (device int32 [n_seqs]), the new ones included:
+ * its new token i of n sits at position seq_lens[b] - n + i.  block_table (device int32 [n_seqs][max_blocks]) maps
+ * page position / page_size of a sequence to a physical page; NULL: sequence b is page b.
+ * max_tokens and max_ctx (host) bound the new tokens and the length of every sequence.  A sequence whose device values
+ * break these bounds (more new tokens than max_tokens or than its length, a length above max_ctx, rows outside
+ * [0, n_tokens)) is left out of the call: status bit 1 is set, its outputs are zeros (attention, read) or not written
+ * (append).
+ */
+typedef struct tq_batch {
+  int32_t n_seqs;      /* >= 0 */
+  int32_t n_tokens;    /* rows of q, k, v and the outputs, >= 0 */
+  int32_t max_tokens;  /* >= 0 */
+  int32_t max_ctx;     /* >= 0, at most max_blocks * page_size, or page_size without a block table */
+  int32_t max_blocks;
+  const int32_t* cu_tokens;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+} tq_batch;
+
+/*
+ * Appends the batch's new keys and values to layer `layer` of the views, keys rotated on the way when `rope` is not
+ * NULL (to positions[t], device int32 [n_tokens], or where positions is NULL to the token's position in its sequence).
+ * k / v element (t, h, i): k[t * k_token_stride + h * d + i], same type for both, 16-byte aligned, strides multiples
+ * of 16 bytes and >= H d.  The rotated key is quantised from fp32 without a rounding in between.  K: Q8_0.  V: Q8_0 or
+ * turbo2/3/4_mse.  Other formats return TQ_ERR_UNSUPPORTED (turbo K: tq_rope, then tq_encode_kv).  Values in fp16
+ * without a rotation give the bytes of tq_encode_kv for Q8_0 (a NaN element is stored as 0; an infinite one, or one so
+ * large that the fp16 scale overflows, gives an infinite scale, whose values read back as NaN).  A token whose page is out of range is skipped and sets
+ * status bit 2.  Two tokens of one call must not share a slot.
+ */
+tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void* k, int64_t k_token_stride,
+                       const void* v, int64_t v_token_stride, tq_dtype dtype, const tq_rope_table* rope,
+                       const int32_t* positions, const tq_cache_view* k_view, const tq_cache_view* v_view, int layer,
+                       tq_stream_t stream);
+
+/*
+ * Reads the batch's rows back from layer `layer`: k_out and v_out [n_tokens][H][d] of type dtype, contiguous, 16-byte
+ * aligned, in the original space (K as stored, its rotation kept).  Either pair may be NULL, not both.  With
+ * cu_tokens covering whole sequences this gathers them.  Formats: Q8_0 and turbo2/3/4_mse; others TQ_ERR_UNSUPPORTED.
+ * Tokens whose page is out of range give zeros and status bit 2.
+ */
+tq_status tq_read_kv(const tq_context* ctx, const tq_batch* batch, const tq_cache_view* k_view, void* k_out,
+                     const tq_cache_view* v_view, void* v_out, tq_dtype dtype, int layer, tq_stream_t stream);
+
+/* Changes to the scores of tq_chunk_attention; zeros and NULLs: none. */
+typedef struct tq_score_mods {
+  float softcap;               /* c > 0: s = c tanh(s / c), before the distance bias */
+  int32_t window;              /* w > 0: the token at position p sees no key j <= p - w */
+  const float* slopes;         /* device float [n_q_heads]: s -= slopes[h] |p - j| */
+  const int32_t* first_keys;   /* device int32 [n_tokens]: token t sees no key j < first_keys[t] (packed documents) */
+  const int32_t* prefix_lens;  /* device int32 [n_seqs]: the keys j < prefix_lens[b] of sequence b are seen by all its
+                                  tokens, before or after them (the window and first_keys still apply) */
+} tq_score_mods;
+
+/*
+ * Workspace of tq_chunk_attention for a batch of these host sizes (the device pointers are not looked at); 0 for
+ * invalid arguments.
+ */
+size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, int n_q_heads, int n_kv_heads);
+
+/*
+ * Attention of a ragged batch of chunks, one token to thousands per sequence, over the paged cache, whose new tokens
+ * are already in it (tq_append_kv).  The token at position p of a sequence of length n sees the keys j < n with
+ * j <= p or j < its prefix length, as the score modifications leave them;
+ *   s_j = softmax_scale <q, k_j> (capped, then biased), out = sum_j softmax(s)_j v_j;
+ * a row that sees no key gives zeros.  A row that sees a key whose stored K or V has an infinite or NaN scale or norm is
+ * NaN in all coordinates; a key that a row does not see never reaches it, whatever is stored there.
+ *   q: element (t, h, i) at q[t * q_token_stride + h * d + i], type q_dtype, 16-byte aligned, stride a multiple of 16
+ *   bytes and >= n_q_heads d.  out: [n_tokens][n_q_heads][d] of type out_dtype, contiguous, 16-byte aligned.
+ *   Query head h reads KV head h / (n_q_heads / n_kv_heads); n_q_heads a multiple of n_kv_heads.
+ *   K: Q8_0.  V: Q8_0 or turbo2/3/4_mse.  Others: TQ_ERR_UNSUPPORTED (turbo K: tq_decode_attention,
+ *   tq_prefill_attention).
+ *   workspace: device, tq_chunk_workspace_bytes() bytes, 256-byte aligned; calls that may overlap need their own.
+ * The operands of the products are fp16 (queries scaled by a power of two per row, so that no type overflows), the
+ * sums and the softmax fp32.  Stored q8_0 scales above 511.5 (values above 64960) are read as 511.5.  The result of a
+ * call does not depend on what else runs.  A block-table entry out of range sets status bit 2, and its keys are left
+ * out.
+ */
+tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const void* q, tq_dtype q_dtype,
+                             int64_t q_token_stride, int n_q_heads, const tq_cache_view* k_view,
+                             const tq_cache_view* v_view, int layer, float softmax_scale, const tq_score_mods* mods,
+                             void* workspace, size_t workspace_bytes, void* out, tq_dtype out_dtype,
+                             tq_stream_t stream);
+
 /* ---- dequantize (reconstruction; test and debugging path) ---- */
 
 /*

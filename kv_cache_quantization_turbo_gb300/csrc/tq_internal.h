@@ -127,6 +127,56 @@ cudaError_t launch_prefill(const DevTables& t, const DecodeArgs& qa, const DevVi
 cudaError_t launch_decode(const DevTables& t, const DecodeArgs& a, const DecodePlan& plan,
                           void* workspace, int sm_count, cudaStream_t s);
 
+// ---- the serving step (tq_step.cpp, tq_rope.cu, tq_append.cu, tq_chunk.cu) ----
+
+// Device side of a tq_batch.
+struct DevBatch {
+  int n_seqs, n_tokens, max_tokens, max_ctx, max_blocks;
+  const int32_t* cu;
+  const int32_t* seq_lens;
+  const int32_t* block_table;  // null: sequence b is page b
+};
+
+cudaError_t launch_rope(const tq_rope_table& rope, const void* x, int dtype, int n_tokens, int n_heads,
+                        long long x_stride, const int32_t* positions, int inverse, void* out, long long out_stride,
+                        int sm_count, cudaStream_t s);
+
+struct AppendArgs {
+  DevBatch b;
+  DevView k, v;
+  DevTables tab;
+  int layer;
+  const void* xk;       // append: inputs; read: unused
+  const void* xv;
+  long long k_stride, v_stride;
+  const int32_t* positions;
+  int has_rope;
+  tq_rope_table rope;
+  void* k_out;          // read: outputs (either may be null)
+  void* v_out;
+};
+cudaError_t launch_append(const AppendArgs& a, int dtype, int sm_count, cudaStream_t s);
+cudaError_t launch_read(const AppendArgs& a, int dtype, int sm_count, cudaStream_t s);
+
+struct ChunkArgs {
+  DevBatch b;
+  DevView k, v;
+  DevTables tab;
+  int layer, n_q_heads, G;
+  const void* q;
+  int q_dtype, out_dtype;
+  long long q_stride;
+  void* out;
+  float scale;
+  float softcap;
+  int window;
+  const float* slopes;
+  const int32_t* first_keys;
+  const int32_t* prefix_lens;
+};
+size_t chunk_workspace(int sm_count, int d, const tq_batch& b, int n_q_heads, int n_kv_heads);
+cudaError_t launch_chunk(const ChunkArgs& a, float lam_v, void* workspace, int sm_count, cudaStream_t s);
+
 // Everything the decode kernels receive (by value).
 struct DecodeLaunch {
   DecodeArgs a;

@@ -35,6 +35,37 @@ class tq_cache_view(ctypes.Structure):
     ]
 
 
+class tq_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+        ("scaling", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+        ("original_ctx", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+        ("attn_factor", ctypes.c_double),
+    ]
+
+
+class tq_rope_table(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+        ("attn_factor", ctypes.c_float), ("turns", ctypes.c_uint64 * 128),
+    ]
+
+
+class tq_batch(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+        ("max_ctx", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("cu_tokens", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+    ]
+
+
+class tq_score_mods(ctypes.Structure):
+    _fields_ = [
+        ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+        ("first_keys", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _U32 = ctypes.c_uint32
@@ -67,6 +98,14 @@ _SIGS = {
                                         _P, _P]),
     "tq_prefill_workspace_bytes": (_SZ, [_P, _I, _I]),
     "tq_prefill_attention": (_I, [_P, _P, _I, _I, _I, _VP, _VP, _I, _I, _P, _I, _I, _F, _P, _SZ, _P, _P]),
+    "tq_rope_build": (_I, [ctypes.POINTER(tq_rope_params), ctypes.POINTER(tq_rope_table)]),
+    "tq_rope": (_I, [_P, ctypes.POINTER(tq_rope_table), _P, _I, _I, _I, _I64, _P, _I, _P, _I64, _P]),
+    "tq_append_kv": (_I, [_P, ctypes.POINTER(tq_batch), _P, _I64, _P, _I64, _I, ctypes.POINTER(tq_rope_table), _P,
+                          _VP, _VP, _I, _P]),
+    "tq_read_kv": (_I, [_P, ctypes.POINTER(tq_batch), _VP, _P, _VP, _P, _I, _I, _P]),
+    "tq_chunk_workspace_bytes": (_SZ, [_P, ctypes.POINTER(tq_batch), _I, _I]),
+    "tq_chunk_attention": (_I, [_P, ctypes.POINTER(tq_batch), _P, _I, _I64, _I, _VP, _VP, _I, _F,
+                                ctypes.POINTER(tq_score_mods), _P, _SZ, _P, _I, _P]),
     "tq_context_tables_hash": (_I, [_P, ctypes.POINTER(ctypes.c_uint64)]),
     "tq_cache_save": (_I, [_P, _VP, _I, ctypes.c_char_p]),
     "tq_cache_file_info": (_I, [ctypes.c_char_p, _VP, ctypes.POINTER(ctypes.c_uint64)]),
@@ -385,3 +424,153 @@ def tq_prefill_attention(ctx: int, q, q_is_fp16: int, n_tokens: int, n_q_heads: 
     return _lib.tq_prefill_attention(ctx, _ptr(q), q_is_fp16, n_tokens, n_q_heads, ka[0], va[0], layer, seq,
                                      _ptr(block_table), max_blocks, start, softmax_scale, _ptr(workspace),
                                      workspace_bytes, _ptr(out), _stream(stream))
+
+
+# ---- one serving step: rotate, append, attend a ragged batch ----
+
+DTYPES = {"float32": 0, "float16": 1, "bfloat16": 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "wavelength": 3, "yarn": 4}
+
+
+def _dtype(t) -> int:
+    """The library's element type of a tensor; -1 (refused by every call) for any other."""
+    return DTYPES.get(str(t.dtype).rsplit(".", 1)[-1], -1)
+
+
+def _rows(t, heads: int | None = None) -> int:
+    """Token stride of a [tokens, heads, d] tensor on a GPU whose heads are consecutive d-vectors."""
+    if not t.is_cuda:
+        raise ValueError(f"a tensor on the GPU is wanted, not on {t.device}")
+    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
+        raise ValueError(f"a [tokens, heads, d] tensor with contiguous heads is wanted: {tuple(t.shape)}, "
+                         f"strides {t.stride()}")
+    if heads is not None and t.shape[1] != heads:
+        raise ValueError(f"{heads} heads are wanted: {tuple(t.shape)}")
+    return max(t.stride(0), t.shape[1] * t.shape[2]) if t.shape[0] <= 1 else t.stride(0)
+
+
+@dataclass
+class Batch:
+    """A ragged batch (tq_batch) and the device tensors that own its arrays (int32): cu_tokens [n_seqs + 1],
+    seq_lens [n_seqs], block_table [n_seqs, max_blocks] or None."""
+    cu_tokens: object
+    seq_lens: object
+    block_table: object
+    n_tokens: int
+    max_tokens: int
+    max_ctx: int
+
+    def __post_init__(self):
+        n = self.seq_lens.numel()
+        if self.cu_tokens.numel() != n + 1:
+            raise ValueError(f"cu_tokens has {self.cu_tokens.numel()} entries for {n} sequences")
+        bt = self.block_table
+        if bt is not None and (bt.dim() != 2 or bt.shape[0] != n):
+            raise ValueError(f"block_table {tuple(bt.shape)} for {n} sequences")
+        for t in (self.cu_tokens, self.seq_lens, bt):
+            if t is not None and (_short(t) != "int32" or not t.is_contiguous()):
+                raise ValueError("the batch's arrays are contiguous int32 tensors")
+        self._c = tq_batch(n, self.n_tokens, self.max_tokens, self.max_ctx, 0 if bt is None else bt.shape[1],
+                           _ptr(self.cu_tokens), _ptr(self.seq_lens), _ptr(bt))
+
+    def c_batch(self) -> tq_batch:
+        return self._c
+
+
+@dataclass
+class ScoreMods:
+    """Changes to the scores (tq_score_mods) and the device tensors they read: slopes float32 [n_q_heads],
+    first_keys int32 [n_tokens], prefix_lens int32 [n_seqs], each None for none."""
+    softcap: float = 0.0
+    window: int = 0
+    slopes: object = None
+    first_keys: object = None
+    prefix_lens: object = None
+
+    def __post_init__(self):
+        for t, want in ((self.slopes, "float32"), (self.first_keys, "int32"), (self.prefix_lens, "int32")):
+            if t is not None and (_short(t) != want or not t.is_contiguous()):
+                raise ValueError(f"a contiguous {want} tensor is wanted: {t.dtype}, strides {t.stride()}")
+        self._c = tq_score_mods(self.softcap, self.window, _ptr(self.slopes), _ptr(self.first_keys),
+                                _ptr(self.prefix_lens))
+
+    def c_mods(self) -> tq_score_mods:
+        return self._c
+
+
+def _short(t) -> str:
+    return str(t.dtype).rsplit(".", 1)[-1]
+
+
+def _positions(positions, n: int):
+    if positions is not None and (_short(positions) != "int32" or positions.numel() != n or
+                                  not positions.is_contiguous()):
+        raise ValueError(f"positions: {n} contiguous int32 values are wanted")
+    return _ptr(positions)
+
+
+def tq_rope_build(head_dim: int, rotary_dim: int | None = None, layout="half", scaling="none", base: float = 10000.0,
+                  factor: float = 1.0, original_ctx: float = 0.0, low: float = 0.0, high: float = 0.0,
+                  attn_factor: float = 0.0) -> tq_rope_table:
+    """The rotation's table (a host structure that later calls take by value)."""
+    p = tq_rope_params(head_dim, head_dim if rotary_dim is None else rotary_dim,
+                       ROPE_LAYOUTS[layout] if isinstance(layout, str) else layout,
+                       ROPE_SCALINGS[scaling] if isinstance(scaling, str) else scaling, base, factor, original_ctx,
+                       low, high, attn_factor)
+    t = tq_rope_table()
+    _check(_lib.tq_rope_build(ctypes.byref(p), ctypes.byref(t)), "tq_rope_build")
+    return t
+
+
+def tq_rope(ctx: int, table: tq_rope_table, x, positions, out, inverse: bool = False, stream=None) -> int:
+    """x, out: [tokens, heads, d] tensors of one type (out may be x); positions: int32 [tokens]."""
+    if out.shape != x.shape or out.dtype != x.dtype or x.shape[-1] != table.head_dim:
+        raise ValueError(f"x {tuple(x.shape)} {x.dtype}, out {tuple(out.shape)} {out.dtype}")
+    return _lib.tq_rope(ctx, ctypes.byref(table), _ptr(x), _dtype(x), x.shape[0], x.shape[1], _rows(x),
+                        _positions(positions, x.shape[0]), int(inverse), _ptr(out), _rows(out), _stream(stream))
+
+
+def tq_append_kv(ctx: int, batch: Batch, k, v, k_view, v_view, layer: int, rope: tq_rope_table | None = None,
+                 positions=None, stream=None) -> int:
+    """k, v: [n_tokens, H, d] tensors of one type (slices of a fused projection are fine)."""
+    if k.dtype != v.dtype or k.shape != v.shape or k.shape[0] != batch.n_tokens or k.shape[2] != k_view.head_dim:
+        raise ValueError(f"k {tuple(k.shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype}, {batch.n_tokens} tokens")
+    ka, va = _view_arg(k_view), _view_arg(v_view)
+    return _lib.tq_append_kv(ctx, ctypes.byref(batch.c_batch()), _ptr(k), _rows(k, k_view.n_kv_heads), _ptr(v),
+                             _rows(v, v_view.n_kv_heads), _dtype(k), None if rope is None else ctypes.byref(rope),
+                             _positions(positions, batch.n_tokens), ka[0], va[0], layer, _stream(stream))
+
+
+def tq_read_kv(ctx: int, batch: Batch, k_view, k_out, v_view, v_out, layer: int, stream=None) -> int:
+    """k_out, v_out: contiguous [n_tokens, H, d] tensors of one type; a pair may be None."""
+    outs = [(view, t) for view, t in ((k_view, k_out), (v_view, v_out)) if t is not None]
+    for view, t in outs:
+        if tuple(t.shape) != (batch.n_tokens, view.n_kv_heads, view.head_dim) or not t.is_contiguous() or \
+                t.dtype != outs[0][1].dtype:
+            raise ValueError(f"output {tuple(t.shape)} {t.dtype} for {batch.n_tokens} tokens")
+    ka, va = _view_arg(k_view), _view_arg(v_view)
+    return _lib.tq_read_kv(ctx, ctypes.byref(batch.c_batch()), ka[0] if ka else None, _ptr(k_out),
+                           va[0] if va else None, _ptr(v_out), _dtype(outs[0][1]) if outs else 0, layer,
+                           _stream(stream))
+
+
+def tq_chunk_workspace_bytes(ctx: int, batch: Batch, n_q_heads: int, n_kv_heads: int) -> int:
+    return _lib.tq_chunk_workspace_bytes(ctx, ctypes.byref(batch.c_batch()), n_q_heads, n_kv_heads)
+
+
+def tq_chunk_attention(ctx: int, batch: Batch, q, k_view, v_view, layer: int, softmax_scale: float, workspace,
+                       workspace_bytes: int, out, mods: ScoreMods | None = None, stream=None) -> int:
+    """q: [n_tokens, n_q_heads, d]; out: contiguous, the same shape, its type may differ."""
+    if q.shape[0] != batch.n_tokens or out.shape != q.shape or not out.is_contiguous() or \
+            q.shape[2] != k_view.head_dim:
+        raise ValueError(f"q {tuple(q.shape)}, out {tuple(out.shape)} for {batch.n_tokens} tokens")
+    if mods is not None:
+        for t, n in ((mods.slopes, q.shape[1]), (mods.first_keys, batch.n_tokens),
+                     (mods.prefix_lens, batch.seq_lens.numel())):
+            if t is not None and t.numel() != n:
+                raise ValueError(f"{n} values are wanted: {tuple(t.shape)}")
+    ka, va = _view_arg(k_view), _view_arg(v_view)
+    return _lib.tq_chunk_attention(ctx, ctypes.byref(batch.c_batch()), _ptr(q), _dtype(q), _rows(q), q.shape[1], ka[0],
+                                   va[0], layer, softmax_scale, None if mods is None else ctypes.byref(mods.c_mods()),
+                                   _ptr(workspace), workspace_bytes, _ptr(out), _dtype(out), _stream(stream))
