@@ -1,117 +1,198 @@
-// Attention of a ragged batch of chunks over the paged cache: one warp per row (token, query head), one pass over the
-// row's visible keys with the running maximum and sum of the softmax.
+// Plan and host side of the chunk attention (the attention itself: tq_chunk_tc.cuh).
+//
+// The sequences' lengths are on the device, so a one-block kernel lists the entries (up to rows_per_entry rows of a
+// sequence and the keys that any of them sees) and sums up their work.  It runs in a few microseconds for the sizes
+// that a step has, and clears the counters with which the main kernel joins partial results.
 #include "tq_batch.cuh"
+#include "tq_chunk.h"
 
 namespace tq {
 namespace {
 
-constexpr int kWarps = 4;
+using ck::Args;
+using ck::Entry;
+using ck::PlanHead;
 
-template <int D>
-__device__ __forceinline__ void load_vector(const DevView& V, const float* cb, long long vec, int lane,
-                                            float (&x)[D / 32]) {
-  constexpr int E = D / 32;
-  const unsigned char* pay = V.payload + vec * V.pay_bytes;
-  const __half* hdr = reinterpret_cast<const __half*>(V.header + vec * V.hdr_bytes);
-  if (V.format == TQ_FMT_Q8_0) {
-    const float delta = __half2float(hdr[E * lane / 32]);
+constexpr int kPlanThreads = 1024;
+
+struct PlanArgs {
+  ChunkArgs c;
+  PlanHead* head;
+  Entry* entries;
+  int* seq_base;  // [n_seqs + 1]: entries of the sequences before
+  unsigned int* counters;
+  int max_entries, rows, keys;
+};
+
+// Exclusive prefix sum of x over the block; *total receives the sum.
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long v = x;
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = (float)reinterpret_cast<const int8_t*>(pay)[E * lane + e] * delta;
-  } else {
-    const float n = __half2float(hdr[0]);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      x[e] = n * cb[stream_code(reinterpret_cast<const uint32_t*>(pay), E * lane + e, V.code_bits)];
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long y = __shfl_up_sync(kFull, v, m);
+    if (lane >= m) v += y;
   }
+  __syncthreads();  // the sums of the scan before are not read any more
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  long long before = 0, all = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    const long long s = warp_sums[w];
+    if (w < warp) before += s;
+    all += s;
+  }
+  *total = all;
+  return before + v - x;
 }
 
-__device__ __forceinline__ float q_at(const ChunkArgs& a, long long i) {
-  if (a.q_dtype == TQ_DTYPE_F32) return static_cast<const float*>(a.q)[i];
-  if (a.q_dtype == TQ_DTYPE_F16) return __half2float(static_cast<const __half*>(a.q)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[i]);
-}
-
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) chunk_kernel(const __grid_constant__ ChunkArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = (int)(row / a.n_q_heads), h = (int)(row - (long long)t * a.n_q_heads);
-  if (t >= a.b.n_tokens) return;
-  const int b = seq_of_row(a.b, t);
-  if (b == a.b.n_seqs) return;
-  const SeqOf s = seq_of(a.b, b);
-  float acc[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  if (!s.ok) {
-    if (lane == 0) atomicOr(a.tab.status, kFlagSeqLen);
-  } else {
-    const int pos = s.len - s.n + (t - s.first);
-    int lo = 0, hi = pos + 1;
-    if (a.prefix_lens) hi = min(s.len, max(hi, a.prefix_lens[b]));
-    if (a.window) lo = max(lo, pos - a.window + 1);
-    if (a.first_keys) lo = max(lo, a.first_keys[t]);
-    float q[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = q_at(a, (long long)t * a.q_stride + (long long)h * D + E * lane + e);
-    const float slope = a.slopes ? a.slopes[h] : 0.f;
-    const float* cb = a.tab.centroids + (a.v.format == TQ_FMT_Q8_0 ? 0 : (a.v.idx_bits - 1) * 8);
-    for (int j = lo; j < hi; ++j) {
-      const long long v0 = position_vector(a.b, a.k, a.layer, b, j);
-      if (v0 < 0) {
-        if (lane == 0) atomicOr(a.tab.status, kFlagBlockTable);
-        continue;
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
+  __shared__ long long warp_sums[kPlanThreads / 32];
+  const ChunkArgs& a = p.c;
+  const int tid = threadIdx.x, G = a.G;
+  long long carry = 0, total;
+  for (int b0 = 0; b0 < a.b.n_seqs; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    long long ne = 0;
+    if (b < a.b.n_seqs) {
+      const SeqOf s = seq_of(a.b, b);
+      ne = ((long long)s.n * G + p.rows - 1) / p.rows;
+      if (!s.ok) {  // flagged, its rows (those that are in range) are zeros
+        atomicOr(a.tab.status, kFlagSeqLen);
+        const int esz = a.out_dtype == TQ_DTYPE_F32 ? 4 : 2;
+        const int r0 = max(0, a.b.cu[b]), r1 = min(a.b.n_tokens, a.b.cu[b + 1]);
+        if (r0 < r1) {
+          const long long row = (long long)a.n_q_heads * a.k.d * esz / 16;  // 16-byte units of a token
+          uint4* o = static_cast<uint4*>(a.out);
+          for (long long i = r0 * row; i < r1 * row; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
       }
-      const long long vec = v0 + (long long)(h / a.G) * a.k.page_size;
-      float k[E], v[E];
-      load_vector<D>(a.k, cb, vec, lane, k);
-      float sc = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) sc = fmaf(q[e], k[e], sc);
-      sc = warp_sum(sc) * a.scale;
-      if (a.softcap > 0.f) sc = a.softcap * tanhf(sc / a.softcap);
-      sc -= slope * (float)abs(pos - j);
-      const __half* vh = reinterpret_cast<const __half*>(a.v.header + vec * a.v.hdr_bytes);
-      for (int i = 0; i < a.v.hdr_bytes / 2; ++i)
-        if (!isfinite(__half2float(vh[i]))) sc = NAN;
-      const float mn = fmaxf(m, sc), mu = mn == -INFINITY ? 0.f : mn, al = __expf(m - mu), p = __expf(sc - mu);
-      load_vector<D>(a.v, cb, vec, lane, v);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], al, p * v[e]);
-      l = fmaf(l, al, p);
-      m = mn;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= inv;
-    if (a.v.format != TQ_FMT_Q8_0) {
-      warp_wht<D>(acc, lane);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= (float)a.tab.signs[E * lane + e];
+    const long long at = carry + block_scan(ne, warp_sums, &total);
+    if (b < a.b.n_seqs) p.seq_base[b] = (int)min(at, (long long)p.max_entries);
+    carry += total;
+  }
+  // more entries than rows can hold: sequences that overlap (cu_tokens not ascending); the last ones are left out
+  if (carry > p.max_entries) {
+    if (tid == 0) atomicOr(a.tab.status, kFlagSeqLen);
+    carry = p.max_entries;
+  }
+  const int E = (int)carry;
+  __syncthreads();
+  carry = 0;
+  for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
+    const int e = e0 + tid;
+    Entry en{};
+    if (e < E) {
+      int lo = 0, hi = a.b.n_seqs;  // the last sequence with seq_base <= e
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.seq_base[mid] <= e) lo = mid;
+        else hi = mid;
+      }
+      const SeqOf s = seq_of(a.b, lo);
+      en.seq = lo;
+      en.row0 = (e - p.seq_base[lo]) * p.rows;
+      const int rows = min(p.rows, s.n * G - en.row0);
+      const int i0 = en.row0 / G, i1 = (en.row0 + rows - 1) / G;  // tokens
+      const int pos0 = s.len - s.n;
+      const int prefix = a.prefix_lens ? a.prefix_lens[lo] : 0;
+      int first = 0x7FFFFFFF, last = 0;
+      if (a.first_keys) {
+        for (int i = i0; i <= i1; ++i) {
+          const int pos = pos0 + i;
+          const int h = min(s.len, max(pos + 1, prefix));
+          int l = max(0, a.first_keys[s.first + i]);
+          if (a.window) l = max(l, pos - a.window + 1);
+          if (l < h) {
+            first = min(first, l);
+            last = max(last, h);
+          }
+        }
+      } else {
+        first = a.window ? max(0, pos0 + i0 - a.window + 1) : 0;
+        last = min(s.len, max(pos0 + i1 + 1, prefix));
+      }
+      if (first < last) {
+        en.lo = first;
+        en.hi = last;
+        en.n_tiles = (last + p.keys - 1) / p.keys - first / p.keys;
+      }
     }
+    const long long at = carry + block_scan(e < E ? en.n_tiles + ck::kOverhead : 0, warp_sums, &total);
+    if (e < E) {
+      en.start = at;
+      p.entries[e] = en;
+    }
+    carry += total;
   }
-  const long long o = row * D + E * lane;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (a.out_dtype == TQ_DTYPE_F32) from_float(static_cast<float*>(a.out) + o + e, acc[e]);
-    else if (a.out_dtype == TQ_DTYPE_F16) from_float(static_cast<__half*>(a.out) + o + e, acc[e]);
-    else from_float(static_cast<__nv_bfloat16*>(a.out) + o + e, acc[e]);
-  }
+  for (long long i = tid; i < (long long)E * a.k.H * 2; i += kPlanThreads) p.counters[i] = 0u;
+  if (tid == 0) *p.head = PlanHead{carry, E};
+}
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+// The parts of the workspace, in order: head, entries, seq_base, counters, partial results.
+struct Layout {
+  size_t entries, seq_base, counters, part_o, part_ml, bytes;
+  long long max_entries;
+  int rows_cap;
+};
+
+Layout layout(int sm_count, int d, long long n_seqs, long long n_tokens, long long max_tokens, int n_q_heads,
+              int n_kv_heads) {
+  Layout l;
+  const long long G = n_q_heads / n_kv_heads, rows = ck::rows_per_entry(d);
+  const long long of_tokens = (n_tokens * G) / rows + n_seqs, per_seq = (max_tokens * G + rows - 1) / rows;
+  // sum of ceil(n_b G / rows): at most both bounds
+  l.max_entries = per_seq == 0 ? 0 : (of_tokens < n_seqs * per_seq ? of_tokens : n_seqs * per_seq);
+  l.rows_cap = (int)(max_tokens * G < 128 ? max_tokens * G : 128);
+  l.entries = 256;
+  l.seq_base = l.entries + up(l.max_entries * sizeof(Entry));
+  l.counters = l.seq_base + up((n_seqs + 1) * sizeof(int));
+  l.part_o = l.counters + up(l.max_entries * n_kv_heads * 2 * sizeof(unsigned));
+  l.part_ml = l.part_o + up((size_t)sm_count * 4 * l.rows_cap * d * sizeof(float));
+  l.bytes = l.part_ml + up((size_t)sm_count * 4 * l.rows_cap * 2 * sizeof(float));
+  return l;
 }
 
 }  // namespace
 
-size_t chunk_workspace(int, int, const tq_batch&, int, int) { return 256; }
+size_t chunk_workspace(int sm_count, int d, const tq_batch& b, int n_q_heads, int n_kv_heads) {
+  return layout(sm_count, d, b.n_seqs, b.n_tokens, b.max_tokens, n_q_heads, n_kv_heads).bytes;
+}
 
-cudaError_t launch_chunk(const ChunkArgs& a, float, void*, int, cudaStream_t s) {
-  const long long rows = (long long)a.b.n_tokens * a.n_q_heads;
-  const long long grid = (rows + kWarps - 1) / kWarps;
-  if (grid >= (1LL << 31)) return cudaErrorInvalidValue;
-  if (a.k.d == 64) chunk_kernel<64><<<(unsigned)grid, kWarps * 32, 0, s>>>(a);
-  else if (a.k.d == 128) chunk_kernel<128><<<(unsigned)grid, kWarps * 32, 0, s>>>(a);
-  else chunk_kernel<256><<<(unsigned)grid, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, int sm_count, cudaStream_t s) {
+  const Layout l = layout(sm_count, c.k.d, c.b.n_seqs, c.b.n_tokens, c.b.max_tokens, c.n_q_heads, c.k.H);
+  if (l.max_entries * c.k.H * 2 >= (1LL << 31)) return cudaErrorInvalidValue;  // counter indices are 32-bit
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  PlanArgs p{};
+  p.c = c;
+  p.head = reinterpret_cast<PlanHead*>(ws);
+  p.entries = reinterpret_cast<Entry*>(ws + l.entries);
+  p.seq_base = reinterpret_cast<int*>(ws + l.seq_base);
+  p.counters = reinterpret_cast<unsigned int*>(ws + l.counters);
+  p.max_entries = (int)l.max_entries;
+  p.rows = ck::rows_per_entry(c.k.d);
+  p.keys = ck::keys_per_tile(c.k.d);
+  plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  Args a{};
+  a.c = c;
+  a.plan = p.head;
+  a.entries = p.entries;
+  a.counters = p.counters;
+  a.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
+  a.rows_cap = l.rows_cap;
+  a.scale = (c.scale < 0.f ? -c.scale : c.scale) * 1.4426950408889634074f;
+  a.q_sign = c.scale > 0.f ? 1.f : c.scale < 0.f ? -1.f : 0.f;
+  a.inv_lam_v = 1.f / lam_v;
+  const int vb = c.v.format == TQ_FMT_Q8_0 ? 0 : c.v.idx_bits;
+  if (c.k.d == 64) return ck::launch_d64(a, vb, sm_count, s);
+  if (c.k.d == 128) return ck::launch_d128(a, vb, sm_count, s);
+  return ck::launch_d256(a, vb, sm_count, s);
 }
 
 }  // namespace tq
