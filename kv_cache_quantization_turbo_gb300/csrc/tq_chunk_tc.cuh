@@ -8,22 +8,25 @@
 // decode row the long axis is so split over the whole GPU; with a large chunk every SM works to the end.
 //
 // A tile is BN keys.  A step is one score product S = Q K^T (M 128, N BN, K D), its softmax and O += P V (M 128, N D,
-// K BN).  Entries of more than 128 rows (D <= 128) have two row tiles, and steps alternate between them on one key tile;
-// smaller ones have one, and steps alternate between two independent accumulators on successive key tiles, joined at
-// the end like any other partial results.  Either way step u uses score buffer u % 2 and warpgroup u % 2, and the
-// tensor core works on one buffer while the other is in the softmax.  At D = 256 tensor memory holds one accumulator,
-// and one warpgroup takes every step.
+// K BN), the last two in parts of 64 keys.  Entries of more than 128 rows (D <= 128) have two row tiles, and steps
+// alternate between them on one key tile; smaller ones have one, and steps alternate between two independent
+// accumulators on successive key tiles, joined at the end like any other partial results.  Either way step u uses score
+// buffer u % 2 and warpgroup u % 2, and the tensor core works for one while the other is in the softmax.  At D = 256
+// tensor memory holds one accumulator, and one warpgroup takes every step.
 //
 // Warps, meeting on mbarriers only:
-//   0-3, 4-7   softmax: one row per thread.  S from tensor memory to registers, score modifications and masks, online
-//              softmax with a lazily raised reference (O in tensor memory is rescaled only when the maximum passes the
-//              reference by 2^8), P as fp16 into the columns of S, the left operand of the value product.
-//   8-11       producers: codes to fp16 values, K and V alike, 16 coordinates per step of a thread, into swizzled
-//              operand tiles (K: K-major; the same bytes read MN-major are V).  A q8_0 code becomes its value by a byte
-//              permute into 1024 + u, an exact subtraction and one rounded product with the scale.
-//   12         one thread issues the products, in the order QK(0), QK(1), PV(0), QK(2), PV(1), ...
-//   13         finds each key's place through the block table a few tiles ahead, and asks for its bytes in L2
-//   14         reads the plan a few items ahead
+//   0-3, 4-7   softmax: one row per thread, S read 32 columns at a time.  The weights 2^(s - reference) are taken against
+//              the reference so far; only where it is unset, or a row's tile sums to more than fp16 weights can hold,
+//              does a second reading find the row's maximum, raise the reference and rescale O in tensor memory.  Tiles
+//              with score modifications or masks are changed in place before.  P as fp16 goes over S, the left operand
+//              of the value product.
+//   8-15       producers: codes to fp16 values, K and V alike, into swizzled operand tiles (K: K-major; the same bytes
+//              read MN-major are V).  A q8_0 code becomes its value by a byte permute into 1024 + u, an exact
+//              subtraction and one rounded product with the scale.
+//   16, 17     issue the products, one warp for each softmax warpgroup: QK, PV, PV, QK, ... in order.  (One warp for both
+//              took longer to go round than the products.)
+//   18, 19     18 reads the plan; both find each key's place through the block table a few tiles ahead, and ask for its
+//              bytes in L2
 // The scales of fp16 operands: queries are multiplied by a power of two per row (any input type fits then), turbo
 // values carry lambda so that the codebook is nearly exact in fp16.  Rounding to fp16 (2^-11 relative at most per
 // operand) is what the tensor core's full rate asks for; sums are fp32.
@@ -36,20 +39,23 @@
 namespace tq {
 namespace ck {
 
-constexpr int kThreads = 512;
-constexpr int kProdWarps = 4;
-constexpr int kIssuer = 12, kLocator = 13, kScheduler = 14;
-constexpr int kItemReaders = 8 + kProdWarps + 2;
+constexpr int kThreads = 640;
+constexpr int kProdWarps = 8;
+constexpr int kIssuer = 16, kLocator = 18, kLocWarps = 2;
+constexpr int kItemReaders = 8 + kProdWarps + 2 + kLocWarps - 1;  // (the first locator writes the items)
 constexpr int NI = 3;       // items known ahead
 constexpr int NL = 6;       // tiles located ahead of the producers
 constexpr int kMissRing = 16;
 constexpr int kMinUnits = 2;
-constexpr float kLazy = 8.0f;
+constexpr float kBias = 4.0f;     // a fresh reference makes the row's largest weight 2^kBias
+constexpr float kTop = 32768.0f;  // the reference is raised where a tile's weights sum to more: each is below 65504
 constexpr float kLog2e = 1.4426950408889634074f;
-// registers per thread after the split: 256 * 168 + 128 * 112 + 128 * 56 <= 512 * 128
-constexpr int kRegsSoftmax = 168, kRegsProducer = 112, kRegsOther = 56;
-static_assert(256 * kRegsSoftmax + 128 * kRegsProducer + 128 * kRegsOther <= 512 * 128, "register split");
-constexpr int kRegsNeeded = 256 * kRegsSoftmax + 128 * kRegsProducer + 128 * kRegsOther;
+// Registers per thread after the split; its sum has to be within the launch's (checked at the launch).
+constexpr int kRegsSoftmax = 120, kRegsProducer = 88, kRegsOther = 64;
+constexpr int kRegsNeeded = 256 * kRegsSoftmax + 32 * kProdWarps * kRegsProducer + 128 * kRegsOther;
+static_assert(kRegsNeeded <= kThreads * 96, "register split");
+
+constexpr int HN = 64;  // keys of a part
 
 template <int D>
 struct Shape {
@@ -70,8 +76,10 @@ struct Shape {
   static constexpr int total = bars + 64 * 8;
   static constexpr int alloc = total + 1024;
   static_assert(alloc <= 227 * 1024, "shared memory");
+  static constexpr int PH = BN / HN;                   // parts of a step
   // tensor memory columns: S [2][BN], O [kQTiles][D]
   static constexpr int tO = 2 * BN;
+  static_assert(tO + kQTiles * D <= 512, "tensor memory");
 };
 
 struct Item {
@@ -88,8 +96,8 @@ static_assert(sizeof(Item) <= 128, "item");
 
 struct Bars {
   uint64_t k_full[3], k_free[3], v_full[3], v_free[3];
-  uint64_t s_done[2], p_full[2], pv_done[2];
-  uint64_t drained, q_full, item_full[NI], item_free[NI], loc_full[NL], loc_free[NL];
+  uint64_t s_done[2], p_full[4], pv_done[4];  // per buffer, per buffer and part
+  uint64_t drained[2], q_full, item_full[NI], item_free[NI], loc_full[NL], loc_free[NL];
   uint32_t tmem;
 };
 static_assert(sizeof(Bars) <= 64 * 8, "barriers");
@@ -100,22 +108,85 @@ template <int R>
 __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
   return (uint32_t)((chunk >> 3) * (128 * R) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
-// Start offset of a K step (16 elements) in a K-major tile of R rows.
-template <int R>
-__host__ __device__ constexpr uint32_t kstep(int ks) {
-  return (uint32_t)((ks >> 2) * (128 * R) + (ks & 3) * 32);
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
+// Waits for this thread's tensor-memory loads, x among them (an operand, so that no use of x moves before the wait).
+__device__ __forceinline__ void loaded(uint32_t (&x)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                 "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]),
+                 "+r"(x[16]), "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]),
+                 "+r"(x[23]), "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29]),
+                 "+r"(x[30]), "+r"(x[31])::"memory");
+}
+__device__ __forceinline__ void loaded(uint32_t (&x)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                 "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]),
+                 "+r"(x[15])::"memory");
+}
+// Stores 16 consecutive 32-bit columns of this warp's tensor-memory lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
 // A wait that gives up for good once one has run out: the role then runs through its loops without waiting (every
 // named barrier is still met), and the error is reported at the end.
 __device__ __forceinline__ void wait(bool& ok, uint64_t* bar, uint32_t parity) {
   if (ok) ok = tc::mbar_wait(bar, parity & 1u);
+}
+
+// A value that all lanes share, in a form that the compiler knows to be shared.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(kFull, x, 0); }
+
+// Four tensor instructions of the lane with one = 1, K = 64 in all: D += A B^T.  Descriptors as low word and the common
+// high word; acc = 0 starts the sum.  mma4_ss: A and B K-major in shared memory, one 64-element block of each.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc,
+                                        uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a, b;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.u32 e, %6, 0;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t"
+      "add.u32 a, %1, 2;\n\tadd.u32 b, %2, 2;\n\tmov.b64 x, {a, %3};\n\tmov.b64 y, {b, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+      "add.u32 a, %1, 4;\n\tadd.u32 b, %2, 4;\n\tmov.b64 x, {a, %3};\n\tmov.b64 y, {b, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+      "add.u32 a, %1, 6;\n\tadd.u32 b, %2, 6;\n\tmov.b64 x, {a, %3};\n\tmov.b64 y, {b, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(one));
+}
+// mma4_ts: A in tensor memory (8 columns per instruction), B MN-major (2048 bytes per instruction).
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc,
+                                        uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a, b;\n\t.reg .b64 y;\n\t"
+      "setp.ne.u32 e, %6, 0;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\tmov.b64 y, {b, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\tmov.b64 y, {b, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\tmov.b64 y, {b, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(one));
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(tc::smem_addr(bar)),
+      "r"(one)
+      : "memory");
 }
 
 // The same for a whole warp, whose lanes stay of one mind.
@@ -140,11 +211,12 @@ __device__ __forceinline__ void q8_pairs(uint32_t w, uint32_t& a, uint32_t& b) {
   b = *reinterpret_cast<const uint32_t*>(&q);
 }
 
-// A scale clamped to where 127 times it is finite in fp16, duplicated; the sign of bad is left to the caller.
-__device__ __forceinline__ uint32_t clamp_scale(uint16_t s) {
-  const __half lim = __ushort_as_half(0x5FFE), nlim = __ushort_as_half(0xDFFE);  // 511.5
-  const __half h = __hmax(__hmin(__ushort_as_half(s), lim), nlim);
-  return (uint32_t)__half_as_ushort(h) * 0x10001u;
+// A duplicated scale clamped to where 127 times it is finite in fp16.
+__device__ __forceinline__ uint32_t clamp_scale(uint32_t s2) {
+  const uint32_t lim = 0x5FFE5FFEu, nlim = 0xDFFEDFFEu;  // 511.5
+  const __half2 h = __hmax2(__hmin2(*reinterpret_cast<const __half2*>(&s2), *reinterpret_cast<const __half2*>(&lim)),
+                            *reinterpret_cast<const __half2*>(&nlim));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ bool not_finite(uint32_t s) { return (s & 0x7C00u) == 0x7C00u; }
 
@@ -160,36 +232,41 @@ template <int R>
 __device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // ---------------------------------------------------------------------------
-// scheduler: the CTA's items, in order
+// the CTA's items, in order
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ void schedule(const Args& a, Bars* B, Item* items, bool& ok) {
-  const PlanHead head = *a.plan;
-  const long long T = head.units, U = T * a.c.k.H;
-  // every CTA that takes part has at least kMinUnits units (so no CTA inside an entry's range is without work)
-  const long long nC = max(1LL, min((long long)gridDim.x, U / kMinUnits)), c = blockIdx.x;
-  long long u = c < nC ? U * c / nC : 0;
-  const long long u1 = c < nC ? U * (c + 1) / nC : 0;
+struct Items {
+  long long T, U, nC, u, u1;
+  int n_entries, h, e;
+
   // the CTA whose range holds a unit
-  auto cta_of = [&](long long x) { return (int)(((x + 1) * nC - 1) / U); };
-  int cnt = 0;
-  auto put = [&](const Item& it) {
-    const int s = cnt % NI;
-    if (cnt >= NI) wait(ok, &B->item_free[s], cnt / NI - 1);
-    items[s] = it;
-    tc::mbar_arrive(&B->item_full[s]);
-    ++cnt;
-  };
-  if (u < u1) {
-    int h = (int)(u / T);
-    long long off = u - (long long)h * T;
-    int e = 0;  // the last entry that starts at or before off
-    for (int step = 1 << 30; step > 0; step >>= 1)
-      if (e + step < head.n_entries && a.entries[e + step].start <= off) e += step;
-    while (u < u1) {
+  __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * nC - 1) / U); }
+
+  __device__ void start(const Args& a) {
+    const PlanHead head = *a.plan;
+    T = head.units;
+    n_entries = head.n_entries;
+    U = T * a.c.k.H;
+    // every CTA that takes part has at least kMinUnits units (so no CTA inside an entry's range is without work)
+    nC = max(1LL, min((long long)gridDim.x, U / kMinUnits));
+    const long long c = blockIdx.x;
+    u = c < nC ? U * c / nC : 0;
+    u1 = c < nC ? U * (c + 1) / nC : 0;
+    h = e = 0;
+    if (u < u1) {
+      h = (int)(u / T);
+      const long long off = u - (long long)h * T;
+      for (int step = 1 << 30; step > 0; step >>= 1)  // the last entry that starts at or before off
+        if (e + step < n_entries && a.entries[e + step].start <= off) e += step;
+    }
+  }
+
+  __device__ void next(const Args& a, Item& it) {
+    it.kind = 0;
+    it.n = 0;
+    while (u < u1 && it.kind == 0) {
       const Entry en = a.entries[e];
-      const long long base = (long long)h * T + en.start, w = en.n_tiles + kOverhead;
-      Item it;
+      const long long base = (long long)h * T + en.start;
       it.kvh = h;
       it.seq = en.seq;
       it.row0 = en.row0;
@@ -202,68 +279,78 @@ __device__ void schedule(const Args& a, Bars* B, Item* items, bool& ok) {
       it.lo = en.lo;
       it.hi = en.hi;
       it.two = D != 256 && it.rows > 128;
-      it.counter = (h * head.n_entries + e) * 2;
+      it.counter = (h * n_entries + e) * 2;
       const long long t0 = max(0LL, u - base - kOverhead), t1 = min((long long)en.n_tiles, u1 - base - kOverhead);
       if (en.n_tiles == 0) {
         it.kind = u == base ? 2 : 0;  // by the CTA that holds its first unit
-        it.n = 0;
-      } else {
-        it.kind = t0 < t1 ? 1 : 0;
+      } else if (t0 < t1) {
+        it.kind = 1;
         it.tile = en.lo / Shape<D>::BN + (int)t0;
         it.n = (int)(t1 - t0);
         it.first_cta = cta_of(base + kOverhead);
         it.n_ctas = cta_of(base + kOverhead + en.n_tiles - 1) - it.first_cta + 1;
         it.slot = t0 == 0 ? 1 : 0;
       }
-      if (it.kind) put(it);
-      u = base + w;
-      if (++e == head.n_entries) {
+      u = base + en.n_tiles + kOverhead;
+      if (++e == n_entries) {
         e = 0;
         ++h;
       }
     }
   }
-  Item end;
-  end.kind = 0;
-  put(end);
-}
+};
 
 // ---------------------------------------------------------------------------
 // locator: the vector of every key of a tile, and its bytes asked for in L2
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+// The two locator warps take half of a tile's rows each; lane's rows are BN / 2 * half + lane + 32 i.  page[i] is the
+// physical page of a row, read one tile ahead.
 template <int D>
-__device__ void locate_tile(const Args& a, const Item& it, int t, long long* loc, uint32_t* miss, int lane) {
+__device__ __forceinline__ void read_pages(const Args& a, const Item& it, int t, int half, int lane,
+                                           int (&page)[Shape<D>::BN / 64]) {
+  const DevBatch& b = a.c.b;
+#pragma unroll
+  for (int i = 0; i < Shape<D>::BN / 64; ++i) {
+    const int j = t * Shape<D>::BN + Shape<D>::BN / 2 * half + 32 * i + lane;
+    const int lp = (int)((uint32_t)j / (uint32_t)a.c.k.page_size);
+    page[i] = b.block_table ? -1 : it.seq;
+    if (b.block_table && j >= it.lo && j < it.hi && lp < b.max_blocks)
+      page[i] = __ldg(b.block_table + (long long)it.seq * b.max_blocks + lp);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void locate_tile(const Args& a, const Item& it, int t, int half, int lane,
+                                            const int (&page)[Shape<D>::BN / 64], long long* loc, uint32_t* miss) {
   constexpr int BN = Shape<D>::BN;
   const DevView &K = a.c.k, &V = a.c.v;
+  const long long first = (long long)a.c.layer * K.num_pages;
 #pragma unroll
-  for (int i = 0; i < BN / 32; ++i) {
-    const int j = t * BN + 32 * i + lane;
-    long long vec = -1;
-    bool bad = false;
-    if (j >= it.lo && j < it.hi) {
-      vec = position_vector(a.c.b, K, a.c.layer, it.seq, j);
-      bad = vec < 0;
-      if (!bad) {
-        vec += (long long)it.kvh * K.page_size;
-        const unsigned char* pk = K.payload + vec * K.pay_bytes;
-        const unsigned char* pv = V.payload + vec * V.pay_bytes;
-        prefetch_l2(pk);
-        prefetch_l2(pv);
-        if constexpr (D == 256) {
-          prefetch_l2(pk + 128);
-          if (V.pay_bytes > 128) prefetch_l2(pv + 128);
-        }
-        prefetch_l2(K.header + vec * K.hdr_bytes);
-        prefetch_l2(V.header + vec * V.hdr_bytes);
-      }
-    }
-    loc[32 * i + lane] = vec;
-    const uint32_t m = __ballot_sync(kFull, bad);
+  for (int i = 0; i < BN / 64; ++i) {
+    const int at = BN / 2 * half + 32 * i + lane, j = t * BN + at;
+    const bool want = j >= it.lo && j < it.hi;
+    const bool on = want && page[i] >= 0 && page[i] < K.num_pages;
+    const int off = j - (int)((uint32_t)j / (uint32_t)K.page_size) * K.page_size;
+    const long long vec = on ? ((first + page[i]) * K.H + it.kvh) * K.page_size + off : -1;
+    loc[at] = vec;
+    const uint32_t m = __ballot_sync(kFull, want && !on);
     if (lane == 0) {
-      miss[i] = m;
+      miss[BN / 64 * half + i] = m;
       if (m) atomicOr(a.c.tab.status, kFlagBlockTable);
+    }
+    if (on) {
+      const unsigned char* pk = K.payload + vec * K.pay_bytes;
+      const unsigned char* pv = V.payload + vec * V.pay_bytes;
+      prefetch_l2(pk);
+      prefetch_l2(pv);
+      if constexpr (D == 256) {
+        prefetch_l2(pk + 128);
+        if (V.pay_bytes > 128) prefetch_l2(pv + 128);
+      }
+      prefetch_l2(K.header + vec * K.hdr_bytes);
+      prefetch_l2(V.header + vec * V.hdr_bytes);
     }
   }
 }
@@ -271,122 +358,178 @@ __device__ void locate_tile(const Args& a, const Item& it, int t, long long* loc
 // ---------------------------------------------------------------------------
 // producers
 // ---------------------------------------------------------------------------
+
+// Loads that leave zeros where on is false, without a branch around them and without a use of the value: all of a
+// tile's loads are in flight at once.
+__device__ __forceinline__ uint4 load16(const void* p, bool on) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"((uint32_t)on));
+  return v;
+}
+__device__ __forceinline__ uint32_t load4(const void* p, bool on) {
+  uint32_t v = 0u;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u32 %0, [%1];\n\t}\n"
+               : "+r"(v)
+               : "l"(p), "r"((uint32_t)on));
+  return v;
+}
+__device__ __forceinline__ uint16_t load2(const void* p, bool on) {
+  uint16_t v = 0;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}\n"
+               : "+h"(v)
+               : "l"(p), "r"((uint32_t)on));
+  return v;
+}
+
+// A thread's units (16 coordinates each) of a tile: rows row0 + 64 i, and of each the quarter lane % 4 of every 64
+// coordinates.  The eight lanes that a 16-byte store is served together for are then two neighbouring rows of four
+// chunks, all in different banks; a row's place is looked up once for all its blocks.
 template <int D, int VB>
 struct Producer {
   static constexpr int BN = Shape<D>::BN;
-  static constexpr int CH = D / 16;                       // units (16 coordinates) per vector
-  static constexpr int UN = BN * CH / (32 * kProdWarps);  // units per thread and tile
-  static constexpr int VW = VB == 0 ? 4 : VB == 3 ? 2 : 1;  // words of a V unit's codes
+  static constexpr int RN = BN / 64, BK = D / 64;  // rows and 64-blocks per thread
+  static_assert(kProdWarps * 8 == 64, "rows per pass");
 
-  struct Raw {
-    uint4 k[UN];
-    uint32_t sc[UN];  // K scale in the low half, V scale (or norm) in the high half
+  struct RawK {
+    uint4 w[RN][BK];
+    uint32_t k[RN][BK];               // K scales of the two 32-blocks of a 64-block
+    uint32_t v[RN][VB == 0 ? BK : 1];  // V scales, or the norm
+  };
+  struct RawV {
+    uint4 w[VB == 0 ? RN : 1][BK];
+    uint32_t c[VB == 2 ? RN : 1][BK];                  // 16 codes of 2 bits
+    uint16_t h[VB & 1 ? RN : 1][BK][VB == 3 ? 3 : 1];  // 16 codes of 1 or 3 bits
   };
 
+  static __device__ __forceinline__ int row_of(int ptid, int i) { return 64 * i + (ptid >> 2); }
+
   // Codes of K and the scales of K and V for the thread's units of a located tile.
-  static __device__ __forceinline__ void load_k(const Args& a, const long long* loc, int ptid, Raw& r) {
+  static __device__ __forceinline__ void load_k(const Args& a, const long long* loc, int ptid, RawK& r) {
     const DevView &K = a.c.k, &V = a.c.v;
+    const int c = ptid & 3;
 #pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      const int unit = ptid + 32 * kProdWarps * i, row = unit / CH, c = unit % CH;
-      const long long vec = loc[row];
-      r.k[i] = make_uint4(0u, 0u, 0u, 0u);
-      r.sc[i] = 0u;
-      if (vec >= 0) {
-        r.k[i] = __ldg(reinterpret_cast<const uint4*>(K.payload + vec * D) + c);
-        const uint32_t hk = __ldg(reinterpret_cast<const unsigned short*>(K.header + vec * (D / 16)) + (c >> 1));
-        const uint32_t hv =
-            VB == 0 ? __ldg(reinterpret_cast<const unsigned short*>(V.header + vec * (D / 16)) + (c >> 1))
-                    : __ldg(reinterpret_cast<const unsigned short*>(V.header + vec * 2));
-        r.sc[i] = hk | (hv << 16);
-      }
-    }
-  }
-
-  static __device__ __forceinline__ void load_v(const Args& a, const long long* loc, int ptid, uint32_t (&v)[UN][VW]) {
-    const DevView& V = a.c.v;
+    for (int i = 0; i < RN; ++i) {
+      const long long vec = loc[row_of(ptid, i)];
+      const bool on = vec >= 0;
+      const unsigned char* pk = K.payload + vec * D + 16 * c;
+      const unsigned char* hk = K.header + vec * (D / 16);
+      const unsigned char* hv = V.header + vec * (VB == 0 ? D / 16 : 2);
 #pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      const int unit = ptid + 32 * kProdWarps * i, row = unit / CH, c = unit % CH;
-      const long long vec = loc[row];
+      for (int b = 0; b < BK; ++b) r.w[i][b] = load16(pk + 64 * b, on);
 #pragma unroll
-      for (int k = 0; k < VW; ++k) v[i][k] = 0u;
-      if (vec >= 0) {
-        if constexpr (VB == 0) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(V.payload + vec * D) + c);
-          v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
-        } else {
-          const unsigned short* p = reinterpret_cast<const unsigned short*>(V.payload + vec * (D * VB / 8)) + VB * c;
-          v[i][0] = __ldg(p);
-          if constexpr (VB >= 2) v[i][0] |= (uint32_t)__ldg(p + 1) << 16;
-          if constexpr (VB == 3) v[i][1] = __ldg(p + 2);
-        }
-      }
-    }
-  }
-
-  // 16 values (8 fp16 pairs) of a unit to its two chunks of the tile; lanes of odd 64-blocks store the second chunk
-  // first, so that the eight lanes of a row hit eight different chunks.
-  static __device__ __forceinline__ void put(unsigned char* tile, int row, int c, const uint32_t (&h)[8]) {
-    const bool swap = (c >> 2) & 1;
-    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-    *reinterpret_cast<uint4*>(tile + tile_at<BN>(row, 2 * c + (swap ? 1 : 0))) = swap ? hi : lo;
-    *reinterpret_cast<uint4*>(tile + tile_at<BN>(row, 2 * c + (swap ? 0 : 1))) = swap ? lo : hi;
-  }
-
-  static __device__ __forceinline__ void q8_unit(const uint32_t (&w)[4], uint32_t scale2, uint32_t (&h)[8]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t x, y;
-      q8_pairs(w[k], x, y);
-      h[2 * k] = mul_h2(x, scale2);
-      h[2 * k + 1] = mul_h2(y, scale2);
-    }
-  }
-
-  static __device__ __forceinline__ void convert_k(const Raw& r, unsigned char* tile, int ptid) {
-#pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      const int unit = ptid + 32 * kProdWarps * i, row = unit / CH, c = unit % CH;
-      const uint32_t w[4] = {r.k[i].x, r.k[i].y, r.k[i].z, r.k[i].w};
-      uint32_t s2 = clamp_scale((uint16_t)r.sc[i]);
-      // a key whose stored K or V is not finite poisons the scores of the rows that see it (the value product of the
-      // others must not meet it)
-      if (not_finite(r.sc[i]) || not_finite(r.sc[i] >> 16)) s2 = 0x7E007E00u;
-      uint32_t h[8];
-      q8_unit(w, s2, h);
-      put(tile, row, c, h);
-    }
-  }
-
-  static __device__ __forceinline__ void convert_v(const uint32_t (&v)[UN][VW], const uint32_t (&sc)[UN],
-                                                   const uint32_t* tab, unsigned char* tile, int ptid) {
-#pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      const int unit = ptid + 32 * kProdWarps * i, row = unit / CH, c = unit % CH;
-      const uint32_t raw = sc[i] >> 16;
-      uint32_t h[8];
+      for (int b = 0; b < BK; ++b) r.k[i][b] = load4(hk + 4 * b, on);
       if constexpr (VB == 0) {
-        const uint32_t s2 = not_finite(raw) ? 0u : clamp_scale((uint16_t)raw);
-        const uint32_t w[4] = {v[i][0], v[i][1], v[i][2], v[i][3]};
-        q8_unit(w, s2, h);
-      } else {
-        const uint32_t s2 = not_finite(raw) ? 0u : raw * 0x10001u;
-        // the codebook (up to 8 fp16 levels) as byte tables: low bytes in lo0, lo1, high bytes in hi0, hi1
-        const uint32_t lo0 = tab[0], lo1 = tab[1], hi0 = tab[2], hi1 = tab[3];
-        const uint64_t codes = VB == 3 ? (uint64_t)v[i][0] | ((uint64_t)v[i][VW - 1] << 32) : (uint64_t)v[i][0];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {  // four codes: nibble selectors of a byte permute
-          const uint32_t x = (uint32_t)(codes >> (4 * VB * g));
-          constexpr uint32_t m = (1u << VB) - 1u;
-          const uint32_t sel = (x & m) | ((x << (4 - VB)) & (m << 4)) | ((x << (8 - 2 * VB)) & (m << 8)) |
-                               ((x << (12 - 3 * VB)) & (m << 12));
-          const uint32_t lb = __byte_perm(lo0, lo1, sel), hb = __byte_perm(hi0, hi1, sel);
-          h[2 * g] = mul_h2(__byte_perm(lb, hb, 0x5140), s2);
-          h[2 * g + 1] = mul_h2(__byte_perm(lb, hb, 0x7362), s2);
+        for (int b = 0; b < BK; ++b) r.v[i][b] = load4(hv + 4 * b, on);
+      } else {
+        r.v[i][0] = load2(hv, on);
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void load_v(const Args& a, const long long* loc, int ptid, RawV& r) {
+    const DevView& V = a.c.v;
+    const int c = ptid & 3;
+#pragma unroll
+    for (int i = 0; i < RN; ++i) {
+      const long long vec = loc[row_of(ptid, i)];
+      const bool on = vec >= 0;
+      const unsigned char* p = V.payload + vec * (VB == 0 ? D : D * VB / 8) + (VB == 0 ? 16 : 2 * VB) * c;
+#pragma unroll
+      for (int b = 0; b < BK; ++b) {
+        if constexpr (VB == 0) r.w[i][b] = load16(p + 64 * b, on);
+        if constexpr (VB == 2) r.c[i][b] = load4(p + 16 * b, on);
+        if constexpr (VB == 1 || VB == 3) {
+#pragma unroll
+          for (int k = 0; k < VB; ++k) r.h[i][b][k] = load2(p + 8 * VB * b + 2 * k, on);
         }
       }
-      put(tile, row, c, h);
+    }
+  }
+
+  // Converts the 16 codes of a q8_0 unit and stores them as chunks 2 c, 2 c + 1 of 64-block b of a row; at: the
+  // chunks' offsets in the block, c0 and c1.
+  static __device__ __forceinline__ void put_q8(unsigned char* tile, uint32_t c0, uint32_t c1, const uint4& w,
+                                                uint32_t s2) {
+    uint32_t x, y;
+    uint4 h;
+    q8_pairs(w.x, x, y);
+    h.x = mul_h2(x, s2);
+    h.y = mul_h2(y, s2);
+    q8_pairs(w.y, x, y);
+    h.z = mul_h2(x, s2);
+    h.w = mul_h2(y, s2);
+    *reinterpret_cast<uint4*>(tile + c0) = h;
+    q8_pairs(w.z, x, y);
+    h.x = mul_h2(x, s2);
+    h.y = mul_h2(y, s2);
+    q8_pairs(w.w, x, y);
+    h.z = mul_h2(x, s2);
+    h.w = mul_h2(y, s2);
+    *reinterpret_cast<uint4*>(tile + c1) = h;
+  }
+
+  // The thread's half of a pair of scales, duplicated.
+  static __device__ __forceinline__ uint32_t scale_of(uint32_t pair, int c) {
+    return __byte_perm(pair, 0u, c & 2 ? 0x3232 : 0x1010);
+  }
+
+  static __device__ __forceinline__ void convert_k(const RawK& r, unsigned char* tile, int ptid) {
+    const int c = ptid & 3;
+#pragma unroll
+    for (int i = 0; i < RN; ++i) {
+      const int row = row_of(ptid, i);
+      const uint32_t c0 = tile_at<BN>(row, 2 * c), c1 = tile_at<BN>(row, 2 * c + 1);
+#pragma unroll
+      for (int b = 0; b < BK; ++b) {
+        const uint32_t sk = scale_of(r.k[i][b], c);
+        const uint32_t sv = VB == 0 ? scale_of(r.v[i][VB == 0 ? b : 0], c) : r.v[i][0];
+        uint32_t s2 = clamp_scale(sk);
+        // a key whose stored K or V is not finite poisons the scores of the rows that see it (the value product of
+        // the others must not meet it)
+        if (not_finite(sk) || not_finite(sv)) s2 = 0x7E007E00u;
+        put_q8(tile + b * (128 * BN), c0, c1, r.w[i][b], s2);
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void convert_v(const RawV& r, const uint32_t (&sv)[RN][VB == 0 ? BK : 1],
+                                                   const uint32_t (&tab)[4], unsigned char* tile, int ptid) {
+    const int c = ptid & 3;
+#pragma unroll
+    for (int i = 0; i < RN; ++i) {
+      const int row = row_of(ptid, i);
+      const uint32_t c0 = tile_at<BN>(row, 2 * c), c1 = tile_at<BN>(row, 2 * c + 1);
+#pragma unroll
+      for (int b = 0; b < BK; ++b) {
+        if constexpr (VB == 0) {
+          const uint32_t s = scale_of(sv[i][b], c);
+          put_q8(tile + b * (128 * BN), c0, c1, r.w[i][b], not_finite(s) ? 0u : clamp_scale(s));
+        } else {
+          const uint32_t s2 = not_finite(sv[i][0]) ? 0u : sv[i][0] * 0x10001u;
+          uint64_t codes;
+          if constexpr (VB == 2) codes = r.c[i][b];
+          else if constexpr (VB == 1) codes = r.h[i][b][0];
+          else codes = (uint64_t)r.h[i][b][0] | ((uint64_t)r.h[i][b][VB - 2] << 16) | ((uint64_t)r.h[i][b][VB - 1] << 32);
+          uint32_t h[8];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {  // four codes: nibble selectors of byte permutes over the level table
+            const uint32_t x = (uint32_t)(codes >> (4 * VB * g));
+            constexpr uint32_t m = (1u << VB) - 1u;
+            const uint32_t sel = (x & m) | ((x << (4 - VB)) & (m << 4)) | ((x << (8 - 2 * VB)) & (m << 8)) |
+                                 ((x << (12 - 3 * VB)) & (m << 12));
+            const uint32_t lb = __byte_perm(tab[0], tab[1], sel), hb = __byte_perm(tab[2], tab[3], sel);
+            h[2 * g] = mul_h2(__byte_perm(lb, hb, 0x5140), s2);
+            h[2 * g + 1] = mul_h2(__byte_perm(lb, hb, 0x7362), s2);
+          }
+          *reinterpret_cast<uint4*>(tile + b * (128 * BN) + c0) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(tile + b * (128 * BN) + c1) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
     }
   }
 };
@@ -400,7 +543,7 @@ __device__ __forceinline__ void load_queries(const Args& a, const Item& it, cons
                                              int warp, int lane) {
   constexpr int LQ = D / 8, RP = 32 / LQ;  // lanes per row, rows per warp and pass
   const int c = lane % LQ, G = a.c.G;
-  constexpr int U = 4;
+  constexpr int U = 2;
   for (int r0 = warp * RP + lane / LQ; __any_sync(kFull, r0 < it.rows); r0 += 8 * RP * U) {
     float x[U][8];
 #pragma unroll
@@ -464,11 +607,11 @@ __device__ __forceinline__ void store8(void* out, int dtype, long long at, const
 template <int D, int VB>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Args a) {
   using Sh = Shape<D>;
-  constexpr int BN = Sh::BN, NB = Sh::NB;
+  constexpr int BN = Sh::BN, NB = Sh::NB, PH = Sh::PH;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = tc::smem_addr(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   Bars* B = reinterpret_cast<Bars*>(sm + Sh::bars);
   Item* items = reinterpret_cast<Item*>(sm + Sh::items);
   long long* loc = reinterpret_cast<long long*>(sm + Sh::loc);
@@ -481,22 +624,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       for (int i = 0; i < 3; ++i) {
         tc::mbar_init(&B->k_full[i], kProdWarps);
         tc::mbar_init(&B->v_full[i], kProdWarps);
-        tc::mbar_init(&B->k_free[i], 1);
-        tc::mbar_init(&B->v_free[i], 1);
+        tc::mbar_init(&B->k_free[i], 2);  // one by each issuer, or both by the only one that uses the tile
+        tc::mbar_init(&B->v_free[i], 2);
       }
-      for (int i = 0; i < 2; ++i) {
-        tc::mbar_init(&B->s_done[i], 1);
+      tc::mbar_init(&B->s_done[0], 1);
+      tc::mbar_init(&B->s_done[1], 1);
+      for (int i = 0; i < 4; ++i) {
         tc::mbar_init(&B->p_full[i], 4);
         tc::mbar_init(&B->pv_done[i], 1);
       }
       tc::mbar_init(&B->q_full, 8);
-      tc::mbar_init(&B->drained, 1);
+      tc::mbar_init(&B->drained[0], 1);
+      tc::mbar_init(&B->drained[1], 1);
       for (int i = 0; i < NI; ++i) {
         tc::mbar_init(&B->item_full[i], 1);
         tc::mbar_init(&B->item_free[i], kItemReaders);
       }
       for (int i = 0; i < NL; ++i) {
-        tc::mbar_init(&B->loc_full[i], 1);
+        tc::mbar_init(&B->loc_full[i], kLocWarps);
         tc::mbar_init(&B->loc_free[i], kProdWarps);
       }
     }
@@ -516,88 +661,121 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = B->tmem;
+  const uint32_t tmem = (uint32_t)uniform((int)B->tmem);
   pdl_wait();  // the plan
   bool ok = true;
   int icnt = 0;  // items so far
-  int gu = 0;    // steps so far
   int gt = 0;    // key tiles so far
 
-  if (warp >= 12) {
+  if (warp >= 8 + kProdWarps) {
     setmaxnreg_dec<kRegsOther>();
-    if (warp == kScheduler) {
-      if (lane == 0) schedule<D>(a, B, items, ok);
-    } else if (warp == kLocator) {
+    if (warp >= kLocator) {
+      const int half = warp - kLocator;
+      Items<D> src;
+      if (half == 0) src.start(a);
+      for (;; ++icnt) {
+        const int is = icnt % NI;
+        if (half == 0) {
+          if (icnt >= NI) wait_warp(ok, &B->item_free[is], icnt / NI - 1);
+          Item it;
+          src.next(a, it);  // (the lanes alike)
+          if (lane == 0) {
+            items[is] = it;
+            tc::mbar_arrive(&B->item_full[is]);
+          }
+          __syncwarp();
+        } else {
+          wait_warp(ok, &B->item_full[is], icnt / NI);
+        }
+        const Item& it = items[is];
+        if (!ok || it.kind == 0) break;
+        const int n = it.n, t0 = it.tile;
+        int page[BN / 64], next[BN / 64];
+        if (n > 0) read_pages<D>(a, it, t0, half, lane, page);
+        for (int j = 0; j < n && ok; ++j, ++gt) {
+          const int s = gt % NL;
+          if (j + 1 < n) read_pages<D>(a, it, t0 + j + 1, half, lane, next);
+          if (gt >= NL) wait_warp(ok, &B->loc_free[s], gt / NL - 1);
+          locate_tile<D>(a, it, t0 + j, half, lane, page, loc + s * BN, miss + (gt % kMissRing) * 4);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&B->loc_full[s]);
+#pragma unroll
+          for (int i = 0; i < BN / 64; ++i) page[i] = next[i];
+        }
+        __syncwarp();
+        if (half && lane == 0) tc::mbar_arrive(&B->item_free[is]);
+      }
+    } else {
+      // The whole warp runs the same code, one lane's predicate on the tensor instructions: descriptors and addresses
+      // then stay in uniform registers, where those instructions take them from.  (With one lane in a branch, every
+      // operand was moved there first, and issuing a product took longer than the product.)
+      const uint32_t one = lane == 0;
+      const int w = warp - kIssuer;  // this issuer's warpgroup
+      int c = 0;                     // its steps so far
+      auto buffer = [&](int x) { return D == 256 ? x & 1 : w; };
+      auto phase = [&](int x) { return D == 256 ? x >> 1 : x; };
+      constexpr uint32_t id_qk = tc::idesc_f16_f32(128, BN);
+      constexpr uint32_t id_pv = tc::idesc_f16_f32(128, D) | (1u << 16);  // B (V) MN-major
+      const uint32_t hi = (uint32_t)(tc::desc_sw128(0) >> 32);  // the same for all operands
+      const uint32_t q_lo = (uint32_t)tc::desc_sw128(sb + Sh::q), k_lo = (uint32_t)tc::desc_sw128(sb + Sh::k);
+      const uint32_t v_lo = (uint32_t)tc::desc_sw128_mn(sb + Sh::v, BN * 128);
       for (;; ++icnt) {
         const int is = icnt % NI;
         wait_warp(ok, &B->item_full[is], icnt / NI);
-        const Item it = items[is];
-        if (!ok || it.kind == 0) break;
-        for (int j = 0; j < it.n && ok; ++j, ++gt) {
-          const int s = gt % NL;
-          if (gt >= NL) wait_warp(ok, &B->loc_free[s], gt / NL - 1);
-          locate_tile<D>(a, it, it.tile + j, loc + s * BN, miss + (gt % kMissRing) * 4, lane);
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&B->loc_full[s]);
+        const int kind = uniform(items[is].kind), n = uniform(items[is].n), two = uniform(items[is].two);
+        if (!ok || kind == 0) break;
+        wait_warp(ok, &B->q_full, icnt);
+        if (kind == 1) {
+          // own steps: every tile (two row tiles: step i is tile i), or every other one; D = 256: the first issuer all
+          const int first = two || D == 256 ? 0 : w, stride = two || D == 256 ? 1 : 2;
+          const int steps = D == 256 && w ? 0 : (n - first + stride - 1) / stride;
+          const uint32_t dq = q_lo + (uint32_t)(two ? w * (Sh::kQTile >> 4) : 0);
+          const bool alone = !two;  // no other issuer uses the tile
+          auto qk = [&](int i) {
+            const int j = gt + first + stride * i, b = j % NB, s = buffer(c + i);
+            wait_warp(ok, &B->k_full[b], j / NB);
+            if (!ok) return;
+            // (no tcgen05 fence: K comes through shared memory, and the score buffer's last readers were seen by the
+            // value product that took their weights)
+            const uint32_t dk = k_lo + (uint32_t)(b * (Sh::kTileB >> 4));
+#pragma unroll
+            for (int kb = 0; kb < D / 64; ++kb)
+              mma4_ss(tmem + s * BN, dq + kb * (128 * 128 >> 4), dk + kb * (128 * BN >> 4), hi, id_qk, kb > 0, one);
+            commit(&B->s_done[s], one);
+            commit(&B->k_free[b], one);
+            if (alone) commit(&B->k_free[b], one);
+          };
+          auto pv = [&](int i) {
+            const int j = gt + first + stride * i, b = j % NB, s = buffer(c + i);
+            wait_warp(ok, &B->v_full[b], j / NB);
+#pragma unroll
+            for (int h = 0; h < PH; ++h) {
+              wait_warp(ok, &B->p_full[s * PH + h], phase(c + i));
+              if (!ok) return;
+              tc::fence_after_sync();
+              mma4_ts(tmem + Sh::tO + w * D, tmem + s * BN + h * (HN / 2),
+                      v_lo + (uint32_t)(b * (Sh::kTileB >> 4) + h * (HN * 128 >> 4)), hi, id_pv, i > 0 || h > 0, one);
+              commit(&B->pv_done[s * PH + h], one);
+            }
+            commit(&B->v_free[b], one);
+            if (alone) commit(&B->v_free[b], one);
+          };
+          // D = 256: one score buffer ahead; else a step's score product needs the buffer of the step before
+          constexpr int kAhead = D == 256 ? 1 : 0;
+          if (steps > 0) qk(0);
+          for (int i = 0; i < steps && ok; ++i) {
+            if (kAhead && i + 1 < steps) qk(i + 1);
+            pv(i);
+            if (!kAhead && i + 1 < steps) qk(i + 1);
+          }
+          c += steps;
+          gt += n;
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
       }
-    } else if (warp == kIssuer) {
-      if (lane == 0) {
-        constexpr uint32_t id_qk = tc::idesc_f16_f32(128, BN);
-        constexpr uint32_t id_pv = tc::idesc_f16_f32(128, D) | (1u << 16);  // B (V) MN-major
-        for (;; ++icnt) {
-          const int is = icnt % NI;
-          wait(ok, &B->item_full[is], icnt / NI);
-          const int kind = items[is].kind, n = items[is].n, two = items[is].two;
-          if (!ok || kind == 0) break;
-          if (kind == 1) {
-            wait(ok, &B->q_full, icnt);
-            const int steps = n << two;
-            auto qk = [&](int u) {
-              const int j = gt + (u >> two), b = j % NB, s = (gu + u) & 1;
-              if (!two || !(u & 1)) wait(ok, &B->k_full[b], j / NB);
-              if (!ok) return;
-              tc::fence_after_sync();
-              const uint64_t dq = tc::desc_sw128(sb + Sh::q + (two ? (u & 1) * Sh::kQTile : 0));
-              const uint64_t dk = tc::desc_sw128(sb + Sh::k + b * Sh::kTileB);
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks)
-                tc::mma_f16(tmem + s * BN, dq + (kstep<128>(ks) >> 4), dk + (kstep<BN>(ks) >> 4), id_qk, ks > 0);
-              tc::commit(&B->s_done[s]);
-              if (!two || (u & 1)) tc::commit(&B->k_free[b]);
-            };
-            auto pv = [&](int u) {
-              const int j = gt + (u >> two), b = j % NB, s = (gu + u) & 1;
-              wait(ok, &B->p_full[s], (gu + u) >> 1);
-              if (!two || !(u & 1)) wait(ok, &B->v_full[b], j / NB);
-              if (!ok) return;
-              tc::fence_after_sync();
-              const uint32_t o = tmem + Sh::tO + (D == 256 ? 0 : (u & 1) * D);
-              const bool fresh = u < (D == 256 ? 1 : 2);
-              const uint64_t dv = tc::desc_sw128_mn(sb + Sh::v + b * Sh::kTileB, BN * 128);
-#pragma unroll
-              for (int ks = 0; ks < BN / 16; ++ks)
-                tc::mma_f16_ts(o, tmem + s * BN + 8 * ks, dv + (uint64_t)(ks * (2048 >> 4)), id_pv, !fresh || ks > 0);
-              tc::commit(&B->pv_done[s]);
-              if (!two || (u & 1)) tc::commit(&B->v_free[b]);
-            };
-            qk(0);
-            for (int u = 0; u < steps && ok; ++u) {
-              if (u + 1 < steps) qk(u + 1);
-              pv(u);
-            }
-            gu += steps;
-            gt += n;
-          } else {
-            wait(ok, &B->q_full, icnt);
-          }
-          tc::mbar_arrive(&B->item_free[is]);
-        }
-        tc::commit(&B->drained);  // products still in flight end before the tensor memory is freed
-        tc::mbar_wait(&B->drained, 0u, 1 << 16);
-      }
+      commit(&B->drained[w], one);  // products still in flight end before the tensor memory is freed
+      tc::mbar_wait(&B->drained[w], 0u, 1 << 16);
     }
     __syncwarp();
   } else if (warp >= 8) {
@@ -609,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < 4; ++i) tab[i] = reinterpret_cast<const uint32_t*>(sm + Sh::tab)[i];
     }
-    typename P::Raw kr;
+    typename P::RawK kr;
     bool loaded = false;  // kr holds the next tile
     for (;; ++icnt) {
       const int is = icnt % NI;
@@ -624,14 +802,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           P::load_k(a, lv, ptid, kr);
         }
         loaded = false;
-        uint32_t vr[P::UN][P::VW], sc[P::UN];
+        typename P::RawV vr;
+        uint32_t sv[P::RN][VB == 0 ? P::BK : 1];
         P::load_v(a, lv, ptid, vr);  // in flight while K is converted
-#pragma unroll
-        for (int i = 0; i < P::UN; ++i) sc[i] = kr.sc[i];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&B->loc_free[s]);
         if (gt >= NB) wait_warp(ok, &B->k_free[b], gt / NB - 1);
         P::convert_k(kr, sm + Sh::k + b * Sh::kTileB, ptid);
+#pragma unroll
+        for (int i = 0; i < P::RN; ++i)
+#pragma unroll
+          for (int e = 0; e < (VB == 0 ? P::BK : 1); ++e) sv[i][e] = kr.v[i][e];
         arrive_smem(&B->k_full[b], lane);
         if (j + 1 < n) {  // the next tile's K in flight while V is converted
           const int s1 = (gt + 1) % NL;
@@ -640,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           loaded = true;
         }
         if (gt >= NB) wait_warp(ok, &B->v_free[b], gt / NB - 1);
-        P::convert_v(vr, sc, tab, sm + Sh::v + b * Sh::kTileB, ptid);
+        P::convert_v(vr, sv, tab, sm + Sh::v + b * Sh::kTileB, ptid);
         arrive_smem(&B->v_full[b], lane);
       }
       __syncwarp();
@@ -649,9 +830,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
     const int wg = warp >> 2, r = tid & 127;
+    int c0 = 0;  // this warpgroup's steps so far
+    auto buffer = [&](int x) { return D == 256 ? x & 1 : wg; };
+    auto phase = [&](int x) { return D == 256 ? x >> 1 : x; };
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const float cap = a.c.softcap;
-    const bool mods = cap > 0.f || a.c.slopes != nullptr;
+    const bool mods = a.c.softcap > 0.f || a.c.slopes != nullptr;
     for (;; ++icnt) {
       const int is = icnt % NI;
       wait_warp(ok, &B->item_full[is], icnt / NI);
@@ -694,110 +877,134 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (a.c.slopes) slope = a.c.slopes[head] * kLog2e;
       }
       const int all_lo = __reduce_max_sync(kFull, lo), all_hi = __reduce_min_sync(kFull, hi);
-      const int steps = it.n << it.two;
-      const int u0 = D == 256 ? (wg == 0 ? 0 : steps) : wg, du = D == 256 ? 1 : 2;
+      const int first = it.two || D == 256 ? 0 : wg, stride = it.two || D == 256 ? 1 : 2;
+      const int steps = D == 256 && wg ? 0 : (it.n - first + stride - 1) / stride;
       const uint32_t t_o = tmem + Sh::tO + (D == 256 ? 0 : wg * D) + lanes;
+      const bool live = valid && lo < hi;  // sees some key
+      const bool any_valid = __any_sync(kFull, valid);  // a warp without rows only keeps the barriers
       float m = -INFINITY, l = 0.f;
-      int last = -1;
-      for (int u = u0; u < steps; u += du) {
-        const int jt = u >> it.two, s = (gu + u) & 1;
-        const int key0 = (it.tile + jt) * BN;
-        wait_warp(ok, &B->s_done[s], (gu + u) >> 1);
+      bool unset = true;  // (of the warp) a row that sees keys has no reference yet
+      int last = -1, last_phase = 0;  // barrier and phase of the last part's value product
+      for (int i = 0; i < steps; ++i) {
+        const int s = buffer(c0 + i), jt = first + stride * i;
+        wait_warp(ok, &B->s_done[s], phase(c0 + i));
         tc::fence_after_sync();
-        const uint32_t t_s = tmem + s * BN + lanes;
-        float x[BN];
-        {
-          uint32_t* w = reinterpret_cast<uint32_t*>(x);
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c) tc::tmem_ld32_nw(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(w + 32 * c));
-          tc::tmem_wait_ld();
-        }
-        float f = sl;
-        if (mods) {  // to log2 units here
-          if (cap > 0.f) {
-            const float fi = 2.f * sl / cap, fo = cap * kLog2e;  // sl holds log2 e: 2^(fi x) = e^(2 s / cap)
-#pragma unroll
-            for (int e = 0; e < BN; ++e) x[e] = fo * (1.f - __fdividef(2.f, 1.f + ex2(x[e] * fi)));
-          } else {
-#pragma unroll
-            for (int e = 0; e < BN; ++e) x[e] *= sl;
-          }
-          const float d0 = (float)(pos - key0);
-#pragma unroll
-          for (int e = 0; e < BN; ++e) x[e] = fmaf(-slope, fabsf(d0 - (float)e), x[e]);
-          f = 1.f;
-        }
-        const uint32_t* mw = miss + ((gt + jt) % kMissRing) * 4;
-        uint32_t any_miss = 0;
-#pragma unroll
-        for (int i = 0; i < BN / 32; ++i) any_miss |= mw[i];
-        if (key0 < all_lo || key0 + BN > all_hi || any_miss) {
-#pragma unroll
-          for (int i = 0; i < BN / 32; ++i) {
-            // visible keys of this 32-group as a bit mask
-            const int p = min(max(lo - key0 - 32 * i, 0), 32), q = min(max(hi - key0 - 32 * i, 0), 32);
-            const uint32_t below_q = q == 32 ? 0xFFFFFFFFu : (1u << q) - 1u;
-            const uint32_t from_p = p == 32 ? 0u : 0xFFFFFFFFu << p;
-            const uint32_t vis = below_q & from_p & ~mw[i];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[32 * i + e] = (vis >> e) & 1u ? x[32 * i + e] : -INFINITY;
-          }
-        }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int e = 4; e < BN; e += 8) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = e + 4 + k < BN ? fmaxf(fmaxf(mx[k], x[e + k]), x[e + 4 + k]) : fmaxf(mx[k], x[e + k]);
-        }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-        // (rows that are not there hold whatever shared memory had: they have no say, so that results do not vary)
-        if (__any_sync(kFull, valid && mt > m + kLazy)) {
-          const float mn = fmaxf(m, mt);
-          const float al = mn == -INFINITY ? 1.f : ex2(m - mn);
-          l *= al;
-          if (last >= 0) {  // the product of this warpgroup's last step is complete
-            if constexpr (D == 256) {
-              wait_warp(ok, &B->pv_done[last & 1], last >> 1);
-              tc::fence_after_sync();
-            }
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tc::tmem_ld32(t_o + 32 * c, o);
+        for (int h = 0; h < PH; ++h) {
+          const int key0 = (it.tile + jt) * BN + h * HN;
+          const uint32_t t_s = tmem + s * BN + h * HN + lanes;
+          if (any_valid) {
+            const uint2 mw = *reinterpret_cast<const uint2*>(miss + ((gt + jt) % kMissRing) * 4 + 2 * h);
+            // steps that need more than a scale are changed in place, in tensor memory
+            const bool special = mods || key0 < all_lo || key0 + HN > all_hi || (mw.x | mw.y) != 0u;
+            if (special) {
+              uint32_t xa[16];
+              const float cap = a.c.softcap, cap_i = 2.f * sl / cap;  // sl holds log2 e: 2^(cap_i x) = e^(2 s / cap)
+#pragma unroll 1
+              for (int c = 0; c < HN / 16; ++c) {
+                tc::tmem_ld16_nw(t_s + 16 * c, xa);
+                loaded(xa);
+                if (cap > 0.f) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-              tc::tmem_st32(t_o + 32 * c, o);
+                  for (int e = 0; e < 16; ++e)
+                    xa[e] = __float_as_uint(cap * kLog2e *
+                                            (1.f - __fdividef(2.f, 1.f + ex2(__uint_as_float(xa[e]) * cap_i))));
+                } else if (mods) {
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) xa[e] = __float_as_uint(__uint_as_float(xa[e]) * sl);
+                }
+                if (slope != 0.f) {
+                  const float d0 = (float)(pos - key0 - 16 * c);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    xa[e] = __float_as_uint(fmaf(-slope, fabsf(d0 - (float)e), __uint_as_float(xa[e])));
+                }
+                // visible keys of these 16 as a bit mask
+                const int p = min(max(lo - key0 - 16 * c, 0), 16), q = min(max(hi - key0 - 16 * c, 0), 16);
+                const uint32_t vis = ((1u << q) - 1u) & (0xFFFFFFFFu << p) & ~((c & 2 ? mw.y : mw.x) >> (16 * (c & 1)));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) xa[e] = (vis >> e) & 1u ? xa[e] : 0xFF800000u;
+                tmem_st16(t_s + 16 * c, xa);
+              }
+              tc::tmem_wait_st();
             }
-          }
-          m = mn;
-        }
-        const float mu = m == -INFINITY ? 0.f : m;
-        const float2 f2 = make_float2(f, f), m2 = make_float2(-mu, -mu);
-        float2 l2[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+            // Weights against the reference so far, and only where that is unset or turns out too low (a row's tile sums
+            // to more than kTop) the row's maximum, a new reference and the weights again: S is still there.
+            const float f = mods ? 1.f : sl;  // scores to log2 units (special tiles are in them already where mods is set)
+            bool raise = unset;
+            uint32_t pk[HN / 2];
+            float sum;
+#pragma unroll 1
+            for (;;) {
+              uint32_t xa[32], xb[32];
+              if (raise) {
+                float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < HN / 16; ++c) {
+                  uint32_t x[16];
+                  tc::tmem_ld16_nw(t_s + 16 * c, x);
+                  loaded(x);
 #pragma unroll
-        for (int c = 0; c < BN / 64; ++c) {
-          uint32_t pk[32];
+                  for (int e = 0; e < 16; e += 4) {
+                    mx0 = fmaxf(fmaxf(mx0, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+                    mx1 = fmaxf(fmaxf(mx1, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
+                  }
+                }
+                const float mn = fmaxf(m, fmaf(fmaxf(mx0, mx1), f, -kBias));
+                const float al = mn == -INFINITY ? 1.f : ex2(m - mn);
+                m = mn;
+                l *= al;
+                unset = __any_sync(kFull, live && m == -INFINITY);
+                if (last >= 0) {  // O, once the product of this warpgroup's last part is complete
+                  wait_warp(ok, &B->pv_done[last], last_phase);
+                  tc::fence_after_sync();
+#pragma unroll 1
+                  for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    tc::tmem_ld16_nw(t_o + 16 * c, o);
+                    loaded(o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int i = 64 * c + 2 * e;
-            float2 p = __ffma2_rn(make_float2(x[i], x[i + 1]), f2, m2);
-            p.x = ex2(p.x);
-            p.y = ex2(p.y);
-            l2[e & 1] = __fadd2_rn(l2[e & 1], p);
-            pk[e] = narrow(p.x, p.y, (const __half*)nullptr);
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                    tmem_st16(t_o + 16 * c, o);
+                  }
+                }
+              }
+              tc::tmem_ld32_nw(t_s, xa);
+              tc::tmem_ld32_nw(t_s + 32, xb);
+              loaded(xa);
+              loaded(xb);
+              const float mu = m == -INFINITY ? 0.f : m;
+              const float2 f2 = make_float2(f, f), m2 = make_float2(-mu, -mu);
+              float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t a0 = e < 16 ? xa[(2 * e) & 31] : xb[(2 * e) & 31];
+                const uint32_t a1 = e < 16 ? xa[(2 * e + 1) & 31] : xb[(2 * e + 1) & 31];
+                float2 p = __ffma2_rn(make_float2(__uint_as_float(a0), __uint_as_float(a1)), f2, m2);
+                p.x = ex2(p.x);
+                p.y = ex2(p.y);
+                l2[e & 1] = __fadd2_rn(l2[e & 1], p);
+                pk[e] = narrow(p.x, p.y, (const __half*)nullptr);
+              }
+              sum = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+              // (rows that are not there hold whatever shared memory had: they have no say, so that results do not vary)
+              if (raise || !__any_sync(kFull, live && sum > kTop)) break;
+              raise = true;
+            }
+            l += sum;
+            tc::tmem_st32(tmem + s * BN + h * (HN / 2) + lanes, pk);  // over scores that have been read
           }
-          tc::tmem_st32(t_s + 32 * c, pk);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&B->p_full[s * PH + h]);
+          last = s * PH + h;
+          last_phase = phase(c0 + i);
         }
-        l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&B->p_full[s]);
-        last = gu + u;
       }
-      if (last >= 0) wait_warp(ok, &B->pv_done[last & 1], last >> 1);
+      if (last >= 0) wait_warp(ok, &B->pv_done[last], last_phase);
       tc::fence_after_sync();
-      gu += steps;
+      c0 += steps;
       gt += it.n;
       const bool mine = D != 256 || wg == 0;  // this warpgroup holds rows
 
@@ -827,9 +1034,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           };
           if constexpr (VB == 0) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < D / 32 && any_valid; ++c) {
               uint32_t o[32];
-              tc::tmem_ld32(t_o + 32 * c, o);
+              tc::tmem_ld32_nw(t_o + 32 * c, o);
+              loaded(o);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 float y[8];
@@ -839,46 +1047,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
             }
           } else {
-            constexpr int N = D == 256 ? 128 : D;
-            float o[N];
-            float4* half = reinterpret_cast<float4*>(sm + Sh::q);  // D = 256: the transform of the first half
+            // diag(s) H: the transform of D = 64 n coordinates is one over the n blocks, taken while they are read
+            // (block p of the result: the blocks with signs (-1)^|p & k|), then one over 64 in registers
+#pragma unroll 1
+            for (int p = 0; p < D / 64 && any_valid; ++p) {
+              float z[64];
 #pragma unroll
-            for (int p = 0; p < D / N; ++p) {
-              {
-                uint32_t* w = reinterpret_cast<uint32_t*>(o);
+              for (int e = 0; e < 64; ++e) z[e] = 0.f;
+#pragma unroll 1
+              for (int k = 0; k < D / 64; ++k) {
+                const float sgn = __popc(p & k) & 1 ? -1.f : 1.f;
 #pragma unroll
-                for (int c = 0; c < N / 32; ++c)
-                  tc::tmem_ld32_nw(t_o + p * N + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(w + 32 * c));
-                tc::tmem_wait_ld();
-              }
-              thread_wht<N>(o);
-              if (D == 256 && p == 0) {
+                for (int c = 0; c < 2; ++c) {
+                  uint32_t o[32];
+                  tc::tmem_ld32_nw(t_o + 64 * k + 32 * c, o);
+                  loaded(o);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) half[r * 32 + (c ^ (r & 31))] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < N / 8; ++k) {
-              float y[8], z[8];
-#pragma unroll
-              for (int e = 0; e < 8; e += 4) {
-                float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (D == 256) b = half[r * 32 + ((2 * k + e / 4) ^ (r & 31))];
-                const float bb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int c = 8 * k + e + i;
-                  const float sgn = norm * (float)a.c.tab.signs[c];
-                  if (D == 256) {
-                    y[e + i] = zero ? 0.f : (bb[i] + o[c]) * sgn;
-                    z[e + i] = zero ? 0.f : (bb[i] - o[c]) * norm * (float)a.c.tab.signs[128 + c];
-                  } else {
-                    y[e + i] = zero ? 0.f : o[c] * sgn;
-                  }
+                  for (int e = 0; e < 32; ++e) z[32 * c + e] = fmaf(sgn, __uint_as_float(o[e]), z[32 * c + e]);
                 }
               }
-              emit(8 * k, y);
-              if (D == 256) emit(128 + 8 * k, z);
+              thread_wht<64>(z);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  y[e] = zero ? 0.f : z[8 * k + e] * norm * (float)a.c.tab.signs[64 * p + 8 * k + e];
+                emit(64 * p + 8 * k, y);
+              }
             }
           }
         } else if (whole && valid) {
