@@ -51,7 +51,7 @@ constexpr float kBias = 4.0f;     // a fresh reference makes the row's largest w
 constexpr float kTop = 32768.0f;  // the reference is raised where a tile's weights sum to more: each is below 65504
 constexpr float kLog2e = 1.4426950408889634074f;
 // Registers per thread after the split; its sum has to be within the launch's (checked at the launch).
-constexpr int kRegsSoftmax = 120, kRegsProducer = 88, kRegsOther = 64;
+constexpr int kRegsSoftmax = 136, kRegsProducer = 72, kRegsOther = 64;
 constexpr int kRegsNeeded = 256 * kRegsSoftmax + 32 * kProdWarps * kRegsProducer + 128 * kRegsOther;
 static_assert(kRegsNeeded <= kThreads * 96, "register split");
 
@@ -99,6 +99,7 @@ struct Bars {
   uint64_t s_done[2], p_full[4], pv_done[4];  // per buffer, per buffer and part
   uint64_t drained[2], q_full, item_full[NI], item_free[NI], loc_full[NL], loc_free[NL];
   uint32_t tmem;
+  volatile int lead;  // tiles of which the first warpgroup's first weights have been taken (two row tiles)
 };
 static_assert(sizeof(Bars) <= 64 * 8, "barriers");
 
@@ -129,6 +130,27 @@ __device__ __forceinline__ void loaded(uint32_t (&x)[16]) {
                  "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]),
                  "+r"(x[15])::"memory");
 }
+// 64 consecutive columns of this warp's tensor-memory lanes, waited for in the same statement: no use of x can move
+// before the wait, and no register is copied to keep it so.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&x)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+        "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]),
+        "=r"(x[16]), "=r"(x[17]), "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]),
+        "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31]),
+        "=r"(x[32]), "=r"(x[33]), "=r"(x[34]), "=r"(x[35]), "=r"(x[36]), "=r"(x[37]), "=r"(x[38]), "=r"(x[39]),
+        "=r"(x[40]), "=r"(x[41]), "=r"(x[42]), "=r"(x[43]), "=r"(x[44]), "=r"(x[45]), "=r"(x[46]), "=r"(x[47]),
+        "=r"(x[48]), "=r"(x[49]), "=r"(x[50]), "=r"(x[51]), "=r"(x[52]), "=r"(x[53]), "=r"(x[54]), "=r"(x[55]),
+        "=r"(x[56]), "=r"(x[57]), "=r"(x[58]), "=r"(x[59]), "=r"(x[60]), "=r"(x[61]), "=r"(x[62]), "=r"(x[63])
+      : "r"(taddr)
+      : "memory");
+}
 // Stores 16 consecutive 32-bit columns of this warp's tensor-memory lanes.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -141,8 +163,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 
 // A wait that gives up for good once one has run out: the role then runs through its loops without waiting (every
 // named barrier is still met), and the error is reported at the end.
+// Polls without a suspend-time hint: with one of 1 us a wait took up to a microsecond longer than the phase.  2^23 polls
+// are a second or more.  SLEEP: nanoseconds between polls, for roles with time in hand (polling takes instruction slots
+// from the others).
+template <int SLEEP = 0>
 __device__ __forceinline__ void wait(bool& ok, uint64_t* bar, uint32_t parity) {
-  if (ok) ok = tc::mbar_wait(bar, parity & 1u);
+  if (!ok) return;
+  uint32_t done = 0;
+  const uint32_t at = tc::smem_addr(bar);
+  for (int i = 0; i < (1 << 23) && !done; ++i) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(at), "r"(parity & 1u)
+        : "memory");
+    if (SLEEP > 0 && !done) __nanosleep(SLEEP);
+  }
+  ok = done != 0;
 }
 
 // A value that all lanes share, in a form that the compiler knows to be shared.
@@ -190,8 +228,9 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
 }
 
 // The same for a whole warp, whose lanes stay of one mind.
+template <int SLEEP = 0>
 __device__ __forceinline__ void wait_warp(bool& ok, uint64_t* bar, uint32_t parity) {
-  wait(ok, bar, parity);
+  wait<SLEEP>(ok, bar, parity);
   ok = __all_sync(kFull, ok);
 }
 
@@ -385,14 +424,15 @@ __device__ __forceinline__ uint16_t load2(const void* p, bool on) {
   return v;
 }
 
-// A thread's units (16 coordinates each) of a tile: rows row0 + 64 i, and of each the quarter lane % 4 of every 64
-// coordinates.  The eight lanes that a 16-byte store is served together for are then two neighbouring rows of four
+// Four warps make the K tiles, four the V tiles.  A thread's units (16 coordinates each) of a tile: rows row0 + 32 i, and
+// of each the quarter lane % 4 of every 64 coordinates; row i of the next tile is asked for as soon as row i of this one
+// is converted.  The eight lanes that a 16-byte store is served together for are then two neighbouring rows of four
 // chunks, all in different banks; a row's place is looked up once for all its blocks.
 template <int D, int VB>
 struct Producer {
   static constexpr int BN = Shape<D>::BN;
-  static constexpr int RN = BN / 64, BK = D / 64;  // rows and 64-blocks per thread
-  static_assert(kProdWarps * 8 == 64, "rows per pass");
+  static constexpr int RN = BN / 32, BK = D / 64;  // rows and 64-blocks per thread
+  static_assert(kProdWarps / 2 * 8 == 32, "rows per pass");
 
   struct RawK {
     uint4 w[RN][BK];
@@ -400,55 +440,55 @@ struct Producer {
     uint32_t v[RN][VB == 0 ? BK : 1];  // V scales, or the norm
   };
   struct RawV {
+    uint32_t s[RN][VB == 0 ? BK : 1];  // scales, or the norm
     uint4 w[VB == 0 ? RN : 1][BK];
     uint32_t c[VB == 2 ? RN : 1][BK];                  // 16 codes of 2 bits
     uint16_t h[VB & 1 ? RN : 1][BK][VB == 3 ? 3 : 1];  // 16 codes of 1 or 3 bits
   };
 
-  static __device__ __forceinline__ int row_of(int ptid, int i) { return 64 * i + (ptid >> 2); }
+  static __device__ __forceinline__ int row_of(int ptid, int i) { return 32 * i + (ptid >> 2); }
 
-  // Codes of K and the scales of K and V for the thread's units of a located tile.
-  static __device__ __forceinline__ void load_k(const Args& a, const long long* loc, int ptid, RawK& r) {
+  // Row i of a located tile.
+  static __device__ __forceinline__ void load_k(const Args& a, const long long* loc, int ptid, int i, RawK& r) {
     const DevView &K = a.c.k, &V = a.c.v;
     const int c = ptid & 3;
+    const long long vec = loc[row_of(ptid, i)];
+    const bool on = vec >= 0;
+    const unsigned char* pk = K.payload + vec * D + 16 * c;
+    const unsigned char* hk = K.header + vec * (D / 16);
+    const unsigned char* hv = V.header + vec * (VB == 0 ? D / 16 : 2);
 #pragma unroll
-    for (int i = 0; i < RN; ++i) {
-      const long long vec = loc[row_of(ptid, i)];
-      const bool on = vec >= 0;
-      const unsigned char* pk = K.payload + vec * D + 16 * c;
-      const unsigned char* hk = K.header + vec * (D / 16);
-      const unsigned char* hv = V.header + vec * (VB == 0 ? D / 16 : 2);
+    for (int b = 0; b < BK; ++b) r.w[i][b] = load16(pk + 64 * b, on);
 #pragma unroll
-      for (int b = 0; b < BK; ++b) r.w[i][b] = load16(pk + 64 * b, on);
+    for (int b = 0; b < BK; ++b) r.k[i][b] = load4(hk + 4 * b, on);
+    if constexpr (VB == 0) {
 #pragma unroll
-      for (int b = 0; b < BK; ++b) r.k[i][b] = load4(hk + 4 * b, on);
-      if constexpr (VB == 0) {
-#pragma unroll
-        for (int b = 0; b < BK; ++b) r.v[i][b] = load4(hv + 4 * b, on);
-      } else {
-        r.v[i][0] = load2(hv, on);
-      }
+      for (int b = 0; b < BK; ++b) r.v[i][b] = load4(hv + 4 * b, on);
+    } else {
+      r.v[i][0] = load2(hv, on);
     }
   }
 
-  static __device__ __forceinline__ void load_v(const Args& a, const long long* loc, int ptid, RawV& r) {
+  static __device__ __forceinline__ void load_v(const Args& a, const long long* loc, int ptid, int i, RawV& r) {
     const DevView& V = a.c.v;
     const int c = ptid & 3;
+    const long long vec = loc[row_of(ptid, i)];
+    const bool on = vec >= 0;
+    const unsigned char* p = V.payload + vec * (VB == 0 ? D : D * VB / 8) + (VB == 0 ? 16 : 2 * VB) * c;
+    const unsigned char* hv = V.header + vec * (VB == 0 ? D / 16 : 2);
 #pragma unroll
-    for (int i = 0; i < RN; ++i) {
-      const long long vec = loc[row_of(ptid, i)];
-      const bool on = vec >= 0;
-      const unsigned char* p = V.payload + vec * (VB == 0 ? D : D * VB / 8) + (VB == 0 ? 16 : 2 * VB) * c;
+    for (int b = 0; b < BK; ++b) {
+      if constexpr (VB == 0) {
+        r.w[i][b] = load16(p + 64 * b, on);
+        r.s[i][b] = load4(hv + 4 * b, on);
+      }
+      if constexpr (VB == 2) r.c[i][b] = load4(p + 16 * b, on);
+      if constexpr (VB == 1 || VB == 3) {
 #pragma unroll
-      for (int b = 0; b < BK; ++b) {
-        if constexpr (VB == 0) r.w[i][b] = load16(p + 64 * b, on);
-        if constexpr (VB == 2) r.c[i][b] = load4(p + 16 * b, on);
-        if constexpr (VB == 1 || VB == 3) {
-#pragma unroll
-          for (int k = 0; k < VB; ++k) r.h[i][b][k] = load2(p + 8 * VB * b + 2 * k, on);
-        }
+        for (int k = 0; k < VB; ++k) r.h[i][b][k] = load2(p + 8 * VB * b + 2 * k, on);
       }
     }
+    if constexpr (VB != 0) r.s[i][0] = load2(hv, on);
   }
 
   // Converts the 16 codes of a q8_0 unit and stores them as chunks 2 c, 2 c + 1 of 64-block b of a row; at: the
@@ -478,57 +518,49 @@ struct Producer {
     return __byte_perm(pair, 0u, c & 2 ? 0x3232 : 0x1010);
   }
 
-  static __device__ __forceinline__ void convert_k(const RawK& r, unsigned char* tile, int ptid) {
-    const int c = ptid & 3;
+  static __device__ __forceinline__ void convert_k(const RawK& r, unsigned char* tile, int ptid, int i) {
+    const int c = ptid & 3, row = row_of(ptid, i);
+    const uint32_t c0 = tile_at<BN>(row, 2 * c), c1 = tile_at<BN>(row, 2 * c + 1);
 #pragma unroll
-    for (int i = 0; i < RN; ++i) {
-      const int row = row_of(ptid, i);
-      const uint32_t c0 = tile_at<BN>(row, 2 * c), c1 = tile_at<BN>(row, 2 * c + 1);
-#pragma unroll
-      for (int b = 0; b < BK; ++b) {
-        const uint32_t sk = scale_of(r.k[i][b], c);
-        const uint32_t sv = VB == 0 ? scale_of(r.v[i][VB == 0 ? b : 0], c) : r.v[i][0];
-        uint32_t s2 = clamp_scale(sk);
-        // a key whose stored K or V is not finite poisons the scores of the rows that see it (the value product of
-        // the others must not meet it)
-        if (not_finite(sk) || not_finite(sv)) s2 = 0x7E007E00u;
-        put_q8(tile + b * (128 * BN), c0, c1, r.w[i][b], s2);
-      }
+    for (int b = 0; b < BK; ++b) {
+      const uint32_t sk = scale_of(r.k[i][b], c);
+      const uint32_t sv = VB == 0 ? scale_of(r.v[i][VB == 0 ? b : 0], c) : r.v[i][0];
+      uint32_t s2 = clamp_scale(sk);
+      // a key whose stored K or V is not finite poisons the scores of the rows that see it (the value product of the
+      // others must not meet it)
+      if (not_finite(sk) || not_finite(sv)) s2 = 0x7E007E00u;
+      put_q8(tile + b * (128 * BN), c0, c1, r.w[i][b], s2);
     }
   }
 
-  static __device__ __forceinline__ void convert_v(const RawV& r, const uint32_t (&sv)[RN][VB == 0 ? BK : 1],
-                                                   const uint32_t (&tab)[4], unsigned char* tile, int ptid) {
-    const int c = ptid & 3;
+  static __device__ __forceinline__ void convert_v(const RawV& r, const uint32_t (&tab)[4], unsigned char* tile, int ptid,
+                                                   int i) {
+    const int c = ptid & 3, row = row_of(ptid, i);
+    const uint32_t c0 = tile_at<BN>(row, 2 * c), c1 = tile_at<BN>(row, 2 * c + 1);
 #pragma unroll
-    for (int i = 0; i < RN; ++i) {
-      const int row = row_of(ptid, i);
-      const uint32_t c0 = tile_at<BN>(row, 2 * c), c1 = tile_at<BN>(row, 2 * c + 1);
+    for (int b = 0; b < BK; ++b) {
+      if constexpr (VB == 0) {
+        const uint32_t s = scale_of(r.s[i][b], c);
+        put_q8(tile + b * (128 * BN), c0, c1, r.w[i][b], not_finite(s) ? 0u : clamp_scale(s));
+      } else {
+        const uint32_t s2 = not_finite(r.s[i][0]) ? 0u : r.s[i][0] * 0x10001u;
+        uint64_t codes;
+        if constexpr (VB == 2) codes = r.c[i][b];
+        else if constexpr (VB == 1) codes = r.h[i][b][0];
+        else codes = (uint64_t)r.h[i][b][0] | ((uint64_t)r.h[i][b][VB - 2] << 16) | ((uint64_t)r.h[i][b][VB - 1] << 32);
+        uint32_t h[8];
 #pragma unroll
-      for (int b = 0; b < BK; ++b) {
-        if constexpr (VB == 0) {
-          const uint32_t s = scale_of(sv[i][b], c);
-          put_q8(tile + b * (128 * BN), c0, c1, r.w[i][b], not_finite(s) ? 0u : clamp_scale(s));
-        } else {
-          const uint32_t s2 = not_finite(sv[i][0]) ? 0u : sv[i][0] * 0x10001u;
-          uint64_t codes;
-          if constexpr (VB == 2) codes = r.c[i][b];
-          else if constexpr (VB == 1) codes = r.h[i][b][0];
-          else codes = (uint64_t)r.h[i][b][0] | ((uint64_t)r.h[i][b][VB - 2] << 16) | ((uint64_t)r.h[i][b][VB - 1] << 32);
-          uint32_t h[8];
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {  // four codes: nibble selectors of byte permutes over the level table
-            const uint32_t x = (uint32_t)(codes >> (4 * VB * g));
-            constexpr uint32_t m = (1u << VB) - 1u;
-            const uint32_t sel = (x & m) | ((x << (4 - VB)) & (m << 4)) | ((x << (8 - 2 * VB)) & (m << 8)) |
-                                 ((x << (12 - 3 * VB)) & (m << 12));
-            const uint32_t lb = __byte_perm(tab[0], tab[1], sel), hb = __byte_perm(tab[2], tab[3], sel);
-            h[2 * g] = mul_h2(__byte_perm(lb, hb, 0x5140), s2);
-            h[2 * g + 1] = mul_h2(__byte_perm(lb, hb, 0x7362), s2);
-          }
-          *reinterpret_cast<uint4*>(tile + b * (128 * BN) + c0) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(tile + b * (128 * BN) + c1) = make_uint4(h[4], h[5], h[6], h[7]);
+        for (int g = 0; g < 4; ++g) {  // four codes: nibble selectors of byte permutes over the level table
+          const uint32_t x = (uint32_t)(codes >> (4 * VB * g));
+          constexpr uint32_t m = (1u << VB) - 1u;
+          const uint32_t sel = (x & m) | ((x << (4 - VB)) & (m << 4)) | ((x << (8 - 2 * VB)) & (m << 8)) |
+                               ((x << (12 - 3 * VB)) & (m << 12));
+          const uint32_t lb = __byte_perm(tab[0], tab[1], sel), hb = __byte_perm(tab[2], tab[3], sel);
+          h[2 * g] = mul_h2(__byte_perm(lb, hb, 0x5140), s2);
+          h[2 * g + 1] = mul_h2(__byte_perm(lb, hb, 0x7362), s2);
         }
+        *reinterpret_cast<uint4*>(tile + b * (128 * BN) + c0) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(tile + b * (128 * BN) + c1) = make_uint4(h[4], h[5], h[6], h[7]);
       }
     }
   }
@@ -622,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     tc::tmem_alloc(&B->tmem, 512);
     if (lane == 0) {
       for (int i = 0; i < 3; ++i) {
-        tc::mbar_init(&B->k_full[i], kProdWarps);
-        tc::mbar_init(&B->v_full[i], kProdWarps);
+        tc::mbar_init(&B->k_full[i], kProdWarps / 2);
+        tc::mbar_init(&B->v_full[i], kProdWarps / 2);
         tc::mbar_init(&B->k_free[i], 2);  // one by each issuer, or both by the only one that uses the tile
         tc::mbar_init(&B->v_free[i], 2);
       }
@@ -634,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         tc::mbar_init(&B->pv_done[i], 1);
       }
       tc::mbar_init(&B->q_full, 8);
+      B->lead = 0;
       tc::mbar_init(&B->drained[0], 1);
       tc::mbar_init(&B->drained[1], 1);
       for (int i = 0; i < NI; ++i) {
@@ -676,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       for (;; ++icnt) {
         const int is = icnt % NI;
         if (half == 0) {
-          if (icnt >= NI) wait_warp(ok, &B->item_free[is], icnt / NI - 1);
+          if (icnt >= NI) wait_warp<100>(ok, &B->item_free[is], icnt / NI - 1);
           Item it;
           src.next(a, it);  // (the lanes alike)
           if (lane == 0) {
@@ -685,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           }
           __syncwarp();
         } else {
-          wait_warp(ok, &B->item_full[is], icnt / NI);
+          wait_warp<100>(ok, &B->item_full[is], icnt / NI);
         }
         const Item& it = items[is];
         if (!ok || it.kind == 0) break;
@@ -695,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         for (int j = 0; j < n && ok; ++j, ++gt) {
           const int s = gt % NL;
           if (j + 1 < n) read_pages<D>(a, it, t0 + j + 1, half, lane, next);
-          if (gt >= NL) wait_warp(ok, &B->loc_free[s], gt / NL - 1);
+          if (gt >= NL) wait_warp<100>(ok, &B->loc_free[s], gt / NL - 1);
           locate_tile<D>(a, it, t0 + j, half, lane, page, loc + s * BN, miss + (gt % kMissRing) * 4);
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&B->loc_full[s]);
@@ -733,6 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const bool alone = !two;  // no other issuer uses the tile
           auto qk = [&](int i) {
             const int j = gt + first + stride * i, b = j % NB, s = buffer(c + i);
+            if (two && w) {
+              // The second warpgroup half a tile behind the first: in step, both would be in the softmax, and both waiting
+              // for the tensor core, at the same time.
+              for (int k = 0; k < (1 << 22) && B->lead <= j && ok; ++k) {}
+              if (B->lead <= j) ok = false;
+              ok = __all_sync(kFull, ok);
+            }
             wait_warp(ok, &B->k_full[b], j / NB);
             if (!ok) return;
             // (no tcgen05 fence: K comes through shared memory, and the score buffer's last readers were seen by the
@@ -756,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               mma4_ts(tmem + Sh::tO + w * D, tmem + s * BN + h * (HN / 2),
                       v_lo + (uint32_t)(b * (Sh::kTileB >> 4) + h * (HN * 128 >> 4)), hi, id_pv, i > 0 || h > 0, one);
               commit(&B->pv_done[s * PH + h], one);
+              if (two && !w && h == 0 && one) B->lead = j + 1;
             }
             commit(&B->v_free[b], one);
             if (alone) commit(&B->v_free[b], one);
@@ -770,6 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           }
           c += steps;
           gt += n;
+          if (!two && !w && one) B->lead = gt;  // (the next item may have two row tiles)
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
@@ -781,51 +823,50 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   } else if (warp >= 8) {
     setmaxnreg_dec<kRegsProducer>();
     using P = Producer<D, VB>;
-    const int ptid = tid - 256;
-    uint32_t tab[4] = {0u, 0u, 0u, 0u};
-    if constexpr (VB > 0) {
+    const int ptid = tid & 127;
+    // One role's tiles: convert row i, ask for row i of the next tile; raw holds the codes between.
+    auto produce = [&](auto& raw, auto load, auto convert, uint64_t* full, uint64_t* free, int tiles_at) {
+      for (;; ++icnt) {
+        const int is = icnt % NI;
+        wait_warp<40>(ok, &B->item_full[is], icnt / NI);
+        const int kind = items[is].kind, n = items[is].n;
+        if (!ok || kind == 0) break;
+        if (n > 0) {
+          wait_warp<40>(ok, &B->loc_full[gt % NL], gt / NL);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tab[i] = reinterpret_cast<const uint32_t*>(sm + Sh::tab)[i];
-    }
-    typename P::RawK kr;
-    bool loaded = false;  // kr holds the next tile
-    for (;; ++icnt) {
-      const int is = icnt % NI;
-      wait_warp(ok, &B->item_full[is], icnt / NI);
-      const int kind = items[is].kind, n = items[is].n;
-      if (!ok || kind == 0) break;
-      for (int j = 0; j < n && ok; ++j, ++gt) {
-        const int s = gt % NL, b = gt % NB;
-        const long long* lv = loc + s * BN;
-        if (!loaded) {
-          wait_warp(ok, &B->loc_full[s], gt / NL);
-          P::load_k(a, lv, ptid, kr);
+          for (int i = 0; i < P::RN; ++i) load(a, loc + (gt % NL) * BN, ptid, i, raw);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&B->loc_free[gt % NL]);
         }
-        loaded = false;
-        typename P::RawV vr;
-        uint32_t sv[P::RN][VB == 0 ? P::BK : 1];
-        P::load_v(a, lv, ptid, vr);  // in flight while K is converted
+        for (int j = 0; j < n && ok; ++j, ++gt) {
+          const int b = gt % NB, s1 = (gt + 1) % NL;
+          const bool more = j + 1 < n;
+          if (more) wait_warp<40>(ok, &B->loc_full[s1], (gt + 1) / NL);
+          if (gt >= NB) wait_warp<40>(ok, &free[b], gt / NB - 1);
+#pragma unroll
+          for (int i = 0; i < P::RN; ++i) {
+            convert(raw, sm + tiles_at + b * Sh::kTileB, ptid, i);
+            if (more) load(a, loc + s1 * BN, ptid, i, raw);
+          }
+          arrive_smem(&full[b], lane);
+          if (more && lane == 0) tc::mbar_arrive(&B->loc_free[s1]);
+        }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&B->loc_free[s]);
-        if (gt >= NB) wait_warp(ok, &B->k_free[b], gt / NB - 1);
-        P::convert_k(kr, sm + Sh::k + b * Sh::kTileB, ptid);
-#pragma unroll
-        for (int i = 0; i < P::RN; ++i)
-#pragma unroll
-          for (int e = 0; e < (VB == 0 ? P::BK : 1); ++e) sv[i][e] = kr.v[i][e];
-        arrive_smem(&B->k_full[b], lane);
-        if (j + 1 < n) {  // the next tile's K in flight while V is converted
-          const int s1 = (gt + 1) % NL;
-          wait_warp(ok, &B->loc_full[s1], (gt + 1) / NL);
-          P::load_k(a, loc + s1 * BN, ptid, kr);
-          loaded = true;
-        }
-        if (gt >= NB) wait_warp(ok, &B->v_free[b], gt / NB - 1);
-        P::convert_v(vr, sv, tab, sm + Sh::v + b * Sh::kTileB, ptid);
-        arrive_smem(&B->v_full[b], lane);
+        if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
       }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
+    };
+    if (warp < 8 + kProdWarps / 2) {
+      typename P::RawK raw;
+      produce(raw, P::load_k, P::convert_k, B->k_full, B->k_free, Sh::k);
+    } else {
+      uint32_t tab[4] = {0u, 0u, 0u, 0u};
+      if constexpr (VB > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tab[i] = reinterpret_cast<const uint32_t*>(sm + Sh::tab)[i];
+      }
+      typename P::RawV raw;
+      produce(raw, P::load_v, [&](const typename P::RawV& r, unsigned char* tile, int t, int i) { P::convert_v(r, tab, tile, t, i); },
+              B->v_full, B->v_free, Sh::v);
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
@@ -887,7 +928,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       int last = -1, last_phase = 0;  // barrier and phase of the last part's value product
       for (int i = 0; i < steps; ++i) {
         const int s = buffer(c0 + i), jt = first + stride * i;
-        wait_warp(ok, &B->s_done[s], phase(c0 + i));
+        if ((warp & 3) == 0) wait_warp(ok, &B->s_done[s], phase(c0 + i));
+        tc::bar_sync(2 + wg, 128);
         tc::fence_after_sync();
 #pragma unroll 1
         for (int h = 0; h < PH; ++h) {
@@ -936,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             float sum;
 #pragma unroll 1
             for (;;) {
-              uint32_t xa[32], xb[32];
+              uint32_t x[64];
               if (raise) {
                 float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
@@ -969,18 +1011,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                   }
                 }
               }
-              tc::tmem_ld32_nw(t_s, xa);
-              tc::tmem_ld32_nw(t_s + 32, xb);
-              loaded(xa);
-              loaded(xb);
+              tmem_ld64(t_s, x);
               const float mu = m == -INFINITY ? 0.f : m;
               const float2 f2 = make_float2(f, f), m2 = make_float2(-mu, -mu);
               float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const uint32_t a0 = e < 16 ? xa[(2 * e) & 31] : xb[(2 * e) & 31];
-                const uint32_t a1 = e < 16 ? xa[(2 * e + 1) & 31] : xb[(2 * e + 1) & 31];
-                float2 p = __ffma2_rn(make_float2(__uint_as_float(a0), __uint_as_float(a1)), f2, m2);
+                float2 p = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2, m2);
                 p.x = ex2(p.x);
                 p.y = ex2(p.y);
                 l2[e & 1] = __fadd2_rn(l2[e & 1], p);
@@ -1009,8 +1046,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const bool mine = D != 256 || wg == 0;  // this warpgroup holds rows
 
       // ---- the result: O / l where this warpgroup alone has the rows, else a partial result ----
-      const int parts = D == 256 || it.two ? it.n_ctas : 2 * it.n_ctas;
-      const bool whole = parts == 1;
+      const int shares = D == 256 || it.two ? it.n_ctas : 2 * it.n_ctas;
+      const bool whole = shares == 1;
       // partial slots: [CTA][start or end of its range][warpgroup][rows][D], then m and l of each
       auto slot_of = [&](int cta, int which, int w) { return ((long long)cta * 2 + which) * 2 + w; };
       const long long my_slot = slot_of(blockIdx.x, it.slot, wg);
@@ -1086,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           __threadfence();
           tc::bar_sync(2 + wg, 128);
           int done = 0;
-          if (r == 0) done = (int)atomicAdd(a.counters + it.counter + (it.two ? wg : 0), 1u) == parts - 1;
+          if (r == 0) done = (int)atomicAdd(a.counters + it.counter + (it.two ? wg : 0), 1u) == shares - 1;
           const bool join = tc::bar_sync_or(2 + wg, 128, done != 0);
           if (join) {
             __threadfence();
@@ -1095,7 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             for (int i = r; i < nrows * (D / 8); i += 128) {
               const int jr = i / (D / 8), jc = i % (D / 8);
               float top = -INFINITY;
-              for (int p = 0; p < parts; ++p) {
+              for (int p = 0; p < shares; ++p) {
                 const int ci = p / per;
                 const long long sl_ = slot_of(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? p % 2 : wg);
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + sl_ * a.rows_cap * 2) + jr);
@@ -1103,7 +1140,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
               if (top == -INFINITY) top = 0.f;
               float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, lt = 0.f;
-              for (int p = 0; p < parts; ++p) {
+              for (int p = 0; p < shares; ++p) {
                 const int ci = p / per;
                 const long long sl_ = slot_of(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? p % 2 : wg);
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + sl_ * a.rows_cap * 2) + jr);
