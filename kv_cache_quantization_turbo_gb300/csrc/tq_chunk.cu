@@ -13,7 +13,8 @@ using ck::Args;
 using ck::Entry;
 using ck::PlanHead;
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
+constexpr int kNear = 1024;  // sequences whose entry counts are kept in shared memory
 
 struct PlanArgs {
   ChunkArgs c;
@@ -36,18 +37,19 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
   __syncthreads();  // the sums of the scan before are not read any more
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  long long before = 0, all = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    const long long s = warp_sums[w];
-    if (w < warp) before += s;
-    all += s;
+  long long w = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long y = __shfl_up_sync(kFull, w, m);
+    if (lane >= m) w += y;
   }
-  *total = all;
-  return before + v - x;
+  *total = __shfl_sync(kFull, w, 31);
+  return __shfl_sync(kFull, w, warp) - warp_sums[warp] + v - x;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
   __shared__ long long warp_sums[kPlanThreads / 32];
+  __shared__ int near_base[kNear];
   const ChunkArgs& a = p.c;
   const int tid = threadIdx.x, G = a.G;
   long long carry = 0, total;
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       }
     }
     const long long at = carry + block_scan(ne, warp_sums, &total);
-    if (b < a.b.n_seqs) p.seq_base[b] = (int)min(at, (long long)p.max_entries);
+    if (b < a.b.n_seqs) (a.b.n_seqs <= kNear ? near_base : p.seq_base)[b] = (int)min(at, (long long)p.max_entries);
     carry += total;
   }
   // more entries than rows can hold: sequences that overlap (cu_tokens not ascending); the last ones are left out
@@ -78,46 +80,63 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     carry = p.max_entries;
   }
   const int E = (int)carry;
+  const int* seq_base = a.b.n_seqs <= kNear ? near_base : p.seq_base;
   __syncthreads();
   carry = 0;
   for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
     const int e = e0 + tid;
     Entry en{};
+    SeqOf s{};
+    int i0 = 0, i1 = -1, prefix = 0;  // tokens of the entry
     if (e < E) {
       int lo = 0, hi = a.b.n_seqs;  // the last sequence with seq_base <= e
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.seq_base[mid] <= e) lo = mid;
+        if (seq_base[mid] <= e) lo = mid;
         else hi = mid;
       }
-      const SeqOf s = seq_of(a.b, lo);
+      s = seq_of(a.b, lo);
       en.seq = lo;
-      en.row0 = (e - p.seq_base[lo]) * p.rows;
+      en.row0 = (e - seq_base[lo]) * p.rows;
       const int rows = min(p.rows, s.n * G - en.row0);
-      const int i0 = en.row0 / G, i1 = (en.row0 + rows - 1) / G;  // tokens
-      const int pos0 = s.len - s.n;
-      const int prefix = a.prefix_lens ? a.prefix_lens[lo] : 0;
-      int first = 0x7FFFFFFF, last = 0;
-      if (a.first_keys) {
-        for (int i = i0; i <= i1; ++i) {
-          const int pos = pos0 + i;
-          const int h = min(s.len, max(pos + 1, prefix));
-          int l = max(0, a.first_keys[s.first + i]);
-          if (a.window) l = max(l, pos - a.window + 1);
-          if (l < h) {
-            first = min(first, l);
-            last = max(last, h);
+      i0 = en.row0 / G;
+      i1 = (en.row0 + rows - 1) / G;
+      prefix = a.prefix_lens ? a.prefix_lens[lo] : 0;
+    }
+    int first = 0x7FFFFFFF, last = 0;
+    if (a.first_keys) {
+      // a warp looks at its lanes' entries one after another, 32 tokens at a time
+      const int lane = tid & 31;
+      for (int l = 0; l < 32; ++l) {
+        const int j0 = __shfl_sync(kFull, i0, l), j1 = __shfl_sync(kFull, i1, l), pre = __shfl_sync(kFull, prefix, l);
+        const int row = __shfl_sync(kFull, s.first, l), len = __shfl_sync(kFull, s.len, l);
+        const int pos0 = len - __shfl_sync(kFull, s.n, l);
+        int f = 0x7FFFFFFF, t = 0;
+        for (int i = j0 + lane; i <= j1; i += 32) {
+          const int pos = pos0 + i, h = min(len, max(pos + 1, pre));
+          int k = max(0, __ldg(a.first_keys + row + i));
+          if (a.window) k = max(k, pos - a.window + 1);
+          if (k < h) {
+            f = min(f, k);
+            t = max(t, h);
           }
         }
-      } else {
-        first = a.window ? max(0, pos0 + i0 - a.window + 1) : 0;
-        last = min(s.len, max(pos0 + i1 + 1, prefix));
+        f = __reduce_min_sync(kFull, f);
+        t = __reduce_max_sync(kFull, t);
+        if (lane == l) {
+          first = f;
+          last = t;
+        }
       }
-      if (first < last) {
-        en.lo = first;
-        en.hi = last;
-        en.n_tiles = (last + p.keys - 1) / p.keys - first / p.keys;
-      }
+    } else if (e < E) {
+      const int pos0 = s.len - s.n;
+      first = a.window ? max(0, pos0 + i0 - a.window + 1) : 0;
+      last = min(s.len, max(pos0 + i1 + 1, prefix));
+    }
+    if (first < last) {
+      en.lo = first;
+      en.hi = last;
+      en.n_tiles = (last + p.keys - 1) / p.keys - first / p.keys;
     }
     const long long at = carry + block_scan(e < E ? en.n_tiles + ck::kOverhead : 0, warp_sums, &total);
     if (e < E) {

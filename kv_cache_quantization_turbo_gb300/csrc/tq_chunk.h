@@ -29,7 +29,7 @@ struct Args {
   const PlanHead* plan;
   const Entry* entries;
   unsigned int* counters;  // [KV head][entry][row tile]: partial results so far
-  float* part_o;           // [CTA][2][2][rows_cap][D]
+  float* part_o;           // [CTA][2][2][D / 4][rows_cap][4]
   float* part_ml;          // [CTA][2][2][rows_cap][2]: reference (log2 units), sum
   int rows_cap;
   float scale, q_sign;     // |softmax_scale| log2 e and its sign (0 for a scale of 0)

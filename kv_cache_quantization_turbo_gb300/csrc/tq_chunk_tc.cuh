@@ -99,7 +99,6 @@ struct Bars {
   uint64_t s_done[2], p_full[4], pv_done[4];  // per buffer, per buffer and part
   uint64_t drained[2], q_full, item_full[NI], item_free[NI], loc_full[NL], loc_free[NL];
   uint32_t tmem;
-  volatile int lead;  // tiles of which the first warpgroup's first weights have been taken (two row tiles)
 };
 static_assert(sizeof(Bars) <= 64 * 8, "barriers");
 
@@ -380,7 +379,8 @@ __device__ __forceinline__ void locate_tile(const Args& a, const Item& it, int t
       if (m) atomicOr(a.c.tab.status, kFlagBlockTable);
     }
     if (on) {
-      const unsigned char* pk = K.payload + vec * K.pay_bytes;
+      // (a line per lane: bulk requests for the runs of a page measured 7 % slower on a paged decode batch)
+      const unsigned char* pk = K.payload + vec * D;
       const unsigned char* pv = V.payload + vec * V.pay_bytes;
       prefetch_l2(pk);
       prefetch_l2(pv);
@@ -574,34 +574,35 @@ template <int D, class T>
 __device__ __forceinline__ void load_queries(const Args& a, const Item& it, const T* q, unsigned char* sq, float* rs,
                                              int warp, int lane) {
   constexpr int LQ = D / 8, RP = 32 / LQ;  // lanes per row, rows per warp and pass
+  constexpr int W = sizeof(T) / 2;         // 16-byte words of 8 elements
+  constexpr int U = 8 / W;                 // rows in flight
   const int c = lane % LQ, G = a.c.G;
-  constexpr int U = 2;
   for (int r0 = warp * RP + lane / LQ; __any_sync(kFull, r0 < it.rows); r0 += 8 * RP * U) {
-    float x[U][8];
+    uint4 raw[U][W];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = r0 + 8 * RP * u;
-      if (r < it.rows) {
-        const int row = it.row0 + r, i = row / G, g = row - i * G;
-        load_row<8>(q + (long long)(it.tok0 + i) * a.c.q_stride + (long long)(it.kvh * G + g) * D + 8 * c, x[u]);
-      }
+      const int r = r0 + 8 * RP * u, row = it.row0 + r, i = row / G, g = row - i * G;
+      const T* src = q + (long long)(it.tok0 + i) * a.c.q_stride + (long long)(it.kvh * G + g) * D + 8 * c;
+#pragma unroll
+      for (int k = 0; k < W; ++k) raw[u][k] = load16(reinterpret_cast<const uint4*>(src) + k, r < it.rows);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = r0 + 8 * RP * u;
-      const bool on = r < it.rows;
+      float x[8];
+      load_row<8>(reinterpret_cast<const T*>(raw[u]), x);
       uint32_t top = 0;  // bits of the largest magnitude (NaN above all)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, on ? __float_as_uint(x[u][e]) & 0x7FFFFFFFu : 0u);
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
 #pragma unroll
       for (int m = 1; m < LQ; m <<= 1) top = max(top, __shfl_xor_sync(kFull, top, m));
       uint32_t ex = min(max(top >> 23, 1u), 253u);
       if (top >= 0x7F800000u) ex = 127u;  // infinite or NaN: as it is
       const float f = a.q_sign * __uint_as_float((254u - ex) << 23);
-      if (on) {
+      if (r < it.rows) {
         uint32_t h[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = narrow(x[u][2 * e] * f, x[u][2 * e + 1] * f, (const __half*)nullptr);
+        for (int e = 0; e < 4; ++e) h[e] = narrow(x[2 * e] * f, x[2 * e + 1] * f, (const __half*)nullptr);
         *reinterpret_cast<uint4*>(sq + (r >> 7) * Shape<D>::kQTile + tile_at<128>(r & 127, c)) =
             make_uint4(h[0], h[1], h[2], h[3]);
         if (c == 0) rs[r] = __uint_as_float(ex << 23);
@@ -666,7 +667,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         tc::mbar_init(&B->pv_done[i], 1);
       }
       tc::mbar_init(&B->q_full, 8);
-      B->lead = 0;
       tc::mbar_init(&B->drained[0], 1);
       tc::mbar_init(&B->drained[1], 1);
       for (int i = 0; i < NI; ++i) {
@@ -766,13 +766,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const bool alone = !two;  // no other issuer uses the tile
           auto qk = [&](int i) {
             const int j = gt + first + stride * i, b = j % NB, s = buffer(c + i);
-            if (two && w) {
-              // The second warpgroup half a tile behind the first: in step, both would be in the softmax, and both waiting
-              // for the tensor core, at the same time.
-              for (int k = 0; k < (1 << 22) && B->lead <= j && ok; ++k) {}
-              if (B->lead <= j) ok = false;
-              ok = __all_sync(kFull, ok);
-            }
             wait_warp(ok, &B->k_full[b], j / NB);
             if (!ok) return;
             // (no tcgen05 fence: K comes through shared memory, and the score buffer's last readers were seen by the
@@ -796,7 +789,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               mma4_ts(tmem + Sh::tO + w * D, tmem + s * BN + h * (HN / 2),
                       v_lo + (uint32_t)(b * (Sh::kTileB >> 4) + h * (HN * 128 >> 4)), hi, id_pv, i > 0 || h > 0, one);
               commit(&B->pv_done[s * PH + h], one);
-              if (two && !w && h == 0 && one) B->lead = j + 1;
             }
             commit(&B->v_free[b], one);
             if (alone) commit(&B->v_free[b], one);
@@ -811,7 +803,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           }
           c += steps;
           gt += n;
-          if (!two && !w && one) B->lead = gt;  // (the next item may have two row tiles)
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
@@ -928,8 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       int last = -1, last_phase = 0;  // barrier and phase of the last part's value product
       for (int i = 0; i < steps; ++i) {
         const int s = buffer(c0 + i), jt = first + stride * i;
-        if ((warp & 3) == 0) wait_warp(ok, &B->s_done[s], phase(c0 + i));
-        tc::bar_sync(2 + wg, 128);
+        wait_warp(ok, &B->s_done[s], phase(c0 + i));
         tc::fence_after_sync();
 #pragma unroll 1
         for (int h = 0; h < PH; ++h) {
@@ -983,13 +973,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < HN / 16; ++c) {
-                  uint32_t x[16];
-                  tc::tmem_ld16_nw(t_s + 16 * c, x);
-                  loaded(x);
+                  uint32_t y[16];
+                  tc::tmem_ld16_nw(t_s + 16 * c, y);
+                  loaded(y);
 #pragma unroll
                   for (int e = 0; e < 16; e += 4) {
-                    mx0 = fmaxf(fmaxf(mx0, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
-                    mx1 = fmaxf(fmaxf(mx1, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
+                    mx0 = fmaxf(fmaxf(mx0, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
+                    mx1 = fmaxf(fmaxf(mx1, __uint_as_float(y[e + 2])), __uint_as_float(y[e + 3]));
                   }
                 }
                 const float mn = fmaxf(m, fmaf(fmaxf(mx0, mx1), f, -kBias));
@@ -1048,10 +1038,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       // ---- the result: O / l where this warpgroup alone has the rows, else a partial result ----
       const int shares = D == 256 || it.two ? it.n_ctas : 2 * it.n_ctas;
       const bool whole = shares == 1;
-      // partial slots: [CTA][start or end of its range][warpgroup][rows][D], then m and l of each
+      // partial slots: [CTA][start or end of its range][warpgroup], O and then m and l of each
       auto slot_of = [&](int cta, int which, int w) { return ((long long)cta * 2 + which) * 2 + w; };
       const long long my_slot = slot_of(blockIdx.x, it.slot, wg);
-      float* po = a.part_o + my_slot * a.rows_cap * D + (long long)r * D;
+      // (a share's O: [D / 4][rows_cap] float4, so that the rows of a warp are consecutive)
+      float4* po = reinterpret_cast<float4*>(a.part_o + my_slot * a.rows_cap * D) + r;
       float norm = a.inv_lam_v;  // folds 1 / lambda and the transform's 1 / sqrt(D)
       if constexpr (VB > 0) norm *= inv_sqrt_dim<D>();
       if (mine) {
@@ -1067,7 +1058,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           auto emit = [&](int col, const float (&y)[8]) {  // eight columns of this thread's row
             if (!valid) return;
             if (whole) store8(a.c.out, a.c.out_dtype, out_at + col, y);
-            else store_row<8>(po + col, y);
+            else {
+              po[(col >> 2) * a.rows_cap] = make_float4(y[0], y[1], y[2], y[3]);
+              po[((col >> 2) + 1) * a.rows_cap] = make_float4(y[4], y[5], y[6], y[7]);
+            }
           };
           if constexpr (VB == 0) {
 #pragma unroll 1
@@ -1129,37 +1123,56 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             __threadfence();
             const int nrows = min(128, it.rows - (it.two ? 128 * wg : 0));
             const int per = D == 256 || it.two ? 1 : 2;  // partial results per CTA
-            for (int i = r; i < nrows * (D / 8); i += 128) {
-              const int jr = i / (D / 8), jc = i % (D / 8);
+#pragma unroll 1
+            for (int i = r; i < nrows * (D / 4); i += 128) {
+              const int jr = i % nrows, jc = i / nrows;
+              // (many loads in flight together; what a share without weight holds is not looked at)
+              auto share = [&](int p) {
+                const int q = min(p, shares - 1), ci = per == 2 ? q >> 1 : q;
+                return slot_of(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? q & 1 : wg) * a.rows_cap;
+              };
+              auto ml_of = [&](long long at) { return __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2) + jr); };
               float top = -INFINITY;
-              for (int p = 0; p < shares; ++p) {
-                const int ci = p / per;
-                const long long sl_ = slot_of(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? p % 2 : wg);
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + sl_ * a.rows_cap * 2) + jr);
-                if (ml.y != 0.f) top = fmaxf(top, ml.x);
+#pragma unroll 1
+              for (int p0 = 0; p0 < shares; p0 += 8) {
+                float2 ml[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) ml[k] = ml_of(share(p0 + k));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].y != 0.f ? ml[k].x : -INFINITY);
               }
               if (top == -INFINITY) top = 0.f;
-              float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, lt = 0.f;
-              for (int p = 0; p < shares; ++p) {
-                const int ci = p / per;
-                const long long sl_ = slot_of(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? p % 2 : wg);
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + sl_ * a.rows_cap * 2) + jr);
-                if (ml.y == 0.f) continue;
-                const float w = ex2(ml.x - top);
-                lt = fmaf(w, ml.y, lt);
-                const float4* src = reinterpret_cast<const float4*>(a.part_o + (sl_ * a.rows_cap + jr) * D + 8 * jc);
-                const float4 x0 = __ldcg(src), x1 = __ldcg(src + 1);
-                acc[0] = fmaf(w, x0.x, acc[0]); acc[1] = fmaf(w, x0.y, acc[1]);
-                acc[2] = fmaf(w, x0.z, acc[2]); acc[3] = fmaf(w, x0.w, acc[3]);
-                acc[4] = fmaf(w, x1.x, acc[4]); acc[5] = fmaf(w, x1.y, acc[5]);
-                acc[6] = fmaf(w, x1.z, acc[6]); acc[7] = fmaf(w, x1.w, acc[7]);
+              float acc[4] = {0.f, 0.f, 0.f, 0.f}, lt = 0.f;
+#pragma unroll 1
+              for (int p0 = 0; p0 < shares; p0 += 4) {
+                float2 ml[4];
+                float4 x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const long long at = share(p0 + k);
+                  ml[k] = ml_of(at);
+                  x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + (long long)jc * a.rows_cap + jr);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (p0 + k >= shares || ml[k].y == 0.f) continue;
+                  const float w = ex2(ml[k].x - top);
+                  lt = fmaf(w, ml[k].y, lt);
+                  acc[0] = fmaf(w, x[k].x, acc[0]);
+                  acc[1] = fmaf(w, x[k].y, acc[1]);
+                  acc[2] = fmaf(w, x[k].z, acc[2]);
+                  acc[3] = fmaf(w, x[k].w, acc[3]);
+                }
               }
               const float inv = lt == 0.f ? 0.f : 1.f / lt;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) acc[e] *= inv;
+              for (int e = 0; e < 4; ++e) acc[e] *= inv;
               const int jrow = it.row0 + (it.two ? 128 * wg : 0) + jr, jt = jrow / a.c.G;
               const int jh = it.kvh * a.c.G + (jrow - jt * a.c.G);
-              store8(a.c.out, a.c.out_dtype, ((long long)(it.tok0 + jt) * a.c.n_q_heads + jh) * D + 8 * jc, acc);
+              const long long at = ((long long)(it.tok0 + jt) * a.c.n_q_heads + jh) * D + 4 * jc;
+              if (a.c.out_dtype == TQ_DTYPE_F32) store_row<4>(static_cast<float*>(a.c.out) + at, acc);
+              else if (a.c.out_dtype == TQ_DTYPE_F16) store_row<4>(static_cast<__half*>(a.c.out) + at, acc);
+              else store_row<4>(static_cast<__nv_bfloat16*>(a.c.out) + at, acc);
             }
           }
         }

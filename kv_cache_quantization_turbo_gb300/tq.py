@@ -433,21 +433,29 @@ ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "wavelength": 3, "yarn": 4}
 
 
+_DTYPE_OF: dict = {}  # torch dtype -> element type, filled as types come up
+
+
 def _dtype(t) -> int:
     """The library's element type of a tensor; -1 (refused by every call) for any other."""
-    return DTYPES.get(str(t.dtype).rsplit(".", 1)[-1], -1)
+    d = t.dtype
+    code = _DTYPE_OF.get(d)
+    if code is None:
+        code = _DTYPE_OF[d] = DTYPES.get(_short(t), -1)
+    return code
 
 
-def _rows(t, heads: int | None = None) -> int:
-    """Token stride of a [tokens, heads, d] tensor on a GPU whose heads are consecutive d-vectors."""
+def _rows(t, shape, heads: int | None = None) -> int:
+    """Token stride of a [tokens, heads, d] tensor on a GPU whose heads are consecutive d-vectors; shape: t.shape."""
     if not t.is_cuda:
         raise ValueError(f"a tensor on the GPU is wanted, not on {t.device}")
-    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
-        raise ValueError(f"a [tokens, heads, d] tensor with contiguous heads is wanted: {tuple(t.shape)}, "
-                         f"strides {t.stride()}")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"{heads} heads are wanted: {tuple(t.shape)}")
-    return max(t.stride(0), t.shape[1] * t.shape[2]) if t.shape[0] <= 1 else t.stride(0)
+    if len(shape) != 3 or (heads is not None and shape[1] != heads):
+        raise ValueError(f"a [tokens, {'heads' if heads is None else heads}, d] tensor is wanted: {tuple(shape)}")
+    n, h, d = shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 or (h > 1 and s1 != d)) and n * h * d:
+        raise ValueError(f"heads have to be consecutive vectors: {tuple(shape)}, strides {t.stride()}")
+    return s0 if n > 1 else max(s0, h * d)
 
 
 @dataclass
@@ -499,15 +507,24 @@ class ScoreMods:
         return self._c
 
 
+_NAME_OF: dict = {}  # torch dtype -> its name
+
+
 def _short(t) -> str:
-    return str(t.dtype).rsplit(".", 1)[-1]
+    d = t.dtype
+    name = _NAME_OF.get(d)
+    if name is None:
+        name = _NAME_OF[d] = str(d).rsplit(".", 1)[-1]
+    return name
 
 
 def _positions(positions, n: int):
-    if positions is not None and (_short(positions) != "int32" or positions.numel() != n or
-                                  not positions.is_contiguous()):
-        raise ValueError(f"positions: {n} contiguous int32 values are wanted")
-    return _ptr(positions)
+    if positions is None:
+        return None
+    if _short(positions) != "int32" or positions.numel() != n or not positions.is_contiguous() or \
+            not positions.is_cuda:
+        raise ValueError(f"positions: {n} contiguous int32 values on the GPU are wanted")
+    return positions.data_ptr()
 
 
 def tq_rope_build(head_dim: int, rotary_dim: int | None = None, layout="half", scaling="none", base: float = 10000.0,
@@ -525,20 +542,23 @@ def tq_rope_build(head_dim: int, rotary_dim: int | None = None, layout="half", s
 
 def tq_rope(ctx: int, table: tq_rope_table, x, positions, out, inverse: bool = False, stream=None) -> int:
     """x, out: [tokens, heads, d] tensors of one type (out may be x); positions: int32 [tokens]."""
-    if out.shape != x.shape or out.dtype != x.dtype or x.shape[-1] != table.head_dim:
-        raise ValueError(f"x {tuple(x.shape)} {x.dtype}, out {tuple(out.shape)} {out.dtype}")
-    return _lib.tq_rope(ctx, ctypes.byref(table), _ptr(x), _dtype(x), x.shape[0], x.shape[1], _rows(x),
-                        _positions(positions, x.shape[0]), int(inverse), _ptr(out), _rows(out), _stream(stream))
+    shape = x.shape
+    if out.shape != shape or out.dtype != x.dtype or shape[-1] != table.head_dim:
+        raise ValueError(f"x {tuple(shape)} {x.dtype}, out {tuple(out.shape)} {out.dtype}")
+    return _lib.tq_rope(ctx, ctypes.byref(table), x.data_ptr(), _dtype(x), shape[0], shape[1], _rows(x, shape),
+                        _positions(positions, shape[0]), int(inverse), out.data_ptr(), _rows(out, shape),
+                        _stream(stream))
 
 
 def tq_append_kv(ctx: int, batch: Batch, k, v, k_view, v_view, layer: int, rope: tq_rope_table | None = None,
                  positions=None, stream=None) -> int:
     """k, v: [n_tokens, H, d] tensors of one type (slices of a fused projection are fine)."""
-    if k.dtype != v.dtype or k.shape != v.shape or k.shape[0] != batch.n_tokens or k.shape[2] != k_view.head_dim:
-        raise ValueError(f"k {tuple(k.shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype}, {batch.n_tokens} tokens")
+    shape = k.shape
+    if k.dtype != v.dtype or shape != v.shape or shape[0] != batch.n_tokens or shape[-1] != k_view.head_dim:
+        raise ValueError(f"k {tuple(shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype}, {batch.n_tokens} tokens")
     ka, va = _view_arg(k_view), _view_arg(v_view)
-    return _lib.tq_append_kv(ctx, ctypes.byref(batch.c_batch()), _ptr(k), _rows(k, k_view.n_kv_heads), _ptr(v),
-                             _rows(v, v_view.n_kv_heads), _dtype(k), None if rope is None else ctypes.byref(rope),
+    return _lib.tq_append_kv(ctx, ctypes.byref(batch.c_batch()), k.data_ptr(), _rows(k, shape, k_view.n_kv_heads),
+                             v.data_ptr(), _rows(v, shape, v_view.n_kv_heads), _dtype(k), None if rope is None else ctypes.byref(rope),
                              _positions(positions, batch.n_tokens), ka[0], va[0], layer, _stream(stream))
 
 
@@ -546,7 +566,7 @@ def tq_read_kv(ctx: int, batch: Batch, k_view, k_out, v_view, v_out, layer: int,
     """k_out, v_out: contiguous [n_tokens, H, d] tensors of one type; a pair may be None."""
     outs = [(view, t) for view, t in ((k_view, k_out), (v_view, v_out)) if t is not None]
     for view, t in outs:
-        if tuple(t.shape) != (batch.n_tokens, view.n_kv_heads, view.head_dim) or not t.is_contiguous() or \
+        if t.shape != (batch.n_tokens, view.n_kv_heads, view.head_dim) or not t.is_contiguous() or not t.is_cuda or \
                 t.dtype != outs[0][1].dtype:
             raise ValueError(f"output {tuple(t.shape)} {t.dtype} for {batch.n_tokens} tokens")
     ka, va = _view_arg(k_view), _view_arg(v_view)
@@ -562,15 +582,16 @@ def tq_chunk_workspace_bytes(ctx: int, batch: Batch, n_q_heads: int, n_kv_heads:
 def tq_chunk_attention(ctx: int, batch: Batch, q, k_view, v_view, layer: int, softmax_scale: float, workspace,
                        workspace_bytes: int, out, mods: ScoreMods | None = None, stream=None) -> int:
     """q: [n_tokens, n_q_heads, d]; out: contiguous, the same shape, its type may differ."""
-    if q.shape[0] != batch.n_tokens or out.shape != q.shape or not out.is_contiguous() or \
-            q.shape[2] != k_view.head_dim:
-        raise ValueError(f"q {tuple(q.shape)}, out {tuple(out.shape)} for {batch.n_tokens} tokens")
+    shape = q.shape
+    if shape[0] != batch.n_tokens or out.shape != shape or not out.is_contiguous() or not out.is_cuda or \
+            shape[-1] != k_view.head_dim:
+        raise ValueError(f"q {tuple(shape)}, out {tuple(out.shape)} for {batch.n_tokens} tokens")
     if mods is not None:
-        for t, n in ((mods.slopes, q.shape[1]), (mods.first_keys, batch.n_tokens),
+        for t, n in ((mods.slopes, shape[1]), (mods.first_keys, batch.n_tokens),
                      (mods.prefix_lens, batch.seq_lens.numel())):
             if t is not None and t.numel() != n:
                 raise ValueError(f"{n} values are wanted: {tuple(t.shape)}")
     ka, va = _view_arg(k_view), _view_arg(v_view)
-    return _lib.tq_chunk_attention(ctx, ctypes.byref(batch.c_batch()), _ptr(q), _dtype(q), _rows(q), q.shape[1], ka[0],
+    return _lib.tq_chunk_attention(ctx, ctypes.byref(batch.c_batch()), q.data_ptr(), _dtype(q), _rows(q, shape), shape[1], ka[0],
                                    va[0], layer, softmax_scale, None if mods is None else ctypes.byref(mods.c_mods()),
                                    _ptr(workspace), workspace_bytes, _ptr(out), _dtype(out), _stream(stream))
