@@ -427,8 +427,8 @@ tq_status tq_rope(const tq_context* ctx, const tq_rope_table* table, const void*
 
 /*
  * A ragged batch of new tokens.  Sequence b has the tokens [cu_tokens[b], cu_tokens[b + 1]) of the call's n_tokens
- * rows (device int32 [n_seqs + 1], from 0 on, not decreasing; rows behind cu_tokens[n_seqs] are padding: not read,
- * and left as they are in every output) and seq_lens[b] tokens in all (device int32 [n_seqs]), the new ones included:
+ * rows (device int32 [n_seqs + 1], from 0 on, not decreasing; rows behind cu_tokens[n_seqs] are padding: what they
+ * hold has no effect, and in every output they are left as they are) and seq_lens[b] tokens in all (device int32 [n_seqs]), the new ones included:
  * its new token i of n sits at position seq_lens[b] - n + i.  block_table (device int32 [n_seqs][max_blocks]) maps
  * page position / page_size of a sequence to a physical page; NULL: sequence b is page b.
  * max_tokens and max_ctx (host) bound the new tokens and the length of every sequence.  A sequence whose device values
