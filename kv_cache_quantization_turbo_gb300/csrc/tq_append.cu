@@ -3,10 +3,11 @@
 // A CTA takes `tc` consecutive tokens, K or V.  A group of d / 16 lanes holds one vector, 16 consecutive coordinates per
 // lane; its first vector is asked for before anything else.  Meanwhile one warp per token finds the token's sequence and
 // place in the cache, and the CTA computes the rotation's angles once per token for all its heads (16 sincospi per lane
-// and vector instead made a 4096-token chunk take 23 us, not MEASURE_APPEND).  From the load to the stored bytes a vector
-// stays in registers: the q8_0 scale of a 32-block is shared by two lanes, the turbo rotation runs four butterfly stages
+// and vector instead made a 4096-token chunk of 8 heads of 128 take 23 us; it takes 17, of which the bytes need 4: bound by
+// the chain of dependent loads that finds a place, and its two barriers).  From the load to the stored bytes a vector stays
+// in registers: the q8_0 scale of a 32-block is shared by two lanes, the turbo rotation runs four butterfly stages
 // in a lane and log2(d / 16) across the group.  Bytes: both inputs once, the stored vectors once (append), the reverse
-// (read).
+// (read: 10 us for the rows of that chunk).
 #include "tq_batch.cuh"
 
 namespace tq {
@@ -377,8 +378,8 @@ __global__ void __launch_bounds__(kApThreads) read_kernel(const __grid_constant_
 }
 
 // Tokens per CTA: as many, up to 16, as leave a CTA of each half for every SM (a decode batch takes one token each, the
-// shortest chain; a chunk shares places and angles, and all its CTAs are resident at once: 8 tokens each, in two rounds,
-// took 17 us for a 4096-token chunk, 16 take MEASURE_APPEND).
+// shortest chain; a chunk shares places and angles: 16 instead of 8 tokens are 16 us instead of 19 for 1.7K tokens of 8
+// heads of 64, and the same 17 us for 4096 tokens of 8 heads of 128).
 template <class F>
 cudaError_t with_launch(const AppendArgs& a, int sm_count, F run) {
   Launch L{};

@@ -15,14 +15,14 @@
 // tensor memory holds one accumulator, and one warpgroup takes every step.
 //
 // Warps, meeting on mbarriers only:
-//   0-3, 4-7   softmax: one row per thread, S read 32 columns at a time.  The weights 2^(s - reference) are taken against
-//              the reference so far; only where it is unset, or a row's tile sums to more than fp16 weights can hold,
-//              does a second reading find the row's maximum, raise the reference and rescale O in tensor memory.  Tiles
-//              with score modifications or masks are changed in place before.  P as fp16 goes over S, the left operand
-//              of the value product.
-//   8-15       producers: codes to fp16 values, K and V alike, into swizzled operand tiles (K: K-major; the same bytes
-//              read MN-major are V).  A q8_0 code becomes its value by a byte permute into 1024 + u, an exact
-//              subtraction and one rounded product with the scale.
+//   0-3, 4-7   softmax: one row per thread, 64 scores at a time.  The weights 2^(s - reference) are taken against the
+//              reference so far; only where it is unset, or a row's 64 keys sum to more than fp16 weights can hold, does a
+//              second reading find their maximum, raise the reference and rescale O in tensor memory.  Scores with
+//              modifications or masks are changed in place before.  P as fp16 goes over S, the left operand of the value
+//              product.
+//   8-11, 12-15  producers of the K and of the V tiles: codes to fp16 values in swizzled operand tiles (K: K-major; the
+//              same bytes read MN-major are V).  A q8_0 code becomes its value by a byte permute into 1024 + u, an exact
+//              subtraction and one rounded product with the scale; a turbo code by byte permutes over the level table.
 //   16, 17     issue the products, one warp for each softmax warpgroup: QK, PV, PV, QK, ... in order.  (One warp for both
 //              took longer to go round than the products.)
 //   18, 19     18 reads the plan; both find each key's place through the block table a few tiles ahead, and ask for its
@@ -30,6 +30,15 @@
 // The scales of fp16 operands: queries are multiplied by a power of two per row (any input type fits then), turbo
 // values carry lambda so that the codebook is nearly exact in fp16.  Rounding to fp16 (2^-11 relative at most per
 // operand) is what the tensor core's full rate asks for; sums are fp32.
+//
+// What bounds it.  Many rows: a tensor instruction of M 128, K 16 takes 65 cycles for any N up to 128 (measured alone), so
+// a tile of two row tiles (32 instructions) takes 2.1 K cycles; it takes 4.9 K, because a warpgroup's softmax of 128 keys,
+// which shares its SM sub-partition's instruction slots with two producer warps, and the products before and after it are
+// a chain (scores and weights share their tensor memory).  Without the softmax the loop runs at 1.56 ms, without softmax
+// and conversion at 1.22 ms, with both at 2.02 ms for a 4096-token chunk at 32K context, 32 query heads of 128 (1.02
+// PFLOP/s).  64-key score products with twice the buffers take the same 65 cycles each for half the keys: 2.15 ms.  Few
+// rows: a tile is 34.8 KB of cache, 1.5 K cycles of this GPU's bandwidth; it takes 3.5 K (64 sequences of 1K to 16K
+// tokens, 8 KV heads: 348 us, 2.5 TB/s), bound by the round of a tile through its two buffers.
 #pragma once
 
 #include "tq_batch.cuh"
@@ -162,8 +171,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 
 // A wait that gives up for good once one has run out: the role then runs through its loops without waiting (every
 // named barrier is still met), and the error is reported at the end.
-// Polls without a suspend-time hint: with one of 1 us a wait took up to a microsecond longer than the phase.  2^23 polls
-// are a second or more.  SLEEP: nanoseconds between polls, for roles with time in hand (polling takes instruction slots
+// Polls without a suspend-time hint (with one of 1 us waits took longer); 2^23 polls are some tenths of a second at least.
+// SLEEP: nanoseconds between polls, for roles with time in hand (polling takes instruction slots
 // from the others).
 template <int SLEEP = 0>
 __device__ __forceinline__ void wait(bool& ok, uint64_t* bar, uint32_t parity) {
@@ -759,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (!ok || kind == 0) break;
         wait_warp(ok, &B->q_full, icnt);
         if (kind == 1) {
-          // own steps: every tile (two row tiles: step i is tile i), or every other one; D = 256: the first issuer all
+          // own steps: every tile with two row tiles, else every other one; D = 256: the first issuer all
           const int first = two || D == 256 ? 0 : w, stride = two || D == 256 ? 1 : 2;
           const int steps = D == 256 && w ? 0 : (n - first + stride - 1) / stride;
           const uint32_t dq = q_lo + (uint32_t)(two ? w * (Sh::kQTile >> 4) : 0);

@@ -216,6 +216,17 @@ class Paged:
         return out
 
 
+    def stored_all(self):
+        """Oracle values of every slot (one KV head): [slots, 1, d]."""
+        out = []
+        for view, fmt in ((self.kv, "q8_0"), (self.vv, self.vfmt)):
+            p, h = C.read_vectors(view, self.layer)
+            s = np.arange(view.num_pages * self.page)
+            out.append(C.oracle_dequant(fmt, C.gpu_codes(fmt, self.d, C.slot_major(p, s, self.page),
+                                                         C.slot_major(h, s, self.page)), self.ctx.signs, self.ctx.S))
+        return out
+
+
 def status(ctx):
     return tq.tq_get_status(ctx.h)[1]
 
@@ -613,6 +624,59 @@ def test_attend_full_width_sampled_rows(ctxs):
     P = Paged(ctxs[128], 128, 2, [2048], [6000], 64, outliers=0.01)
     rows = [0, 1, 31, 32, 63, 64, 127, 128, 500, 1023, 1024, 2016, 2046, 2047]
     check_attend(P, 4, torch.bfloat16, rows=rows)
+
+
+def test_attend_more_sequences_than_the_plan_keeps_near(ctxs):
+    """1500 sequences of one or two tokens (their entry counts go through the workspace), some without any."""
+    new = [1 + (i % 7 == 0) - (i % 11 == 5) for i in range(1500)]
+    lens = [max(n, 1 + (i * 37) % 50) for i, n in enumerate(new)]
+    P = Paged(ctxs[64], 64, 1, new, lens, 16, fill=False)
+    x = W.normal_tensor((int(sum(lens)), 1, 64), seed=3, device="cuda").half()
+    slots = torch.as_tensor(np.concatenate([P.slots(b, np.arange(n)) for b, n in enumerate(lens)]), device="cuda")
+    C.encode(P.ctx, P.kv, x, True, slots=slots)
+    C.encode(P.ctx, P.vv, x.flip(0).contiguous(), False, slots=slots)
+    q = W.normal_tensor((P.n_tokens, 2, 64), seed=4, device="cuda").half()
+    got = f64(attend(P, q))
+    q64, keys, worst = f64(q), P.stored_all(), 0.0
+    for b in list(range(0, 60)) + [1022, 1023, 1024, 1025, 1498, 1499]:
+        at = np.nonzero(P.seq == b)[0]
+        if len(at):
+            k, v = (y[P.slots(b, np.arange(lens[b]))] for y in keys)
+            want = S.chunk_attention(q64[at], k, v, P.pos[at], 1 / 8)
+            worst = max(worst, C.rel_err_per_head(got[at], want).max())
+    assert worst < C.ATTN_RTOL + half_step(torch.float16)
+    assert np.isfinite(got).all() and (got != 9.0).any(-1).all()
+
+
+def test_pages_beyond_32_bit_offsets(ctxs):
+    """A cache of more than 4 GiB per view: append, read and attention through pages at its end."""
+    d, H, page = 128, 8, 16
+    n_pages = (1 << 32) // (page * H * d) + 400
+    kv, vv = (tq.alloc_view("q8_0", d, H, page, n_pages) for _ in range(2))
+    assert kv.payload.numel() > 1 << 32
+    T = 100
+    table = (n_pages - 1 - 3 * torch.arange(7, device="cuda")).to(torch.int32).view(1, 7)
+    dev = dict(dtype=torch.int32, device="cuda")
+    batch = tq.Batch(torch.tensor([0, T], **dev), torch.tensor([T], **dev), table, T, T, T)
+    k, v, q = (W.normal_tensor((T, H, d), seed=i, device="cuda").half() for i in range(3))
+    ctx = ctxs[128]
+    assert tq.tq_append_kv(ctx.h, batch, k, v, kv, vv, 0) == tq.TQ_OK
+    rk, rv = torch.empty_like(k), torch.empty_like(v)
+    assert tq.tq_read_kv(ctx.h, batch, kv, rk, vv, rv, 0) == tq.TQ_OK
+    out = torch.empty_like(q)
+    n = tq.tq_chunk_workspace_bytes(ctx.h, batch, H, H)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert tq.tq_chunk_attention(ctx.h, batch, q, kv, vv, 0, 1 / math.sqrt(d), ws, n, out) == tq.TQ_OK
+    torch.cuda.synchronize()
+    assert status(ctx) == 0
+    want_k = S.q8_0_values(f64(k))
+    # scales rounded once to fp16 on both sides, values to fp16; ties of codes are the encoder's own (fp32 quotients)
+    assert np.abs(f64(rk) - want_k).max() < 1.5 * np.abs(f64(k)).max() / 127
+    want = S.chunk_attention(f64(q), f64(rk), f64(rv), np.arange(T), 1 / math.sqrt(d))
+    # the values read back are rounded to fp16 once more: 2^-11 each on K and V
+    assert C.rel_err_per_head(f64(out), want).max() < C.ATTN_RTOL + 3 * half_step(torch.float16)
+    del kv, vv
+    torch.cuda.empty_cache()
 
 
 def test_attend_refusals(ctxs):
