@@ -418,8 +418,9 @@ tq_status tq_rope_build(const tq_rope_params* params, tq_rope_table* table);
  * positions[t] (device int32 [n_tokens]) times the table's angles, in the other direction with inverse = 1, which is
  * the gradient of the rotation (its transpose, attn_factor included).  Computed in fp32, rounded once.  out may be x
  * with the same stride (in place); other overlaps are not allowed.  x and out 16-byte aligned, strides multiples of
- * 16 bytes, else TQ_ERR_INVALID_ARG.  The context's device must be current (TQ_ERR_INVALID_ARG otherwise, here and in
- * the calls below); the table's head_dim must be the context's.
+ * 16 bytes, else TQ_ERR_INVALID_ARG; without tokens (n_tokens = 0, here and in the calls below) the arrays of rows and
+ * positions may be NULL.  The context's device must be current (TQ_ERR_INVALID_ARG otherwise, here and in the calls
+ * below); the table's head_dim must be the context's.
  */
 tq_status tq_rope(const tq_context* ctx, const tq_rope_table* table, const void* x, tq_dtype dtype, int n_tokens,
                   int n_heads, int64_t x_token_stride, const int32_t* positions, int inverse, void* out,
@@ -495,7 +496,8 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
  * a row that sees no key gives zeros.  A row that sees a key whose stored K or V has an infinite or NaN scale or norm is
  * NaN in all coordinates; a key that a row does not see never reaches it, whatever is stored there.
  *   q: element (t, h, i) at q[t * q_token_stride + h * d + i], type q_dtype, 16-byte aligned, stride a multiple of 16
- *   bytes and >= n_q_heads d.  out: [n_tokens][n_q_heads][d] of type out_dtype, contiguous, 16-byte aligned.
+ *   bytes and >= n_q_heads d.  out: [n_tokens][n_q_heads][d] of type out_dtype, contiguous, 16-byte aligned, apart
+ *   from q.
  *   Query head h reads KV head h / (n_q_heads / n_kv_heads); n_q_heads a multiple of n_kv_heads.
  *   K: Q8_0.  V: Q8_0 or turbo2/3/4_mse.  Others: TQ_ERR_UNSUPPORTED (turbo K: tq_decode_attention,
  *   tq_prefill_attention).

@@ -16,9 +16,9 @@ int dtype_bytes(tq_dtype t) {
   return t == TQ_DTYPE_F32 ? 4 : (t == TQ_DTYPE_F16 || t == TQ_DTYPE_BF16) ? 2 : 0;
 }
 
-// The kernels read and write rows with 16-byte accesses.
-bool rows_ok(const void* p, int64_t stride, int64_t row, int esz) {
-  return p && !(reinterpret_cast<uintptr_t>(p) & 15) && stride >= row && (stride * esz) % 16 == 0;
+// The kernels read and write rows with 16-byte accesses.  Without rows (n == 0) there need not be memory for them.
+bool rows_ok(const void* p, int64_t stride, int64_t row, int esz, int n) {
+  return (p || n == 0) && !(reinterpret_cast<uintptr_t>(p) & 15) && stride >= row && (stride * esz) % 16 == 0;
 }
 
 // A launch goes to the current device: a context of another one would be read from the wrong GPU.
@@ -39,6 +39,7 @@ bool batch_ok(const tq_batch* b) {
 }
 
 bool batch_fits(const tq_batch* b, const DevView& v) {
+  if (b->n_seqs == 0) return true;
   if (b->block_table) return b->max_blocks >= 1 && (int64_t)b->max_blocks * v.page_size >= b->max_ctx;
   return b->max_ctx <= v.page_size && b->n_seqs <= v.num_pages;
 }
@@ -115,9 +116,10 @@ tq_status tq_rope(const tq_context* ctx, const tq_rope_table* table, const void*
     return TQ_ERR_INVALID_ARG;
   if (inverse != 0 && inverse != 1) return TQ_ERR_INVALID_ARG;
   const int64_t row = (int64_t)n_heads * ctx->d;
-  if (!rows_ok(x, x_token_stride, row, esz) || !rows_ok(out, out_token_stride, row, esz) || !positions)
+  if (!rows_ok(x, x_token_stride, row, esz, n_tokens) || !rows_ok(out, out_token_stride, row, esz, n_tokens) ||
+      (!positions && n_tokens))
     return TQ_ERR_INVALID_ARG;
-  if (x == out && x_token_stride != out_token_stride) return TQ_ERR_INVALID_ARG;
+  if (x == out && n_tokens && x_token_stride != out_token_stride) return TQ_ERR_INVALID_ARG;
   if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
   if (n_tokens == 0) return TQ_OK;
   return cuda_status(launch_rope(*table, x, dtype, n_tokens, n_heads, x_token_stride, positions, inverse, out,
@@ -137,7 +139,8 @@ tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void*
     return TQ_ERR_INVALID_ARG;
   if (rope && !table_ok(ctx, rope)) return TQ_ERR_INVALID_ARG;
   const int64_t row = (int64_t)a.k.H * ctx->d;
-  if (!rows_ok(k, k_token_stride, row, esz) || !rows_ok(v, v_token_stride, row, esz)) return TQ_ERR_INVALID_ARG;
+  if (!rows_ok(k, k_token_stride, row, esz, batch->n_tokens) || !rows_ok(v, v_token_stride, row, esz, batch->n_tokens))
+    return TQ_ERR_INVALID_ARG;
   if (!batch_fits(batch, a.k) || !on_device(ctx)) return TQ_ERR_INVALID_ARG;
   if (a.k.format != TQ_FMT_Q8_0 || !stored_ok(a.v)) return TQ_ERR_UNSUPPORTED;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return TQ_OK;
@@ -158,7 +161,8 @@ tq_status tq_read_kv(const tq_context* ctx, const tq_batch* batch, const tq_cach
                      const tq_cache_view* v_view, void* v_out, tq_dtype dtype, int layer, tq_stream_t stream) {
   const int esz = dtype_bytes(dtype);
   if (!ctx || !batch_ok(batch) || !esz || layer < 0 || (!k_view && !v_view)) return TQ_ERR_INVALID_ARG;
-  if (!k_view != !k_out || !v_view != !v_out) return TQ_ERR_INVALID_ARG;
+  if ((!k_view && k_out) || (!v_view && v_out)) return TQ_ERR_INVALID_ARG;
+  if (batch->n_tokens && (!k_view != !k_out || !v_view != !v_out)) return TQ_ERR_INVALID_ARG;
   AppendArgs a{};
   for (int i = 0; i < 2; ++i) {
     const tq_cache_view* view = i ? v_view : k_view;
@@ -203,7 +207,7 @@ tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const
       a.k.num_pages != a.v.num_pages || layer >= a.k.n_layers || layer >= a.v.n_layers)
     return TQ_ERR_INVALID_ARG;
   const int64_t row = (int64_t)n_q_heads * d;
-  if (!rows_ok(q, q_token_stride, row, esz) || !out || (reinterpret_cast<uintptr_t>(out) & 15))
+  if (!rows_ok(q, q_token_stride, row, esz, batch->n_tokens) || !rows_ok(out, row, row, osz, batch->n_tokens))
     return TQ_ERR_INVALID_ARG;
   if (mods && (!(mods->softcap >= 0.0f) || !std::isfinite(mods->softcap) || mods->window < 0)) return TQ_ERR_INVALID_ARG;
   if (!batch_fits(batch, a.k) || !on_device(ctx)) return TQ_ERR_INVALID_ARG;

@@ -455,13 +455,14 @@ def _rows(t, shape, heads: int | None = None) -> int:
     s0, s1, s2 = t.stride()
     if (s2 != 1 or (h > 1 and s1 != d)) and n * h * d:
         raise ValueError(f"heads have to be consecutive vectors: {tuple(shape)}, strides {t.stride()}")
-    return s0 if n > 1 else max(s0, h * d)
+    return s0 if n > 1 else h * d
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class Batch:
     """A ragged batch (tq_batch) and the device tensors that own its arrays (int32): cu_tokens [n_seqs + 1],
-    seq_lens [n_seqs], block_table [n_seqs, max_blocks] or None."""
+    seq_lens [n_seqs], block_table [n_seqs, max_blocks] or None.  The tensors' contents may change between calls, the
+    fields not."""
     cu_tokens: object
     seq_lens: object
     block_table: object
@@ -474,22 +475,23 @@ class Batch:
         if self.cu_tokens.numel() != n + 1:
             raise ValueError(f"cu_tokens has {self.cu_tokens.numel()} entries for {n} sequences")
         bt = self.block_table
-        if bt is not None and (bt.dim() != 2 or bt.shape[0] != n):
+        if bt is not None and (bt.dim() != 2 or bt.shape[0] != n or (n and not bt.shape[1])):
             raise ValueError(f"block_table {tuple(bt.shape)} for {n} sequences")
         for t in (self.cu_tokens, self.seq_lens, bt):
-            if t is not None and (_short(t) != "int32" or not t.is_contiguous()):
-                raise ValueError("the batch's arrays are contiguous int32 tensors")
-        self._c = tq_batch(n, self.n_tokens, self.max_tokens, self.max_ctx, 0 if bt is None else bt.shape[1],
-                           _ptr(self.cu_tokens), _ptr(self.seq_lens), _ptr(bt))
+            if t is not None and (_short(t) != "int32" or not t.is_contiguous() or not t.is_cuda):
+                raise ValueError("the batch's arrays are contiguous int32 tensors on the GPU")
+        object.__setattr__(self, "_c", tq_batch(n, self.n_tokens, self.max_tokens, self.max_ctx,
+                                                0 if bt is None else bt.shape[1], _ptr(self.cu_tokens),
+                                                _ptr(self.seq_lens), _ptr(bt)))
 
     def c_batch(self) -> tq_batch:
         return self._c
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class ScoreMods:
     """Changes to the scores (tq_score_mods) and the device tensors they read: slopes float32 [n_q_heads],
-    first_keys int32 [n_tokens], prefix_lens int32 [n_seqs], each None for none."""
+    first_keys int32 [n_tokens], prefix_lens int32 [n_seqs], each None for none; contents may change between calls."""
     softcap: float = 0.0
     window: int = 0
     slopes: object = None
@@ -498,10 +500,11 @@ class ScoreMods:
 
     def __post_init__(self):
         for t, want in ((self.slopes, "float32"), (self.first_keys, "int32"), (self.prefix_lens, "int32")):
-            if t is not None and (_short(t) != want or not t.is_contiguous()):
-                raise ValueError(f"a contiguous {want} tensor is wanted: {t.dtype}, strides {t.stride()}")
-        self._c = tq_score_mods(self.softcap, self.window, _ptr(self.slopes), _ptr(self.first_keys),
-                                _ptr(self.prefix_lens))
+            if t is not None and (_short(t) != want or not t.is_contiguous() or not t.is_cuda):
+                raise ValueError(f"a contiguous {want} tensor on the GPU is wanted: {t.dtype}, strides {t.stride()}, "
+                                 f"{t.device}")
+        object.__setattr__(self, "_c", tq_score_mods(self.softcap, self.window, _ptr(self.slopes),
+                                                     _ptr(self.first_keys), _ptr(self.prefix_lens)))
 
     def c_mods(self) -> tq_score_mods:
         return self._c
@@ -558,8 +561,9 @@ def tq_append_kv(ctx: int, batch: Batch, k, v, k_view, v_view, layer: int, rope:
         raise ValueError(f"k {tuple(shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype}, {batch.n_tokens} tokens")
     ka, va = _view_arg(k_view), _view_arg(v_view)
     return _lib.tq_append_kv(ctx, ctypes.byref(batch.c_batch()), k.data_ptr(), _rows(k, shape, k_view.n_kv_heads),
-                             v.data_ptr(), _rows(v, shape, v_view.n_kv_heads), _dtype(k), None if rope is None else ctypes.byref(rope),
-                             _positions(positions, batch.n_tokens), ka[0], va[0], layer, _stream(stream))
+                             v.data_ptr(), _rows(v, shape, v_view.n_kv_heads), _dtype(k),
+                             None if rope is None else ctypes.byref(rope), _positions(positions, batch.n_tokens),
+                             ka[0], va[0], layer, _stream(stream))
 
 
 def tq_read_kv(ctx: int, batch: Batch, k_view, k_out, v_view, v_out, layer: int, stream=None) -> int:
@@ -592,6 +596,7 @@ def tq_chunk_attention(ctx: int, batch: Batch, q, k_view, v_view, layer: int, so
             if t is not None and t.numel() != n:
                 raise ValueError(f"{n} values are wanted: {tuple(t.shape)}")
     ka, va = _view_arg(k_view), _view_arg(v_view)
-    return _lib.tq_chunk_attention(ctx, ctypes.byref(batch.c_batch()), q.data_ptr(), _dtype(q), _rows(q, shape), shape[1], ka[0],
-                                   va[0], layer, softmax_scale, None if mods is None else ctypes.byref(mods.c_mods()),
-                                   _ptr(workspace), workspace_bytes, _ptr(out), _dtype(out), _stream(stream))
+    return _lib.tq_chunk_attention(ctx, ctypes.byref(batch.c_batch()), q.data_ptr(), _dtype(q), _rows(q, shape),
+                                   shape[1], ka[0], va[0], layer, softmax_scale,
+                                   None if mods is None else ctypes.byref(mods.c_mods()), _ptr(workspace),
+                                   workspace_bytes, _ptr(out), _dtype(out), _stream(stream))

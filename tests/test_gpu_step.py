@@ -817,3 +817,120 @@ def test_calls_on_two_streams_at_once(ctxs):
     torch.cuda.synchronize()
     for a, o in zip(alone, outs):
         assert torch.equal(a, o)
+
+
+# ---------------------------------------------------------------------------
+# calls at the edges of what the documentation allows
+# ---------------------------------------------------------------------------
+
+def test_no_tokens_need_no_memory(ctxs):
+    """Empty tensors have no address: every call with no tokens succeeds, with no sequences and with idle ones."""
+    ctx, d, dev = ctxs[64], 64, dict(dtype=torch.int32, device="cuda")
+    rope = tq.tq_rope_build(d)
+    x = torch.empty((0, 2, d), device="cuda")
+    assert x.data_ptr() == 0
+    assert tq.tq_rope(ctx.h, rope, x, torch.empty(0, **dev), x) == tq.TQ_OK
+    kv, vv = (tq.alloc_view("q8_0", d, 2, 16, 4) for _ in range(2))
+    before = kv.payload.clone()
+    for n, bt in ((0, None), (0, torch.empty((0, 3), **dev)), (2, torch.zeros((2, 3), **dev))):
+        b = tq.Batch(torch.zeros(n + 1, **dev), torch.full((n,), 5, **dev), bt, 0, 0, 40)
+        assert tq.tq_append_kv(ctx.h, b, x, x, kv, vv, 0, rope=rope) == tq.TQ_OK
+        assert tq.tq_read_kv(ctx.h, b, kv, x, vv, x, 0) == tq.TQ_OK
+        ws = torch.empty(max(1, tq.tq_chunk_workspace_bytes(ctx.h, b, 4, 2)), dtype=torch.uint8, device="cuda")
+        q = torch.empty((0, 4, d), device="cuda")
+        assert tq.tq_chunk_attention(ctx.h, b, q, kv, vv, 0, 0.1, ws, ws.numel(), q) == tq.TQ_OK
+    torch.cuda.synchronize()
+    assert torch.equal(before, kv.payload) and status(ctx) == 0
+
+
+def test_only_padding_rows(ctxs):
+    """Rows without a sequence that owns them: max_tokens 0, nothing is read or written."""
+    P = Paged(ctxs[128], 128, 1, [0, 0], [30, 7], 16, padding=6)
+    q = torch.ones((6, 2, 128), dtype=torch.float16, device="cuda")
+    out = attend(P, q)
+    torch.cuda.synchronize()
+    assert (out == 9.0).all() and status(P.ctx) == 0
+
+
+def test_one_token_slices_of_odd_strides(ctxs):
+    """The stride of a single token does not matter; that of two has to keep rows 16-byte aligned."""
+    ctx, t = ctxs[64], tq.tq_rope_build(64)
+    buf = torch.zeros((3, 2 * 64 + 1), dtype=torch.float16, device="cuda")
+    x = buf.as_strided((1, 2, 64), (129, 64, 1))
+    assert tq.tq_rope(ctx.h, t, x, torch.ones(1, dtype=torch.int32, device="cuda"), x) == tq.TQ_OK
+    two = buf.as_strided((2, 2, 64), (129, 64, 1))
+    assert tq.tq_rope(ctx.h, t, two, torch.ones(2, dtype=torch.int32, device="cuda"), two) == tq.TQ_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_scale_of_any_sign(ctxs, d):
+    """A negative scale is the negated query; a scale of 0 weighs all seen keys alike."""
+    P = Paged(ctxs[d], d, 2, [140, 1, 3], [300, 700, 3], 16)
+    for mods in ({}, dict(softcap=8.0, window=90)):
+        check_attend(P, 2, torch.float16, scale=-1 / math.sqrt(d), **mods)
+    q = W.normal_tensor((P.n_tokens, 4, d), seed=2, device="cuda").half()
+    n = tq.tq_chunk_workspace_bytes(P.ctx.h, P.batch, 4, 2)
+    ws, out = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(q)
+    assert tq.tq_chunk_attention(P.ctx.h, P.batch, q, P.kv, P.vv, 0, 0.0, ws, n, out) == tq.TQ_OK
+    torch.cuda.synchronize()
+    for b in range(3):
+        at = np.nonzero(P.seq == b)[0]
+        v = P.stored(b)[1].repeat(2, axis=1)
+        want = np.stack([v[:p + 1].mean(0) for p in P.pos[at]])
+        # weights of 1 are exact; the values' rounding as in row_bound, six deviations of a mean
+        mean_sq = np.stack([np.sqrt((v[:p + 1] ** 2).sum((0, 2))) / (p + 1) for p in P.pos[at]])
+        bound = 6 * 2.0 ** -11 / math.sqrt(3) * mean_sq / np.maximum(np.linalg.norm(want, axis=-1), 1e-30)
+        err = C.rel_err_per_head(f64(out)[at], want)
+        assert (err < bound + half_step(torch.float16) + 1e-6).all(), (b, (err - bound).max())
+
+
+def test_attend_sequences_that_share_pages(ctxs):
+    """Two sequences with the same leading pages (a shared prompt) and own last pages, and one sequence twice."""
+    P = Paged(ctxs[128], 128, 2, [3, 3, 3], [64, 64, 64], 16)
+    t = P.table.copy()
+    t[1, :3] = t[0, :3]
+    t[2] = t[0]
+    P.table = t
+    P.set_batch([0, 3, 6, 9], [64, 64, 64])
+    q = W.normal_tensor((3, 4, 128), seed=6, device="cuda").half().repeat(3, 1, 1)
+    out = attend(P, q)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:3], out[6:])
+    for b in range(2):
+        k, v = P.stored(b)
+        want = S.chunk_attention(f64(q)[:3], k, v, P.pos[:3], 1 / math.sqrt(128))
+        assert C.rel_err_per_head(f64(out)[3 * b:3 * b + 3], want).max() < C.ATTN_RTOL + half_step(out.dtype)
+    assert not torch.equal(out[:3], out[3:6])
+
+
+def test_attend_prefixes_outside_the_sequence_and_rising_bias(ctxs):
+    """Prefix lengths below zero and behind the end, slopes below zero (far keys favoured)."""
+    P = Paged(ctxs[64], 64, 2, [130, 2], [200, 500], 16)
+    check_attend(P, 2, torch.float16, prefix=[-5, 2 ** 31 - 1])
+    check_attend(P, 2, torch.float16, prefix=[2 ** 31 - 1, -2 ** 31], window=2 ** 31 - 1)
+    q = W.normal_tensor((132, 4, 64), seed=3, device="cuda").half()
+    slopes = torch.tensor([-0.5, 0.0, -0.01, 2.0], device="cuda")
+    out = attend(P, q, mods=tq.ScoreMods(slopes=slopes))
+    torch.cuda.synchronize()
+    for b in range(2):
+        at = np.nonzero(P.seq == b)[0]
+        k, v = P.stored(b)
+        want = S.chunk_attention(f64(q)[at], k, v, P.pos[at], 1 / 8, slopes=f64(slopes))
+        bound = row_bound(f64(q)[at], k, v, P.pos[at], want, torch.float16, 1 / 8, slopes=f64(slopes))
+        assert (C.rel_err_per_head(f64(out)[at], want) < np.maximum(bound, C.ATTN_RTOL) + half_step(out.dtype)).all()
+
+
+def test_batches_are_fixed_and_on_the_gpu(ctxs):
+    P = Paged(ctxs[64], 64, 1, [1], [5], 16)
+    b = P.batch
+    with pytest.raises(AttributeError):
+        b.max_ctx = 100
+    with pytest.raises(AttributeError):
+        tq.ScoreMods().window = 3
+    with pytest.raises(ValueError):
+        tq.Batch(b.cu_tokens.cpu(), b.seq_lens, b.block_table, 1, 1, 5)
+    with pytest.raises(ValueError):
+        tq.Batch(b.cu_tokens, b.seq_lens, b.block_table[:, :0].contiguous(), 1, 1, 5)
+    with pytest.raises(ValueError):
+        tq.ScoreMods(slopes=torch.zeros(2))
