@@ -1,0 +1,533 @@
+// Chunk attention of entries of few rows (decode, short speculative steps) over q8_0 K and V.
+//
+// A tensor instruction of tcgen05 takes as long for 4 rows as for 128, and a tile's way through its two buffers, five
+// roles and their barriers is what a decode step then waits for.  Here a warp works alone: it takes every NW-th slice of 16
+// keys of its CTA's range, copies the next slices' codes and scales asynchronously to a ring of its own, turns codes into
+// fp16 fragments in registers, and keeps its own softmax reference, sum and output; no barrier until the range ends.  The
+// products are the warp-wide m16n8k16 ones (fp16 operands, fp32 sums):
+//   S = Q K^T: 16 rows (8 of them idle for NT = 1), N = 8 keys; a lane holds 16 coordinates of one key at a time, so the
+//     contraction index is permuted, alike for Q and K.
+//   O^T = V^T P^T: M = 16 coordinates, N = 8 rows; the accumulators of S are its right operand as they stand, and a lane
+//     pairs the codes of two keys by byte permutes.
+// The ranges, the join of entries that several CTAs share and the meaning of every mask are those of tq_chunk_tc.cuh;
+// weights are taken against a reference that is raised only when a weight would pass 2^15.
+#include "tq_chunk_tc.cuh"
+#include "tq_warp_mma.cuh"
+
+namespace tq {
+namespace ck {
+namespace {
+
+constexpr int NW = 6;      // warps of a CTA; two CTAs per SM hide each other's starts and ends of ranges
+constexpr int SK = 16;     // keys of a slice
+constexpr float kMaxExp = 15.f;
+
+template <int D>
+struct Few {
+  static constexpr int NS = 512 / D;          // slices of a warp's ring
+  static constexpr int SB = D / 32;           // scales of a vector
+  static constexpr int k = 0, v = SK * D;     // parts of a slice
+  static constexpr int ks = 2 * SK * D, vs = ks + SK * SB * 2;
+  static constexpr int slice = vs + SK * SB * 2;
+  static constexpr int ring = NW * NS * slice;
+  static constexpr int items = ring;          // Item [2]
+  static constexpr int miss = items + 2 * 128;  // uint32 [NW][NS]: keys of the slice whose page is out of range
+  static constexpr int ml = miss + NW * NS * 4;  // float2 [NW][16]
+  static constexpr int flag = ml + NW * 16 * 8;
+  static constexpr int walk = flag + 16;      // Items<D>
+  static constexpr int total = walk + 64;
+  static constexpr int OS = D + 4;            // floats of a row of a warp's O (in the ring, once it is read)
+  static_assert(NW * 16 * OS * 4 <= ring || D == 256, "merge area");
+  static_assert(NW * 8 * OS * 4 <= ring, "merge area");
+  static_assert(2 * (total + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+// Chunk of 16 bytes of a row, so that the lanes' reads of the products' operands meet different banks: a K read takes four
+// chunks in a row of two keys, a V read two chunks of every second key.
+template <int D>
+__device__ __forceinline__ int k_at(int key, int chunk) { return key * D + ((D == 64 ? chunk : chunk ^ ((key & 1) << 2)) << 4); }
+template <int D>
+__device__ __forceinline__ int v_at(int key, int chunk) {
+  return key * D + ((D == 64 ? chunk ^ ((key >> 1) & 3) : chunk ^ (key & 6)) << 4);
+}
+
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+
+struct Spot {
+  int page, off;
+};
+
+// Page and offset of a key, -1 where the key is not wanted.
+__device__ __forceinline__ Spot spot_of(const Args& a, const Item& it, int j, int end) {
+  const DevBatch& b = a.c.b;
+  Spot s{-1, 0};
+  if (j >= it.lo && j < end) {
+    const int ps = a.c.k.page_size, lp = (int)((uint32_t)j / (uint32_t)ps);
+    s.off = j - lp * ps;
+    s.page = it.seq;
+    if (b.block_table) s.page = lp < b.max_blocks ? __ldg(b.block_table + (long long)it.seq * b.max_blocks + lp) : -1;
+  }
+  return s;
+}
+
+// A lane's part of a row of Q as fragments of the left operand, times a power of two that brings the row's largest magnitude
+// to [1, 2); returns that power's inverse.
+template <int D, class T>
+__device__ __forceinline__ float load_q(const Args& a, const T* src, bool valid, int t, uint32_t (&f)[D / 16][2]) {
+  uint32_t top = 0;
+  float x[D / 64][16];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    if (valid) {
+      load_row<16>(src + (4 * i + t) * 16, x[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
+  }
+  top = max(top, __shfl_xor_sync(kFull, top, 1));
+  top = max(top, __shfl_xor_sync(kFull, top, 2));
+  uint32_t ex = min(max(top >> 23, 1u), 253u);
+  if (top >= 0x7F800000u) ex = 127u;  // infinite or NaN: as it is
+  const float m = a.q_sign * __uint_as_float((254u - ex) << 23);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      f[4 * i + w][0] = narrow(x[i][4 * w] * m, x[i][4 * w + 1] * m, (const __half*)nullptr);
+      f[4 * i + w][1] = narrow(x[i][4 * w + 2] * m, x[i][4 * w + 3] * m, (const __half*)nullptr);
+    }
+  return __uint_as_float(ex << 23);
+}
+
+template <int D>
+__device__ __forceinline__ float load_q_any(const Args& a, long long at, bool valid, int t, uint32_t (&f)[D / 16][2]) {
+  if (a.c.q_dtype == TQ_DTYPE_F32) return load_q<D>(a, static_cast<const float*>(a.c.q) + at, valid, t, f);
+  if (a.c.q_dtype == TQ_DTYPE_F16) return load_q<D>(a, static_cast<const __half*>(a.c.q) + at, valid, t, f);
+  return load_q<D>(a, static_cast<const __nv_bfloat16*>(a.c.q) + at, valid, t, f);
+}
+
+// Clamps the scales of a lane's vector as the large kernel does; true where one of them is not finite (it becomes 0).
+template <int D>
+__device__ __noinline__ bool mend_scales(__half* s) {
+  bool poison = false;
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t h = __half_as_ushort(s[i]);
+    if (not_finite(h)) {
+      poison = true;
+      s[i] = __ushort_as_half(0);
+    } else if ((h & 0x7FFFu) > 0x5FFEu) {
+      s[i] = __ushort_as_half((unsigned short)((h & 0x8000u) | 0x5FFEu));  // 511.5
+    }
+  }
+  return poison;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__ Args a) {
+  using F = Few<D>;
+  constexpr int NS = F::NS;
+  extern __shared__ __align__(128) unsigned char sm[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  Item* items = reinterpret_cast<Item*>(sm + F::items);
+  unsigned char* ring = sm + warp * NS * F::slice;
+  const uint32_t ring_s = tc::smem_addr(ring);
+  uint32_t* miss = reinterpret_cast<uint32_t*>(sm + F::miss) + warp * NS;
+  float2* ml = reinterpret_cast<float2*>(sm + F::ml);
+  int* flag = reinterpret_cast<int*>(sm + F::flag);
+  const DevView &K = a.c.k, &V = a.c.v;
+  const bool mods = a.c.softcap > 0.f || a.c.slopes != nullptr;
+  pdl_wait();  // the plan
+  Items<D>* walk = reinterpret_cast<Items<D>*>(sm + F::walk);
+  static_assert(sizeof(Items<D>) <= 64, "items");
+  if (tid == 0) {
+    walk->start(a);
+    walk->next(a, items[0]);
+  }
+  __syncthreads();
+  for (int n_item = 0;; ++n_item) {
+    const Item& it = items[n_item & 1];
+    if (it.kind == 0) break;
+    const int G = a.c.G, rows = it.rows;
+    auto out_of = [&](int r) {  // where row r's result goes
+      const int row = it.row0 + r, ti = row / G;
+      return ((long long)(it.tok0 + ti) * a.c.n_q_heads + it.kvh * G + (row - ti * G)) * D;
+    };
+    auto next_item = [&]() {
+      if (tid == 0) walk->next(a, items[(n_item + 1) & 1]);
+    };
+    if (it.kind == 2) {
+      next_item();
+      for (int i = tid; i < rows * (D / 8); i += NW * 32) {
+        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        store8(a.c.out, a.c.out_dtype, out_of(i / (D / 8)) + 8 * (i % (D / 8)), z);
+      }
+      __syncthreads();
+      continue;
+    }
+    constexpr int BN = Shape<D>::BN;
+    const int j0 = max(it.tile * BN, it.lo) & ~(SK - 1), end = min((it.tile + it.n) * BN, it.hi);
+    const int mine = ((end - j0 + SK - 1) / SK - warp + NW - 1) / NW;  // this warp's slices
+    const long long first = (long long)a.c.layer * K.num_pages;
+    auto key_of = [&](int k) { return j0 + SK * (warp + NW * k); };
+    // asks for slice k of this warp; sp: the place of key lane % 16 of it
+    auto issue = [&](int k, const Spot& sp) {
+      if (k < mine) {
+        const int j = key_of(k) + (lane & 15), st = k % NS;
+        const bool on = sp.page >= 0 && sp.page < K.num_pages;
+        const long long vec = on ? ((first + sp.page) * K.H + it.kvh) * K.page_size + sp.off : 0;
+        const uint32_t off = __ballot_sync(kFull, j >= it.lo && j < end && !on) & 0xFFFFu;
+        if (lane == 0) {
+          miss[st] = off;
+          if (off) atomicOr(a.c.tab.status, kFlagBlockTable);
+        }
+        const uint32_t base = ring_s + st * F::slice;
+        {
+          const unsigned char* h = lane < 16 ? K.header + vec * (D / 16) : V.header + vec * (D / 16);
+          const uint32_t dst = base + (lane < 16 ? F::ks : F::vs) + (lane & 15) * (D / 16);
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) copy_async<4>(dst + 4 * i, h + 4 * i, on);
+        }
+        constexpr int LPK = D / 16;  // lanes of a key
+        const int c = lane % LPK;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const int key = i * (32 / LPK) + lane / LPK;
+          const long long kv = __shfl_sync(kFull, vec, key);
+          const bool kon = __shfl_sync(kFull, (int)on, key) != 0;
+          copy_async<16>(base + F::k + k_at<D>(key, c), K.payload + kv * D + 16 * c, kon);
+          copy_async<16>(base + F::v + v_at<D>(key, c), V.payload + kv * D + 16 * c, kon);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    {
+      Spot sp[NS - 1];
+#pragma unroll
+      for (int k = 0; k < NS - 1; ++k) sp[k] = spot_of(a, it, k < mine ? key_of(k) + (lane & 15) : 0x7FFFFFFF, end);
+#pragma unroll
+      for (int k = 0; k < NS - 1; ++k) issue(k, sp[k]);
+    }
+    Spot ahead = spot_of(a, it, NS - 1 < mine ? key_of(NS - 1) + (lane & 15) : 0x7FFFFFFF, end);
+    next_item();
+
+    // this lane's rows g and g + 8
+    uint32_t q[NT][D / 16][2];
+    float sl[NT], slope[NT], m[NT], l[NT];
+    int lo[NT], hi[NT], pos[NT];
+    int all_lo = 0, all_hi = 0x7FFFFFFF;
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int r = g + 8 * u;
+      const bool valid = r < rows;
+      const int row = it.row0 + (valid ? r : 0), ti = row / G, head = it.kvh * G + (row - ti * G), tok = it.tok0 + ti;
+      const float rs = load_q_any<D>(a, (long long)tok * a.c.q_stride + (long long)head * D, valid, t, q[u]);
+      sl[u] = fmaxf(a.scale * rs, 1.2e-38f);
+      slope[u] = a.c.slopes ? a.c.slopes[head] * kLog2e : 0.f;
+      pos[u] = it.pos0 + ti;
+      lo[u] = 0;  // rows that are not there see everything: they never need a mask
+      hi[u] = 0x7FFFFFFF;
+      if (valid) {
+        hi[u] = min(it.len, max(pos[u] + 1, it.prefix));
+        if (a.c.window) lo[u] = max(lo[u], pos[u] - a.c.window + 1);
+        if (a.c.first_keys) lo[u] = max(lo[u], a.c.first_keys[tok]);
+      }
+      all_lo = max(all_lo, lo[u]);
+      all_hi = min(all_hi, hi[u]);
+      m[u] = -INFINITY;
+      l[u] = 0.f;
+    }
+    all_lo = __reduce_max_sync(kFull, all_lo);
+    all_hi = __reduce_min_sync(kFull, all_hi);
+    float o[NT][D / 16][4];
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[u][i][e] = 0.f;
+
+#pragma unroll 1
+    for (int k = 0; k < mine; ++k) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+      __syncwarp();  // slice k is there, and slice k - 1 has been read
+      issue(k + NS - 1, ahead);
+      ahead = spot_of(a, it, k + NS < mine ? key_of(k + NS) + (lane & 15) : 0x7FFFFFFF, end);
+      const int st = k % NS, key0 = key_of(k);
+      unsigned char* sk = ring + st * F::slice;
+      uint32_t poison = 0;
+      {
+        __half* s = reinterpret_cast<__half*>(sk + (lane < 16 ? F::ks : F::vs) + (lane & 15) * (D / 16));
+        bool big = false;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+          big |= __vcmpgtu2(reinterpret_cast<const uint32_t*>(s)[i] & 0x7FFF7FFFu, 0x5FFE5FFEu) != 0;
+        if (__any_sync(kFull, big)) {
+          const uint32_t p = __ballot_sync(kFull, mend_scales<D>(s));
+          poison = (p | p >> 16) & 0xFFFFu;
+          __syncwarp();
+        }
+      }
+      // scores: x[key tile][keys 2 t, 2 t + 1 of row g, then of row g + 8]
+      float x[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int key = 8 * n + g;
+        x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(sk + F::k + k_at<D>(key, 4 * i + t));
+          const uint32_t s1 = *reinterpret_cast<const uint16_t*>(sk + F::ks + key * (D / 16) + ((4 * i + t) >> 1) * 2);
+          const uint32_t s2 = __byte_perm(s1, s1, 0x1010), w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t b0, b1;
+            q8_pairs(w[c], b0, b1);
+            wm::mma_16816(x[n], q[0][4 * i + c][0], NT > 1 ? q[NT - 1][4 * i + c][0] : 0u, q[0][4 * i + c][1],
+                          NT > 1 ? q[NT - 1][4 * i + c][1] : 0u, mul_h2(b0, s2), mul_h2(b1, s2));
+          }
+        }
+      }
+      const uint32_t gone = miss[st];
+      const bool masked = key0 < all_lo || key0 + SK > all_hi || (gone | poison) != 0u || key0 < it.lo || key0 + SK > end;
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& s = x[n][2 * u + e];
+            s *= sl[u];
+            if (mods) {
+              const float cap = a.c.softcap;  // sl holds log2 e
+              if (cap > 0.f) s = cap * kLog2e * (1.f - __fdividef(2.f, 1.f + ex2(s * (2.f / cap))));
+              if (slope[u] != 0.f) s = fmaf(-slope[u], fabsf((float)(pos[u] - (key0 + 8 * n + 2 * t + e))), s);
+            }
+            if (masked) {
+              const int c = 8 * n + 2 * t + e, j = key0 + c;
+              if ((poison >> c) & 1u) s = __uint_as_float(0x7FC00000u);
+              if (j < lo[u] || j >= hi[u] || j < it.lo || j >= end || ((gone >> c) & 1u)) s = -INFINITY;
+            }
+          }
+      }
+      bool raise = false;
+      float mx[NT];
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        mx[u] = fmaxf(fmaxf(x[0][2 * u], x[0][2 * u + 1]), fmaxf(x[1][2 * u], x[1][2 * u + 1]));
+        raise |= mx[u] - m[u] > kMaxExp;
+      }
+      if (__any_sync(kFull, raise)) {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          float top = mx[u];
+          top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+          const float mn = fmaxf(m[u], top - kBias);
+          const float al = mn == -INFINITY ? 1.f : ex2(m[u] - mn);
+          m[u] = mn;
+          l[u] *= al;
+          const float a0 = __shfl_sync(kFull, al, 8 * t), a1 = __shfl_sync(kFull, al, 8 * t + 4);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[u][i][0] *= a0;
+            o[u][i][1] *= a1;
+            o[u][i][2] *= a0;
+            o[u][i][3] *= a1;
+          }
+        }
+      }
+      uint32_t p[NT][2];
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        const float mu = m[u] == -INFINITY ? 0.f : m[u];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float e0 = ex2(x[n][2 * u] - mu), e1 = ex2(x[n][2 * u + 1] - mu);
+          l[u] += e0 + e1;
+          p[u][n] = narrow(e0, e1, (const __half*)nullptr);
+        }
+      }
+      // O^T += V^T P^T: this lane's coordinates are D / 8 consecutive ones (D = 256: two runs of 16) of four keys
+      const int keys[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
+#pragma unroll
+      for (int c = 0; c < (D + 127) / 128; ++c) {
+        constexpr int W = D == 64 ? 2 : 4;
+        const int chunk = D == 64 ? g >> 1 : 8 * c + g;
+        uint32_t w[4][W], s1[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const unsigned char* at = sk + F::v + v_at<D>(keys[y], chunk);
+          if constexpr (D == 64) {
+            const uint2 z = *reinterpret_cast<const uint2*>(at + 8 * (g & 1));
+            w[y][0] = z.x; w[y][1] = z.y;
+          } else {
+            const uint4 z = *reinterpret_cast<const uint4*>(at);
+            w[y][0] = z.x; w[y][1] = z.y; w[y][2] = z.z; w[y][3] = z.w;
+          }
+          s1[y] = *reinterpret_cast<const uint16_t*>(sk + F::vs + keys[y] * (D / 16) + (chunk >> 1) * 2);
+        }
+        const uint32_t sab = __byte_perm(s1[0], s1[1], 0x5410), scd = __byte_perm(s1[2], s1[3], 0x5410);
+#pragma unroll
+        for (int z = 0; z < W; ++z) {
+          uint32_t f[2][4];  // bytes 0 to 3 of the first two keys, of the second two
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            q8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x5140), f[h][0], f[h][1]);
+            q8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x7362), f[h][2], f[h][3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[h][e] = mul_h2(f[h][e], h ? scd : sab);
+          }
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            wm::mma_16816(o[u][(c * W + z) * 2], f[0][0], f[0][1], f[1][0], f[1][1], p[u][0], p[u][1]);
+            wm::mma_16816(o[u][(c * W + z) * 2 + 1], f[0][2], f[0][3], f[1][2], f[1][3], p[u][0], p[u][1]);
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the rings have been read
+
+    // ---- the warps' results, joined in their order ----
+    float* mo = reinterpret_cast<float*>(sm);  // [NW][8 NT][OS]
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      l[u] += __shfl_xor_sync(kFull, l[u], 1);
+      l[u] += __shfl_xor_sync(kFull, l[u], 2);
+      if (t == 0) ml[warp * 16 + 8 * u + g] = make_float2(m[u], l[u]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float* row = mo + (warp * 8 * NT + 8 * u + 2 * t + e) * F::OS;
+        constexpr int W = D == 64 ? 2 : 4;
+#pragma unroll
+        for (int c = 0; c < (D + 127) / 128; ++c)
+#pragma unroll
+          for (int z = 0; z < W; ++z) {
+            const float(&x)[4] = o[u][(c * W + z) * 2], (&y)[4] = o[u][(c * W + z) * 2 + 1];
+            *reinterpret_cast<float4*>(row + (D == 64 ? 8 * g : 128 * c + 16 * g) + 4 * z) =
+                make_float4(x[e], x[2 + e], y[e], y[2 + e]);
+          }
+      }
+    }
+    __syncthreads();
+    const bool whole = it.n_ctas == 1;
+    auto slot_of = [&](int cta, int which) { return ((long long)cta * 2 + which) * a.rows_cap; };
+    auto store4 = [&](long long at, const float (&y)[4]) {
+      if (a.c.out_dtype == TQ_DTYPE_F32) store_row<4>(static_cast<float*>(a.c.out) + at, y);
+      else if (a.c.out_dtype == TQ_DTYPE_F16) store_row<4>(static_cast<__half*>(a.c.out) + at, y);
+      else store_row<4>(static_cast<__nv_bfloat16*>(a.c.out) + at, y);
+    };
+    const long long my_slot = slot_of(blockIdx.x, it.slot);
+    for (int i = tid; i < rows * (D / 4); i += NW * 32) {
+      const int r = i / (D / 4), c = i % (D / 4);
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w * 16 + r].x);
+      const float at_m = top == -INFINITY ? 0.f : top;
+      float y[4] = {0.f, 0.f, 0.f, 0.f}, lt = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float2 z = ml[w * 16 + r];
+        if (z.y == 0.f) continue;  // a share without weight is not looked at
+        const float f = ex2(z.x - at_m);
+        const float4 v = *reinterpret_cast<const float4*>(mo + (w * 8 * NT + r) * F::OS + 4 * c);
+        lt = fmaf(f, z.y, lt);
+        y[0] = fmaf(f, v.x, y[0]);
+        y[1] = fmaf(f, v.y, y[1]);
+        y[2] = fmaf(f, v.z, y[2]);
+        y[3] = fmaf(f, v.w, y[3]);
+      }
+      if (whole) {
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] *= inv;
+        store4(out_of(r) + 4 * c, y);
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (my_slot + r) * D + 4 * c) = make_float4(y[0], y[1], y[2], y[3]);
+        if (c == 0) *reinterpret_cast<float2*>(a.part_ml + (my_slot + r) * 2) = make_float2(top, lt);
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) *flag = (int)atomicAdd(a.counters + it.counter, 1u) == it.n_ctas - 1;
+      __syncthreads();
+      if (*flag) {
+        __threadfence();
+        auto share = [&](int p) {
+          const int ci = min(p, it.n_ctas - 1);
+          return slot_of(it.first_cta + ci, ci == 0 ? 1 : 0);
+        };
+        for (int i = tid; i < rows * (D / 4); i += NW * 32) {
+          const int r = i / (D / 4), c = i % (D / 4);
+          float top = -INFINITY, lt = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int p0 = 0; p0 < it.n_ctas; p0 += 8) {
+            float2 z[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) z[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (share(p0 + k) + r) * 2));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, z[k].y != 0.f ? z[k].x : -INFINITY);
+          }
+          if (top == -INFINITY) top = 0.f;
+#pragma unroll 1
+          for (int p0 = 0; p0 < it.n_ctas; p0 += 8) {
+            float2 z[8];
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const long long at = share(p0 + k) + r;
+              z[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2));
+              v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * c));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (p0 + k >= it.n_ctas || z[k].y == 0.f) continue;
+              const float f = ex2(z[k].x - top);
+              lt = fmaf(f, z[k].y, lt);
+              y[0] = fmaf(f, v[k].x, y[0]);
+              y[1] = fmaf(f, v[k].y, y[1]);
+              y[2] = fmaf(f, v[k].z, y[2]);
+              y[3] = fmaf(f, v[k].w, y[3]);
+            }
+          }
+          const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] *= inv;
+          store4(out_of(r) + 4 * c, y);
+        }
+      }
+    }
+    __syncthreads();  // before the rings, the item and the flag are written again
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_few_t(const Args& a, int sm_count, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::total);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(few_kernel<D, NT>, dim3((unsigned)(2 * sm_count)), dim3(NW * 32), Few<D>::total, s, a);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace
+
+int few_rows(int d) { return d == 256 ? 8 : 16; }
+
+cudaError_t launch_few(const Args& a, long long rows, int sm_count, cudaStream_t s) {
+  if (a.c.k.d == 256) return launch_few_t<256, 1>(a, sm_count, s);
+  if (a.c.k.d == 128) return rows > 8 ? launch_few_t<128, 2>(a, sm_count, s) : launch_few_t<128, 1>(a, sm_count, s);
+  return rows > 8 ? launch_few_t<64, 2>(a, sm_count, s) : launch_few_t<64, 1>(a, sm_count, s);
+}
+
+}  // namespace ck
+}  // namespace tq

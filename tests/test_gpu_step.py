@@ -934,3 +934,106 @@ def test_batches_are_fixed_and_on_the_gpu(ctxs):
         tq.Batch(b.cu_tokens, b.seq_lens, b.block_table[:, :0].contiguous(), 1, 1, 5)
     with pytest.raises(ValueError):
         tq.ScoreMods(slopes=torch.zeros(2))
+
+
+# ---------------------------------------------------------------------------
+# entries of few rows (decode and short speculative steps take a kernel of their own)
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G,new,lens,page", [
+    (1, [1], [1], 16),
+    (4, [1, 0, 1, 1], [15, 9, 16, 17], 16),
+    (8, [1], [9000], 16),
+    (2, [4, 1, 3], [4, 4000, 1537], 24),
+    (5, [1] * 30, list(range(3, 3003, 100)), 1),
+    (7, [2, 1], [1000, 2], 100),
+    (16, [1, 1], [129, 257], 64),
+    (1, [16, 7], [500, 7], 8),
+    (3, [5], [2100], 256),
+])
+def test_attend_few_rows(ctxs, d, G, new, lens, page):
+    check_attend(Paged(ctxs[d], d, 2, new, lens, page, padding=1), G, torch.float16)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("mods", [dict(softcap=5.0), dict(window=1), dict(window=50), dict(bias=True),
+                                  dict(prefix=[500, 8, 0, 10 ** 6]),
+                                  dict(softcap=20.0, window=700, bias=True, prefix=[30, 0, 100, 9])])
+def test_attend_few_rows_score_modifications(ctxs, d, mods):
+    P = Paged(ctxs[d], d, 2, [4, 1, 0, 3], [1900, 290, 4, 33], 16)
+    check_attend(P, 2, torch.float16, **mods)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_few_rows_documents_types_and_outliers(ctxs, d):
+    P = Paged(ctxs[d], d, 1, [8, 2, 1], [777, 400, 64], 16, outliers=0.01)
+    first = P.pos - P.pos % 37
+    first[[1, 8]] = [10 ** 9, P.pos[8] + 1]  # rows that see nothing
+    first[10] = 64                           # a whole entry
+    for dtype, out in ((torch.float32, torch.float32), (torch.bfloat16, torch.float16), (torch.float16, torch.bfloat16)):
+        check_attend(P, 1, dtype, out, first=first)
+        check_attend(P, 1, dtype, out)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_few_rows_masked_values_do_not_leak(ctxs, d):
+    """Infinite and NaN scales, one key each: rows that see them are NaN, the others as without them."""
+    for which, bad in (("k", float("nan")), ("v", float("inf")), ("k", float("-inf")), ("v", float("nan"))):
+        P = Paged(ctxs[d], d, 1, [6, 1], [260, 50], 16)
+        q = W.normal_tensor((7, 1, d), seed=4, device="cuda").half()
+        first = np.array([0, 131, 130, 140, 0, 259, 0])
+        m = mods_of(P, 1, first=first)
+        clean = attend(P, q, mods=m)
+        view = P.kv if which == "k" else P.vv
+        s = int(P.slots(0, [130])[0])
+        h = view.header.view(torch.float16).view(-1, d // 32)
+        h[s, -1] = bad
+        got = attend(P, q, mods=m)
+        torch.cuda.synchronize()
+        sees = torch.tensor([1, 0, 1, 0, 1, 0, 0], dtype=torch.bool)
+        assert torch.isnan(got[sees]).all()
+        assert torch.equal(got[~sees], clean[~sees]) and torch.isfinite(clean).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_few_rows_out_of_range(ctxs, d):
+    ctx = ctxs[d]
+    P = Paged(ctx, d, 1, [2, 1], [600, 40], 16)
+    q = W.normal_tensor((3, 2, d), seed=8, device="cuda").half()
+    good = P.table
+    P.table = good.copy()
+    P.table[0, [1, 20]] = [-7, 10 ** 6]
+    P.set_batch([0, 2, 3], [600, 40])
+    out = attend(P, q)
+    torch.cuda.synchronize()
+    assert status(ctx) == 2
+    P.table = good
+    k, v = P.stored(0)
+    missing = np.isin(np.arange(600) // 16, [1, 20])
+    want = S.chunk_attention(f64(q)[:2], k, v, P.pos[:2], 1 / math.sqrt(d), missing=missing)
+    assert C.rel_err_per_head(f64(out)[:2], want).max() < C.ATTN_RTOL + half_step(out.dtype)
+    for cu, lens in (([0, 2, 3], [600, 0]), ([0, 2, 3], [600, 601]), ([0, 2, 4], [600, 40])):
+        P.set_batch(cu, lens)
+        out = attend(P, q)
+        torch.cuda.synchronize()
+        assert status(ctx) == 1 and out[:2].any() and not out[2:].any(), (cu, lens)
+
+
+def test_attend_few_rows_is_deterministic_and_isolated(ctxs):
+    """Repeats are equal, whatever the workspace held; a NaN query row stays alone; scaled queries give the same."""
+    P = Paged(ctxs[128], 128, 2, [1, 3, 1], [30000, 2000, 700], 16)
+    q = W.normal_tensor((5, 8, 128), seed=5, device="cuda").to(torch.bfloat16)
+    n = tq.tq_chunk_workspace_bytes(P.ctx.h, P.batch, 8, 2)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    first = attend(P, q, workspace=ws)
+    for fill in (0, 255, 77):
+        assert torch.equal(attend(P, q, workspace=ws.fill_(fill)), first)
+    assert torch.equal(attend(P, q * 2.0 ** 40, scale=2.0 ** -40 / math.sqrt(128)), first)
+    q2 = q.clone()
+    q2[2, 5] = float("nan")
+    got = attend(P, q2)
+    torch.cuda.synchronize()
+    assert torch.isnan(got[2, 5]).all()
+    got[2, 5] = first[2, 5]
+    assert torch.equal(got, first)
