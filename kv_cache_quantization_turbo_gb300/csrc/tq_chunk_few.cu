@@ -18,13 +18,14 @@ namespace tq {
 namespace ck {
 namespace {
 
-constexpr int NW = 6;      // warps of a CTA; two CTAs per SM hide each other's starts and ends of ranges
 constexpr int SK = 16;     // keys of a slice
 constexpr float kMaxExp = 15.f;
 
-template <int D>
+// Two CTAs per SM hide each other's starts and ends of ranges.
+template <int D, int NT>
 struct Few {
-  static constexpr int NS = 512 / D;          // slices of a warp's ring
+  static constexpr int NW = D == 256 || NT > 1 ? 6 : 8;  // warps of a CTA: as many as have the registers
+  static constexpr int NS = 24 * 128 / (D * NW);         // slices of a warp's ring
   static constexpr int SB = D / 32;           // scales of a vector
   static constexpr int k = 0, v = SK * D;     // parts of a slice
   static constexpr int ks = 2 * SK * D, vs = ks + SK * SB * 2;
@@ -37,8 +38,7 @@ struct Few {
   static constexpr int walk = flag + 16;      // Items<D>
   static constexpr int total = walk + 64;
   static constexpr int OS = D + 4;            // floats of a row of a warp's O (in the ring, once it is read)
-  static_assert(NW * 16 * OS * 4 <= ring || D == 256, "merge area");
-  static_assert(NW * 8 * OS * 4 <= ring, "merge area");
+  static_assert(NS >= 2 && NW * 8 * NT * OS * 4 <= ring, "merge area");
   static_assert(2 * (total + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
@@ -63,15 +63,21 @@ struct Spot {
   int page, off;
 };
 
-// Page and offset of a key, -1 where the key is not wanted.
-__device__ __forceinline__ Spot spot_of(const Args& a, const Item& it, int j, int end) {
+// Page and offset of a key, -1 where the key is not wanted.  inv: floor((2^32 - 1) / page_size), with which the quotient is
+// at most one too small.
+__device__ __forceinline__ Spot spot_of(const Args& a, const Item& it, int j, int end, uint32_t inv) {
   const DevBatch& b = a.c.b;
   Spot s{-1, 0};
-  if (j >= it.lo && j < end) {
-    const int ps = a.c.k.page_size, lp = (int)((uint32_t)j / (uint32_t)ps);
+  if (j < end) {
+    if (!b.block_table) return Spot{it.seq, j};
+    const int ps = a.c.k.page_size;
+    int lp = (int)__umulhi((uint32_t)j, inv);
     s.off = j - lp * ps;
-    s.page = it.seq;
-    if (b.block_table) s.page = lp < b.max_blocks ? __ldg(b.block_table + (long long)it.seq * b.max_blocks + lp) : -1;
+    if (s.off >= ps) {
+      ++lp;
+      s.off -= ps;
+    }
+    if (lp < b.max_blocks) s.page = __ldg(b.block_table + (long long)it.seq * b.max_blocks + lp);
   }
   return s;
 }
@@ -132,9 +138,9 @@ __device__ __noinline__ bool mend_scales(__half* s) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__ Args a) {
-  using F = Few<D>;
-  constexpr int NS = F::NS;
+__global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __grid_constant__ Args a) {
+  using F = Few<D, NT>;
+  constexpr int NS = F::NS, NW = F::NW;
   extern __shared__ __align__(128) unsigned char sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   Item* items = reinterpret_cast<Item*>(sm + F::items);
@@ -145,6 +151,9 @@ __global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__
   int* flag = reinterpret_cast<int*>(sm + F::flag);
   const DevView &K = a.c.k, &V = a.c.v;
   const bool mods = a.c.softcap > 0.f || a.c.slopes != nullptr;
+  // where the 16 keys of a slice, which begin at a multiple of 16, are consecutive vectors
+  const bool runs = !a.c.b.block_table || K.page_size % SK == 0;
+  const uint32_t inv = 0xFFFFFFFFu / (uint32_t)K.page_size;
   pdl_wait();  // the plan
   Items<D>* walk = reinterpret_cast<Items<D>*>(sm + F::walk);
   static_assert(sizeof(Items<D>) <= 64, "items");
@@ -178,50 +187,79 @@ __global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__
     const int mine = ((end - j0 + SK - 1) / SK - warp + NW - 1) / NW;  // this warp's slices
     const long long first = (long long)a.c.layer * K.num_pages;
     auto key_of = [&](int k) { return j0 + SK * (warp + NW * k); };
-    // asks for slice k of this warp; sp: the place of key lane % 16 of it
-    auto issue = [&](int k, const Spot& sp) {
+    // asks for slice k of this warp into stage st; sp: the place of key lane % 16 of it, or (runs) of its first key
+    auto issue = [&](int k, int st, const Spot& sp) {
       if (k < mine) {
-        const int j = key_of(k) + (lane & 15), st = k % NS;
-        const bool on = sp.page >= 0 && sp.page < K.num_pages;
-        const long long vec = on ? ((first + sp.page) * K.H + it.kvh) * K.page_size + sp.off : 0;
-        const uint32_t off = __ballot_sync(kFull, j >= it.lo && j < end && !on) & 0xFFFFu;
-        if (lane == 0) {
-          miss[st] = off;
-          if (off) atomicOr(a.c.tab.status, kFlagBlockTable);
-        }
+        const int n0 = key_of(k), c0 = max(it.lo - n0, 0), c1 = min(end - n0, SK);  // the keys [c0, c1) are wanted
+        const bool there = sp.page >= 0 && sp.page < K.num_pages;
         const uint32_t base = ring_s + st * F::slice;
-        {
-          const unsigned char* h = lane < 16 ? K.header + vec * (D / 16) : V.header + vec * (D / 16);
-          const uint32_t dst = base + (lane < 16 ? F::ks : F::vs) + (lane & 15) * (D / 16);
+        constexpr int LPK = D / 16, KPI = 32 / LPK;  // lanes of a key, keys of a copy
+        const int kl = lane / LPK, c = lane % LPK;
+        const long long vec = there ? ((first + sp.page) * K.H + it.kvh) * K.page_size + sp.off : 0;
+        auto mark = [&](uint32_t off) {
+          if (lane == 0) {
+            miss[st] = off;
+            if (off) atomicOr(a.c.tab.status, kFlagBlockTable);
+          }
+        };
+        if (runs) {
+          const uint32_t want = (1u << c1) - (1u << c0);
+          mark(there ? 0u : want);
+          const unsigned char *pk = K.payload + vec * D + 16 * lane, *pv = V.payload + vec * D + 16 * lane;
+          const unsigned char *hk = K.header + vec * (D / 16) + 4 * lane, *hv = V.header + vec * (D / 16) + 4 * lane;
+          auto go = [&](auto on) {  // on(key): the key is there
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              const int key = i * KPI + kl;
+              copy_async<16>(base + F::k + k_at<D>(key, c), pk + 512 * i, on(key));
+              copy_async<16>(base + F::v + v_at<D>(key, c), pv + 512 * i, on(key));
+            }
+#pragma unroll
+            for (int i = 0; i < (D + 127) / 128; ++i) {
+              const int at = 4 * lane + 128 * i;
+              if (D < 128 && lane >= D / 4) break;
+              copy_async<4>(base + F::ks + at, hk + 128 * i, on(at / (D / 16)));
+              copy_async<4>(base + F::vs + at, hv + 128 * i, on(at / (D / 16)));
+            }
+          };
+          if (there && c0 == 0 && c1 == SK) go([](int) { return true; });
+          else go([&](int key) { return there && key >= c0 && key < c1; });
+        } else {
+          const int mk = lane & 15;
+          const bool on = there && mk >= c0 && mk < c1;
+          mark(__ballot_sync(kFull, mk >= c0 && mk < c1 && !there) & 0xFFFFu);
+          const unsigned char* h = (lane < 16 ? K.header : V.header) + (on ? vec : 0) * (D / 16);
+          const uint32_t dst = base + (lane < 16 ? F::ks : F::vs) + mk * (D / 16);
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) copy_async<4>(dst + 4 * i, h + 4 * i, on);
-        }
-        constexpr int LPK = D / 16;  // lanes of a key
-        const int c = lane % LPK;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int key = i * (32 / LPK) + lane / LPK;
-          const long long kv = __shfl_sync(kFull, vec, key);
-          const bool kon = __shfl_sync(kFull, (int)on, key) != 0;
-          copy_async<16>(base + F::k + k_at<D>(key, c), K.payload + kv * D + 16 * c, kon);
-          copy_async<16>(base + F::v + v_at<D>(key, c), V.payload + kv * D + 16 * c, kon);
+          for (int i = 0; i < D / 32; ++i) {
+            const int key = i * KPI + kl;
+            const long long kv = __shfl_sync(kFull, on ? vec : -1, key);
+            const long long at = (kv < 0 ? 0 : kv) * D + 16 * c;
+            copy_async<16>(base + F::k + k_at<D>(key, c), K.payload + at, kv >= 0);
+            copy_async<16>(base + F::v + v_at<D>(key, c), V.payload + at, kv >= 0);
+          }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    auto spot = [&](int k) {
+      return spot_of(a, it, k < mine ? key_of(k) + (runs ? 0 : lane & 15) : 0x7FFFFFFF, end, inv);
+    };
     {
       Spot sp[NS - 1];
 #pragma unroll
-      for (int k = 0; k < NS - 1; ++k) sp[k] = spot_of(a, it, k < mine ? key_of(k) + (lane & 15) : 0x7FFFFFFF, end);
+      for (int k = 0; k < NS - 1; ++k) sp[k] = spot(k);
 #pragma unroll
-      for (int k = 0; k < NS - 1; ++k) issue(k, sp[k]);
+      for (int k = 0; k < NS - 1; ++k) issue(k, k, sp[k]);
     }
-    Spot ahead = spot_of(a, it, NS - 1 < mine ? key_of(NS - 1) + (lane & 15) : 0x7FFFFFFF, end);
+    Spot ahead = spot(NS - 1);
     next_item();
 
     // this lane's rows g and g + 8
     uint32_t q[NT][D / 16][2];
-    float sl[NT], slope[NT], m[NT], l[NT];
+    float sl[NT], f[NT], slope[NT], m[NT], l[NT];
     int lo[NT], hi[NT], pos[NT];
     int all_lo = 0, all_hi = 0x7FFFFFFF;
 #pragma unroll
@@ -231,6 +269,7 @@ __global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__
       const int row = it.row0 + (valid ? r : 0), ti = row / G, head = it.kvh * G + (row - ti * G), tok = it.tok0 + ti;
       const float rs = load_q_any<D>(a, (long long)tok * a.c.q_stride + (long long)head * D, valid, t, q[u]);
       sl[u] = fmaxf(a.scale * rs, 1.2e-38f);
+      f[u] = mods ? 1.f : sl[u];  // scores to log2 units (those with modifications are in them already)
       slope[u] = a.c.slopes ? a.c.slopes[head] * kLog2e : 0.f;
       pos[u] = it.pos0 + ti;
       lo[u] = 0;  // rows that are not there see everything: they never need a mask
@@ -255,13 +294,14 @@ __global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[u][i][e] = 0.f;
 
+    int st = 0;
 #pragma unroll 1
-    for (int k = 0; k < mine; ++k) {
+    for (int k = 0; k < mine; ++k, st = st + 1 == NS ? 0 : st + 1) {
       asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
       __syncwarp();  // slice k is there, and slice k - 1 has been read
-      issue(k + NS - 1, ahead);
-      ahead = spot_of(a, it, k + NS < mine ? key_of(k + NS) + (lane & 15) : 0x7FFFFFFF, end);
-      const int st = k % NS, key0 = key_of(k);
+      issue(k + NS - 1, st == 0 ? NS - 1 : st - 1, ahead);
+      ahead = spot(k + NS);
+      const int key0 = key_of(k);
       unsigned char* sk = ring + st * F::slice;
       uint32_t poison = 0;
       {
@@ -298,31 +338,32 @@ __global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__
       }
       const uint32_t gone = miss[st];
       const bool masked = key0 < all_lo || key0 + SK > all_hi || (gone | poison) != 0u || key0 < it.lo || key0 + SK > end;
+      if (mods || masked) {
 #pragma unroll
-      for (int u = 0; u < NT; ++u) {
+        for (int u = 0; u < NT; ++u) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& s = x[n][2 * u + e];
-            s *= sl[u];
-            if (mods) {
-              const float cap = a.c.softcap;  // sl holds log2 e
-              if (cap > 0.f) s = cap * kLog2e * (1.f - __fdividef(2.f, 1.f + ex2(s * (2.f / cap))));
-              if (slope[u] != 0.f) s = fmaf(-slope[u], fabsf((float)(pos[u] - (key0 + 8 * n + 2 * t + e))), s);
-            }
-            if (masked) {
+            for (int e = 0; e < 2; ++e) {
+              float& s = x[n][2 * u + e];
               const int c = 8 * n + 2 * t + e, j = key0 + c;
+              if (mods) {
+                s *= sl[u];
+                const float cap = a.c.softcap;  // sl holds log2 e
+                if (cap > 0.f) s = cap * kLog2e * (1.f - __fdividef(2.f, 1.f + ex2(s * (2.f / cap))));
+                if (slope[u] != 0.f) s = fmaf(-slope[u], fabsf((float)(pos[u] - j)), s);
+              }
               if ((poison >> c) & 1u) s = __uint_as_float(0x7FC00000u);
               if (j < lo[u] || j >= hi[u] || j < it.lo || j >= end || ((gone >> c) & 1u)) s = -INFINITY;
             }
-          }
+        }
       }
       bool raise = false;
       float mx[NT];
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         mx[u] = fmaxf(fmaxf(x[0][2 * u], x[0][2 * u + 1]), fmaxf(x[1][2 * u], x[1][2 * u + 1]));
+        mx[u] *= f[u];
         raise |= mx[u] - m[u] > kMaxExp;
       }
       if (__any_sync(kFull, raise)) {
@@ -351,7 +392,7 @@ __global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__
         const float mu = m[u] == -INFINITY ? 0.f : m[u];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float e0 = ex2(x[n][2 * u] - mu), e1 = ex2(x[n][2 * u + 1] - mu);
+          const float e0 = ex2(fmaf(x[n][2 * u], f[u], -mu)), e1 = ex2(fmaf(x[n][2 * u + 1], f[u], -mu));
           l[u] += e0 + e1;
           p[u][n] = narrow(e0, e1, (const __half*)nullptr);
         }
@@ -378,18 +419,18 @@ __global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__
         const uint32_t sab = __byte_perm(s1[0], s1[1], 0x5410), scd = __byte_perm(s1[2], s1[3], 0x5410);
 #pragma unroll
         for (int z = 0; z < W; ++z) {
-          uint32_t f[2][4];  // bytes 0 to 3 of the first two keys, of the second two
+          uint32_t y[2][4];  // bytes 0 to 3 of the first two keys, of the second two
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            q8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x5140), f[h][0], f[h][1]);
-            q8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x7362), f[h][2], f[h][3]);
+            q8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x5140), y[h][0], y[h][1]);
+            q8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x7362), y[h][2], y[h][3]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[h][e] = mul_h2(f[h][e], h ? scd : sab);
+            for (int e = 0; e < 4; ++e) y[h][e] = mul_h2(y[h][e], h ? scd : sab);
           }
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
-            wm::mma_16816(o[u][(c * W + z) * 2], f[0][0], f[0][1], f[1][0], f[1][1], p[u][0], p[u][1]);
-            wm::mma_16816(o[u][(c * W + z) * 2 + 1], f[0][2], f[0][3], f[1][2], f[1][3], p[u][0], p[u][1]);
+            wm::mma_16816(o[u][(c * W + z) * 2], y[0][0], y[0][1], y[1][0], y[1][1], p[u][0], p[u][1]);
+            wm::mma_16816(o[u][(c * W + z) * 2 + 1], y[0][2], y[0][3], y[1][2], y[1][3], p[u][0], p[u][1]);
           }
         }
       }
@@ -463,47 +504,76 @@ __global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__
       __syncthreads();
       if (*flag) {
         __threadfence();
-        auto share = [&](int p) {
-          const int ci = min(p, it.n_ctas - 1);
-          return slot_of(it.first_cta + ci, ci == 0 ? 1 : 0);
-        };
-        for (int i = tid; i < rows * (D / 4); i += NW * 32) {
-          const int r = i / (D / 4), c = i % (D / 4);
-          float top = -INFINITY, lt = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int p0 = 0; p0 < it.n_ctas; p0 += 8) {
-            float2 z[8];
+        // the shares' references and sums first, then, per four columns of a row, PG threads take every PG-th share each
+        const int n_sh = it.n_ctas;
+        constexpr int TH = NW * 32;
+        float2* sh = reinterpret_cast<float2*>(sm);  // [n_sh][rows]: weight of a share, its sum times that
+        auto share = [&](int p) { return slot_of(it.first_cta + p, p == 0 ? 1 : 0); };
+        for (int i = tid; i < n_sh * rows; i += TH)
+          sh[i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (share(i / rows) + i % rows) * 2));
+        __syncthreads();
+        for (int r = warp; r < rows; r += NW) {
+          float top = -INFINITY;
+          for (int p = lane; p < n_sh; p += 32) top = fmaxf(top, sh[p * rows + r].y != 0.f ? sh[p * rows + r].x : -INFINITY);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) z[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (share(p0 + k) + r) * 2));
-#pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, z[k].y != 0.f ? z[k].x : -INFINITY);
-          }
+          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
           if (top == -INFINITY) top = 0.f;
+          float lt = 0.f;
+          for (int p = lane; p < n_sh; p += 32) {
+            const float2 z = sh[p * rows + r];
+            const float w = z.y == 0.f ? 0.f : ex2(z.x - top);
+            lt += w * z.y;
+            sh[p * rows + r] = make_float2(w, z.y);
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) lt += __shfl_xor_sync(kFull, lt, d);
+          if (lane == 0) ml[r] = make_float2(lt == 0.f ? 0.f : 1.f / lt, 0.f);
+        }
+        __syncthreads();
+        float4* part = reinterpret_cast<float4*>(sm + F::ring) - TH;  // (behind the weights)
+        const int units = rows * (D / 4);
+        int pg = 1;  // threads of a unit
+        while (2 * pg * units <= TH) pg *= 2;
+        for (int i0 = 0; i0 < units; i0 += TH / pg) {
+          const int i = i0 + tid % (TH / pg), q0 = tid / (TH / pg);
+          const int r = i / (D / 4), c = i % (D / 4);
+          float y[4] = {0.f, 0.f, 0.f, 0.f};
+          if (i < units && q0 < pg) {
 #pragma unroll 1
-          for (int p0 = 0; p0 < it.n_ctas; p0 += 8) {
-            float2 z[8];
-            float4 v[8];
+            for (int p0 = q0; p0 < n_sh; p0 += 8 * pg) {
+              float4 v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const long long at = share(p0 + k) + r;
-              z[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2));
-              v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * c));
-            }
+              for (int k = 0; k < 8; ++k)
+                v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (share(min(p0 + k * pg, n_sh - 1)) + r) * D + 4 * c));
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (p0 + k >= it.n_ctas || z[k].y == 0.f) continue;
-              const float f = ex2(z[k].x - top);
-              lt = fmaf(f, z[k].y, lt);
-              y[0] = fmaf(f, v[k].x, y[0]);
-              y[1] = fmaf(f, v[k].y, y[1]);
-              y[2] = fmaf(f, v[k].z, y[2]);
-              y[3] = fmaf(f, v[k].w, y[3]);
+              for (int k = 0; k < 8; ++k) {
+                if (p0 + k * pg >= n_sh) continue;
+                const float2 z = sh[(p0 + k * pg) * rows + r];
+                if (z.y == 0.f) continue;  // a share without weight is not looked at
+                y[0] = fmaf(z.x, v[k].x, y[0]);
+                y[1] = fmaf(z.x, v[k].y, y[1]);
+                y[2] = fmaf(z.x, v[k].z, y[2]);
+                y[3] = fmaf(z.x, v[k].w, y[3]);
+              }
             }
           }
-          const float inv = lt == 0.f ? 0.f : 1.f / lt;
+          if (pg > 1) {
+            part[tid] = make_float4(y[0], y[1], y[2], y[3]);
+            __syncthreads();
+          }
+          if (i < units && q0 == 0) {
+            for (int q = 1; q < pg; ++q) {
+              const float4 z = part[tid + q * (TH / pg)];
+              y[0] += z.x;
+              y[1] += z.y;
+              y[2] += z.z;
+              y[3] += z.w;
+            }
+            const float n = ml[r].x;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] *= inv;
-          store4(out_of(r) + 4 * c, y);
+            for (int e = 0; e < 4; ++e) y[e] *= n;
+            store4(out_of(r) + 4 * c, y);
+          }
         }
       }
     }
@@ -513,9 +583,12 @@ __global__ void __launch_bounds__(NW * 32, 2) few_kernel(const __grid_constant__
 
 template <int D, int NT>
 cudaError_t launch_few_t(const Args& a, int sm_count, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D>::total);
+  using F = Few<D, NT>;
+  // (the weights of an entry's shares, at most one per CTA, and the threads' sums have to fit the ring)
+  if (2LL * sm_count * 8 * NT * 8 + F::NW * 32 * 16 > F::ring) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::total);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(few_kernel<D, NT>, dim3((unsigned)(2 * sm_count)), dim3(NW * 32), Few<D>::total, s, a);
+  e = launch_pdl(few_kernel<D, NT>, dim3((unsigned)(2 * sm_count)), dim3(F::NW * 32), F::total, s, a);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
