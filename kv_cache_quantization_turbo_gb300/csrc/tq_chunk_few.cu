@@ -5,10 +5,10 @@
 // keys of its CTA's range, copies the next slices' codes and scales asynchronously to a ring of its own, turns codes into
 // fp16 fragments in registers, and keeps its own softmax reference, sum and output; no barrier until the range ends.  The
 // products are the warp-wide m16n8k16 ones (fp16 operands, fp32 sums):
-//   S = Q K^T: 16 rows (8 of them idle for NT = 1), N = 8 keys; a lane holds 16 coordinates of one key at a time, so the
-//     contraction index is permuted, alike for Q and K.
-//   O^T = V^T P^T: M = 16 coordinates, N = 8 rows; the accumulators of S are its right operand as they stand, and a lane
-//     pairs the codes of two keys by byte permutes.
+//   S^T = K Q^T: M = 16 keys, N = 8 rows; a lane holds 16 coordinates of a key at a time, so the contraction index is
+//     permuted, alike for K and Q.
+//   O^T = V^T P^T: M = 16 coordinates, N = 8 rows; a lane pairs the codes of two keys by byte permutes, and P^T is S^T's
+//     accumulators with two 8 x 8 transposes.  A lane's columns are the same rows of Q in both products.
 // The ranges, the join of entries that several CTAs share and the meaning of every mask are those of tq_chunk_tc.cuh;
 // weights are taken against a reference that is raised only when a weight would pass 2^15.
 #include "tq_chunk_tc.cuh"
@@ -34,7 +34,8 @@ struct Few {
   static constexpr int items = ring;          // Item [2]
   static constexpr int miss = items + 2 * 128;  // uint32 [NW][NS]: keys of the slice whose page is out of range
   static constexpr int ml = miss + NW * NS * 4;  // float2 [NW][16]
-  static constexpr int flag = ml + NW * 16 * 8;
+  static constexpr int row = ml + NW * 16 * 8;   // Row [16]
+  static constexpr int flag = row + 16 * 16;
   static constexpr int walk = flag + 16;      // Items<D>
   static constexpr int total = walk + 64;
   static constexpr int OS = D + 4;            // floats of a row of a warp's O (in the ring, once it is read)
@@ -51,6 +52,12 @@ __device__ __forceinline__ int v_at(int key, int chunk) {
   return key * D + ((D == 64 ? chunk ^ ((key >> 1) & 3) : chunk ^ (key & 6)) << 4);
 }
 
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {  // an 8 x 8 matrix of fp16, a pair per lane
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
 template <int N>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
   if constexpr (N == 16)
@@ -58,6 +65,11 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool o
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
 }
+
+struct Row {
+  int lo, hi, pos;  // the keys [lo, hi) it sees; its position
+  float slope;      // in log2 units
+};
 
 struct Spot {
   int page, off;
@@ -82,7 +94,7 @@ __device__ __forceinline__ Spot spot_of(const Args& a, const Item& it, int j, in
   return s;
 }
 
-// A lane's part of a row of Q as fragments of the left operand, times a power of two that brings the row's largest magnitude
+// A lane's part of a row of Q as fragments of the right operand, times a power of two that brings the row's largest magnitude
 // to [1, 2); returns that power's inverse.
 template <int D, class T>
 __device__ __forceinline__ float load_q(const Args& a, const T* src, bool valid, int t, uint32_t (&f)[D / 16][2]) {
@@ -148,6 +160,7 @@ __global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __gri
   const uint32_t ring_s = tc::smem_addr(ring);
   uint32_t* miss = reinterpret_cast<uint32_t*>(sm + F::miss) + warp * NS;
   float2* ml = reinterpret_cast<float2*>(sm + F::ml);
+  Row* row_of = reinterpret_cast<Row*>(sm + F::row);
   int* flag = reinterpret_cast<int*>(sm + F::flag);
   const DevView &K = a.c.k, &V = a.c.v;
   const bool mods = a.c.softcap > 0.f || a.c.slopes != nullptr;
@@ -185,7 +198,8 @@ __global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __gri
     constexpr int BN = Shape<D>::BN;
     const int j0 = max(it.tile * BN, it.lo) & ~(SK - 1), end = min((it.tile + it.n) * BN, it.hi);
     const int mine = ((end - j0 + SK - 1) / SK - warp + NW - 1) / NW;  // this warp's slices
-    const long long first = (long long)a.c.layer * K.num_pages;
+    const long long page_b = (long long)K.H * K.page_size * D;  // payload bytes of a page, where the head's begin, a lane's
+    const long long first_b = (long long)a.c.layer * K.num_pages * page_b + (long long)it.kvh * K.page_size * D;
     auto key_of = [&](int k) { return j0 + SK * (warp + NW * k); };
     // asks for slice k of this warp into stage st; sp: the place of key lane % 16 of it, or (runs) of its first key
     auto issue = [&](int k, int st, const Spot& sp) {
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __gri
         const uint32_t base = ring_s + st * F::slice;
         constexpr int LPK = D / 16, KPI = 32 / LPK;  // lanes of a key, keys of a copy
         const int kl = lane / LPK, c = lane % LPK;
-        const long long vec = there ? ((first + sp.page) * K.H + it.kvh) * K.page_size + sp.off : 0;
+        const long long at0 = there ? first_b + sp.page * page_b + (long long)sp.off * D : 0;  // of the payloads
         auto mark = [&](uint32_t off) {
           if (lane == 0) {
             miss[st] = off;
@@ -205,8 +219,8 @@ __global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __gri
         if (runs) {
           const uint32_t want = (1u << c1) - (1u << c0);
           mark(there ? 0u : want);
-          const unsigned char *pk = K.payload + vec * D + 16 * lane, *pv = V.payload + vec * D + 16 * lane;
-          const unsigned char *hk = K.header + vec * (D / 16) + 4 * lane, *hv = V.header + vec * (D / 16) + 4 * lane;
+          const unsigned char *pk = K.payload + at0 + 16 * lane, *pv = V.payload + at0 + 16 * lane;
+          const unsigned char *hk = K.header + (at0 >> 4) + 4 * lane, *hv = V.header + (at0 >> 4) + 4 * lane;
           auto go = [&](auto on) {  // on(key): the key is there
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
@@ -228,15 +242,15 @@ __global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __gri
           const int mk = lane & 15;
           const bool on = there && mk >= c0 && mk < c1;
           mark(__ballot_sync(kFull, mk >= c0 && mk < c1 && !there) & 0xFFFFu);
-          const unsigned char* h = (lane < 16 ? K.header : V.header) + (on ? vec : 0) * (D / 16);
+          const unsigned char* h = (lane < 16 ? K.header : V.header) + (on ? at0 >> 4 : 0);
           const uint32_t dst = base + (lane < 16 ? F::ks : F::vs) + mk * (D / 16);
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) copy_async<4>(dst + 4 * i, h + 4 * i, on);
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const int key = i * KPI + kl;
-            const long long kv = __shfl_sync(kFull, on ? vec : -1, key);
-            const long long at = (kv < 0 ? 0 : kv) * D + 16 * c;
+            const long long kv = __shfl_sync(kFull, on ? at0 : -1, key);
+            const long long at = (kv < 0 ? 0 : kv) + 16 * c;
             copy_async<16>(base + F::k + k_at<D>(key, c), K.payload + at, kv >= 0);
             copy_async<16>(base + F::v + v_at<D>(key, c), V.payload + at, kv >= 0);
           }
@@ -257,35 +271,38 @@ __global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __gri
     Spot ahead = spot(NS - 1);
     next_item();
 
-    // this lane's rows g and g + 8
+    if (tid < 16) {
+      Row r{0, 0x7FFFFFFF, 0, 0.f};  // rows that are not there see everything: they never need a mask
+      if (tid < rows) {
+        const int row = it.row0 + tid, ti = row / G;
+        r.pos = it.pos0 + ti;
+        r.hi = min(it.len, max(r.pos + 1, it.prefix));
+        if (a.c.window) r.lo = max(r.lo, r.pos - a.c.window + 1);
+        if (a.c.first_keys) r.lo = max(r.lo, a.c.first_keys[it.tok0 + ti]);
+        if (a.c.slopes) r.slope = a.c.slopes[it.kvh * G + (row - ti * G)] * kLog2e;
+      }
+      row_of[tid] = r;
+    }
+    // Q's row g (and 8 + g) as fragments; everything else of this lane belongs to the rows 2 t, 2 t + 1 (and 8 more)
     uint32_t q[NT][D / 16][2];
-    float sl[NT], f[NT], slope[NT], m[NT], l[NT];
-    int lo[NT], hi[NT], pos[NT];
-    int all_lo = 0, all_hi = 0x7FFFFFFF;
+    float sl[NT][2], m[NT][2], l[NT][2];
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       const int r = g + 8 * u;
       const bool valid = r < rows;
       const int row = it.row0 + (valid ? r : 0), ti = row / G, head = it.kvh * G + (row - ti * G), tok = it.tok0 + ti;
       const float rs = load_q_any<D>(a, (long long)tok * a.c.q_stride + (long long)head * D, valid, t, q[u]);
-      sl[u] = fmaxf(a.scale * rs, 1.2e-38f);
-      f[u] = mods ? 1.f : sl[u];  // scores to log2 units (those with modifications are in them already)
-      slope[u] = a.c.slopes ? a.c.slopes[head] * kLog2e : 0.f;
-      pos[u] = it.pos0 + ti;
-      lo[u] = 0;  // rows that are not there see everything: they never need a mask
-      hi[u] = 0x7FFFFFFF;
-      if (valid) {
-        hi[u] = min(it.len, max(pos[u] + 1, it.prefix));
-        if (a.c.window) lo[u] = max(lo[u], pos[u] - a.c.window + 1);
-        if (a.c.first_keys) lo[u] = max(lo[u], a.c.first_keys[tok]);
+      const float x = fmaxf(a.scale * rs, 1.2e-38f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sl[u][e] = __shfl_sync(kFull, x, 8 * t + 4 * e);
+        m[u][e] = -INFINITY;
+        l[u][e] = 0.f;
       }
-      all_lo = max(all_lo, lo[u]);
-      all_hi = min(all_hi, hi[u]);
-      m[u] = -INFINITY;
-      l[u] = 0.f;
     }
-    all_lo = __reduce_max_sync(kFull, all_lo);
-    all_hi = __reduce_min_sync(kFull, all_hi);
+    __syncthreads();  // the rows
+    const int all_lo = __reduce_max_sync(kFull, row_of[lane & 15].lo);
+    const int all_hi = __reduce_min_sync(kFull, row_of[lane & 15].hi);
     float o[NT][D / 16][4];
 #pragma unroll
     for (int u = 0; u < NT; ++u)
@@ -316,25 +333,40 @@ __global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __gri
           __syncwarp();
         }
       }
-      // scores: x[key tile][keys 2 t, 2 t + 1 of row g, then of row g + 8]
-      float x[2][4];
+      // scores: x[rows 8 u + ..][key g of rows 2 t, 2 t + 1, then key g + 8]
+      float x[NT][4];
+      {
+        float x2[NT][2][4];  // two chains
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int key = 8 * n + g;
-        x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x2[u][e >> 2][e & 3] = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(sk + F::k + k_at<D>(key, 4 * i + t));
-          const uint32_t s1 = *reinterpret_cast<const uint16_t*>(sk + F::ks + key * (D / 16) + ((4 * i + t) >> 1) * 2);
-          const uint32_t s2 = __byte_perm(s1, s1, 0x1010), w[4] = {w4.x, w4.y, w4.z, w4.w};
+          const uint4 wa = *reinterpret_cast<const uint4*>(sk + F::k + k_at<D>(g, 4 * i + t));
+          const uint4 wb = *reinterpret_cast<const uint4*>(sk + F::k + k_at<D>(g + 8, 4 * i + t));
+          const unsigned char* sc = sk + F::ks + g * (D / 16) + ((4 * i + t) >> 1) * 2;
+          const uint32_t s1 = *reinterpret_cast<const uint16_t*>(sc), s2 = *reinterpret_cast<const uint16_t*>(sc + D / 2);
+          const uint32_t sa = __byte_perm(s1, s1, 0x1010), sb = __byte_perm(s2, s2, 0x1010);
+          const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t b0, b1;
-            q8_pairs(w[c], b0, b1);
-            wm::mma_16816(x[n], q[0][4 * i + c][0], NT > 1 ? q[NT - 1][4 * i + c][0] : 0u, q[0][4 * i + c][1],
-                          NT > 1 ? q[NT - 1][4 * i + c][1] : 0u, mul_h2(b0, s2), mul_h2(b1, s2));
+            uint32_t a0, a1, a2, a3;
+            q8_pairs(va[c], a0, a2);
+            q8_pairs(vb[c], a1, a3);
+            a0 = mul_h2(a0, sa);
+            a1 = mul_h2(a1, sb);
+            a2 = mul_h2(a2, sa);
+            a3 = mul_h2(a3, sb);
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+              wm::mma_16816(x2[u][c & 1], a0, a1, a2, a3, q[u][4 * i + c][0], q[u][4 * i + c][1]);
           }
         }
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][e] = x2[u][0][e] + x2[u][1][e];
       }
       const uint32_t gone = miss[st];
       const bool masked = key0 < all_lo || key0 + SK > all_hi || (gone | poison) != 0u || key0 < it.lo || key0 + SK > end;
@@ -342,60 +374,64 @@ __global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __gri
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& s = x[n][2 * u + e];
-              const int c = 8 * n + 2 * t + e, j = key0 + c;
-              if (mods) {
-                s *= sl[u];
-                const float cap = a.c.softcap;  // sl holds log2 e
-                if (cap > 0.f) s = cap * kLog2e * (1.f - __fdividef(2.f, 1.f + ex2(s * (2.f / cap))));
-                if (slope[u] != 0.f) s = fmaf(-slope[u], fabsf((float)(pos[u] - j)), s);
-              }
-              if ((poison >> c) & 1u) s = __uint_as_float(0x7FC00000u);
-              if (j < lo[u] || j >= hi[u] || j < it.lo || j >= end || ((gone >> c) & 1u)) s = -INFINITY;
+          for (int e = 0; e < 4; ++e) {
+            float& s = x[u][e];
+            const Row r = row_of[8 * u + 2 * t + (e & 1)];
+            const int c = g + 4 * (e & 2), j = key0 + c;
+            if (mods) {
+              s *= sl[u][e & 1];
+              const float cap = a.c.softcap;  // sl holds log2 e
+              if (cap > 0.f) s = cap * kLog2e * (1.f - __fdividef(2.f, 1.f + ex2(s * (2.f / cap))));
+              if (r.slope != 0.f) s = fmaf(-r.slope, fabsf((float)(r.pos - j)), s);
             }
+            if ((poison >> c) & 1u) s = __uint_as_float(0x7FC00000u);
+            if (j < r.lo || j >= r.hi || j < it.lo || j >= end || ((gone >> c) & 1u)) s = -INFINITY;
+          }
         }
       }
+      // (scores that have been modified are in log2 units already)
       bool raise = false;
-      float mx[NT];
+      float mx[NT][2];
 #pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        mx[u] = fmaxf(fmaxf(x[0][2 * u], x[0][2 * u + 1]), fmaxf(x[1][2 * u], x[1][2 * u + 1]));
-        mx[u] *= f[u];
-        raise |= mx[u] - m[u] > kMaxExp;
-      }
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[u][e] = fmaxf(x[u][e], x[u][2 + e]) * (mods ? 1.f : sl[u][e]);
+          raise |= mx[u][e] - m[u][e] > kMaxExp;
+        }
       if (__any_sync(kFull, raise)) {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-          float top = mx[u];
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-          const float mn = fmaxf(m[u], top - kBias);
-          const float al = mn == -INFINITY ? 1.f : ex2(m[u] - mn);
-          m[u] = mn;
-          l[u] *= al;
-          const float a0 = __shfl_sync(kFull, al, 8 * t), a1 = __shfl_sync(kFull, al, 8 * t + 4);
+          float al[2];
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            o[u][i][0] *= a0;
-            o[u][i][1] *= a1;
-            o[u][i][2] *= a0;
-            o[u][i][3] *= a1;
+          for (int e = 0; e < 2; ++e) {
+            float top = mx[u][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+            const float mn = fmaxf(m[u][e], top - kBias);
+            al[e] = mn == -INFINITY ? 1.f : ex2(m[u][e] - mn);
+            m[u][e] = mn;
+            l[u][e] *= al[e];
           }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[u][i][e] *= al[e & 1];
         }
       }
       uint32_t p[NT][2];
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        const float mu = m[u] == -INFINITY ? 0.f : m[u];
+        float w[4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float e0 = ex2(fmaf(x[n][2 * u], f[u], -mu)), e1 = ex2(fmaf(x[n][2 * u + 1], f[u], -mu));
-          l[u] += e0 + e1;
-          p[u][n] = narrow(e0, e1, (const __half*)nullptr);
+        for (int e = 0; e < 2; ++e) {
+          const float mu = m[u][e] == -INFINITY ? 0.f : m[u][e], f = mods ? 1.f : sl[u][e];
+          w[e] = ex2(fmaf(x[u][e], f, -mu));
+          w[2 + e] = ex2(fmaf(x[u][2 + e], f, -mu));
+          l[u][e] += w[e] + w[2 + e];
         }
+        p[u][0] = transpose8(narrow(w[0], w[1], (const __half*)nullptr));
+        p[u][1] = transpose8(narrow(w[2], w[3], (const __half*)nullptr));
       }
       // O^T += V^T P^T: this lane's coordinates are D / 8 consecutive ones (D = 256: two runs of 16) of four keys
       const int keys[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
@@ -442,11 +478,11 @@ __global__ void __launch_bounds__(Few<D, NT>::NW * 32, 2) few_kernel(const __gri
     float* mo = reinterpret_cast<float*>(sm);  // [NW][8 NT][OS]
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      l[u] += __shfl_xor_sync(kFull, l[u], 1);
-      l[u] += __shfl_xor_sync(kFull, l[u], 2);
-      if (t == 0) ml[warp * 16 + 8 * u + g] = make_float2(m[u], l[u]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[u][e] += __shfl_xor_sync(kFull, l[u][e], d);
+        if (g == 0) ml[warp * 16 + 8 * u + 2 * t + e] = make_float2(m[u][e], l[u][e]);
         float* row = mo + (warp * 8 * NT + 8 * u + 2 * t + e) * F::OS;
         constexpr int W = D == 64 ? 2 : 4;
 #pragma unroll
