@@ -19,7 +19,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["tq_api.cpp", "tq_encode.cu", "tq_decode.cu", "tq_decode_mma64.cu", "tq_decode_mma128.cu",
            "tq_decode_mma256.cu", "tq_decode_static.cu", "tq_dequant.cu", "tq_persist.cpp",
            "tq_prefill.cu", "tq_step.cpp", "tq_rope.cu", "tq_append.cu", "tq_chunk.cu",
-           "tq_chunk64.cu", "tq_chunk128.cu", "tq_chunk256.cu", "tq_chunk_few.cu"]
+           "tq_chunk64.cu", "tq_chunk128.cu", "tq_chunk256.cu", "tq_few64.cu",
+           "tq_few128.cu", "tq_few256.cu"]
 
 
 def _nvcc() -> str:

@@ -210,7 +210,11 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, int s
   a.inv_lam_v = 1.f / lam_v;
   const int vb = c.v.format == TQ_FMT_Q8_0 ? 0 : c.v.idx_bits;
   const long long most = (long long)c.b.max_tokens * c.G;  // rows of an entry
-  if (vb == 0 && most <= ck::few_rows(c.k.d)) return ck::launch_few(a, most, sm_count, s);
+  if (most <= ck::few_rows(c.k.d)) {
+    if (c.k.d == 64) return ck::launch_few64(a, (int)most, vb, sm_count, s);
+    if (c.k.d == 128) return ck::launch_few128(a, (int)most, vb, sm_count, s);
+    return ck::launch_few256(a, (int)most, vb, sm_count, s);
+  }
   if (c.k.d == 64) return ck::launch_d64(a, vb, sm_count, s);
   if (c.k.d == 128) return ck::launch_d128(a, vb, sm_count, s);
   return ck::launch_d256(a, vb, sm_count, s);

@@ -40,9 +40,11 @@ cudaError_t launch_d64(const Args& a, int vb, int sm_count, cudaStream_t s);
 cudaError_t launch_d128(const Args& a, int vb, int sm_count, cudaStream_t s);
 cudaError_t launch_d256(const Args& a, int vb, int sm_count, cudaStream_t s);
 
-// Entries of at most few_rows(d) rows over q8_0 values (tq_chunk_few.cu); its 2 sm_count CTAs use two partial results each.
-int few_rows(int d);
-cudaError_t launch_few(const Args& a, long long rows, int sm_count, cudaStream_t s);
+// Entries of at most few_rows(d) rows (tq_chunk_few.cuh); their 2 sm_count CTAs use two partial results each.
+constexpr int few_rows(int d) { return d == 256 ? 8 : 16; }
+cudaError_t launch_few64(const Args& a, int rows, int vb, int sm_count, cudaStream_t s);
+cudaError_t launch_few128(const Args& a, int rows, int vb, int sm_count, cudaStream_t s);
+cudaError_t launch_few256(const Args& a, int rows, int vb, int sm_count, cudaStream_t s);
 
 }  // namespace ck
 }  // namespace tq

@@ -1037,3 +1037,39 @@ def test_attend_few_rows_is_deterministic_and_isolated(ctxs):
     assert torch.isnan(got[2, 5]).all()
     got[2, 5] = first[2, 5]
     assert torch.equal(got, first)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("vfmt", ["turbo2_mse", "turbo3_mse", "turbo4_mse"])
+@pytest.mark.parametrize("page", [16, 24, 101])
+def test_attend_few_rows_turbo_values(ctxs, d, vfmt, page):
+    """Pages of whole slices, pages that end inside one, and contiguous sequences of an odd capacity (odd vectors)."""
+    contiguous = page == 101
+    lens = [100, 17, 99, 31] if contiguous else [1900, 17, 600, 31]
+    P = Paged(ctxs[d], d, 3, [2, 1, 0, 3], lens, page, vfmt, contiguous=contiguous, padding=2, outliers=0.01)
+    check_attend(P, 1, torch.float16)
+    check_attend(P, 2, torch.bfloat16, torch.float32, window=40, bias=True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_few_rows_contiguous_and_layers(ctxs, d):
+    P = Paged(ctxs[d], d, 2, [1, 4], [77, 90], 91, n_layers=3, layer=2, contiguous=True)
+    check_attend(P, 2, torch.float16)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 24])
+def test_attend_few_rows_bad_turbo_norms_do_not_leak(ctxs, d, page):
+    for which, bad in (("k", float("inf")), ("v", float("inf")), ("v", float("nan"))):
+        P = Paged(ctxs[d], d, 1, [4], [260], page, "turbo3_mse")
+        q = W.normal_tensor((4, 1, d), seed=4, device="cuda").half()
+        m = mods_of(P, 1, first=[0, 131, 130, 140])
+        clean = attend(P, q, mods=m)
+        view = P.kv if which == "k" else P.vv
+        h = view.header.view(torch.float16).view(-1, d // 32 if which == "k" else 1)
+        h[int(P.slots(0, [130])[0]), -1] = bad
+        got = attend(P, q, mods=m)
+        torch.cuda.synchronize()
+        sees = torch.tensor([1, 0, 1, 0], dtype=torch.bool)
+        assert torch.isnan(got[sees]).all()
+        assert torch.equal(got[~sees], clean[~sees]) and torch.isfinite(clean).all()
