@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __shared__ int near_base[kNear];
   const ChunkArgs& a = p.c;
   const int tid = threadIdx.x, G = a.G;
+  pdl_launch_dependents();  // the main kernel's start overlaps this one
   long long carry = 0, total;
   for (int b0 = 0; b0 < a.b.n_seqs; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -99,9 +100,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       en.seq = lo;
       en.row0 = (e - seq_base[lo]) * p.rows;
       const int rows = min(p.rows, s.n * G - en.row0);
+      en.rows = rows;
+      en.tok0 = s.first;
+      en.pos0 = s.len - s.n;
+      en.len = s.len;
       i0 = en.row0 / G;
       i1 = (en.row0 + rows - 1) / G;
-      prefix = a.prefix_lens ? a.prefix_lens[lo] : 0;
+      prefix = en.prefix = a.prefix_lens ? a.prefix_lens[lo] : 0;
     }
     int first = 0x7FFFFFFF, last = 0;
     if (a.first_keys) {

@@ -16,7 +16,8 @@ constexpr int keys_per_tile(int d) { return d == 256 ? 64 : 128; }
 // work units of the entries before it.
 struct Entry {
   long long start;
-  int seq, row0, lo, hi, n_tiles, pad;
+  int seq, row0, rows, lo, hi, n_tiles;
+  int tok0, pos0, len, prefix;  // of its sequence: first row and position of the new tokens, length, prefix length
 };
 
 struct PlanHead {

@@ -87,13 +87,12 @@ struct Spot {
   int page, off;
 };
 
-// Page and offset of a key, -1 where the key is not wanted.  inv: floor((2^32 - 1) / page_size), with which the quotient is
+// Page and offset of a key, -1 where the key is not wanted.  pages: the sequence's row of the block table, if there is one.  inv: floor((2^32 - 1) / page_size), with which the quotient is
 // at most one too small.
-__device__ __forceinline__ Spot spot_of(const Args& a, const Item& it, int j, int end, uint32_t inv) {
-  const DevBatch& b = a.c.b;
+__device__ __forceinline__ Spot spot_of(const Args& a, const int32_t* pages, int seq, int j, int end, uint32_t inv) {
   Spot s{-1, 0};
   if (j < end) {
-    if (!b.block_table) return Spot{it.seq, j};
+    if (!pages) return Spot{seq, j};
     const int ps = a.c.k.page_size;
     int lp = (int)__umulhi((uint32_t)j, inv);
     s.off = j - lp * ps;
@@ -101,7 +100,7 @@ __device__ __forceinline__ Spot spot_of(const Args& a, const Item& it, int j, in
       ++lp;
       s.off -= ps;
     }
-    if (lp < b.max_blocks) s.page = __ldg(b.block_table + (long long)it.seq * b.max_blocks + lp);
+    if (lp < a.c.b.max_blocks) s.page = __ldg(pages + lp);
   }
   return s;
 }
@@ -254,7 +253,9 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
     }
     constexpr int BN = Shape<D>::BN;
     const int j0 = max(it.tile * BN, it.lo) & ~(SK - 1), end = min((it.tile + it.n) * BN, it.hi);
-    const long long page_b = (long long)K.H * K.page_size * D;  // payload bytes of a page, where the head's begin, a lane's
+    const int seq = it.seq, low = it.lo;
+    const int32_t* pages = a.c.b.block_table ? a.c.b.block_table + (long long)seq * a.c.b.max_blocks : nullptr;
+    const long long page_b = (long long)K.H * K.page_size * D;  // payload bytes of a page; where the head's begin
     const long long first_b = (long long)a.c.layer * K.num_pages * page_b + (long long)it.kvh * K.page_size * D;
     // Asks for the slice that begins at key n0 into stage st; sp: the place of key lane % 16 of it, or (runs) of its first
     // key.  Returns the norm of V's key lane % 16 (turbo values), which goes to the stage later.
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
         const uint32_t base = ring_s + st * F::slice;
         constexpr int LPK = D / 16, KPI = 32 / LPK;  // lanes of a key, keys of a copy
         const int kl = lane / LPK, c = lane % LPK;
-        const long long at0 = there ? first_b + sp.page * page_b + (long long)sp.off * D : 0;  // of K's payload
+        const long long at0 = there ? first_b + (uint32_t)sp.page * page_b + (long long)sp.off * D : 0;  // of K's payload
         auto mark = [&](uint32_t off) {
           if (off && !missed) {
             missed = true;
@@ -278,9 +279,8 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
             if (off) atomicOr(a.c.tab.status, kFlagBlockTable);
           }
         };
-        const int c0 = max(it.lo - n0, 0), c1 = min(end - n0, SK);  // the keys [c0, c1) are wanted
+        const int c0 = max(low - n0, 0), c1 = min(end - n0, SK);  // the keys [c0, c1) are wanted
         if (runs) {
-          mark(there ? 0u : (1u << c1) - (1u << c0));
           const unsigned char *pk = K.payload + at0 + 16 * lane, *hk = K.header + (at0 >> 4) + 4 * lane;
           auto go = [&](auto on) {  // on(key): the key is there
 #pragma unroll
@@ -310,8 +310,13 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
               if (on(lane & 15)) norm = __ldg(reinterpret_cast<const uint16_t*>(V.header) + vec + (lane & 15));
             }
           };
-          if (there && c0 == 0 && c1 == SK) go([](int) { return true; });
-          else go([&](int key) { return there && key >= c0 && key < c1; });
+          if (there && low <= n0 && n0 + SK <= end) {
+            go([](int) { return true; });
+            if (missed) mark(0u);
+          } else {
+            go([&](int key) { return there && key >= c0 && key < c1; });
+            mark(there ? 0u : (1u << c1) - (1u << c0));
+          }
         } else {
           const int mk = lane & 15;
           const bool want = mk >= c0 && mk < c1, on = there && want;
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       if (VB > 0 && lane < 16) *reinterpret_cast<uint16_t*>(ring + st * F::slice + F::vs + 2 * lane) = norm;
     };
     constexpr int STEP = SK * NW;
-    auto spot = [&](int n0) { return spot_of(a, it, n0 + (runs ? 0 : lane & 15), end, inv); };
+    auto spot = [&](int n0) { return spot_of(a, pages, seq, n0 + (runs ? 0 : lane & 15), end, inv); };
     int ask = j0 + SK * warp;  // the next slice to ask for
     {
       Spot sp[NS - 1];
@@ -452,10 +457,6 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       {
         float x2[NT][2][4];  // two chains
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x2[u][e >> 2][e & 3] = 0.f;
-#pragma unroll
         for (int i = 0; i < D / 64; ++i) {
           const uint4 wa = *reinterpret_cast<const uint4*>(sk + F::k + k_at<D>(g, 4 * i + t));
           const uint4 wb = *reinterpret_cast<const uint4*>(sk + F::k + k_at<D>(g + 8, 4 * i + t));
@@ -473,8 +474,10 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
             a2 = mul_h2(a2, sa);
             a3 = mul_h2(a3, sb);
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
-              wm::mma_16816(x2[u][c & 1], a0, a1, a2, a3, q[u][4 * i + c][0], q[u][4 * i + c][1]);
+            for (int u = 0; u < NT; ++u) {
+              if (i == 0 && c < 2) wm::mma_16816_zc(x2[u][c], a0, a1, a2, a3, q[u][c][0], q[u][c][1]);
+              else wm::mma_16816(x2[u][c & 1], a0, a1, a2, a3, q[u][4 * i + c][0], q[u][4 * i + c][1]);
+            }
           }
         }
 #pragma unroll
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
               if (r.slope != 0.f) s = fmaf(-r.slope, fabsf((float)(r.pos - j)), s);
             }
             if ((poison >> c) & 1u) s = __uint_as_float(0x7FC00000u);
-            if (j < r.lo || j >= r.hi || j < it.lo || j >= end || ((gone >> c) & 1u)) s = -INFINITY;
+            if (j < r.lo || j >= r.hi || j < low || j >= end || ((gone >> c) & 1u)) s = -INFINITY;
           }
         }
       }
@@ -755,13 +758,13 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
           float y[4] = {0.f, 0.f, 0.f, 0.f};
           if (i < units && q0 < pg) {
 #pragma unroll 1
-            for (int p0 = q0; p0 < n_sh; p0 += 8 * pg) {
-              float4 v[8];
+            for (int p0 = q0; p0 < n_sh; p0 += 12 * pg) {
+              float4 v[12];
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
+              for (int k = 0; k < 12; ++k)
                 v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (share(min(p0 + k * pg, n_sh - 1)) + r) * D + 4 * c));
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
+              for (int k = 0; k < 12; ++k) {
                 if (p0 + k * pg >= n_sh) continue;
                 const float2 z = sh[(p0 + k * pg) * rows + r];
                 if (z.y == 0.f) continue;  // a share without weight is not looked at

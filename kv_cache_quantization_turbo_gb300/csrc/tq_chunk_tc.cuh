@@ -286,8 +286,13 @@ struct Items {
   long long T, U, nC, u, u1;
   int n_entries, h, e;
 
+  // A quotient of numbers >= 0; those of fewer than 32 bits, as good as always, are divided as such.
+  static __device__ __forceinline__ long long div(long long x, long long y) {
+    return ((unsigned long long)(x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+  }
+
   // the CTA whose range holds a unit
-  __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * nC - 1) / U); }
+  __device__ __forceinline__ int cta_of(long long x) const { return (int)div((x + 1) * nC - 1, U); }
 
   __device__ void start(const Args& a) {
     const PlanHead head = *a.plan;
@@ -297,11 +302,11 @@ struct Items {
     // every CTA that takes part has at least kMinUnits units (so no CTA inside an entry's range is without work)
     nC = max(1LL, min((long long)gridDim.x, U / kMinUnits));
     const long long c = blockIdx.x;
-    u = c < nC ? U * c / nC : 0;
-    u1 = c < nC ? U * (c + 1) / nC : 0;
+    u = c < nC ? div(U * c, nC) : 0;
+    u1 = c < nC ? div(U * (c + 1), nC) : 0;
     h = e = 0;
     if (u < u1) {
-      h = (int)(u / T);
+      h = (int)div(u, T);
       const long long off = u - (long long)h * T;
       for (int step = 1 << 30; step > 0; step >>= 1)  // the last entry that starts at or before off
         if (e + step < n_entries && a.entries[e + step].start <= off) e += step;
@@ -317,12 +322,11 @@ struct Items {
       it.kvh = h;
       it.seq = en.seq;
       it.row0 = en.row0;
-      const SeqOf s = seq_of(a.c.b, en.seq);
-      it.tok0 = s.first;
-      it.len = s.len;
-      it.pos0 = s.len - s.n;
-      it.prefix = a.c.prefix_lens ? a.c.prefix_lens[en.seq] : 0;
-      it.rows = min(s.n * a.c.G - en.row0, Shape<D>::kQTiles * 128);
+      it.rows = en.rows;
+      it.tok0 = en.tok0;
+      it.pos0 = en.pos0;
+      it.len = en.len;
+      it.prefix = en.prefix;
       it.lo = en.lo;
       it.hi = en.hi;
       it.two = D != 256 && it.rows > 128;
