@@ -214,6 +214,9 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, int s
   a.q_sign = c.scale > 0.f ? 1.f : c.scale < 0.f ? -1.f : 0.f;
   a.inv_lam_v = 1.f / lam_v;
   const int vb = c.v.format == TQ_FMT_Q8_0 ? 0 : c.v.idx_bits;
+  // Entries of few rows.  48 sequences of 1K to 16K tokens, 8 KV heads of 128, 4 rows each: q8_0 128 us there and 253 in
+  // the large kernel, turbo4 149 and 382; 16 rows: 152 and 275, turbo4 204 and 400; head size 64: 85 and 195; 256: 215 and
+  // 330; 4 sequences of 500 tokens: 20 and 24.  At 256 a lane's registers hold 8 rows.
   const long long most = (long long)c.b.max_tokens * c.G;  // rows of an entry
   if (most <= ck::few_rows(c.k.d)) {
     if (c.k.d == 64) return ck::launch_few64(a, (int)most, vb, sm_count, s);

@@ -5,12 +5,20 @@
 // keys of its CTA's range, copies the next slices' codes and scales asynchronously to a ring of its own, turns codes into
 // fp16 fragments in registers, and keeps its own softmax reference, sum and output; no barrier until the range ends.  The
 // products are the warp-wide m16n8k16 ones (fp16 operands, fp32 sums):
-//   S^T = K Q^T: M = 16 keys, N = 8 rows; a lane holds 16 coordinates of a key at a time, so the contraction index is
-//     permuted, alike for K and Q.
+//   S^T = K Q^T: M = 16 keys, N = 8 rows; the codes are integers that fp16 holds, the scale of a block of 32 goes to its sum
+//     in fp32, so K is not rounded.  A lane holds 8 coordinates of a block at a time: the contraction index is permuted,
+//     alike for K and Q.
 //   O^T = V^T P^T: M = 16 coordinates, N = 8 rows; a lane pairs the codes of two keys by byte permutes, and P^T is S^T's
 //     accumulators with two 8 x 8 transposes.  A lane's columns are the same rows of Q in both products.
 // The ranges, the join of entries that several CTAs share and the meaning of every mask are those of tq_chunk_tc.cuh;
 // weights are taken against a reference that is raised only when a weight would pass 2^15.
+//
+// What bounds it.  64 sequences of 1K to 16K tokens, 8 KV heads of 128, 4 rows: 145 us for 0.87 GB, 6.0 TB/s, 88 % of the
+// copy bandwidth, at 64 % of the instruction slots (507 instructions per slice, of which 180 turn codes into fp16).  Keys as
+// the right operand, 8 of 16 rows idle, took 170 us; scales multiplied into K's fragments 149 us, and rounded K: an error of
+// 1.3e-3 instead of 3.6e-4.  Turbo values: more instructions (a lookup by byte permutes) for fewer bytes, 149 us for 48 such
+// sequences, bound by the instruction slots.  One token at 32K: 20 us after the plan, of which the range's 7 slices per
+// warp take 9 (instruction slots), finding the range, the first copies and Q 5, the join of 38 shares 5.
 #pragma once
 
 #include "tq_chunk_tc.cuh"
@@ -51,10 +59,12 @@ struct Few {
   static_assert(2 * (total + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-// Chunk of 16 bytes of a row, so that the lanes' reads of the products' operands meet different banks: a K read takes four
-// chunks in a row of two keys, a V read two chunks of every second key.
+// Chunk of 16 bytes of a row, so that the lanes' reads of the products' operands meet different banks: a K read takes 32
+// bytes of each of four keys, a V read two chunks of every second key.
 template <int D>
-__device__ __forceinline__ int k_at(int key, int chunk) { return key * D + ((D == 64 ? chunk : chunk ^ ((key & 1) << 2)) << 4); }
+__device__ __forceinline__ int k_at(int key, int chunk) {
+  return key * D + ((D == 64 ? chunk ^ (key & 2) : chunk ^ ((key & 3) << 1)) << 4);
+}
 template <int D>
 __device__ __forceinline__ int v_at(int key, int chunk) {
   return key * D + ((D == 64 ? chunk ^ ((key >> 1) & 3) : chunk ^ (key & 6)) << 4);
@@ -110,17 +120,17 @@ __device__ __forceinline__ Spot spot_of(const Args& a, const int32_t* pages, int
 template <int D, class T>
 __device__ __forceinline__ float load_q(const Args& a, const T* src, bool valid, int t, uint32_t (&f)[D / 16][2]) {
   uint32_t top = 0;
-  float x[D / 64][16];
+  float x[D / 32][8];  // coordinates 8 t .. 8 t + 7 of every 32
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
+  for (int i = 0; i < D / 32; ++i) {
     if (valid) {
-      load_row<16>(src + (4 * i + t) * 16, x[i]);
+      load_row<8>(src + 32 * i + 8 * t, x[i]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
+      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
   }
   top = max(top, __shfl_xor_sync(kFull, top, 1));
   top = max(top, __shfl_xor_sync(kFull, top, 2));
@@ -128,11 +138,11 @@ __device__ __forceinline__ float load_q(const Args& a, const T* src, bool valid,
   if (top >= 0x7F800000u) ex = 127u;  // infinite or NaN: as it is
   const float m = a.q_sign * __uint_as_float((254u - ex) << 23);
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i)
+  for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      f[4 * i + w][0] = narrow(x[i][4 * w] * m, x[i][4 * w + 1] * m, (const __half*)nullptr);
-      f[4 * i + w][1] = narrow(x[i][4 * w + 2] * m, x[i][4 * w + 3] * m, (const __half*)nullptr);
+    for (int w = 0; w < 2; ++w) {
+      f[2 * i + w][0] = narrow(x[i][4 * w] * m, x[i][4 * w + 1] * m, (const __half*)nullptr);
+      f[2 * i + w][1] = narrow(x[i][4 * w + 2] * m, x[i][4 * w + 3] * m, (const __half*)nullptr);
     }
   return __uint_as_float(ex << 23);
 }
@@ -455,35 +465,33 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       // scores: x[rows 8 u + ..][key g of rows 2 t, 2 t + 1, then key g + 8]
       float x[NT][4];
       {
-        float x2[NT][2][4];  // two chains
+        uint32_t sa[D / 64], sb[D / 64];  // the scales of both keys
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          const uint4 wa = *reinterpret_cast<const uint4*>(sk + F::k + k_at<D>(g, 4 * i + t));
-          const uint4 wb = *reinterpret_cast<const uint4*>(sk + F::k + k_at<D>(g + 8, 4 * i + t));
-          const unsigned char* sc = sk + F::ks + g * (D / 16) + ((4 * i + t) >> 1) * 2;
-          const uint32_t s1 = *reinterpret_cast<const uint16_t*>(sc), s2 = *reinterpret_cast<const uint16_t*>(sc + D / 2);
-          const uint32_t sa = __byte_perm(s1, s1, 0x1010), sb = __byte_perm(s2, s2, 0x1010);
-          const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t a0, a1, a2, a3;
-            q8_pairs(va[c], a0, a2);
-            q8_pairs(vb[c], a1, a3);
-            a0 = mul_h2(a0, sa);
-            a1 = mul_h2(a1, sb);
-            a2 = mul_h2(a2, sa);
-            a3 = mul_h2(a3, sb);
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-              if (i == 0 && c < 2) wm::mma_16816_zc(x2[u][c], a0, a1, a2, a3, q[u][c][0], q[u][c][1]);
-              else wm::mma_16816(x2[u][c & 1], a0, a1, a2, a3, q[u][4 * i + c][0], q[u][4 * i + c][1]);
-            }
-          }
+          sa[i] = *reinterpret_cast<const uint32_t*>(sk + F::ks + g * (D / 16) + 4 * i);
+          sb[i] = *reinterpret_cast<const uint32_t*>(sk + F::ks + (g + 8) * (D / 16) + 4 * i);
         }
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
+        for (int i = 0; i < D / 32; ++i) {  // a block of 32: two products of the codes, exact, then its scale
+          const uint2 wa = *reinterpret_cast<const uint2*>(sk + F::k + k_at<D>(g, 2 * i + (t >> 1)) + 8 * (t & 1));
+          const uint2 wb = *reinterpret_cast<const uint2*>(sk + F::k + k_at<D>(g + 8, 2 * i + (t >> 1)) + 8 * (t & 1));
+          const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&sa[i / 2]));
+          const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&sb[i / 2]));
+          const float ka = i & 1 ? fa.y : fa.x, kb = i & 1 ? fb.y : fb.x;
+          uint32_t a0[2], a1[2], a2[2], a3[2];
+          q8_pairs(wa.x, a0[0], a2[0]);
+          q8_pairs(wb.x, a1[0], a3[0]);
+          q8_pairs(wa.y, a0[1], a2[1]);
+          q8_pairs(wb.y, a1[1], a3[1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[u][e] = x2[u][0][e] + x2[u][1][e];
+          for (int u = 0; u < NT; ++u) {
+            float c[4];
+            wm::mma_16816_zc(c, a0[0], a1[0], a2[0], a3[0], q[u][2 * i][0], q[u][2 * i][1]);
+            wm::mma_16816(c, a0[1], a1[1], a2[1], a3[1], q[u][2 * i + 1][0], q[u][2 * i + 1][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[u][e] = i == 0 ? (e < 2 ? ka : kb) * c[e] : fmaf(e < 2 ? ka : kb, c[e], x[u][e]);
+          }
+        }
       }
       const uint32_t gone = missed ? miss[st] : 0u;
       const bool masked = key0 < all_lo || key0 + SK > all_hi || (gone | poison) != 0u;

@@ -1,4 +1,4 @@
-// Chunk attention on the fifth-generation tensor cores: one kernel for every row count, from one token to thousands.
+// Chunk attention on the fifth-generation tensor cores, for entries of more than a few rows.
 //
 // Per KV head, the rows of a sequence are its (new token, query head of the group) pairs, row = token * G + head.  An
 // entry is up to MT consecutive rows and the key tiles that any of them sees (the plan kernel lists them).  The tiles of
@@ -37,8 +37,8 @@
 // a chain (scores and weights share their tensor memory).  Without the softmax the loop runs at 1.56 ms, without softmax
 // and conversion at 1.22 ms, with both at 2.02 ms for a 4096-token chunk at 32K context, 32 query heads of 128 (1.02
 // PFLOP/s).  64-key score products with twice the buffers take the same 65 cycles each for half the keys: 2.15 ms.  Few
-// rows: a tile is 34.8 KB of cache, 1.5 K cycles of this GPU's bandwidth; it takes 3.5 K (64 sequences of 1K to 16K
-// tokens, 8 KV heads: 348 us, 2.5 TB/s), bound by the round of a tile through its two buffers.
+// rows: a tile is 34.8 KB of cache, 1.5 K cycles of this GPU's bandwidth; it takes 3.5 K, bound by the round of a tile
+// through its two buffers.  Entries of up to 16 rows have a kernel of their own (tq_chunk_few.cuh).
 #pragma once
 
 #include "tq_batch.cuh"
