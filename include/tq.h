@@ -429,8 +429,8 @@ tq_status tq_rope(const tq_context* ctx, const tq_rope_table* table, const void*
 /*
  * A ragged batch of new tokens.  Sequence b has the tokens [cu_tokens[b], cu_tokens[b + 1]) of the call's n_tokens
  * rows (device int32 [n_seqs + 1], from 0 on, not decreasing; rows behind cu_tokens[n_seqs] are padding: what they
- * hold has no effect, and in every output they are left as they are) and seq_lens[b] tokens in all (device int32 [n_seqs]), the new ones included:
- * its new token i of n sits at position seq_lens[b] - n + i.  block_table (device int32 [n_seqs][max_blocks]) maps
+ * hold has no effect, and in every output they are left as they are) and seq_lens[b] tokens in all (device int32
+ * [n_seqs]), the new ones included: its new token i of n sits at position seq_lens[b] - n + i.  block_table (device int32 [n_seqs][max_blocks]) maps
  * page position / page_size of a sequence to a physical page; NULL: sequence b is page b.
  * max_tokens and max_ctx (host) bound the new tokens and the length of every sequence.  A sequence whose device values
  * break these bounds (more new tokens than max_tokens or than its length, a length above max_ctx, rows outside
@@ -455,8 +455,8 @@ typedef struct tq_batch {
  * of 16 bytes and >= H d.  The rotated key is quantised from fp32 without a rounding in between.  K: Q8_0.  V: Q8_0 or
  * turbo2/3/4_mse.  Other formats return TQ_ERR_UNSUPPORTED (turbo K: tq_rope, then tq_encode_kv).  Values in fp16
  * without a rotation give the bytes of tq_encode_kv for Q8_0 (a NaN element is stored as 0; an infinite one, or one so
- * large that the fp16 scale overflows, gives an infinite scale, whose values read back as NaN).  A token whose page is out of range is skipped and sets
- * status bit 2.  Two tokens of one call must not share a slot.
+ * large that the fp16 scale overflows, gives an infinite scale, whose values read back as NaN).  A token whose page is
+ * out of range is skipped and sets status bit 2.  Two tokens of one call must not share a slot.
  */
 tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void* k, int64_t k_token_stride,
                        const void* v, int64_t v_token_stride, tq_dtype dtype, const tq_rope_table* rope,
@@ -503,8 +503,8 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
  *   tq_prefill_attention).
  *   workspace: device, tq_chunk_workspace_bytes() bytes, 256-byte aligned; calls that may overlap need their own.
  * The operands of the products are fp16 (queries scaled by a power of two per row, so that no type overflows; a decode
- * step's keys are not rounded), the sums and the softmax fp32.  Stored q8_0 scales above 511.5 (values above 64960) are read as 511.5.  The result of a
- * call does not depend on what else runs.  max_tokens chooses the kernel: a batch of at most 16 rows (max_tokens *
+ * step's keys are not rounded), the sums and the softmax fp32.  Stored q8_0 scales above 511.5 (values above 64960) are
+ * read as 511.5.  The result of a call does not depend on what else runs.  max_tokens chooses the kernel: a batch of at most 16 rows (max_tokens *
  * n_q_heads / n_kv_heads; 8 at head_dim 256) per sequence and KV head takes one that is about twice as fast for them, so
  * a decode step passes max_tokens = 1.  A block-table entry out of range sets status bit 2, and its keys are left
  * out.

@@ -97,8 +97,8 @@ struct Spot {
   int page, off;
 };
 
-// Page and offset of a key, -1 where the key is not wanted.  pages: the sequence's row of the block table, if there is one.  inv: floor((2^32 - 1) / page_size), with which the quotient is
-// at most one too small.
+// Page and offset of a key, -1 where the key is not wanted.  pages: the sequence's row of the block table, if there is
+// one.  inv: floor((2^32 - 1) / page_size), with which the quotient is at most one too small.
 __device__ __forceinline__ Spot spot_of(const Args& a, const int32_t* pages, int seq, int j, int end, uint32_t inv) {
   Spot s{-1, 0};
   if (j < end) {
@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
     const int j0 = max(it.tile * BN, it.lo) & ~(SK - 1), end = min((it.tile + it.n) * BN, it.hi);
     const int seq = it.seq, low = it.lo;
     const int32_t* pages = a.c.b.block_table ? a.c.b.block_table + (long long)seq * a.c.b.max_blocks : nullptr;
-    const long long page_b = (long long)K.H * K.page_size * D;  // payload bytes of a page; where the head's begin
+    // payload bytes of a page; where the layer's bytes of the head begin
+    const long long page_b = (long long)K.H * K.page_size * D;
     const long long first_b = (long long)a.c.layer * K.num_pages * page_b + (long long)it.kvh * K.page_size * D;
     // Asks for the slice that begins at key n0 into stage st; sp: the place of key lane % 16 of it, or (runs) of its first
     // key.  Returns the norm of V's key lane % 16 (turbo values), which goes to the stage later.
@@ -294,7 +295,8 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
           const unsigned char *pk = K.payload + at0 + 16 * lane, *hk = K.header + (at0 >> 4) + 4 * lane;
           auto go = [&](auto on) {  // on(key): the key is there
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) copy_async<16>(base + F::k + k_at<D>(i * KPI + kl, c), pk + 512 * i, on(i * KPI + kl));
+            for (int i = 0; i < D / 32; ++i)
+              copy_async<16>(base + F::k + k_at<D>(i * KPI + kl, c), pk + 512 * i, on(i * KPI + kl));
 #pragma unroll
             for (int i = 0; i < (D + 127) / 128; ++i) {
               const int at = 4 * lane + 128 * i;
@@ -303,7 +305,8 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
             if constexpr (VB == 0) {
               const unsigned char *pv = V.payload + at0 + 16 * lane, *hv = V.header + (at0 >> 4) + 4 * lane;
 #pragma unroll
-              for (int i = 0; i < D / 32; ++i) copy_async<16>(base + F::v + v_at<D>(i * KPI + kl, c), pv + 512 * i, on(i * KPI + kl));
+              for (int i = 0; i < D / 32; ++i)
+                copy_async<16>(base + F::v + v_at<D>(i * KPI + kl, c), pv + 512 * i, on(i * KPI + kl));
 #pragma unroll
               for (int i = 0; i < (D + 127) / 128; ++i) {
                 const int at = 4 * lane + 128 * i;

@@ -1073,3 +1073,49 @@ def test_attend_few_rows_bad_turbo_norms_do_not_leak(ctxs, d, page):
         sees = torch.tensor([1, 0, 1, 0], dtype=torch.bool)
         assert torch.isnan(got[sees]).all()
         assert torch.equal(got[~sees], clean[~sees]) and torch.isfinite(clean).all()
+
+
+@pytest.mark.parametrize("vfmt", ["q8_0", "turbo4_mse"])
+@pytest.mark.parametrize("page", [16, 24])
+def test_attend_few_rows_beyond_32_bit_offsets(ctxs, vfmt, page):
+    """Pages at the end of a cache of more than 4 GiB of keys, in its second layer."""
+    d, H, T = 128, 8, 100
+    n_pages = (1 << 31) // (page * H * d) + 400
+    kv, vv = (tq.alloc_view(f, d, H, page, n_pages, 2) for f in ("q8_0", vfmt))
+    assert kv.payload.numel() > 1 << 32
+    table = (n_pages - 1 - 3 * torch.arange(7, device="cuda")).to(torch.int32).view(1, 7)
+    dev = dict(dtype=torch.int32, device="cuda")
+    whole = tq.Batch(torch.tensor([0, T], **dev), torch.tensor([T], **dev), table, T, T, T)
+    k, v, q = (W.normal_tensor((T, H, d), seed=i, device="cuda").half() for i in range(3))
+    ctx = ctxs[d]
+    assert tq.tq_append_kv(ctx.h, whole, k, v, kv, vv, 1) == tq.TQ_OK
+    rk, rv = (torch.empty((T, H, d), device="cuda") for _ in range(2))
+    assert tq.tq_read_kv(ctx.h, whole, kv, rk, vv, rv, 1) == tq.TQ_OK
+    last = tq.Batch(torch.tensor([0, 2], **dev), torch.tensor([T], **dev), table, 2, 2, T)
+    q = q[:2].contiguous()
+    out = torch.empty_like(q)
+    n = tq.tq_chunk_workspace_bytes(ctx.h, last, H, H)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert tq.tq_chunk_attention(ctx.h, last, q, kv, vv, 1, 1 / math.sqrt(d), ws, n, out) == tq.TQ_OK
+    torch.cuda.synchronize()
+    assert status(ctx) == 0
+    want = S.chunk_attention(f64(q), f64(rk), f64(rv), np.arange(T - 2, T), 1 / math.sqrt(d))
+    assert C.rel_err_per_head(f64(out), want).max() < C.ATTN_RTOL + half_step(torch.float16)
+    del kv, vv
+    torch.cuda.empty_cache()
+
+
+def test_attend_few_rows_on_two_streams_at_once(ctxs):
+    P = Paged(ctxs[128], 128, 2, [2, 1], [5000, 900], 16, "turbo4_mse")
+    qs = [W.normal_tensor((3, 8, 128), seed=i, device="cuda").half() for i in (1, 2)]
+    alone = [attend(P, q) for q in qs]
+    n = tq.tq_chunk_workspace_bytes(P.ctx.h, P.batch, 8, 2)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in qs]
+    outs, streams = [torch.empty_like(q) for q in qs], [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for q, s, o, w in zip(qs, streams, outs, ws):
+            attend(P, q, stream=s, out=o, workspace=w)
+    torch.cuda.synchronize()
+    for a, o in zip(alone, outs):
+        assert torch.equal(a, o)
