@@ -25,6 +25,12 @@ struct PlanArgs {
   int max_entries, rows, keys;
 };
 
+// What an entry's tokens see: the call's row and the position of its first token, their number, length and prefix of the
+// sequence; then (row, tokens) hold the first key that one of them sees and the end of the last.
+struct Look {
+  int row, tokens, pos, len, prefix;
+};
+
 // Exclusive prefix sum of x over the block; *total receives the sum.
 __device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -50,6 +56,7 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
   __shared__ long long warp_sums[kPlanThreads / 32];
   __shared__ int near_base[kNear];
+  __shared__ Look look[kPlanThreads];
   const ChunkArgs& a = p.c;
   const int tid = threadIdx.x, G = a.G;
   pdl_launch_dependents();  // the main kernel's start overlaps this one
@@ -110,29 +117,34 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     int first = 0x7FFFFFFF, last = 0;
     if (a.first_keys) {
-      // a warp looks at its lanes' entries one after another, 32 tokens at a time
-      const int lane = tid & 31;
-      for (int l = 0; l < 32; ++l) {
-        const int j0 = __shfl_sync(kFull, i0, l), j1 = __shfl_sync(kFull, i1, l), pre = __shfl_sync(kFull, prefix, l);
-        const int row = __shfl_sync(kFull, s.first, l), len = __shfl_sync(kFull, s.len, l);
-        const int pos0 = len - __shfl_sync(kFull, s.n, l);
+      // a warp per entry, 32 tokens at a time (a thread's warp looking at its lanes' entries one after another took 13 us
+      // for 7 entries of up to 256 tokens; the call went from 49 to 44 us)
+      look[tid] = Look{s.first + i0, i1 - i0 + 1, s.len - s.n + i0, s.len, prefix};
+      __syncthreads();
+      for (int k = tid >> 5; k < min(kPlanThreads, E - e0); k += kPlanThreads / 32) {
+        const Look y = look[k];
         int f = 0x7FFFFFFF, t = 0;
-        for (int i = j0 + lane; i <= j1; i += 32) {
-          const int pos = pos0 + i, h = min(len, max(pos + 1, pre));
-          int k = max(0, __ldg(a.first_keys + row + i));
-          if (a.window) k = max(k, pos - a.window + 1);
-          if (k < h) {
-            f = min(f, k);
+#pragma unroll 4
+        for (int i = tid & 31; i < y.tokens; i += 32) {
+          const int pos = y.pos + i, h = min(y.len, max(pos + 1, y.prefix));
+          int lo = max(0, __ldg(a.first_keys + y.row + i));
+          if (a.window) lo = max(lo, pos - a.window + 1);
+          if (lo < h) {
+            f = min(f, lo);
             t = max(t, h);
           }
         }
         f = __reduce_min_sync(kFull, f);
         t = __reduce_max_sync(kFull, t);
-        if (lane == l) {
-          first = f;
-          last = t;
+        __syncwarp();
+        if ((tid & 31) == 0) {
+          look[k].row = f;
+          look[k].tokens = t;
         }
       }
+      __syncthreads();
+      first = look[tid].row;
+      last = look[tid].tokens;
     } else if (e < E) {
       const int pos0 = s.len - s.n;
       first = a.window ? max(0, pos0 + i0 - a.window + 1) : 0;
