@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       const uint32_t gone = missed ? miss[st] : 0u;
       const bool masked = key0 < all_lo || key0 + SK > all_hi || (gone | poison) != 0u;
       if (mods || masked) {
+        const float2 cap = cap_factors(a.c.softcap);
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
 #pragma unroll
@@ -508,8 +509,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
             const int c = g + 4 * (e & 2), j = key0 + c;
             if (mods) {
               s *= r.sl;
-              const float cap = a.c.softcap;  // sl holds log2 e
-              if (cap > 0.f) s = cap * kLog2e * (1.f - __fdividef(2.f, 1.f + ex2(s * (2.f / cap))));
+              if (a.c.softcap > 0.f) s = cap_score(s, cap.x, cap.y);  // (sl holds log2 e)
               if (r.slope != 0.f) s = fmaf(-r.slope, fabsf((float)(r.pos - j)), s);
             }
             if ((poison >> c) & 1u) s = __uint_as_float(0x7FC00000u);
