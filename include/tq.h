@@ -454,8 +454,10 @@ typedef struct tq_batch {
  * k / v element (t, h, i): k[t * k_token_stride + h * d + i], same type for both, 16-byte aligned, strides multiples
  * of 16 bytes and >= H d.  The rotated key is quantised from fp32 without a rounding in between.  K: Q8_0.  V: Q8_0 or
  * turbo2/3/4_mse.  Other formats return TQ_ERR_UNSUPPORTED (turbo K: tq_rope, then tq_encode_kv).  Values in fp16
- * without a rotation give the bytes of tq_encode_kv for Q8_0 (a NaN element is stored as 0; an infinite one, or one so
- * large that the fp16 scale overflows, gives an infinite scale, whose values read back as NaN).  A token whose page is
+ * without a rotation give the bytes of tq_encode_kv for Q8_0.  A NaN element of a Q8_0 vector is stored as 0; an infinite
+ * one, or one so large that the fp16 scale overflows (a magnitude of 127 * 65520 or more), gives an infinite scale and
+ * codes of 0, which read back as NaN in its block of 32.  A turbo vector with a NaN or an infinite element, or whose norm
+ * passes fp16 (65520), reads back as NaN in every coordinate (tq_read_kv, tq_chunk_attention).  A token whose page is
  * out of range is skipped and sets status bit 2.  Two tokens of one call must not share a slot.
  */
 tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void* k, int64_t k_token_stride,

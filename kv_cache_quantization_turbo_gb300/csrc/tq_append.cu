@@ -85,6 +85,8 @@ __device__ __forceinline__ void group_wht(float (&x)[kE], int sub) {
 // Stores a vector as q8_0: 16 code bytes per lane, a scale per pair of lanes.  The codes are round(x / delta), halves away
 // from zero, as tq_encode_kv has them (the IEEE quotient, then roundf).  x * (1 / delta) is within 127 * 2^-21 of the
 // quotient, so its nearest integer is the code unless it lies that near a half: only then are the 16 quotients taken.
+// A scale that fp16 does not hold is stored as infinite, with codes of 0: every reader then finds NaN in the block, and not
+// infinities beside them.
 __device__ __forceinline__ void store_q8(const float (&x)[kE], unsigned char* pay, unsigned char* hdr, int sub,
                                          bool keep) {
   float amax = 0.f;
@@ -94,7 +96,7 @@ __device__ __forceinline__ void store_q8(const float (&x)[kE], unsigned char* pa
   const float delta = __fdiv_rn(amax, 127.0f);
   if (!keep) return;
   uint32_t w[4] = {0u, 0u, 0u, 0u};
-  if (delta > 0.f) {
+  if (delta > 0.f && delta < 65520.f) {  // (65520 and more round to infinity)
     const float inv = __fdiv_rn(1.0f, delta), magic = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are the integer
     bool near = !(inv < 3.0e38f);  // (a subnormal delta: its reciprocal is not finite)
 #pragma unroll
@@ -363,7 +365,8 @@ __global__ void __launch_bounds__(kApThreads) read_kernel(const __grid_constant_
         const uint16_t* src = reinterpret_cast<const uint16_t*>(pay) + b * sub;
         uint64_t codes = 0;
         for (int k = 0; k < b; ++k) codes |= (uint64_t)src[k] << (16 * k);
-        const float n = __half2float(*reinterpret_cast<const __half*>(hdr));
+        float n = __half2float(*reinterpret_cast<const __half*>(hdr));
+        n += n - n;  // an infinite norm is NaN in every coordinate (its levels alone could add up to infinities)
 #pragma unroll
         for (int i = 0; i < kE; ++i) x[i] = n * __ldg(cb + ((uint32_t)(codes >> (b * i)) & ((1u << b) - 1u)));
       }

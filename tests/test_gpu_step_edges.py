@@ -27,3 +27,62 @@ def test_attend_caps_of_any_size(ctxs, d, shape, softcap):  # noqa: F811
     out = T.attend(P, torch.zeros((P.n_tokens, 4, d), dtype=torch.float16, device="cuda"), mods=T.mods_of(P, 4, softcap))
     plain = T.attend(P, torch.zeros((P.n_tokens, 4, d), dtype=torch.float16, device="cuda"))
     assert np.isfinite(T.f64(out)).all() and torch.equal(out, plain)
+
+
+# ---------------------------------------------------------------------------
+# scales that fp16 does not hold
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("vfmt", ["q8_0", "turbo2_mse", "turbo3_mse", "turbo4_mse"])
+def test_values_beyond_fp16_scales_read_back_as_nan(ctxs, d, vfmt, dtype):  # noqa: F811
+    """Finite or infinite values whose scale (or norm) overflows: NaN in the block of 32 (or the whole vector), and every
+    other value as without them.  A vector along a row of the rotation's matrix has one large coordinate after it, whose
+    reconstruction would add up infinities of one sign alone."""
+    P = T.Paged(ctxs[d], d, 2, [6, 1], [20, 9], 16, vfmt)
+    k, v = (T.W.normal_tensor((7, 2, d), seed=i, device="cuda") for i in (1, 2))
+    outs = [torch.empty((7, 2, d), device="cuda") for _ in range(4)]
+
+    def step(k, v, out):
+        assert T.tq.tq_append_kv(P.ctx.h, P.batch, k.to(T.DT[dtype]), v.to(T.DT[dtype]), P.kv, P.vv, 0) == T.tq.TQ_OK
+        assert T.tq.tq_read_kv(P.ctx.h, P.batch, P.kv, out[0], P.vv, out[1], 0) == T.tq.TQ_OK
+        return out
+    clean = step(k, v, outs[:2])
+    for x in (k, v):
+        x[0, 0, 5] = 1e8
+        x[1, 1, 40] = -3e38
+        x[2, 0, d - 1] = float("inf")
+        x[3, 1, 0] = float("-inf")
+        x[4, 0] = 1e6 * torch.as_tensor(P.ctx.signs, device="cuda")
+    got = step(k, v, outs[2:])
+    for name, fmt, c, g in (("k", "q8_0", clean[0], got[0]), ("v", vfmt, clean[1], got[1])):
+        gone = torch.zeros((7, 2, d // 32), dtype=torch.bool, device="cuda")
+        if fmt == "q8_0":  # 1e6 / 127 is a scale that fp16 holds
+            for t, h, i in ((0, 0, 5), (1, 1, 40), (2, 0, d - 1), (3, 1, 0)):
+                gone[t, h, i // 32] = True
+        else:
+            for t, h in ((0, 0), (1, 1), (2, 0), (3, 1), (4, 0)):
+                gone[t, h] = True
+        gone = gone.repeat_interleave(32, -1)
+        assert torch.isnan(g[gone]).all(), (name, g[gone])
+        same = ~gone
+        if fmt == "q8_0":
+            same[4, 0] = False
+            # codes of 127 times the scale, off by half a step of fp16; 1e6 by half a step of its type
+            assert (g[4, 0].abs() - 1e6).abs().max() < 1e6 * (2 ** -11 + T.half_step(T.DT[dtype]) + 1e-6)
+        assert torch.equal(g[same], c[same]), name
+    assert T.status(P.ctx) == 0
+    # the stored bytes themselves read back as NaN for every other reader
+    deq = torch.empty((1, 2, d), device="cuda")
+    slot = torch.as_tensor(P.slots(0, P.pos[:1]), device="cuda")
+    assert T.tq.tq_dequantize(P.ctx.h, P.kv, 0, slot, 0, 1, 0, deq) == T.tq.TQ_OK
+    torch.cuda.synchronize()
+    assert torch.isnan(deq[0, 0, :32]).all() and torch.isfinite(deq[0, 0, 32:]).all()
+    # and a row of the attention that sees one of them is NaN, one that does not is not
+    q = T.W.normal_tensor((7, 2, d), seed=3, device="cuda").half()
+    out = T.attend(P, q, mods=T.mods_of(P, 2, window=1))
+    torch.cuda.synchronize()
+    assert torch.isnan(out[0, 0]).all() and torch.isnan(out[1, 1]).all()
+    assert torch.isfinite(out[0, 1]).all() and torch.isfinite(out[1, 0]).all() and torch.isfinite(out[5:]).all()
+
