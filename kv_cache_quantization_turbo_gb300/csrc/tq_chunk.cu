@@ -53,9 +53,30 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
   return __shfl_sync(kFull, w, warp) - warp_sums[warp] + v - x;
 }
 
+// The sequences b0 + tid whose threads say refused break their bounds: flagged, and their rows (those that are in range)
+// are zeros, written by the whole block: 0.5 ms for 8192 tokens of 8 heads of 128 in fp32, 8.5 ms from one thread.  Rare: a plan
+// without such a sequence meets one barrier more.
+__device__ __noinline__ void zero_refused(const ChunkArgs& a, int b0, bool refused, uint32_t* refused_of) {
+  const int tid = threadIdx.x;
+  const uint32_t m = __ballot_sync(kFull, refused);
+  if ((tid & 31) == 0) refused_of[tid >> 5] = m;
+  if (tid == 0) atomicOr(a.tab.status, kFlagSeqLen);
+  __syncthreads();
+  const long long row = (long long)a.n_q_heads * a.k.d * (a.out_dtype == TQ_DTYPE_F32 ? 4 : 2) / 16;  // 16-byte units
+  uint4* o = static_cast<uint4*>(a.out);
+  for (int w = 0; w < kPlanThreads / 32; ++w)
+    for (uint32_t left = refused_of[w]; left; left &= left - 1) {
+      const int b = b0 + 32 * w + __ffs(left) - 1;
+      const long long r0 = max(0, a.b.cu[b]), r1 = min(a.b.n_tokens, a.b.cu[b + 1]);
+      for (long long i = r0 * row + tid; i < r1 * row; i += kPlanThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  __syncthreads();  // before refused_of is written again
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
   __shared__ long long warp_sums[kPlanThreads / 32];
   __shared__ int near_base[kNear];
+  __shared__ uint32_t refused_of[kPlanThreads / 32];
   __shared__ Look look[kPlanThreads];
   const ChunkArgs& a = p.c;
   const int tid = threadIdx.x, G = a.G;
@@ -64,20 +85,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   for (int b0 = 0; b0 < a.b.n_seqs; b0 += kPlanThreads) {
     const int b = b0 + tid;
     long long ne = 0;
+    bool refused = false;
     if (b < a.b.n_seqs) {
       const SeqOf s = seq_of(a.b, b);
       ne = ((long long)s.n * G + p.rows - 1) / p.rows;
-      if (!s.ok) {  // flagged, its rows (those that are in range) are zeros
-        atomicOr(a.tab.status, kFlagSeqLen);
-        const int esz = a.out_dtype == TQ_DTYPE_F32 ? 4 : 2;
-        const int r0 = max(0, a.b.cu[b]), r1 = min(a.b.n_tokens, a.b.cu[b + 1]);
-        if (r0 < r1) {
-          const long long row = (long long)a.n_q_heads * a.k.d * esz / 16;  // 16-byte units of a token
-          uint4* o = static_cast<uint4*>(a.out);
-          for (long long i = r0 * row; i < r1 * row; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
+      refused = !s.ok;
     }
+    if (__syncthreads_or(refused)) zero_refused(a, b0, refused, refused_of);
     const long long at = carry + block_scan(ne, warp_sums, &total);
     if (b < a.b.n_seqs) (a.b.n_seqs <= kNear ? near_base : p.seq_base)[b] = (int)min(at, (long long)p.max_entries);
     carry += total;

@@ -86,3 +86,39 @@ def test_values_beyond_fp16_scales_read_back_as_nan(ctxs, d, vfmt, dtype):  # no
     assert torch.isnan(out[0, 0]).all() and torch.isnan(out[1, 1]).all()
     assert torch.isfinite(out[0, 1]).all() and torch.isfinite(out[1, 0]).all() and torch.isfinite(out[5:]).all()
 
+
+
+# ---------------------------------------------------------------------------
+# sequences that break their bounds
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("G,limit", [(1, None), (1, 4), (4, None)])
+def test_rows_of_a_refused_sequence_are_zeros_soon(ctxs, G, limit):  # noqa: F811
+    """A chunk of 8192 tokens with a length that cannot be: zeros in its rows alone, without holding up the step (34 MB of
+    zeros from one thread took 8.5 ms; 5 ms are allowed)."""
+    d, H, n = 128, 8, 8192 // G
+    new = [3, n, 2]
+    P = T.Paged(ctxs[d], d, H, [3, 1, 2], [40, 1, 30], 16)
+    P.n_tokens = sum(new) + 5
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q = T.W.normal_tensor((P.n_tokens, H * G, d), seed=4, device="cuda")
+    ws_batches = []
+    for lens in ([40, 1, 30], [40, -1, 30]):
+        P.set_batch(cu, lens, max_tokens=limit or n, max_ctx=48)
+        ws_batches.append(P.batch)
+    ws = torch.empty(T.tq.tq_chunk_workspace_bytes(P.ctx.h, P.batch, H * G, H), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 9.0)
+    for batch in ws_batches:
+        P.batch = batch
+        T.attend(P, q, out=out.fill_(9.0), workspace=ws)
+        torch.cuda.synchronize()
+        assert T.status(P.ctx) == 1
+        assert not out[3:3 + n].any() and (out[-5:] == 9.0).all()
+        assert out[:3].any(-1).all() and out[3 + n:-5].any(-1).all() and torch.isfinite(out).all()
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        T.attend(P, q, out=out, workspace=ws)
+        end.record()
+        torch.cuda.synchronize()
+        assert start.elapsed_time(end) < 5.0
+    T.status(P.ctx)
