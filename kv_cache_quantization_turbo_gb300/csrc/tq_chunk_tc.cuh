@@ -51,7 +51,6 @@ namespace ck {
 constexpr int kThreads = 640;
 constexpr int kProdWarps = 8;
 constexpr int kIssuer = 16, kLocator = 18, kLocWarps = 2;
-constexpr int kItemReaders = 8 + kProdWarps + 2 + kLocWarps - 1;  // (the first locator writes the items)
 constexpr int NI = 3;       // items known ahead
 constexpr int NL = 6;       // tiles located ahead of the producers
 constexpr int kMissRing = 16;
@@ -86,6 +85,9 @@ struct Shape {
   static constexpr int alloc = total + 1024;
   static_assert(alloc <= 227 * 1024, "shared memory");
   static constexpr int PH = BN / HN;                   // parts of a step
+  // At 256 the first issuer has every step and the second takes no part: it would poll through the whole of every item.
+  static constexpr int kIssuers = D == 256 ? 1 : 2;
+  static constexpr int kItemReaders = 8 + kProdWarps + kIssuers + kLocWarps - 1;  // (the first locator writes the items)
   // tensor memory columns: S [2][BN], O [kQTiles][D]
   static constexpr int tO = 2 * BN;
   static_assert(tO + kQTiles * D <= 512, "tensor memory");
@@ -106,7 +108,9 @@ static_assert(sizeof(Item) <= 128, "item");
 struct Bars {
   uint64_t k_full[3], k_free[3], v_full[3], v_free[3];
   uint64_t s_done[2], p_full[4], pv_done[4];  // per buffer, per buffer and part
-  uint64_t drained[2], q_full, item_full[NI], item_free[NI], loc_full[NL], loc_free[NL];
+  // q_full is one per item slot: an issuer without a step for an item does not wait for its queries, and only the item
+  // ring (a slot is written again once all have read it) keeps the others from being two phases ahead of it.
+  uint64_t drained[2], q_full[NI], item_full[NI], item_free[NI], loc_full[NL], loc_free[NL];
   uint32_t tmem;
 };
 static_assert(sizeof(Bars) <= 64 * 8, "barriers");
@@ -696,12 +700,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         tc::mbar_init(&B->p_full[i], 4);
         tc::mbar_init(&B->pv_done[i], 1);
       }
-      tc::mbar_init(&B->q_full, 8);
       tc::mbar_init(&B->drained[0], 1);
       tc::mbar_init(&B->drained[1], 1);
       for (int i = 0; i < NI; ++i) {
+        tc::mbar_init(&B->q_full[i], 8);
         tc::mbar_init(&B->item_full[i], 1);
-        tc::mbar_init(&B->item_free[i], kItemReaders);
+        tc::mbar_init(&B->item_free[i], Sh::kItemReaders);
       }
       for (int i = 0; i < NL; ++i) {
         tc::mbar_init(&B->loc_full[i], kLocWarps);
@@ -768,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         __syncwarp();
         if (half && lane == 0) tc::mbar_arrive(&B->item_free[is]);
       }
-    } else {
+    } else if (warp - kIssuer < Sh::kIssuers) {
       // The whole warp runs the same code, one lane's predicate on the tensor instructions: descriptors and addresses
       // then stay in uniform registers, where those instructions take them from.  (With one lane in a branch, every
       // operand was moved there first, and issuing a product took longer than the product.)
@@ -787,11 +791,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         wait_warp(ok, &B->item_full[is], icnt / NI);
         const int kind = uniform(items[is].kind), n = uniform(items[is].n), two = uniform(items[is].two);
         if (!ok || kind == 0) break;
-        wait_warp(ok, &B->q_full, icnt);
         if (kind == 1) {
-          // own steps: every tile with two row tiles, else every other one; D = 256: the first issuer all
+          // own steps: every tile with two row tiles, else every other one; D = 256: all
           const int first = two || D == 256 ? 0 : w, stride = two || D == 256 ? 1 : 2;
-          const int steps = D == 256 && w ? 0 : (n - first + stride - 1) / stride;
+          const int steps = (n - first + stride - 1) / stride;
+          if (steps > 0) wait_warp(ok, &B->q_full[is], icnt / NI);
           const uint32_t dq = q_lo + (uint32_t)(two ? w * (Sh::kQTile >> 4) : 0);
           const bool alone = !two;  // no other issuer uses the tile
           auto qk = [&](int i) {
@@ -911,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         else
           load_queries<D>(a, it, static_cast<const __nv_bfloat16*>(a.c.q), sm + Sh::q, rs, warp, lane);
       }
-      arrive_smem(&B->q_full, lane);
+      arrive_smem(&B->q_full[is], lane);
       tc::bar_sync(1, 256);
 
       // this thread's row

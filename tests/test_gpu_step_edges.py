@@ -122,3 +122,33 @@ def test_rows_of_a_refused_sequence_are_zeros_soon(ctxs, G, limit):  # noqa: F81
         torch.cuda.synchronize()
         assert start.elapsed_time(end) < 5.0
     T.status(P.ctx)
+
+
+# ---------------------------------------------------------------------------
+# many short entries
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_entries_without_a_step_for_one_of_the_issuers(ctxs, d):  # noqa: F811
+    """2400 entries of 20 rows, about 16 for a block: some see nothing (no product at all), some a single key tile (a step
+    for one issuing warp alone), some three (one warp is a step ahead).  Repeats are equal, every row is written."""
+    n_seqs, H, n = 300, 8, 20
+    kind = np.random.default_rng(d).integers(0, 3, n_seqs)
+    lens = np.where(kind == 2, 300, np.where(kind == 1, 60, 25)).tolist()
+    P = T.Paged(ctxs[d], d, H, [n] * n_seqs, lens, 16, fill=False, padding=3)
+    x = T.W.normal_tensor((int(sum(lens)), H, d), seed=1, device="cuda").half()
+    slots = torch.as_tensor(np.concatenate([P.slots(b, np.arange(t)) for b, t in enumerate(lens)]), device="cuda")
+    T.C.encode(P.ctx, P.kv, x, True, slots=slots)
+    T.C.encode(P.ctx, P.vv, x.flip(0).contiguous(), False, slots=slots)
+    first = np.where(kind[P.seq] == 0, 10 ** 9, 0)
+    first = np.concatenate([first, np.zeros(3, np.int64)])
+    some = np.flatnonzero(np.arange(n_seqs) % 37 == 0)
+    out = K.check_attend(P, 1, torch.float16, first=first, rows=np.flatnonzero(np.isin(P.seq, some)))
+    got, empty = T.f64(out)[:P.rows], kind[P.seq] == 0
+    assert np.isfinite(got).all() and not got[empty].any() and got[~empty].any(-1).all()
+    q = T.W.normal_tensor((P.n_tokens, H + 2, d), seed=3, device="cuda").half()[:, 1:1 + H]
+    m = T.mods_of(P, H, first=first)
+    for _ in range(20):
+        again = T.attend(P, q, mods=m)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out) and T.status(P.ctx) == 0
