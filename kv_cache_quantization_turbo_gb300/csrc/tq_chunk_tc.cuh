@@ -108,8 +108,9 @@ static_assert(sizeof(Item) <= 128, "item");
 struct Bars {
   uint64_t k_full[3], k_free[3], v_full[3], v_free[3];
   uint64_t s_done[2], p_full[4], pv_done[4];  // per buffer, per buffer and part
-  // q_full is one per item slot: an issuer without a step for an item does not wait for its queries, and only the item
-  // ring (a slot is written again once all have read it) keeps the others from being two phases ahead of it.
+  // q_full is one per item slot: nothing makes the softmax warps wait for an issuer without a step in an item, and with one
+  // barrier for all items they could complete a second phase before it has seen the first.  An item slot is written again
+  // only once all have left the item.
   uint64_t drained[2], q_full[NI], item_full[NI], item_free[NI], loc_full[NL], loc_free[NL];
   uint32_t tmem;
 };
@@ -791,11 +792,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         wait_warp(ok, &B->item_full[is], icnt / NI);
         const int kind = uniform(items[is].kind), n = uniform(items[is].n), two = uniform(items[is].two);
         if (!ok || kind == 0) break;
+        wait_warp(ok, &B->q_full[is], icnt / NI);
         if (kind == 1) {
           // own steps: every tile with two row tiles, else every other one; D = 256: all
           const int first = two || D == 256 ? 0 : w, stride = two || D == 256 ? 1 : 2;
           const int steps = (n - first + stride - 1) / stride;
-          if (steps > 0) wait_warp(ok, &B->q_full[is], icnt / NI);
           const uint32_t dq = q_lo + (uint32_t)(two ? w * (Sh::kQTile >> 4) : 0);
           const bool alone = !two;  // no other issuer uses the tile
           auto qk = [&](int i) {
