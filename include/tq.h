@@ -409,7 +409,8 @@ typedef struct tq_rope_table {
   uint64_t turns[128];
 } tq_rope_table;
 
-/* Host; TQ_ERR_INVALID_ARG for values outside those noted above, TQ_ERR_UNSUPPORTED for another head_dim. */
+/* Host; TQ_ERR_INVALID_ARG for values outside those noted above and where an angle leaves the range of double (a factor of
+ * 1e-320, say), TQ_ERR_UNSUPPORTED for another head_dim. */
 tq_status tq_rope_build(const tq_rope_params* params, tq_rope_table* table);
 
 /*

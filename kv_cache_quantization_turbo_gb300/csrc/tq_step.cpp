@@ -101,6 +101,7 @@ tq_status tq_rope_build(const tq_rope_params* p, tq_rope_table* out) {
       const double g = std::fmin(std::fmax((i - from) / width, 0.0), 1.0);
       f = g * f / p->factor + (1.0 - g) * f;
     }
+    if (!std::isfinite(f)) return TQ_ERR_INVALID_ARG;  // (its fraction of a turn would be whatever the machine makes of NaN)
     const double turn = f / two_pi, frac = turn - std::floor(turn);
     t.turns[i] = (uint64_t)std::ldexp(frac, 64);  // frac < 1 has 53 bits: below 2^64
   }
