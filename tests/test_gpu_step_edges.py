@@ -87,7 +87,6 @@ def test_values_beyond_fp16_scales_read_back_as_nan(ctxs, d, vfmt, dtype):  # no
     assert torch.isfinite(out[0, 1]).all() and torch.isfinite(out[1, 0]).all() and torch.isfinite(out[5:]).all()
 
 
-
 # ---------------------------------------------------------------------------
 # sequences that break their bounds
 # ---------------------------------------------------------------------------
@@ -152,3 +151,32 @@ def test_entries_without_a_step_for_one_of_the_issuers(ctxs, d):  # noqa: F811
         again = T.attend(P, q, mods=m)
     torch.cuda.synchronize()
     assert torch.equal(again, out) and T.status(P.ctx) == 0
+
+
+# ---------------------------------------------------------------------------
+# scores of any height
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("order", ["rising", "falling", "shuffled"])
+def test_attend_scores_that_rise_and_fall(ctxs, d, shape, order):  # noqa: F811
+    """Scores from -20000 to 20000, exact in every operand (small integers), so that the softmax's reference rises in every
+    part, in none, or now and then; what is left is the rounding of values and weights."""
+    new, lens = SHAPES[shape]
+    P = T.Paged(ctxs[d], d, 1, new, lens, 16)
+    for b, n in enumerate(lens):
+        k = np.zeros((n, 1, d), np.float32)
+        k[:, 0, 0] = np.linspace(-126, 126, n).round()
+        if order == "falling":
+            k = k[::-1].copy()
+        if order == "shuffled":
+            k = k[np.random.default_rng(b).permutation(n)]
+        k[:, 0, 1] = 127.0  # the block's scale is 1
+        T.C.encode(P.ctx, P.kv, torch.as_tensor(k, device="cuda").half(), True,
+                   slots=torch.as_tensor(P.slots(b, np.arange(n)), device="cuda"))
+    q = torch.zeros((P.n_tokens, 2, d), dtype=torch.float16, device="cuda")
+    q[:, 0, 0], q[:, 1, 0] = 1.0, -1.0
+    for scale in (0.01, 1.0, 160.0):
+        K.check_attend(P, 2, torch.float16, scale=scale, q=q)
+        K.check_attend(P, 2, torch.float16, scale=scale, q=q, bias=True, window=150)
