@@ -505,12 +505,12 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
  *   K: Q8_0.  V: Q8_0 or turbo2/3/4_mse.  Others: TQ_ERR_UNSUPPORTED (turbo K: tq_decode_attention,
  *   tq_prefill_attention).
  *   workspace: device, tq_chunk_workspace_bytes() bytes, 256-byte aligned; calls that may overlap need their own.
- * The operands of the products are fp16 (queries scaled by a power of two per row, so that no type overflows; a decode
- * step's keys are not rounded), the sums and the softmax fp32.  Stored q8_0 scales above 511.5 (values above 64960) are
- * read as 511.5.  The result of a call does not depend on what else runs.  max_tokens chooses the kernel: a batch of at most 16 rows (max_tokens *
- * n_q_heads / n_kv_heads; 8 at head_dim 256) per sequence and KV head takes one that is about twice as fast for them, so
- * a decode step passes max_tokens = 1.  A block-table entry out of range sets status bit 2, and its keys are left
- * out.
+ * max_tokens chooses the kernel: a batch of at most 16 rows (max_tokens * n_q_heads / n_kv_heads; 8 at head_dim 256) per
+ * sequence and KV head takes one that is about twice as fast for them, so a decode step passes max_tokens = 1.
+ * The operands of the products are fp16: queries (scaled by a power of two per row, so that no type overflows), keys and
+ * values as scale * code (turbo: norm * level), weights; the sums and the softmax are fp32.  Few rows: keys are exact and
+ * fp32 queries have 22 bits.  Stored q8_0 scales above 511.5 (values above 64960) are read as 511.5.  The result of a call
+ * does not depend on what else runs.  A block-table entry out of range sets status bit 2, and its keys are left out.
  */
 tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const void* q, tq_dtype q_dtype,
                              int64_t q_token_stride, int n_q_heads, const tq_cache_view* k_view,

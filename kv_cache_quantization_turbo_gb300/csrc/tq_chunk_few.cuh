@@ -6,20 +6,22 @@
 // fp16 fragments in registers, and keeps its own softmax reference, sum and output; no barrier until the range ends.  The
 // products are the warp-wide m16n8k16 ones (fp16 operands, fp32 sums):
 //   S^T = K Q^T: M = 16 keys, N = 8 rows; the codes are integers that fp16 holds, the scale of a block of 32 goes to its sum
-//     in fp32, so K is not rounded.  A lane holds 8 coordinates of a block at a time: the contraction index is permuted,
+//     in fp32, so K is not rounded; what fp16 leaves of fp32 queries has products of its own.  A lane holds 8 coordinates of a block at a time: the contraction index is permuted,
 //     alike for K and Q.
 //   O^T = V^T P^T: M = 16 coordinates, N = 8 rows; a lane pairs the codes of two keys by byte permutes, and P^T is S^T's
 //     accumulators with two 8 x 8 transposes.  A lane's columns are the same rows of Q in both products.
 // The ranges, the join of entries that several CTAs share and the meaning of every mask are those of tq_chunk_tc.cuh;
 // weights are taken against a reference that is raised only when a weight would pass 2^15.
 //
-// What bounds it.  64 sequences of 1K to 16K tokens, 8 KV heads of 128, 4 rows: 145 us for 0.87 GB, 6.0 TB/s, 88 % of the
+// What bounds it.  64 sequences of 1K to 16K tokens, 8 KV heads of 128, 4 rows: 147 us for 0.87 GB, 5.9 TB/s, 87 % of the
 // copy bandwidth, at 64 % of the instruction slots (507 instructions per slice, of which 180 turn codes into fp16).  Keys as
 // the right operand, 8 of 16 rows idle, took 170 us; scales multiplied into K's fragments 149 us, and rounded K: an error of
 // 1.3e-3 instead of 3.6e-4.  Turbo values: more instructions (a lookup by byte permutes) for fewer bytes, 149 us for 48 such
 // sequences, bound by the instruction slots.  One token at 32K: 20 us after the plan, of which the range's 7 slices per
 // warp take 9 (instruction slots), finding the range, the first copies and Q 5, the join of 38 shares 5.
 #pragma once
+
+#include <type_traits>
 
 #include "tq_chunk_tc.cuh"
 #include "tq_warp_mma.cuh"
@@ -50,7 +52,8 @@ struct Few {
   static constexpr int tab = miss + NW * 8 * 4;          // uint32 [4]: the V codebook in fp16, low bytes, high bytes
   static constexpr int flag = tab + 16;
   static constexpr int walk = flag + 16;                 // Items<D>
-  static constexpr int total = walk + 64;
+  static constexpr int ql = walk + 64;                   // uint4 [NT][D / 32][32 lanes]: what fp16 leaves of fp32 queries
+  static constexpr int total = ql + NT * D * 16;
   static constexpr int OS = D + 4;                       // floats of a row of a warp's O (in the ring, once it is read)
   static constexpr int mo = NW * 8 * NT * OS * 4, sh = 8 * NT * 320 * 8;  // the warps' O, or the weights of 320 shares
   static constexpr int fin = mo > sh ? mo : sh;          // behind them, float [8 NT][D]: joined rows before their transform
@@ -116,9 +119,12 @@ __device__ __forceinline__ Spot spot_of(const Args& a, const int32_t* pages, int
 }
 
 // A lane's part of a row of Q as fragments of the right operand, times a power of two that brings the row's largest magnitude
-// to [1, 2); returns that power's inverse.
+// to [1, 2); returns that power's inverse.  16-bit queries are exact in fp16 then, down to 2^-24 of the largest.  Of fp32
+// ones rest takes what the rounding leaves, in fp16 again (22 bits in all), which a second product adds to the scores: rest
+// [D / 32] at a stride of 32 lanes, null where another warp writes it.  (Without it 64 decode rows of fp32 queries are off by
+// 5.5e-4, 2.7e-3 at most, with it by 3.5e-4 and 1.7e-3, as fp16 ones are; it costs 2 us of 164, and its branch 1 % elsewhere.)
 template <int D, class T>
-__device__ __forceinline__ float load_q(const Args& a, const T* src, bool valid, int t, uint32_t (&f)[D / 16][2]) {
+__device__ __forceinline__ float load_q(const Args& a, const T* src, bool valid, int t, uint32_t (&f)[D / 16][2], uint4* rest) {
   uint32_t top = 0;
   float x[D / 32][8];  // coordinates 8 t .. 8 t + 7 of every 32
 #pragma unroll
@@ -144,14 +150,29 @@ __device__ __forceinline__ float load_q(const Args& a, const T* src, bool valid,
       f[2 * i + w][0] = narrow(x[i][4 * w] * m, x[i][4 * w + 1] * m, (const __half*)nullptr);
       f[2 * i + w][1] = narrow(x[i][4 * w + 2] * m, x[i][4 * w + 3] * m, (const __half*)nullptr);
     }
+  if constexpr (sizeof(T) == 4) {
+    if (rest) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t r[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 h = widen(f[2 * i + w / 2][w % 2], (const __half*)nullptr);
+          r[w] = narrow(fmaf(x[i][2 * w], m, -h.x), fmaf(x[i][2 * w + 1], m, -h.y), (const __half*)nullptr);
+        }
+        rest[32 * i] = make_uint4(r[0], r[1], r[2], r[3]);
+      }
+    }
+  }
   return __uint_as_float(ex << 23);
 }
 
 template <int D>
-__device__ __forceinline__ float load_q_any(const Args& a, long long at, bool valid, int t, uint32_t (&f)[D / 16][2]) {
-  if (a.c.q_dtype == TQ_DTYPE_F32) return load_q<D>(a, static_cast<const float*>(a.c.q) + at, valid, t, f);
-  if (a.c.q_dtype == TQ_DTYPE_F16) return load_q<D>(a, static_cast<const __half*>(a.c.q) + at, valid, t, f);
-  return load_q<D>(a, static_cast<const __nv_bfloat16*>(a.c.q) + at, valid, t, f);
+__device__ __forceinline__ float load_q_any(const Args& a, long long at, bool valid, int t, uint32_t (&f)[D / 16][2],
+                                            uint4* rest) {
+  if (a.c.q_dtype == TQ_DTYPE_F32) return load_q<D>(a, static_cast<const float*>(a.c.q) + at, valid, t, f, rest);
+  if (a.c.q_dtype == TQ_DTYPE_F16) return load_q<D>(a, static_cast<const __half*>(a.c.q) + at, valid, t, f, rest);
+  return load_q<D>(a, static_cast<const __nv_bfloat16*>(a.c.q) + at, valid, t, f, rest);
 }
 
 // Clamps N scales as the large kernel does (a turbo norm is left as it is); true where one is not finite (it becomes 0).
@@ -210,6 +231,8 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
   float2* ml = reinterpret_cast<float2*>(sm + F::ml);
   Row* row_of = reinterpret_cast<Row*>(sm + F::row);
   int* flag = reinterpret_cast<int*>(sm + F::flag);
+  uint4* q_rest = reinterpret_cast<uint4*>(sm + F::ql);
+  const bool fine = a.c.q_dtype == TQ_DTYPE_F32;
   const DevView &K = a.c.k, &V = a.c.v;
   const bool mods = a.c.softcap > 0.f || a.c.slopes != nullptr;
   // where the 16 keys of a slice, which begin at a multiple of 16, are consecutive vectors
@@ -406,7 +429,8 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       const int r = g + 8 * u;
       const bool valid = r < rows;
       const int row = it.row0 + (valid ? r : 0), ti = row / G, head = it.kvh * G + (row - ti * G), tok = it.tok0 + ti;
-      const float rs = load_q_any<D>(a, (long long)tok * a.c.q_stride + (long long)head * D, valid, t, q[u]);
+      const float rs = load_q_any<D>(a, (long long)tok * a.c.q_stride + (long long)head * D, valid, t, q[u],
+                                     warp == 0 ? q_rest + u * D + lane : nullptr);
       const float x = fmaxf(a.scale * rs, 1.2e-38f);
       if (warp == 0 && t == 0) row_of[r].sl = x;
 #pragma unroll
@@ -474,27 +498,36 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
           sa[i] = *reinterpret_cast<const uint32_t*>(sk + F::ks + g * (D / 16) + 4 * i);
           sb[i] = *reinterpret_cast<const uint32_t*>(sk + F::ks + (g + 8) * (D / 16) + 4 * i);
         }
+        auto products = [&](auto with_rest) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {  // a block of 32: two products of the codes, exact, then its scale
-          const uint2 wa = *reinterpret_cast<const uint2*>(sk + F::k + k_at<D>(g, 2 * i + (t >> 1)) + 8 * (t & 1));
-          const uint2 wb = *reinterpret_cast<const uint2*>(sk + F::k + k_at<D>(g + 8, 2 * i + (t >> 1)) + 8 * (t & 1));
-          const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&sa[i / 2]));
-          const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&sb[i / 2]));
-          const float ka = i & 1 ? fa.y : fa.x, kb = i & 1 ? fb.y : fb.x;
-          uint32_t a0[2], a1[2], a2[2], a3[2];
-          q8_pairs(wa.x, a0[0], a2[0]);
-          q8_pairs(wb.x, a1[0], a3[0]);
-          q8_pairs(wa.y, a0[1], a2[1]);
-          q8_pairs(wb.y, a1[1], a3[1]);
+          for (int i = 0; i < D / 32; ++i) {  // a block of 32: two products of the codes, exact, then its scale
+            const uint2 wa = *reinterpret_cast<const uint2*>(sk + F::k + k_at<D>(g, 2 * i + (t >> 1)) + 8 * (t & 1));
+            const uint2 wb = *reinterpret_cast<const uint2*>(sk + F::k + k_at<D>(g + 8, 2 * i + (t >> 1)) + 8 * (t & 1));
+            const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&sa[i / 2]));
+            const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&sb[i / 2]));
+            const float ka = i & 1 ? fa.y : fa.x, kb = i & 1 ? fb.y : fb.x;
+            uint32_t a0[2], a1[2], a2[2], a3[2];
+            q8_pairs(wa.x, a0[0], a2[0]);
+            q8_pairs(wb.x, a1[0], a3[0]);
+            q8_pairs(wa.y, a0[1], a2[1]);
+            q8_pairs(wb.y, a1[1], a3[1]);
 #pragma unroll
-          for (int u = 0; u < NT; ++u) {
-            float c[4];
-            wm::mma_16816_zc(c, a0[0], a1[0], a2[0], a3[0], q[u][2 * i][0], q[u][2 * i][1]);
-            wm::mma_16816(c, a0[1], a1[1], a2[1], a3[1], q[u][2 * i + 1][0], q[u][2 * i + 1][1]);
+            for (int u = 0; u < NT; ++u) {
+              float c[4];
+              wm::mma_16816_zc(c, a0[0], a1[0], a2[0], a3[0], q[u][2 * i][0], q[u][2 * i][1]);
+              wm::mma_16816(c, a0[1], a1[1], a2[1], a3[1], q[u][2 * i + 1][0], q[u][2 * i + 1][1]);
+              if constexpr (with_rest.value) {
+                const uint4 r = q_rest[u * D + 32 * i + lane];
+                wm::mma_16816(c, a0[0], a1[0], a2[0], a3[0], r.x, r.y);
+                wm::mma_16816(c, a0[1], a1[1], a2[1], a3[1], r.z, r.w);
+              }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[u][e] = i == 0 ? (e < 2 ? ka : kb) * c[e] : fmaf(e < 2 ? ka : kb, c[e], x[u][e]);
+              for (int e = 0; e < 4; ++e) x[u][e] = i == 0 ? (e < 2 ? ka : kb) * c[e] : fmaf(e < 2 ? ka : kb, c[e], x[u][e]);
+            }
           }
-        }
+        };
+        if (fine) products(std::true_type{});
+        else products(std::false_type{});
       }
       const uint32_t gone = missed ? miss[st] : 0u;
       const bool masked = key0 < all_lo || key0 + SK > all_hi || (gone | poison) != 0u;

@@ -180,3 +180,37 @@ def test_attend_scores_that_rise_and_fall(ctxs, d, shape, order):  # noqa: F811
     for scale in (0.01, 1.0, 160.0):
         K.check_attend(P, 2, torch.float16, scale=scale, q=q)
         K.check_attend(P, 2, torch.float16, scale=scale, q=q, bias=True, window=150)
+
+
+# ---------------------------------------------------------------------------
+# queries in fp32
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d,G", [(d, G) for d in (64, 128, 256) for G in (1, 4, 8, 16) if (d, G) != (256, 16)])
+def test_few_rows_take_fp32_queries_in_more_bits_than_fp16(ctxs, d, G):  # noqa: F811
+    """Scores that are all in the bits that fp16 does not hold: q = 1 + n 2^-20 and -1 on two coordinates where a key has
+    c twice gives n c 2^-20, exact in every product and sum here; the scale makes that up to 10.  So the bound is that of
+    the rounding of values and weights alone."""
+    P = T.Paged(ctxs[d], d, 1, [1], [200], 16, "q8_0")
+    rng = np.random.default_rng(G)
+    k = np.zeros((200, 1, d), np.float32)
+    k[:, 0, 0::2] = k[:, 0, 1::2] = rng.integers(-127, 128, (200, d // 2))
+    k[:, 0, 0::32] = k[:, 0, 1::32] = 127.0  # every block's scale is 1
+    T.C.encode(P.ctx, P.kv, torch.as_tensor(k, device="cuda").half(), True,
+               slots=torch.as_tensor(P.slots(0, np.arange(200)), device="cuda"))
+    at = 2 * (16 * rng.integers(0, d // 32, G) + rng.integers(1, 16, G))
+    q = np.zeros((1, G, d), np.float32)
+    q[0, np.arange(G), at] = 1.0 + rng.choice([-511, -300, 200, 400, 511], G) * 2.0 ** -20
+    q[0, np.arange(G), at + 1] = -1.0
+    scale = 10.0 * 2 ** 20 / (127 * 511)
+    out = T.attend(P, torch.as_tensor(q, device="cuda"), torch.float32, scale=scale)
+    torch.cuda.synchronize()
+    kk, vv = P.stored(0)
+    assert np.array_equal(kk, k)
+    q = q.astype(np.float64)
+    want = T.S.chunk_attention(q, kk, vv, P.pos, scale)
+    s = np.einsum("ghd,td->ght", q, kk[:, 0]) * scale
+    w = np.exp(s - s.max(-1, keepdims=True))
+    w /= w.sum(-1, keepdims=True)
+    noise = np.einsum("ght,t->gh", w ** 2, 2 * (2.0 ** -22 / 3) * (vv[:, 0] ** 2).sum(-1))  # as in row_bound
+    K.assert_rows(T.f64(out), want, np.maximum(6 * np.sqrt(noise) / np.linalg.norm(want, axis=-1), T.C.ATTN_RTOL))
