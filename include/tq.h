@@ -376,7 +376,8 @@ typedef enum tq_rope_scaling {
   TQ_ROPE_NONE = 0,
   TQ_ROPE_LINEAR = 1,      /* f_i / factor */
   TQ_ROPE_NTK = 2,         /* base * factor^(r / (r - 2)) in place of base, r = rotary_dim > 2 */
-  TQ_ROPE_WAVELENGTH = 3,  /* s f_i + (1 - s) f_i / factor, s = clamp((original_ctx f_i / 2 pi - low) / (high - low), 0, 1):
+  TQ_ROPE_WAVELENGTH = 3,  /* s f_i + (1 - s) f_i / factor,
+                              s = clamp((original_ctx f_i / 2 pi - low) / (high - low), 0, 1):
                               pairs that turn more than `high` times within original_ctx keep their angle, pairs
                               that turn less than `low` times are stretched (defaults low 1, high 4) */
   TQ_ROPE_YARN = 4         /* g_i f_i / factor + (1 - g_i) f_i, g_i = clamp((i - a) / max(b - a, 0.001), 0, 1),
@@ -409,8 +410,8 @@ typedef struct tq_rope_table {
   uint64_t turns[128];
 } tq_rope_table;
 
-/* Host; TQ_ERR_INVALID_ARG for values outside those noted above and where an angle leaves the range of double (a factor of
- * 1e-320, say), TQ_ERR_UNSUPPORTED for another head_dim. */
+/* Host; TQ_ERR_INVALID_ARG for values outside those noted above and where an angle leaves the range of double (a factor
+ * of 1e-320, say), TQ_ERR_UNSUPPORTED for another head_dim. */
 tq_status tq_rope_build(const tq_rope_params* params, tq_rope_table* table);
 
 /*
@@ -431,8 +432,9 @@ tq_status tq_rope(const tq_context* ctx, const tq_rope_table* table, const void*
  * A ragged batch of new tokens.  Sequence b has the tokens [cu_tokens[b], cu_tokens[b + 1]) of the call's n_tokens
  * rows (device int32 [n_seqs + 1], from 0 on, not decreasing; rows behind cu_tokens[n_seqs] are padding: what they
  * hold has no effect, and in every output they are left as they are) and seq_lens[b] tokens in all (device int32
- * [n_seqs]), the new ones included: its new token i of n sits at position seq_lens[b] - n + i.  block_table (device int32 [n_seqs][max_blocks]) maps
- * page position / page_size of a sequence to a physical page; NULL: sequence b is page b.
+ * [n_seqs]), the new ones included: its new token i of n sits at position seq_lens[b] - n + i.  block_table (device
+ * int32 [n_seqs][max_blocks]) maps page position / page_size of a sequence to a physical page; NULL: sequence b is
+ * page b.
  * max_tokens and max_ctx (host) bound the new tokens and the length of every sequence.  A sequence whose device values
  * break these bounds (more new tokens than max_tokens or than its length, a length above max_ctx, rows outside
  * [0, n_tokens)) is left out of the call: status bit 1 is set, its outputs are zeros (attention, read) or not written
@@ -453,13 +455,13 @@ typedef struct tq_batch {
  * Appends the batch's new keys and values to layer `layer` of the views, keys rotated on the way when `rope` is not
  * NULL (to positions[t], device int32 [n_tokens], or where positions is NULL to the token's position in its sequence).
  * k / v element (t, h, i): k[t * k_token_stride + h * d + i], same type for both, 16-byte aligned, strides multiples
- * of 16 bytes and >= H d.  The rotated key is quantised from fp32 without a rounding in between.  K: Q8_0.  V: Q8_0 or
- * turbo2/3/4_mse.  Other formats return TQ_ERR_UNSUPPORTED (turbo K: tq_rope, then tq_encode_kv).  Values in fp16
- * without a rotation give the bytes of tq_encode_kv for Q8_0.  A NaN element of a Q8_0 vector is stored as 0; an infinite
- * one, or one so large that the fp16 scale overflows (a magnitude of 127 * 65520 or more), gives an infinite scale and
- * codes of 0, which read back as NaN in its block of 32.  A turbo vector with a NaN or an infinite element, or whose norm
- * passes fp16 (65520), reads back as NaN in every coordinate (tq_read_kv, tq_chunk_attention).  A token whose page is
- * out of range is skipped and sets status bit 2.  Two tokens of one call must not share a slot.
+ * of 16 bytes and >= H d.  The rotated key is quantised from fp32 without a rounding in between.  K: Q8_0.  V: Q8_0
+ * or turbo2/3/4_mse.  Other formats return TQ_ERR_UNSUPPORTED (turbo K: tq_rope, then tq_encode_kv).  Values in fp16
+ * without a rotation give the bytes of tq_encode_kv for Q8_0.  A NaN element of a Q8_0 vector is stored as 0; an
+ * infinite one, or one so large that the fp16 scale overflows (a magnitude of 127 * 65520 or more), gives an infinite
+ * scale and codes of 0, which read back as NaN in its block of 32.  A turbo vector with a NaN or an infinite element,
+ * or whose norm passes fp16 (65520), reads back as NaN in every coordinate (tq_read_kv, tq_chunk_attention).  A token
+ * whose page is out of range is skipped and sets status bit 2.  Two tokens of one call must not share a slot.
  */
 tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void* k, int64_t k_token_stride,
                        const void* v, int64_t v_token_stride, tq_dtype dtype, const tq_rope_table* rope,
@@ -477,7 +479,7 @@ tq_status tq_read_kv(const tq_context* ctx, const tq_batch* batch, const tq_cach
 
 /* Changes to the scores of tq_chunk_attention; zeros and NULLs: none. */
 typedef struct tq_score_mods {
-  float softcap;               /* c > 0: s = c tanh(s / c), before the distance bias */
+  float softcap;               /* c > 0: s = c tanh(s / c), before the distance bias; any finite c */
   int32_t window;              /* w > 0: the token at position p sees no key j <= p - w */
   const float* slopes;         /* device float [n_q_heads]: s -= slopes[h] |p - j| */
   const int32_t* first_keys;   /* device int32 [n_tokens]: token t sees no key j < first_keys[t] (packed documents) */
@@ -493,11 +495,16 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
 
 /*
  * Attention of a ragged batch of chunks, one token to thousands per sequence, over the paged cache, whose new tokens
- * are already in it (tq_append_kv).  The token at position p of a sequence of length n sees the keys j < n with
- * j <= p or j < its prefix length, as the score modifications leave them;
+ * are already in it (tq_append_kv).  A decode step over Q8_0 K can take this call or tq_decode_attention.  This one:
+ * one layer a call, as a model runs them (one token at 32K, 8 KV heads of 128, 4 query heads each: 27 us, 37 there;
+ * 64 sequences of 1K to 16K: 145 us, 228 there; turbo4 V 32 and 35, 196 and 207), 16-bit outputs, the score
+ * modifications below. tq_decode_attention: turbo K, Sparse V, or many layers' queries at hand at once (17 and 199 us
+ * a layer).
+ * The token at position p of a sequence of length n sees the keys j < n with j <= p or j < its prefix length, as the
+ * score modifications leave them;
  *   s_j = softmax_scale <q, k_j> (capped, then biased), out = sum_j softmax(s)_j v_j;
- * a row that sees no key gives zeros.  A row that sees a key whose stored K or V has an infinite or NaN scale or norm is
- * NaN in all coordinates; a key that a row does not see never reaches it, whatever is stored there.
+ * a row that sees no key gives zeros.  A row that sees a key whose stored K or V has an infinite or NaN scale or norm
+ * is NaN in all coordinates; a key that a row does not see never reaches it, whatever is stored there.
  *   q: element (t, h, i) at q[t * q_token_stride + h * d + i], type q_dtype, 16-byte aligned, stride a multiple of 16
  *   bytes and >= n_q_heads d.  out: [n_tokens][n_q_heads][d] of type out_dtype, contiguous, 16-byte aligned, apart
  *   from q.
@@ -505,12 +512,15 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
  *   K: Q8_0.  V: Q8_0 or turbo2/3/4_mse.  Others: TQ_ERR_UNSUPPORTED (turbo K: tq_decode_attention,
  *   tq_prefill_attention).
  *   workspace: device, tq_chunk_workspace_bytes() bytes, 256-byte aligned; calls that may overlap need their own.
- * max_tokens chooses the kernel: a batch of at most 16 rows (max_tokens * n_q_heads / n_kv_heads; 8 at head_dim 256) per
- * sequence and KV head takes one that is about twice as fast for them, so a decode step passes max_tokens = 1.
- * The operands of the products are fp16: queries (scaled by a power of two per row, so that no type overflows), keys and
- * values as scale * code (turbo: norm * level), weights; the sums and the softmax are fp32.  Few rows: keys are exact and
- * fp32 queries have 22 bits.  Stored q8_0 scales above 511.5 (values above 64960) are read as 511.5.  The result of a call
- * does not depend on what else runs.  A block-table entry out of range sets status bit 2, and its keys are left out.
+ * max_tokens chooses the kernel: a batch of at most 16 rows (max_tokens * n_q_heads / n_kv_heads; 8 at head_dim 256)
+ * per sequence and KV head takes one that is about twice as fast for them, so a decode step passes max_tokens = 1.
+ * The operands of the products are fp16: queries (scaled by a power of two per row, so that no type overflows), keys
+ * and values as scale * code (turbo: norm * level), weights; the sums and the softmax are fp32.  Few rows: keys are
+ * exact and fp32 queries have 22 bits.  Against fp64, N(0, 1) queries on a cache with 1 % of its channels 20 times
+ * larger (2-norm of all outputs, the output's own rounding included: 2e-4 in fp16, 1.7e-3 in bf16): few rows 3.5e-4
+ * to 4.5e-4, many 5e-4 to 2.0e-3 (fp16 out) and 1.9e-3 to 2.7e-3 (bf16 out).  Stored q8_0 scales above 511.5 (values
+ * above 64960) are read as 511.5.  The result of a call does not depend on what else runs.  A block-table entry out
+ * of range sets status bit 2, and its keys are left out.
  */
 tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const void* q, tq_dtype q_dtype,
                              int64_t q_token_stride, int n_q_heads, const tq_cache_view* k_view,

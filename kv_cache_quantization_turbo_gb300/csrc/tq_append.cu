@@ -3,11 +3,11 @@
 // A CTA takes `tc` consecutive tokens, K or V.  A group of d / 16 lanes holds one vector, 16 consecutive coordinates per
 // lane; its first vector is asked for before anything else.  Meanwhile one warp per token finds the token's sequence and
 // place in the cache, and the CTA computes the rotation's angles once per token for all its heads (16 sincospi per lane
-// and vector instead made a 4096-token chunk of 8 heads of 128 take 23 us; it takes 17, of which the bytes need 4: bound by
+// and vector instead made a 4096-token chunk of 8 heads of 128 take 23 us; it takes 18, of which the bytes need 4: bound by
 // the chain of dependent loads that finds a place, and its two barriers).  From the load to the stored bytes a vector stays
 // in registers: the q8_0 scale of a 32-block is shared by two lanes, the turbo rotation runs four butterfly stages
 // in a lane and log2(d / 16) across the group.  Bytes: both inputs once, the stored vectors once (append), the reverse
-// (read: 10 us for the rows of that chunk).
+// (read: 11 us for the rows of that chunk).
 #include "tq_batch.cuh"
 
 namespace tq {

@@ -54,8 +54,8 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
 }
 
 // The sequences b0 + tid whose threads say refused break their bounds: flagged, and their rows (those that are in range)
-// are zeros, written by the whole block: 0.5 ms for 8192 tokens of 8 heads of 128 in fp32, 8.5 ms from one thread.  Rare: a plan
-// without such a sequence meets one barrier more.
+// are zeros, written by the whole block: 0.5 ms for 8192 tokens of 8 heads of 128 in fp32, 8.5 ms from one thread.
+// Rare: a plan without such a sequence meets one barrier more.
 __device__ __noinline__ void zero_refused(const ChunkArgs& a, int b0, bool refused, uint32_t* refused_of) {
   const int tid = threadIdx.x;
   const uint32_t m = __ballot_sync(kFull, refused);

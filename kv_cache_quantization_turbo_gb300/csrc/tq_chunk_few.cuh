@@ -14,7 +14,7 @@
 // weights are taken against a reference that is raised only when a weight would pass 2^15.
 //
 // What bounds it.  64 sequences of 1K to 16K tokens, 8 KV heads of 128, 4 rows: 147 us for 0.87 GB, 5.9 TB/s, 87 % of the
-// copy bandwidth, at 64 % of the instruction slots (507 instructions per slice, of which 180 turn codes into fp16).  Keys as
+// copy bandwidth, at 64 % of the instruction slots (511 instructions per slice, of which 180 turn codes into fp16).  Keys as
 // the right operand, 8 of 16 rows idle, took 170 us; scales multiplied into K's fragments 149 us, and rounded K: an error of
 // 1.3e-3 instead of 3.6e-4.  Turbo values: more instructions (a lookup by byte permutes) for fewer bytes, 149 us for 48 such
 // sequences, bound by the instruction slots.  One token at 32K: 20 us after the plan, of which the range's 7 slices per

@@ -32,13 +32,21 @@
 // operand) is what the tensor core's full rate asks for; sums are fp32.
 //
 // What bounds it.  Many rows: a tensor instruction of M 128, K 16 takes 65 cycles for any N up to 128 (measured alone), so
-// a tile of two row tiles (32 instructions) takes 2.1 K cycles; it takes 4.9 K, because a warpgroup's softmax of 128 keys,
-// which shares its SM sub-partition's instruction slots with two producer warps, and the products before and after it are
-// a chain (scores and weights share their tensor memory).  Without the softmax the loop runs at 1.56 ms, without softmax
-// and conversion at 1.22 ms, with both at 2.02 ms for a 4096-token chunk at 32K context, 32 query heads of 128 (1.02
-// PFLOP/s).  64-key score products with twice the buffers take the same 65 cycles each for half the keys: 2.15 ms.  Few
-// rows: a tile is 34.8 KB of cache, 1.5 K cycles of this GPU's bandwidth; it takes 3.5 K, bound by the round of a tile
-// through its two buffers.  Entries of up to 16 rows have a kernel of their own (tq_chunk_few.cuh).
+// a tile of two row tiles (32 instructions) takes 2.1 K cycles; it takes 4.9 K.  A row tile's steps follow one another
+// (its scores and weights share one buffer): score product 0.95 K, two softmax parts of 64 keys with 0.4 K around each,
+// value product 0.3 K.  The two row tiles' steps run side by side, so a tile takes as long as one of them, and most of that
+// is the softmax: a part takes 0.43 K cycles alone and 1.0 K beside the producers, which convert every tile again for each
+// entry and share the instruction slots of its SM sub-partition, as do the polls of barriers (5 K of 13.9 K instructions).
+// Without the softmax the loop runs at 1.56 ms, without softmax and conversion at 1.22 ms, with both at 2.03 ms for a
+// 4096-token chunk at 32K context, 32 query heads of 128 (1.02 PFLOP/s).  64-key score products with twice the buffers take
+// the same 65 cycles each for half the keys: 2.15 ms.  Few rows: a tile is 34.8 KB of cache, 1.5 K cycles of this GPU's
+// bandwidth; it takes 3.5 K, bound by the round of a tile through its two buffers.  Entries of up to 16 rows have a kernel
+// of their own (tq_chunk_few.cuh).
+//
+// Error against fp64 (2-norm of all outputs, N(0, 1) queries, 1 % of the channels 20 times larger): 512 tokens at 32K, fp16,
+// 2.0e-3; 4096 tokens, bf16, 2.7e-3, of which the output's type is 1.6e-3; without such channels 5e-4.  Nearly all of it is
+// the rounding of scale * code in K, 2^-12 of each product at most: the scales of a key differ by block of 32, so exact
+// codes would want a score product, and its scores in tensor memory, for each block.
 #pragma once
 
 #include "tq_batch.cuh"

@@ -3,7 +3,7 @@
 // One pass over the data: 2 bytes read and written per fp16 element, so HBM bounds it.  A thread owns P pairs of one
 // head position (P as wide as 16-byte accesses and the pair layout allow) and walks over `hpt` heads of its token, so
 // that the angles are computed once for them: an exact 64-bit fixed-point product and one sincospi per pair.  4096 x 32
-// heads of 128 in bf16: 13.6 us, 4.9 TB/s, 73 % of the copy bandwidth.
+// heads of 128 in bf16: 13.8 us, 4.9 TB/s, 72 % of the copy bandwidth.
 #include "tq_batch.cuh"
 
 namespace tq {
