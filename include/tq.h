@@ -517,7 +517,7 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
  * The operands of the products are fp16: queries (scaled by a power of two per row, so that no type overflows), keys
  * and values as scale * code (turbo: norm * level), weights; the sums and the softmax are fp32.  Few rows: keys are
  * exact and fp32 queries have 22 bits.  Against fp64, N(0, 1) queries on a cache with 1 % of its channels 20 times
- * larger (2-norm of all outputs, the output's own rounding included: 2e-4 in fp16, 1.7e-3 in bf16): few rows 3.5e-4
+ * larger (2-norm of all outputs, the output's own rounding included: 2e-4 in fp16, 1.7e-3 in bf16): few rows 3.3e-4
  * to 4.5e-4, many 5e-4 to 2.0e-3 (fp16 out) and 1.9e-3 to 2.7e-3 (bf16 out).  Stored q8_0 scales above 511.5 (values
  * above 64960) are read as 511.5.  The result of a call does not depend on what else runs.  A block-table entry out
  * of range sets status bit 2, and its keys are left out.

@@ -546,7 +546,7 @@ def tq_rope_build(head_dim: int, rotary_dim: int | None = None, layout="half", s
 def tq_rope(ctx: int, table: tq_rope_table, x, positions, out, inverse: bool = False, stream=None) -> int:
     """x, out: [tokens, heads, d] tensors of one type (out may be x); positions: int32 [tokens]."""
     shape = x.shape
-    if out.shape != shape or out.dtype != x.dtype or shape[-1] != table.head_dim:
+    if len(shape) != 3 or out.shape != shape or out.dtype != x.dtype or shape[-1] != table.head_dim:
         raise ValueError(f"x {tuple(shape)} {x.dtype}, out {tuple(out.shape)} {out.dtype}")
     return _lib.tq_rope(ctx, ctypes.byref(table), x.data_ptr(), _dtype(x), shape[0], shape[1], _rows(x, shape),
                         _positions(positions, shape[0]), int(inverse), out.data_ptr(), _rows(out, shape),
@@ -570,6 +570,8 @@ def tq_read_kv(ctx: int, batch: Batch, k_view, k_out, v_view, v_out, layer: int,
     """k_out, v_out: contiguous [n_tokens, H, d] tensors of one type; a pair may be None."""
     outs = [(view, t) for view, t in ((k_view, k_out), (v_view, v_out)) if t is not None]
     for view, t in outs:
+        if view is None:
+            raise ValueError("an output without the view it is read from")
         if t.shape != (batch.n_tokens, view.n_kv_heads, view.head_dim) or not t.is_contiguous() or not t.is_cuda or \
                 t.dtype != outs[0][1].dtype:
             raise ValueError(f"output {tuple(t.shape)} {t.dtype} for {batch.n_tokens} tokens")

@@ -214,3 +214,12 @@ def test_few_rows_take_fp32_queries_in_more_bits_than_fp16(ctxs, d, G):  # noqa:
     w /= w.sum(-1, keepdims=True)
     noise = np.einsum("ght,t->gh", w ** 2, 2 * (2.0 ** -22 / 3) * (vv[:, 0] ** 2).sum(-1))  # as in row_bound
     K.assert_rows(T.f64(out), want, np.maximum(6 * np.sqrt(noise) / np.linalg.norm(want, axis=-1), T.C.ATTN_RTOL))
+
+
+def test_read_refuses_an_output_without_a_view(ctxs):  # noqa: F811
+    P = T.Paged(ctxs[64], 64, 1, [2], [5], 16)
+    out = torch.zeros((2, 1, 64), device="cuda")
+    for views in ((None, out, P.vv, out), (P.kv, out, None, out)):
+        with pytest.raises(ValueError):
+            T.tq.tq_read_kv(P.ctx.h, P.batch, *views, 0)
+    assert not out.any()

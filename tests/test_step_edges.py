@@ -22,3 +22,12 @@ def test_rope_table_refuses_angles_without_a_number(kw):
 def test_rope_table_takes_factors_far_from_one(kw):
     t = tq.tq_rope_build(128, **kw)
     assert t.attn_factor == 1.0 and all(t.turns[i] == 0 for i in range(64, 128))
+
+
+def test_rope_refuses_tensors_of_other_ranks():
+    torch = pytest.importorskip("torch")
+    t = tq.tq_rope_build(64)
+    for shape in ((64,), (2, 64), (1, 2, 3, 64)):
+        x = torch.zeros(shape)
+        with pytest.raises(ValueError):
+            tq.tq_rope(0, t, x, torch.zeros(shape[0], dtype=torch.int32), x)
