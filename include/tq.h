@@ -79,7 +79,8 @@ typedef enum tq_format {
   TQ_FMT_TURBO3_MSE = 4,
   TQ_FMT_TURBO4_MSE = 5,
   TQ_FMT_Q8_0 = 6,
-  TQ_FMT_MINMAX = 7
+  TQ_FMT_MINMAX = 7,
+  TQ_FMT_F8_BLOCK = 8 /* e4m3 with a scale per 16 tokens and head (tq_append_kv, tq_read_kv, tq_chunk_attention) */
 } tq_format;
 
 /*
@@ -95,11 +96,17 @@ typedef enum tq_format {
  *   q8_0: payload = d int8 values; header = d/32 fp16 scales (block order).
  *   minmax: codes of `bits` bits packed as for turbo; header = d/64 pairs
  *     {fp16 scale, fp16 zero} (group order).
+ *   f8_block: payload = d e4m3 codes (1 sign, 4 exponent, 3 mantissa bits, largest value 448); the header belongs to a
+ *     block of 16 vectors, the tokens [16 k, 16 k + 16) of a page (page_size is a multiple of 16): one 32-bit word
+ *     2^e as fp32, -80 <= e <= 80, whose low 16 bits mark tokens: bit i of a marked token i, every coordinate of which
+ *     reads back as NaN.  A value is code * 2^e.  The codes 0x7F and 0xFF (NaN) are never written; where a cache that
+ *     was filled in another way holds them, what is read from it is not specified.
  *
  * Cache view: a 4-D array of vectors [n_layers][num_pages][n_kv_heads][page_size].
  * The vector at (layer, page, head, p) has index
  *     v = ((layer * num_pages + page) * n_kv_heads + head) * page_size + p
- * and lives at payload + v * tq_payload_bytes(), header + v * tq_header_bytes().
+ * and lives at payload + v * tq_payload_bytes(), header + v * tq_header_bytes() (f8_block: header + v / 16 * 4, the
+ * word of its block).
  * Token slot t of a layer means page = t / page_size, p = t % page_size, so a
  * contiguous cache of capacity C per sequence is the view with page_size = C
  * and page = sequence index (block_table = NULL in tq_decode_attention).
@@ -122,9 +129,12 @@ typedef struct tq_context tq_context;
 
 const char* tq_status_string(tq_status s);
 const char* tq_format_name(tq_format f);
-/* Payload / header bytes of one vector; 0 for an invalid (format, head_dim, bits). */
+/* Payload / header bytes of one vector; 0 for an invalid (format, head_dim, bits).  An f8_block vector has no header of
+ * its own: tq_header_bytes() is 0 for it. */
 size_t tq_payload_bytes(tq_format f, int head_dim, int bits);
 size_t tq_header_bytes(tq_format f, int head_dim, int bits);
+/* Bytes of a view's whole header array (the pointers are not looked at); 0 for an invalid view. */
+size_t tq_view_header_bytes(const tq_cache_view* view);
 /* payload + header, the compressed bytes of one vector. */
 size_t tq_vector_bytes(tq_format f, int head_dim, int bits);
 
@@ -200,7 +210,9 @@ tq_status tq_get_status(tq_context* ctx, uint32_t* flags);
  * slot_begin + t; a slot outside [0, num_pages * page_size) is skipped and
  * flagged.  K views take any format except the _MSE ones; V views take any
  * format; both views must share head_dim and n_kv_heads with the context's d.
- * Turbo K: stage 1 + QJL; turbo _MSE: stage 1; Q8_0; MINMAX.
+ * Turbo K: stage 1 + QJL; turbo _MSE: stage 1; Q8_0; MINMAX.  F8_BLOCK:
+ * TQ_ERR_UNSUPPORTED (its blocks are filled in the order of a sequence:
+ * tq_append_kv).
  */
 tq_status tq_encode_kv(const tq_context* ctx,
                        const tq_cache_view* k_view, const void* k,
@@ -429,6 +441,54 @@ tq_status tq_rope(const tq_context* ctx, const tq_rope_table* table, const void*
                   int64_t out_token_stride, tq_stream_t stream);
 
 /*
+ * Norms of queries and keys per head, and the rotation, in the same pass.  Of each vector x (token t, head h), in fp32:
+ *   r = 1 / sqrt(sum_i x_i^2 / d + eps),  y_i = r x_i weight[i],  out = y rotated as by tq_rope
+ * over all d coordinates, the ones that are not rotated among them.  q and k describe the rows of the queries and of the
+ * keys: either may be NULL (not both), each has its own weight (device [d] of type weight_dtype, any alignment of an
+ * element; NULL: ones), heads and strides; x and out are as in tq_rope (out may be x with the same stride; other overlaps
+ * are not allowed, nor between the two).  eps > 0, 2^-126 at least.  A vector whose squares pass the range of fp32 is
+ * normed all the same; one with a NaN or an infinity gives what the formula gives in fp32: NaN in those coordinates (with a
+ * NaN, in all) and 0 in the others.  Errors as tq_rope.
+ */
+typedef struct tq_norm_rows {
+  const void* x;             /* element (t, h, i) at t * x_token_stride + h * d + i */
+  int64_t x_token_stride;    /* elements, >= n_heads * d, a multiple of 16 bytes */
+  void* out;
+  int64_t out_token_stride;
+  const void* weight;
+  int32_t n_heads;           /* >= 1 */
+} tq_norm_rows;
+
+tq_status tq_norm_rope(const tq_context* ctx, const tq_rope_table* table, const tq_norm_rows* q, const tq_norm_rows* k,
+                       tq_dtype dtype, tq_dtype weight_dtype, float eps, int n_tokens, const int32_t* positions,
+                       tq_stream_t stream);
+
+/*
+ * The gradient of tq_norm_rope.  With g = dout rotated back (its transpose, attn_factor included) and x' = r x:
+ *   dx_i = r (g_i weight[i] - x'_i sum_j(g_j weight[j] x'_j) / d),  dweight[i] = sum over tokens and heads of g_i x'_i.
+ * x, dout and dx are of type dtype (dx may be dout with the same stride); dweight is device float [d], 4-byte aligned,
+ * written and not added to, NULL where it is not wanted.  Sums are fp32, the last ones over partial results fp64, in an
+ * order that depends on the sizes alone.  workspace: device, tq_norm_rope_grad_workspace_bytes() bytes, 256-byte aligned
+ * (TQ_ERR_WORKSPACE); calls that may overlap need their own.  n_heads: the heads of q and k together.
+ */
+typedef struct tq_norm_grad_rows {
+  const void* x;
+  int64_t x_token_stride;
+  const void* dout;
+  int64_t dout_token_stride;
+  const void* weight;
+  void* dx;
+  int64_t dx_token_stride;
+  float* dweight;
+  int32_t n_heads;
+} tq_norm_grad_rows;
+
+size_t tq_norm_rope_grad_workspace_bytes(const tq_context* ctx, int n_tokens, int n_heads);
+tq_status tq_norm_rope_grad(const tq_context* ctx, const tq_rope_table* table, const tq_norm_grad_rows* q,
+                            const tq_norm_grad_rows* k, tq_dtype dtype, tq_dtype weight_dtype, float eps, int n_tokens,
+                            const int32_t* positions, void* workspace, size_t workspace_bytes, tq_stream_t stream);
+
+/*
  * A ragged batch of new tokens.  Sequence b has the tokens [cu_tokens[b], cu_tokens[b + 1]) of the call's n_tokens
  * rows (device int32 [n_seqs + 1], from 0 on, not decreasing; rows behind cu_tokens[n_seqs] are padding: what they
  * hold has no effect, and in every output they are left as they are) and seq_lens[b] tokens in all (device int32
@@ -456,12 +516,21 @@ typedef struct tq_batch {
  * NULL (to positions[t], device int32 [n_tokens], or where positions is NULL to the token's position in its sequence).
  * k / v element (t, h, i): k[t * k_token_stride + h * d + i], same type for both, 16-byte aligned, strides multiples
  * of 16 bytes and >= H d.  The rotated key is quantised from fp32 without a rounding in between.  K: Q8_0.  V: Q8_0
- * or turbo2/3/4_mse.  Other formats return TQ_ERR_UNSUPPORTED (turbo K: tq_rope, then tq_encode_kv).  Values in fp16
+ * or turbo2/3/4_mse; or F8_BLOCK for both.  Others return TQ_ERR_UNSUPPORTED (turbo K: tq_rope, then tq_encode_kv).  Values in fp16
  * without a rotation give the bytes of tq_encode_kv for Q8_0.  A NaN element of a Q8_0 vector is stored as 0; an
  * infinite one, or one so large that the fp16 scale overflows (a magnitude of 127 * 65520 or more), gives an infinite
  * scale and codes of 0, which read back as NaN in its block of 32.  A turbo vector with a NaN or an infinite element,
  * or whose norm passes fp16 (65520), reads back as NaN in every coordinate (tq_read_kv, tq_chunk_attention).  A token
  * whose page is out of range is skipped and sets status bit 2.  Two tokens of one call must not share a slot.
+ *
+ * F8_BLOCK: the positions [16 k, 16 k + 16) of a sequence are a block, with a scale for each head.  Of the new vectors
+ * (keys rotated) that go to it, those with a NaN, an infinity or a magnitude above 448 * 2^80 are marked, with codes of
+ * 0.  e is the smallest integer with max |x| <= 448 * 2^e over the others, -80 at least, and at least the block's e
+ * so far where the block holds earlier tokens of the sequence (positions before the new ones); where that raises e, the
+ * earlier tokens' codes become the e4m3 values nearest to code * 2^(e_before - e), which is exact unless the value falls
+ * below 2^-6 * 2^e.  A new code is the e4m3 value nearest to x / 2^e (a tie goes to the even one).  So the stored values
+ * depend on what was appended in which calls, not on timing; a block that two sequences share must be full, or not
+ * be appended to.
  */
 tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void* k, int64_t k_token_stride,
                        const void* v, int64_t v_token_stride, tq_dtype dtype, const tq_rope_table* rope,
@@ -471,7 +540,8 @@ tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void*
 /*
  * Reads the batch's rows back from layer `layer`: k_out and v_out [n_tokens][H][d] of type dtype, contiguous, 16-byte
  * aligned, in the original space (K as stored, its rotation kept).  Either pair may be NULL, not both.  With
- * cu_tokens covering whole sequences this gathers them.  Formats: Q8_0 and turbo2/3/4_mse; others TQ_ERR_UNSUPPORTED.
+ * cu_tokens covering whole sequences this gathers them.  Formats: Q8_0, turbo2/3/4_mse and F8_BLOCK; others
+ * TQ_ERR_UNSUPPORTED.
  * Tokens whose page is out of range give zeros and status bit 2.
  */
 tq_status tq_read_kv(const tq_context* ctx, const tq_batch* batch, const tq_cache_view* k_view, void* k_out,
@@ -485,6 +555,8 @@ typedef struct tq_score_mods {
   const int32_t* first_keys;   /* device int32 [n_tokens]: token t sees no key j < first_keys[t] (packed documents) */
   const int32_t* prefix_lens;  /* device int32 [n_seqs]: the keys j < prefix_lens[b] of sequence b are seen by all its
                                   tokens, before or after them (the window and first_keys still apply) */
+  int32_t sinks;               /* s > 0: the window hides no key j < f + s, f = first_keys[t] (0 without first_keys, and
+                                  where that is negative): the first tokens stay visible.  Without a window: no effect */
 } tq_score_mods;
 
 /*
@@ -492,6 +564,13 @@ typedef struct tq_score_mods {
  * invalid arguments.
  */
 size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, int n_q_heads, int n_kv_heads);
+
+/*
+ * The workspace with which tq_chunk_attention runs these views and modifications (may be NULL) fastest; never less than
+ * tq_chunk_workspace_bytes(), with which every call runs.  0 for invalid arguments.
+ */
+size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int n_q_heads, const tq_cache_view* k_view,
+                              const tq_cache_view* v_view, const tq_score_mods* mods);
 
 /*
  * Attention of a ragged batch of chunks, one token to thousands per sequence, over the paged cache, whose new tokens
@@ -509,8 +588,9 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
  *   bytes and >= n_q_heads d.  out: [n_tokens][n_q_heads][d] of type out_dtype, contiguous, 16-byte aligned, apart
  *   from q.
  *   Query head h reads KV head h / (n_q_heads / n_kv_heads); n_q_heads a multiple of n_kv_heads.
- *   K: Q8_0.  V: Q8_0 or turbo2/3/4_mse.  Others: TQ_ERR_UNSUPPORTED (turbo K: tq_decode_attention,
- *   tq_prefill_attention).
+ *   K: Q8_0 with V: Q8_0 or turbo2/3/4_mse; or F8_BLOCK for both.  Others: TQ_ERR_UNSUPPORTED (turbo K:
+ *   tq_decode_attention, tq_prefill_attention).  F8_BLOCK codes are fp16 numbers: keys and values are not rounded, and a
+ *   block's scale goes to its scores and weights.
  *   workspace: device, tq_chunk_workspace_bytes() bytes, 256-byte aligned; calls that may overlap need their own.
  * max_tokens chooses the kernel: a batch of at most 16 rows (max_tokens * n_q_heads / n_kv_heads; 8 at head_dim 256)
  * per sequence and KV head takes one that is about twice as fast for them, so a decode step passes max_tokens = 1.
@@ -536,7 +616,7 @@ tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const
  * (device int64 [n]) or slot_begin + t.  Turbo: n diag(s) H c[idx], plus for K
  * formats with include_qjl != 0 the QJL vector-form residual
  * diag(s) H (rnorm sqrt(pi/2)/d S^T (2 sigma - 1)).  Q8_0: q * scale.
- * MINMAX: q * scale + zero.  Skipped (out-of-range) slots are written as zeros.
+ * MINMAX: q * scale + zero.  F8_BLOCK: code * 2^e.  Skipped (out-of-range) slots are written as zeros.
  */
 tq_status tq_dequantize(const tq_context* ctx, const tq_cache_view* view, int layer,
                         const int64_t* slots, int64_t slot_begin, int n,

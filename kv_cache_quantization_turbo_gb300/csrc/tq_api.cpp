@@ -27,13 +27,14 @@ bool format_has_qjl(int f) { return f >= TQ_FMT_TURBO2 && f <= TQ_FMT_TURBO4; }
 
 // Stage-1 index bits of a turbo format ("TurboQuant+ KV cache compression",
 // format table: turbo2/3/4 = 1/2/3 bits + 1 QJL bit; the _MSE forms drop the
-// QJL bit), the min-max bit width, or 8 for q8_0.
+// QJL bit), the min-max bit width, or 8 for q8_0 and f8_block.
 int format_idx_bits(int f, int minmax_bits) {
   switch (f) {
     case TQ_FMT_TURBO2: case TQ_FMT_TURBO2_MSE: return 1;
     case TQ_FMT_TURBO3: case TQ_FMT_TURBO3_MSE: return 2;
     case TQ_FMT_TURBO4: case TQ_FMT_TURBO4_MSE: return 3;
     case TQ_FMT_Q8_0: return 8;
+    case TQ_FMT_F8_BLOCK: return 8;
     case TQ_FMT_MINMAX: return (minmax_bits >= 2 && minmax_bits <= 4) ? minmax_bits : 0;
     default: return 0;
   }
@@ -50,6 +51,7 @@ bool make_dev_view(const tq_cache_view* v, DevView* o) {
     return false;
   if ((reinterpret_cast<uintptr_t>(v->payload) & 15) || (reinterpret_cast<uintptr_t>(v->header) & 3))
     return false;
+  if (f == TQ_FMT_F8_BLOCK && v->page_size % kF8Block) return false;
   o->format = f;
   o->d = v->head_dim;
   o->H = v->n_kv_heads;
@@ -63,7 +65,7 @@ bool make_dev_view(const tq_cache_view* v, DevView* o) {
   o->hdr_bytes = (int)tq_header_bytes((tq_format)f, v->head_dim, v->bits);
   o->payload = static_cast<unsigned char*>(v->payload);
   o->header = static_cast<unsigned char*>(v->header);
-  return o->pay_bytes > 0 && o->hdr_bytes > 0;
+  return o->pay_bytes > 0 && (o->hdr_bytes > 0 || f == TQ_FMT_F8_BLOCK);
 }
 
 }  // namespace tq
@@ -92,6 +94,7 @@ const char* tq_format_name(tq_format f) {
     case TQ_FMT_TURBO4_MSE: return "turbo4_mse";
     case TQ_FMT_Q8_0: return "q8_0";
     case TQ_FMT_MINMAX: return "minmax";
+    case TQ_FMT_F8_BLOCK: return "f8_block";
   }
   return "unknown";
 }
@@ -99,7 +102,7 @@ const char* tq_format_name(tq_format f) {
 size_t tq_payload_bytes(tq_format f, int head_dim, int bits) {
   const int b = format_idx_bits(f, bits);
   if (b == 0 || head_dim < 64 || (head_dim & (head_dim - 1)) || head_dim > kMaxDim) return 0;
-  if (f == TQ_FMT_Q8_0) return (size_t)head_dim;
+  if (f == TQ_FMT_Q8_0 || f == TQ_FMT_F8_BLOCK) return (size_t)head_dim;
   const int w = format_is_turbo(f) ? b + (format_has_qjl(f) ? 1 : 0) : b;
   return (size_t)head_dim * w / 8;
 }
@@ -108,7 +111,17 @@ size_t tq_header_bytes(tq_format f, int head_dim, int bits) {
   if (tq_payload_bytes(f, head_dim, bits) == 0) return 0;
   if (f == TQ_FMT_Q8_0) return (size_t)head_dim / 32 * 2;
   if (f == TQ_FMT_MINMAX) return (size_t)head_dim / 64 * 4;
+  if (f == TQ_FMT_F8_BLOCK) return 0;
   return format_has_qjl(f) ? 4 : 2;
+}
+
+size_t tq_view_header_bytes(const tq_cache_view* v) {
+  if (!v || v->n_kv_heads < 1 || v->page_size < 1 || v->num_pages < 1 || v->n_layers < 1 ||
+      tq_payload_bytes((tq_format)v->format, v->head_dim, v->bits) == 0)
+    return 0;
+  const size_t n = (size_t)v->n_layers * (size_t)v->num_pages * (size_t)v->n_kv_heads * (size_t)v->page_size;
+  if (v->format == TQ_FMT_F8_BLOCK) return v->page_size % kF8Block ? 0 : n / kF8Block * sizeof(uint32_t);
+  return n * tq_header_bytes((tq_format)v->format, v->head_dim, v->bits);
 }
 
 size_t tq_vector_bytes(tq_format f, int head_dim, int bits) {
@@ -383,6 +396,7 @@ tq_status tq_encode_kv(const tq_context* ctx, const tq_cache_view* k_view, const
   if ((reinterpret_cast<uintptr_t>(k) & 15) || (reinterpret_cast<uintptr_t>(v) & 15) || (in_token_stride & 7) ||
       (n_layers > 1 && (in_layer_stride & 7)))
     return TQ_ERR_INVALID_ARG;
+  if ((k_view && kv.format == TQ_FMT_F8_BLOCK) || (v_view && vv.format == TQ_FMT_F8_BLOCK)) return TQ_ERR_UNSUPPORTED;
   if (n_layers == 0 || n_tokens == 0) return TQ_OK;
   if ((int64_t)n_layers * n_tokens * H >= (int64_t(1) << 32)) return TQ_ERR_UNSUPPORTED;  // split the call
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -466,7 +480,8 @@ tq_status tq_decode_attention(const tq_context* ctx, const void* q, int q_is_fp1
 // per-layer views (a format per layer, e.g. Boundary V)
 // ---------------------------------------------------------------------------
 
-// The view of one layer: the view with its arrays advanced to layer `layer` and n_layers = 1.
+// The view of one layer: the view with its arrays advanced to layer `layer` and n_layers = 1 (not for f8_block, which the
+// calls over per-layer views refuse).
 static bool layer_view(const tq_cache_view* v, int layer, int run, DevView* out) {
   if (!make_dev_view(v, out) || layer < 0 || run < 1 || layer + run > out->n_layers) return false;
   const long long vecs = (long long)out->num_pages * out->H * out->page_size;
@@ -502,7 +517,9 @@ tq_status tq_encode_kv_layers(const tq_context* ctx, const tq_cache_view* k_view
   for (int l = 0; l < n_layers; ++l) {
     DevView dv{};
     if (k_views && !layer_view(&k_views[l], k_view_layers[l], 1, &dv)) return TQ_ERR_INVALID_ARG;
+    if (k_views && dv.format == TQ_FMT_F8_BLOCK) return TQ_ERR_UNSUPPORTED;
     if (v_views && !layer_view(&v_views[l], v_view_layers[l], 1, &dv)) return TQ_ERR_INVALID_ARG;
+    if (v_views && dv.format == TQ_FMT_F8_BLOCK) return TQ_ERR_UNSUPPORTED;
   }
   const size_t esz = 2;  // fp16 inputs
   for (int l = 0; l < n_layers;) {

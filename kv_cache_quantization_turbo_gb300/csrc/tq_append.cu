@@ -8,57 +8,12 @@
 // in registers: the q8_0 scale of a 32-block is shared by two lanes, the turbo rotation runs four butterfly stages
 // in a lane and log2(d / 16) across the group.  Bytes: both inputs once, the stored vectors once (append), the reverse
 // (read: 11 us for the rows of that chunk).
-#include "tq_batch.cuh"
+#include "tq_append.cuh"
 
 namespace tq {
 namespace {
 
 constexpr int kApThreads = 256;
-constexpr int kE = 16;     // coordinates per lane
-constexpr int kMaxTc = 16;  // tokens per CTA
-
-struct Launch {
-  AppendArgs a;
-  int tc;
-};
-
-// A token's place: the vector of (position, head 0), -1: nothing to do there; pos: its position in the sequence.
-struct Place {
-  long long vec;
-  int pos;
-  bool padding;  // behind the last sequence
-};
-
-// Called by a whole warp.
-__device__ __forceinline__ Place find_place(const AppendArgs& a, const DevView& v, int t, int lane, bool report) {
-  Place p{-1, 0, true};
-  if (t >= a.b.n_tokens) return p;
-  // the sequence with cu[b] <= t < cu[b + 1]: 32 probes at a time of a shrinking range [lo, hi)
-  int lo = 0, hi = a.b.n_seqs;
-  while (lo < hi) {
-    const int step = (hi - lo + 31) >> 5, at = min(lo + step * (lane + 1), hi) - 1;  // ends of 32 parts
-    const uint32_t above = __ballot_sync(kFull, __ldg(a.b.cu + at + 1) > t);
-    if (!above) {
-      lo = hi = a.b.n_seqs;
-      break;
-    }
-    const int k = __ffs(above) - 1;
-    const int end = min(lo + step * (k + 1), hi);
-    lo += step * k;
-    hi = step == 1 ? lo : end;
-  }
-  if (lo >= a.b.n_seqs || __ldg(a.b.cu + lo) > t) return p;
-  p.padding = false;
-  const SeqOf s = seq_of(a.b, lo);
-  if (!s.ok) {
-    if (report && lane == 0) atomicOr(a.tab.status, kFlagSeqLen);
-    return p;
-  }
-  p.pos = s.len - s.n + (t - s.first);
-  p.vec = position_vector(a.b, v, a.layer, lo, p.pos);
-  if (p.vec < 0 && report && lane == 0) atomicOr(a.tab.status, kFlagBlockTable);
-  return p;
-}
 
 // H x / sqrt(D) of a vector held by a group, unscaled: lane `sub` owns coordinates [16 sub, 16 sub + 16).
 template <int D>
@@ -190,9 +145,6 @@ __device__ __forceinline__ void store_turbo(float (&x)[kE], const float (&bnd)[7
   if (sub == 0) *reinterpret_cast<__half*>(hdr) = __float2half_rn(n);
 }
 
-// Angle p of a token's table, padded so that the lanes of a group read different banks.
-__device__ __forceinline__ int angle_at(int p) { return p + (p >> 4) * 4; }
-
 template <class T, int D, int VB>  // VB: 0 q8_0 values, else turbo-MSE index bits
 __global__ void __launch_bounds__(kApThreads, VB == 0 ? 4 : 2) append_kernel(const __grid_constant__ Launch L) {
   constexpr int LPV = D / kE, GROUPS = kApThreads / LPV, ANG = D / 2 + D / 8;
@@ -227,7 +179,6 @@ __global__ void __launch_bounds__(kApThreads, VB == 0 ? 4 : 2) append_kernel(con
   const tq_rope_table& R = L.a.rope;
   const int half = R.rotary_dim / 2;
   const bool turn = !is_v && L.a.has_rope;
-  const bool interleaved = R.layout == TQ_ROPE_INTERLEAVED;
   if (turn) {
     for (int i = tid; i < n_tok * half; i += kApThreads) {
       const int k = i / half, p = i - k * half;
@@ -260,56 +211,9 @@ __global__ void __launch_bounds__(kApThreads, VB == 0 ? 4 : 2) append_kernel(con
       const int tt = on ? t : 0;
       float x[kE];
       load_row<kE>(reinterpret_cast<const T*>(raw[u]), x);
-      if (turn) {
-        if (interleaved) {
-#pragma unroll
-          for (int i = 0; i < kE; i += 2) {
-            const int e = 16 * sub + i;
-            if (e < R.rotary_dim) {
-              const float c = cs[tt][angle_at(e >> 1)], s = sn[tt][angle_at(e >> 1)], a = x[i], b = x[i + 1];
-              x[i] = a * c - b * s;
-              x[i + 1] = a * s + b * c;
-            }
-          }
-        } else if (half % kE == 0) {  // the partners of the lane's coordinates: those of one other lane
-          const bool rot = 16 * sub < R.rotary_dim, first = 16 * sub < half;
-          const int from = rot ? (first ? half / kE : -half / kE) : 0;
-          uint4 other[W];
-#pragma unroll
-          for (int k = 0; k < W; ++k) {
-            other[k].x = __shfl_sync(kFull, raw[u][k].x, lane + from);
-            other[k].y = __shfl_sync(kFull, raw[u][k].y, lane + from);
-            other[k].z = __shfl_sync(kFull, raw[u][k].z, lane + from);
-            other[k].w = __shfl_sync(kFull, raw[u][k].w, lane + from);
-          }
-          if (rot) {
-            float y[kE];
-            load_row<kE>(reinterpret_cast<const T*>(other), y);
-            const int p0 = angle_at(first ? 16 * sub : 16 * sub - half);
-#pragma unroll
-            for (int i = 0; i < kE; i += 4) {
-              const float4 c = *reinterpret_cast<const float4*>(&cs[tt][p0 + i]);
-              const float4 s = *reinterpret_cast<const float4*>(&sn[tt][p0 + i]);
-              const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x[i + k] = fmaf(cc[k], x[i + k], (first ? -ss[k] : ss[k]) * y[i + k]);
-            }
-          }
-        } else if (on) {  // borders of the halves inside lanes
-          const T* row = in + (long long)t * stride + (long long)h * D;
-#pragma unroll
-          for (int i = 0; i < kE; ++i) {
-            const int e = 16 * sub + i;
-            if (e < R.rotary_dim) {
-              const bool first = e < half;
-              float y[1];
-              load_row<1>(row + i + (first ? half : -half), y);
-              const int pr = angle_at(first ? e : e - half);
-              x[i] = fmaf(cs[t][pr], x[i], (first ? -sn[t][pr] : sn[t][pr]) * y[0]);
-            }
-          }
-        }
-      }
+      if (turn)
+        turn_part<T, D>(x, raw[u], [&] { return in + (long long)t * stride + (long long)h * D; }, R, cs[tt], sn[tt], sub,
+                        lane, on);
       const long long vec = p.vec + (long long)h * V.page_size;
       unsigned char* pay = V.payload + vec * V.pay_bytes;
       unsigned char* hdr = V.header + vec * V.hdr_bytes;
@@ -378,20 +282,6 @@ __global__ void __launch_bounds__(kApThreads) read_kernel(const __grid_constant_
     }
     if (in_range && !p.padding) store_row<kE>(out + ((long long)(t0 + t) * H + h) * D + 16 * sub, x);
   }
-}
-
-// Tokens per CTA: as many, up to 16, as leave a CTA of each half for every SM (a decode batch takes one token each, the
-// shortest chain; a chunk shares places and angles: 16 instead of 8 tokens are 16 us instead of 19 for 1.7K tokens of 8
-// heads of 64, and the same 17 us for 4096 tokens of 8 heads of 128).
-template <class F>
-cudaError_t with_launch(const AppendArgs& a, int sm_count, F run) {
-  Launch L{};
-  L.a = a;
-  int tc = 1;
-  while (tc < kMaxTc && a.b.n_tokens / (tc * 2) >= sm_count) tc *= 2;
-  L.tc = tc;
-  run(L, (unsigned)((a.b.n_tokens + tc - 1) / tc));
-  return cudaGetLastError();
 }
 
 template <class T, int D>

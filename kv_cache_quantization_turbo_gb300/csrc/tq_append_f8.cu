@@ -1,0 +1,256 @@
+// Appending to and reading from an f8_block cache: e4m3 codes with a power-of-two scale for each 16 tokens and head.
+//
+// A block takes part in an append as a whole: its scale is the maximum over its new vectors and what it had.  The CTA
+// whose rows hold a block's first new token takes the block, K or V, and a warp at a time one of its heads: the up to 16
+// vectors go to registers once, 16 coordinates per lane (d / 16 lanes to a vector), are rotated, give the maximum by
+// shuffles, and leave as codes.  Where the scale rises and the block holds earlier tokens, their codes are read, brought
+// to the new scale and written back; a power of two makes that exact but for values that fall below the smallest normal
+// code, so a block can be appended to token by token without losing bits each time.
+#include <cuda_fp8.h>
+
+#include "tq_append.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kF8Threads = 256, kF8Warps = kF8Threads / 32;
+constexpr uint32_t kTooLarge = 0x6BE00000u;  // 448 * 2^80 as fp32: what is above, infinities and NaN are marked
+
+// A block's part in the call: the slot of its first token (head 0), its first new row, the number of new tokens (0: the
+// CTA's row begins no block) and the offset of the first.
+struct Part {
+  long long vec;
+  int row, n, off, pos;
+};
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+__device__ __forceinline__ void values4(uint32_t w, float (&x)[4]) {
+  const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3)));
+  const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3)));
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kF8Threads, D == 256 ? 1 : 2) append_f8_kernel(const __grid_constant__ Launch L) {
+  constexpr int LPV = D / kE, VPP = 32 / LPV, NP = kF8Block / VPP;  // lanes per vector, vectors per pass, passes
+  constexpr int ANG = D / 2 + D / 8, W = kE * sizeof(T) / 16;
+  __shared__ Part part[kMaxTc];
+  __shared__ __align__(16) float cs[kF8Block][ANG], sn[kF8Block][ANG];
+  const AppendArgs& a = L.a;
+  const bool is_v = blockIdx.y != 0;
+  const DevView& V = is_v ? a.v : a.k;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % LPV, g = lane / LPV;
+  const int t0 = blockIdx.x * L.tc, H = V.H, n_tok = min(L.tc, a.b.n_tokens - t0);
+  const long long stride = is_v ? a.v_stride : a.k_stride;
+  const T* in = static_cast<const T*>(is_v ? a.xv : a.xk) + 16 * sub;
+  for (int k = warp; k < n_tok; k += kF8Warps) {
+    SeqOf s{};
+    const Place p = find_row(a, V, t0 + k, lane, !is_v, s);
+    if (lane == 0) {
+      const int off = p.pos % kF8Block;
+      Part q{p.vec - off, t0 + k, 0, off, p.pos};
+      if (p.vec >= 0 && (off == 0 || t0 + k == s.first)) q.n = min(kF8Block - off, s.first + s.n - (t0 + k));
+      part[k] = q;
+    }
+  }
+  __syncthreads();
+  const tq_rope_table& R = a.rope;
+  const int half = R.rotary_dim / 2;
+  const bool turn = !is_v && a.has_rope;
+  for (int k = 0; k < n_tok; ++k) {
+    const Part q = part[k];
+    if (q.n == 0) continue;  // (the CTA's threads alike)
+    if (turn) {
+      __syncthreads();  // the angles of the block before have been used
+      for (int i = tid; i < q.n * half; i += kF8Threads) {
+        const int j = i / half, p = i - j * half;
+        const float2 f = rope_at(R.turns[p], a.positions ? __ldg(a.positions + q.row + j) : q.pos + j, R.attn_factor);
+        cs[j][angle_at(p)] = f.x;
+        sn[j][angle_at(p)] = f.y;
+      }
+      __syncthreads();
+    }
+    for (int h = warp; h < H; h += kF8Warps) {
+      const long long vec = q.vec + (long long)h * V.page_size;  // a multiple of 16
+      uint32_t* word = reinterpret_cast<uint32_t*>(V.header) + vec / kF8Block;
+      uint4* pay = reinterpret_cast<uint4*>(V.payload + vec * D) + sub;  // vector i of the block: LPV i further on
+      const T* src = in + (long long)q.row * stride + (long long)h * D;
+      const uint32_t before = q.off ? *word : 0u;
+      uint4 raw[NP][W];
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int j = p * VPP + g;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          raw[p][w] = j < q.n ? __ldg(reinterpret_cast<const uint4*>(src + (long long)j * stride) + w)
+                              : make_uint4(0u, 0u, 0u, 0u);
+      }
+      float x[NP][kE];
+      uint32_t top = 0, marks = 0;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int j = p * VPP + g;
+        load_row<kE>(reinterpret_cast<const T*>(raw[p]), x[p]);
+        if (p * VPP >= q.n) continue;
+        const bool on = j < q.n;
+        if (turn)
+          turn_part<T, D>(x[p], raw[p], [&] { return src + (long long)j * stride; }, R, cs[on ? j : 0], sn[on ? j : 0],
+                          sub, lane, on);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kE; ++i) m = max(m, __float_as_uint(x[p][i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int s = 1; s < LPV; s <<= 1) m = max(m, __shfl_xor_sync(kFull, m, s));
+        const bool bad = on && m > kTooLarge;
+        if (bad) {
+#pragma unroll
+          for (int i = 0; i < kE; ++i) x[p][i] = 0.f;
+        } else if (on) {
+          top = max(top, m);
+        }
+        const uint32_t b = __ballot_sync(kFull, bad && sub == 0);
+#pragma unroll
+        for (int i = 0; i < VPP; ++i) marks |= ((b >> (i * LPV)) & 1u) << (p * VPP + i);
+      }
+#pragma unroll
+      for (int s = LPV; s < 32; s <<= 1) top = max(top, __shfl_xor_sync(kFull, top, s));
+      // the smallest e with top <= 448 2^e = 1.75 * 2^(e + 8)
+      int e = max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0), kF8MinExp);
+      if (q.off) {
+        const int old = min(max((int)(before >> 23) - 127, kF8MinExp), kF8MaxExp);
+        if (e > old) {  // (the warp's lanes alike)
+          const float f = pow2(old - e < -126 ? -126 : old - e);
+          for (int j = g; j < q.off; j += VPP) {
+            const uint4 c = pay[j * LPV];
+            const uint32_t in4[4] = {c.x, c.y, c.z, c.w};
+            uint32_t out4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float y[4];
+              values4(in4[i], y);
+              out4[i] = codes4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+            }
+            pay[j * LPV] = make_uint4(out4[0], out4[1], out4[2], out4[3]);
+          }
+        } else {
+          e = old;
+        }
+        marks = marks << q.off | (before & ((1u << q.off) - 1u));
+      }
+      const float f = pow2(-e);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int j = p * VPP + g;
+        if (j >= q.n) continue;
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          c[i] = codes4(x[p][4 * i] * f, x[p][4 * i + 1] * f, x[p][4 * i + 2] * f, x[p][4 * i + 3] * f);
+        pay[(q.off + j) * LPV] = make_uint4(c[0], c[1], c[2], c[3]);
+      }
+      if (lane == 0) *word = (uint32_t)(e + 127) << 23 | marks;
+    }
+  }
+}
+
+// Rows of f8_block views back in the original space: a group of d / 16 lanes per vector.
+template <class T, int D>
+__global__ void __launch_bounds__(kF8Threads) read_f8_kernel(const __grid_constant__ Launch L) {
+  constexpr int LPV = D / kE, GROUPS = kF8Threads / LPV, NV = 4;
+  __shared__ Place place[kMaxTc];
+  const bool is_v = L.a.k_out == nullptr || blockIdx.y != 0;
+  const DevView& V = is_v ? L.a.v : L.a.k;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = tid % LPV;
+  const int t0 = blockIdx.x * L.tc, H = V.H;
+  const int n_tok = min(L.tc, L.a.b.n_tokens - t0), n_vec = n_tok * H;
+  for (int k = warp; k < n_tok; k += kF8Warps) {
+    const Place p = find_place(L.a, V, t0 + k, lane, blockIdx.y == 0);
+    if (lane == 0) place[k] = p;
+  }
+  __syncthreads();
+  T* out = static_cast<T*>(is_v ? L.a.v_out : L.a.k_out) + (long long)t0 * H * D + 16 * sub;
+  for (int v0 = tid / LPV; v0 < n_vec; v0 += NV * GROUPS) {
+    uint4 c[NV];
+    uint32_t w[NV];
+    bool padding[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int v = v0 + u * GROUPS, t = v / H, h = v - t * H;
+      const Place p = v < n_vec ? place[t] : Place{-1, 0, true};
+      padding[u] = p.padding;
+      c[u] = make_uint4(0u, 0u, 0u, 0u);
+      w[u] = 0u;
+      if (p.vec >= 0) {
+        const long long vec = p.vec + (long long)h * V.page_size;
+        c[u] = *(reinterpret_cast<const uint4*>(V.payload + vec * D) + sub);
+        w[u] = reinterpret_cast<const uint32_t*>(V.header)[vec / kF8Block];
+        w[u] = (w[u] >> (vec % kF8Block)) & 1u ? 0x7FC00000u : w[u] & 0xFFFF0000u;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      if (padding[u]) continue;
+      const uint32_t in4[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+      float x[kE];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float y[4];
+        values4(in4[i], y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[4 * i + k] = y[k] * __uint_as_float(w[u]);
+      }
+      store_row<kE>(out + (long long)(v0 + u * GROUPS) * D, x);
+    }
+  }
+}
+
+template <class T, int D>
+cudaError_t append_td(const AppendArgs& a, int sm_count, cudaStream_t s) {
+  return with_launch(a, sm_count, [&](const Launch& L, unsigned grid) {
+    append_f8_kernel<T, D><<<dim3(grid, 2), kF8Threads, 0, s>>>(L);
+  });
+}
+
+template <class T, int D>
+cudaError_t read_td(const AppendArgs& a, int sm_count, cudaStream_t s) {
+  return with_launch(a, sm_count, [&](const Launch& L, unsigned grid) {
+    read_f8_kernel<T, D><<<dim3(grid, a.k_out && a.v_out ? 2 : 1), kF8Threads, 0, s>>>(L);
+  });
+}
+
+template <class T>
+cudaError_t append_t(const AppendArgs& a, int sm_count, cudaStream_t s) {
+  if (a.k.d == 64) return append_td<T, 64>(a, sm_count, s);
+  if (a.k.d == 128) return append_td<T, 128>(a, sm_count, s);
+  return append_td<T, 256>(a, sm_count, s);
+}
+
+template <class T>
+cudaError_t read_t(const AppendArgs& a, int sm_count, cudaStream_t s) {
+  const int d = a.k_out ? a.k.d : a.v.d;
+  if (d == 64) return read_td<T, 64>(a, sm_count, s);
+  if (d == 128) return read_td<T, 128>(a, sm_count, s);
+  return read_td<T, 256>(a, sm_count, s);
+}
+
+}  // namespace
+
+cudaError_t launch_append_f8(const AppendArgs& a, int dtype, int sm_count, cudaStream_t s) {
+  if (dtype == TQ_DTYPE_F32) return append_t<float>(a, sm_count, s);
+  if (dtype == TQ_DTYPE_F16) return append_t<__half>(a, sm_count, s);
+  return append_t<__nv_bfloat16>(a, sm_count, s);
+}
+
+cudaError_t launch_read_f8(const AppendArgs& a, int dtype, int sm_count, cudaStream_t s) {
+  if (dtype == TQ_DTYPE_F32) return read_t<float>(a, sm_count, s);
+  if (dtype == TQ_DTYPE_F16) return read_t<__half>(a, sm_count, s);
+  return read_t<__nv_bfloat16>(a, sm_count, s);
+}
+
+}  // namespace tq

@@ -50,6 +50,9 @@ __device__ __forceinline__ long long position_vector(const DevBatch& b, const De
   return ((long long)layer * v.num_pages + page) * v.H * v.page_size + (pos - lp * v.page_size);
 }
 
+// The end of the first s keys from `first` on, which a window does not hide.
+__device__ __forceinline__ int sink_end(int first, int s) { return first > 0x7FFFFFFF - s ? 0x7FFFFFFF : first + s; }
+
 // cos and sin of pair angle `turns` (2^-64 turns per position) at a position, times m.  The product wraps modulo one
 // turn exactly; its top 32 bits, as a signed fraction of half a turn, are what sincospi takes (error below 2^-25 half
 // turns, 1e-7 in the results).

@@ -26,9 +26,10 @@ struct PlanArgs {
 };
 
 // What an entry's tokens see: the call's row and the position of its first token, their number, length and prefix of the
-// sequence; then (row, tokens) hold the first key that one of them sees and the end of the last.
+// sequence; then (row, tokens) hold the first key that one of them sees and the end of the last, (s_lo, s_hi) the same of
+// the sinks ahead of the windows.
 struct Look {
-  int row, tokens, pos, len, prefix;
+  int row, tokens, pos, len, prefix, s_lo, s_hi;
 };
 
 // Exclusive prefix sum of x over the block; *total receives the sum.
@@ -129,45 +130,73 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       i1 = (en.row0 + rows - 1) / G;
       prefix = en.prefix = a.prefix_lens ? a.prefix_lens[lo] : 0;
     }
-    int first = 0x7FFFFFFF, last = 0;
+    int first = 0x7FFFFFFF, last = 0, s_first = 0x7FFFFFFF, s_last = 0;
     if (a.first_keys) {
       // a warp per entry, 32 tokens at a time (a thread's warp looking at its lanes' entries one after another took 13 us
       // for 7 entries of up to 256 tokens; the call went from 49 to 44 us)
-      look[tid] = Look{s.first + i0, i1 - i0 + 1, s.len - s.n + i0, s.len, prefix};
+      look[tid] = Look{s.first + i0, i1 - i0 + 1, s.len - s.n + i0, s.len, prefix, 0, 0};
       __syncthreads();
       for (int k = tid >> 5; k < min(kPlanThreads, E - e0); k += kPlanThreads / 32) {
         const Look y = look[k];
-        int f = 0x7FFFFFFF, t = 0;
+        int f = 0x7FFFFFFF, t = 0, sf = 0x7FFFFFFF, st = 0;
 #pragma unroll 4
         for (int i = tid & 31; i < y.tokens; i += 32) {
           const int pos = y.pos + i, h = min(y.len, max(pos + 1, y.prefix));
-          int lo = max(0, __ldg(a.first_keys + y.row + i));
+          const int own = max(0, __ldg(a.first_keys + y.row + i));
+          int lo = own;
           if (a.window) lo = max(lo, pos - a.window + 1);
           if (lo < h) {
             f = min(f, lo);
             t = max(t, h);
+            if (a.sinks && own < lo) {  // (sinks are keys ahead of a window, so the row sees some of that too)
+              sf = min(sf, own);
+              st = max(st, min(sink_end(own, a.sinks), lo));
+            }
           }
         }
         f = __reduce_min_sync(kFull, f);
         t = __reduce_max_sync(kFull, t);
+        if (a.sinks) {
+          sf = __reduce_min_sync(kFull, sf);
+          st = __reduce_max_sync(kFull, st);
+        }
         __syncwarp();
         if ((tid & 31) == 0) {
           look[k].row = f;
           look[k].tokens = t;
+          look[k].s_lo = sf;
+          look[k].s_hi = st;
         }
       }
       __syncthreads();
       first = look[tid].row;
       last = look[tid].tokens;
+      s_first = look[tid].s_lo;
+      s_last = look[tid].s_hi;
     } else if (e < E) {
       const int pos0 = s.len - s.n;
       first = a.window ? max(0, pos0 + i0 - a.window + 1) : 0;
       last = min(s.len, max(pos0 + i1 + 1, prefix));
+      if (a.sinks) {
+        s_first = 0;
+        s_last = min(a.sinks, max(0, pos0 + i1 - a.window + 1));
+      }
     }
     if (first < last) {
+      // sinks up to the tiles of the windows make one range with them
+      if (s_first < s_last && (s_last + p.keys - 1) / p.keys >= first / p.keys) {
+        first = min(first, s_first);
+        s_last = s_first;
+      }
       en.lo = first;
       en.hi = last;
       en.n_tiles = (last + p.keys - 1) / p.keys - first / p.keys;
+      if (s_first < s_last) {
+        en.s_lo = s_first;
+        en.s_hi = s_last;
+        en.s_tiles = (s_last + p.keys - 1) / p.keys - s_first / p.keys;
+        en.n_tiles += en.s_tiles;
+      }
     }
     const long long at = carry + block_scan(e < E ? en.n_tiles + ck::kOverhead : 0, warp_sums, &total);
     if (e < E) {
@@ -239,7 +268,7 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, int s
   a.scale = (c.scale < 0.f ? -c.scale : c.scale) * 1.4426950408889634074f;
   a.q_sign = c.scale > 0.f ? 1.f : c.scale < 0.f ? -1.f : 0.f;
   a.inv_lam_v = 1.f / lam_v;
-  const int vb = c.v.format == TQ_FMT_Q8_0 ? 0 : c.v.idx_bits;
+  const int vb = c.v.format == TQ_FMT_Q8_0 ? 0 : c.v.format == TQ_FMT_F8_BLOCK ? ck::kF8 : c.v.idx_bits;
   // Entries of few rows.  48 sequences of 1K to 16K tokens, 8 KV heads of 128, 4 rows each: q8_0 128 us there and 253 in
   // the large kernel, turbo4 149 and 382; 16 rows: 152 and 275, turbo4 204 and 400; head size 64: 85 and 195; 256: 215 and
   // 330; 4 sequences of 500 tokens: 20 and 24.  At 256 a lane's registers hold 8 rows.

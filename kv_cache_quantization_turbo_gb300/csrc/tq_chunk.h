@@ -12,11 +12,15 @@ constexpr int kOverhead = 2;
 constexpr int rows_per_entry(int d) { return d == 256 ? 128 : 256; }
 constexpr int keys_per_tile(int d) { return d == 256 ? 64 : 128; }
 
-// Up to rows_per_entry rows of a sequence, the keys [lo, hi) that any of them sees and the tiles that cover them; start:
-// work units of the entries before it.
+// Kinds of V in the kernels: q8_0, turbo-MSE index bits 1 to 3 (both over q8_0 K), or f8_block for K and V.
+constexpr int kF8 = 4;
+
+// Up to rows_per_entry rows of a sequence, the keys that any of them sees and the tiles that cover them: the keys
+// [s_lo, s_hi) ahead of the window (sinks) in the first s_tiles ones, then [lo, hi); start: work units of the entries
+// before it.
 struct Entry {
   long long start;
-  int seq, row0, rows, lo, hi, n_tiles;
+  int seq, row0, rows, lo, hi, n_tiles, s_lo, s_hi, s_tiles;
   int tok0, pos0, len, prefix;  // of its sequence: first row and position of the new tokens, length, prefix length
 };
 

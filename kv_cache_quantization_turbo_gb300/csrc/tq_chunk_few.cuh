@@ -34,14 +34,16 @@ constexpr int SK = 16;     // keys of a slice
 constexpr float kMaxExp = 15.f;
 
 // Two CTAs per SM hide each other's starts and ends of ranges.
-template <int D, int NT, int VB>  // VB: 0 q8_0 values, else turbo-MSE index bits
+template <int D, int NT, int VB>  // VB: 0 q8_0 values, 1 to 3 turbo-MSE index bits, kF8 f8_block keys and values
 struct Few {
+  static constexpr bool kBytes = VB == 0 || VB == kF8;   // V's codes are bytes
   static constexpr int NW = D == 256 || NT > 1 ? 6 : 8;  // warps of a CTA: as many as have the registers
-  static constexpr int VP = VB == 0 ? D : D * VB / 8;    // payload and header bytes of a V vector
+  static constexpr int VP = kBytes ? D : D * VB / 8;     // payload and header bytes of a V vector
   static constexpr int VH = VB == 0 ? D / 16 : 2;
   static constexpr int k = 0, v = SK * D;                // parts of a slice
-  static constexpr int ks = v + SK * VP, vs = ks + SK * D / 16;
-  static constexpr int slice = vs + SK * VH;
+  static constexpr int ks = v + SK * VP;                 // f8_block: a slice is a block, with one word each
+  static constexpr int vs = ks + (VB == kF8 ? 16 : SK * D / 16);
+  static constexpr int slice = vs + (VB == kF8 ? 16 : SK * VH);
   static constexpr int most = 108 * 1024 / (NW * slice);
   static constexpr int NS = most > 8 ? 8 : most;         // slices of a warp's ring
   static constexpr int ring = NW * NS * slice;
@@ -93,7 +95,8 @@ struct Row {
   int lo, hi, pos;  // the keys [lo, hi) it sees; its position
   float slope;      // in log2 units
   float sl;         // what its scores are multiplied by, in log2 units
-  int pad[3];
+  int s_lo, s_hi;   // the sinks [s_lo, s_hi) that it sees ahead of lo, too
+  int pad;
 };
 
 struct Spot {
@@ -222,6 +225,7 @@ template <int D, int NT, int VB>
 __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const __grid_constant__ Args a) {
   using F = Few<D, NT, VB>;
   constexpr int NS = F::NS, NW = F::NW;
+  constexpr bool kTurbo = VB > 0 && VB < kF8;
   extern __shared__ __align__(128) unsigned char sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   Item* items = reinterpret_cast<Item*>(sm + F::items);
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
   const bool runs = !a.c.b.block_table || K.page_size % SK == 0;
   const uint32_t inv = 0xFFFFFFFFu / (uint32_t)K.page_size;
   uint32_t tab[4] = {0u, 0u, 0u, 0u};
-  if constexpr (VB > 0) {
+  if constexpr (kTurbo) {
     if (tid < 4) {  // word tid: low (0, 1) or high (2, 3) bytes of four levels
       uint32_t w = 0;
 #pragma unroll
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
     walk->next(a, items[0]);
   }
   __syncthreads();
-  if constexpr (VB > 0) {
+  if constexpr (kTurbo) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) tab[i] = reinterpret_cast<const uint32_t*>(sm + F::tab)[i];
   }
@@ -285,8 +289,30 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       continue;
     }
     constexpr int BN = Shape<D>::BN;
-    const int j0 = max(it.tile * BN, it.lo) & ~(SK - 1), end = min((it.tile + it.n) * BN, it.hi);
-    const int seq = it.seq, low = it.lo;
+    // The keys of this CTA's tiles, in slices from j0 to end.  Sinks ahead of the windows take the numbers just before
+    // the windows' first slice, base: they lie gap keys further ahead.
+    int j0, end, base, gap = 0, low = it.lo;
+    {
+      const int first = max((it.tile + it.s_n) * BN, it.lo) & ~(SK - 1);
+      end = min((it.tile + it.n) * BN, it.hi);
+      j0 = base = first;
+      if (it.s_n > 0) {
+        const int s0 = max(it.s_tile * BN, it.s_lo) & ~(SK - 1), s1 = min((it.s_tile + it.s_n) * BN, it.s_hi);
+        if (it.n == it.s_n) {  // sinks alone
+          j0 = base = s0;
+          end = s1;
+          low = it.s_lo;
+        } else {
+          j0 = first - ((s1 - s0 + SK - 1) & ~(SK - 1));
+          gap = j0 - s0;
+        }
+      }
+    }
+    const int s_lo = it.s_lo, s_hi = it.s_hi;
+    auto key_of = [&](int n0) { return n0 < base ? n0 - gap : n0; };   // first key of the slice with number n0
+    auto low_of = [&](int n0) { return n0 < base ? s_lo : low; };      // the wanted keys of that slice: from here
+    auto end_of = [&](int n0) { return n0 < base ? s_hi : end; };      // to here
+    const int seq = it.seq;
     const int32_t* pages = a.c.b.block_table ? a.c.b.block_table + (long long)seq * a.c.b.max_blocks : nullptr;
     // payload bytes of a page; where the layer's bytes of the head begin
     const long long page_b = (long long)K.H * K.page_size * D;
@@ -313,19 +339,29 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
             if (off) atomicOr(a.c.tab.status, kFlagBlockTable);
           }
         };
-        const int c0 = max(low - n0, 0), c1 = min(end - n0, SK);  // the keys [c0, c1) are wanted
+        // the keys [c0, c1) are wanted
+        const int c0 = max(low_of(n0) - key_of(n0), 0), c1 = min(end_of(n0) - key_of(n0), SK);
         if (runs) {
           const unsigned char *pk = K.payload + at0 + 16 * lane, *hk = K.header + (at0 >> 4) + 4 * lane;
           auto go = [&](auto on) {  // on(key): the key is there
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
               copy_async<16>(base + F::k + k_at<D>(i * KPI + kl, c), pk + 512 * i, on(i * KPI + kl));
+            if constexpr (VB != kF8) {
 #pragma unroll
-            for (int i = 0; i < (D + 127) / 128; ++i) {
-              const int at = 4 * lane + 128 * i;
-              if (D >= 128 || lane < D / 4) copy_async<4>(base + F::ks + at, hk + 128 * i, on(at / (D / 16)));
+              for (int i = 0; i < (D + 127) / 128; ++i) {
+                const int at = 4 * lane + 128 * i;
+                if (D >= 128 || lane < D / 4) copy_async<4>(base + F::ks + at, hk + 128 * i, on(at / (D / 16)));
+              }
             }
-            if constexpr (VB == 0) {
+            if constexpr (VB == kF8) {  // the slice's two words, and V's codes as K's
+              const unsigned char* hdr = lane ? V.header : K.header;
+              if (lane < 2) copy_async<4>(base + (lane ? F::vs : F::ks), hdr + at0 / (D * kF8Block) * 4, there);
+              const unsigned char* pv = V.payload + at0 + 16 * lane;
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i)
+                copy_async<16>(base + F::v + v_at<D>(i * KPI + kl, c), pv + 512 * i, on(i * KPI + kl));
+            } else if constexpr (VB == 0) {
               const unsigned char *pv = V.payload + at0 + 16 * lane, *hv = V.header + (at0 >> 4) + 4 * lane;
 #pragma unroll
               for (int i = 0; i < D / 32; ++i)
@@ -346,14 +382,14 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
               if (on(lane & 15)) norm = __ldg(reinterpret_cast<const uint16_t*>(V.header) + vec + (lane & 15));
             }
           };
-          if (there && low <= n0 && n0 + SK <= end) {
+          if (there && c0 == 0 && c1 == SK) {
             go([](int) { return true; });
             if (missed) mark(0u);
           } else {
             go([&](int key) { return there && key >= c0 && key < c1; });
             mark(there ? 0u : (1u << c1) - (1u << c0));
           }
-        } else {
+        } else if constexpr (VB != kF8) {  // (f8_block pages are whole slices)
           const int mk = lane & 15;
           const bool want = mk >= c0 && mk < c1, on = there && want;
           mark(__ballot_sync(kFull, want && !there) & 0xFFFFu);
@@ -386,10 +422,12 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       return norm;
     };
     auto put_norm = [&](int st, uint16_t norm) {
-      if (VB > 0 && lane < 16) *reinterpret_cast<uint16_t*>(ring + st * F::slice + F::vs + 2 * lane) = norm;
+      if (kTurbo && lane < 16) *reinterpret_cast<uint16_t*>(ring + st * F::slice + F::vs + 2 * lane) = norm;
     };
     constexpr int STEP = SK * NW;
-    auto spot = [&](int n0) { return spot_of(a, pages, seq, n0 + (runs ? 0 : lane & 15), end, inv); };
+    auto spot = [&](int n0) {
+      return spot_of(a, pages, seq, n0 < end ? key_of(n0) + (runs ? 0 : lane & 15) : end, n0 < end ? end_of(n0) : end, inv);
+    };
     int ask = j0 + SK * warp;  // the next slice to ask for
     {
       Spot sp[NS - 1];
@@ -407,19 +445,23 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
     next_item();
 
     if (tid < 16) {
-      Row r{0, 0x7FFFFFFF, 0, 0.f, 0.f, {0, 0, 0}};  // rows that are not there see everything: they never need a mask
+      Row r{0, 0x7FFFFFFF, 0, 0.f, 0.f, 0, 0, 0};  // rows that are not there see everything: they never need a mask
       if (tid < rows) {
         const int row = it.row0 + tid, ti = row / G;
         r.pos = it.pos0 + ti;
         r.hi = min(it.len, max(r.pos + 1, it.prefix));
         if (a.c.window) r.lo = max(r.lo, r.pos - a.c.window + 1);
-        if (a.c.first_keys) r.lo = max(r.lo, a.c.first_keys[it.tok0 + ti]);
+        if (a.c.first_keys) r.s_lo = max(0, a.c.first_keys[it.tok0 + ti]);
+        r.lo = max(r.lo, r.s_lo);
+        r.s_hi = min(sink_end(r.s_lo, a.c.sinks), r.hi);
         if (a.c.slopes) r.slope = a.c.slopes[it.kvh * G + (row - ti * G)] * kLog2e;
       }
       row_of[tid].lo = r.lo;
       row_of[tid].hi = r.hi;
       row_of[tid].pos = r.pos;
       row_of[tid].slope = r.slope;
+      row_of[tid].s_lo = r.s_lo;
+      row_of[tid].s_hi = r.s_hi;
     }
     // Q's row g (and 8 + g) as fragments; everything else of this lane belongs to the rows 2 t, 2 t + 1 (and 8 more)
     uint32_t q[NT][D / 16][2];
@@ -458,18 +500,37 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
         for (int e = 0; e < 4; ++e) o[u][i][e] = 0.f;
 
     int st = 0;
+    int ve = kF8MinExp;  // f8_block: O is in units of 2^ve, no V scale so far is above
 #pragma unroll 1
-    for (int key0 = j0 + SK * warp; key0 < end; key0 += STEP, st = st + 1 == NS ? 0 : st + 1) {
+    for (int num = j0 + SK * warp; num < end; num += STEP, st = st + 1 == NS ? 0 : st + 1) {
+      const int key0 = key_of(num);
       asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
       const int last = st == 0 ? NS - 1 : st - 1;  // the stage read before, asked for below
-      if (VB > 0 && ask > j0 + SK * warp + STEP * (NS - 1)) put_norm(last == 0 ? NS - 1 : last - 1, norm);
+      if (kTurbo && ask > j0 + SK * warp + STEP * (NS - 1)) put_norm(last == 0 ? NS - 1 : last - 1, norm);
       __syncwarp();  // the slice is there, and the one before it has been read
       norm = issue(ask, last, ahead);
       ask += STEP;
       ahead = spot(ask);
       unsigned char* sk = ring + st * F::slice;
       uint32_t poison = 0;
-      {
+      float k_scale = 1.f, v_scale = 1.f;  // f8_block: the block's, V's over 2^ve
+      if constexpr (VB == kF8) {
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(sk + F::ks), vw = *reinterpret_cast<const uint32_t*>(sk + F::vs);
+        poison = (kw | vw) & 0xFFFFu;
+        k_scale = f8_scale(kw);
+        const int e = f8_exponent(vw);
+        if (e > ve) {  // (the warp's lanes alike)
+          const float down = ex2((float)(ve - e));
+          ve = e;
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) o[u][i][z] *= down;
+        }
+        v_scale = ex2((float)(e - ve));
+      } else {
         __half* s = reinterpret_cast<__half*>(sk + sc_at);
         uint32_t big = 0;
         if constexpr (VB == 0) {
@@ -494,7 +555,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       {
         uint32_t sa[D / 64], sb[D / 64];  // the scales of both keys
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
+        for (int i = 0; i < (VB == kF8 ? 0 : D / 64); ++i) {
           sa[i] = *reinterpret_cast<const uint32_t*>(sk + F::ks + g * (D / 16) + 4 * i);
           sb[i] = *reinterpret_cast<const uint32_t*>(sk + F::ks + (g + 8) * (D / 16) + 4 * i);
         }
@@ -503,6 +564,25 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
           for (int i = 0; i < D / 32; ++i) {  // a block of 32: two products of the codes, exact, then its scale
             const uint2 wa = *reinterpret_cast<const uint2*>(sk + F::k + k_at<D>(g, 2 * i + (t >> 1)) + 8 * (t & 1));
             const uint2 wb = *reinterpret_cast<const uint2*>(sk + F::k + k_at<D>(g + 8, 2 * i + (t >> 1)) + 8 * (t & 1));
+            if constexpr (VB == kF8) {
+              uint32_t a0[2], a1[2], a2[2], a3[2];
+              f8_pairs(wa.x, a0[0], a2[0]);
+              f8_pairs(wb.x, a1[0], a3[0]);
+              f8_pairs(wa.y, a0[1], a2[1]);
+              f8_pairs(wb.y, a1[1], a3[1]);
+#pragma unroll
+              for (int u = 0; u < NT; ++u) {
+                if (i == 0) wm::mma_16816_zc(x[u], a0[0], a1[0], a2[0], a3[0], q[u][0][0], q[u][0][1]);
+                else wm::mma_16816(x[u], a0[0], a1[0], a2[0], a3[0], q[u][2 * i][0], q[u][2 * i][1]);
+                wm::mma_16816(x[u], a0[1], a1[1], a2[1], a3[1], q[u][2 * i + 1][0], q[u][2 * i + 1][1]);
+                if constexpr (with_rest.value) {
+                  const uint4 r = q_rest[u * D + 32 * i + lane];
+                  wm::mma_16816(x[u], a0[0], a1[0], a2[0], a3[0], r.x, r.y);
+                  wm::mma_16816(x[u], a0[1], a1[1], a2[1], a3[1], r.z, r.w);
+                }
+              }
+              continue;
+            }
             const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&sa[i / 2]));
             const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&sb[i / 2]));
             const float ka = i & 1 ? fa.y : fa.x, kb = i & 1 ? fb.y : fb.x;
@@ -542,21 +622,24 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
             const int c = g + 4 * (e & 2), j = key0 + c;
             if (mods) {
               s *= r.sl;
+              if constexpr (VB == kF8) s *= k_scale;
               if (a.c.softcap > 0.f) s = cap_score(s, cap.x, cap.y);  // (sl holds log2 e)
               if (r.slope != 0.f) s = fmaf(-r.slope, fabsf((float)(r.pos - j)), s);
             }
             if ((poison >> c) & 1u) s = __uint_as_float(0x7FC00000u);
-            if (j < r.lo || j >= r.hi || j < low || j >= end || ((gone >> c) & 1u)) s = -INFINITY;
+            const bool seen = j < r.hi && (j >= r.lo || (j >= r.s_lo && j < r.s_hi));
+            if (!seen || j < low_of(num) || j >= end_of(num) || ((gone >> c) & 1u)) s = -INFINITY;
           }
         }
       }
       bool raise = false;
-      float mx[NT][2];
+      float mx[NT][2], fs[NT][2];  // fs: the slice's scores to log2 units
 #pragma unroll
       for (int u = 0; u < NT; ++u)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[u][e] = fmaxf(x[u][e], x[u][2 + e]) * f[u][e];
+          fs[u][e] = VB == kF8 && !mods ? fmaxf(f[u][e] * k_scale, 1.2e-38f) : f[u][e];
+          mx[u][e] = fmaxf(x[u][e], x[u][2 + e]) * fs[u][e];
           raise |= mx[u][e] - m[u][e] > kMaxExp;
         }
       if (__any_sync(kFull, raise)) {
@@ -586,9 +669,13 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
         float w[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          w[e] = ex2(fmaf(x[u][e], f[u][e], -mu[u][e]));
-          w[2 + e] = ex2(fmaf(x[u][2 + e], f[u][e], -mu[u][e]));
+          w[e] = ex2(fmaf(x[u][e], fs[u][e], -mu[u][e]));
+          w[2 + e] = ex2(fmaf(x[u][2 + e], fs[u][e], -mu[u][e]));
           l[u][e] += w[e] + w[2 + e];
+          if constexpr (VB == kF8) {
+            w[e] *= v_scale;
+            w[2 + e] *= v_scale;
+          }
         }
         p[u][0] = transpose8(narrow(w[0], w[1], (const __half*)nullptr));
         p[u][1] = transpose8(narrow(w[2], w[3], (const __half*)nullptr));
@@ -599,10 +686,10 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       for (int c = 0; c < (D + 127) / 128; ++c) {
         constexpr int W = D == 64 ? 2 : 4;
         const int chunk = D == 64 ? g >> 1 : 8 * c + g;
-        uint32_t w[4][W], s1[4];  // q8_0: the codes of a key; turbo: the selectors of W quads
+        uint32_t w[4][W], s1[4] = {0u, 0u, 0u, 0u};  // the codes of a key; turbo: the selectors of W quads
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          if constexpr (VB == 0) {
+          if constexpr (F::kBytes) {
             const unsigned char* at = sk + F::v + v_at<D>(keys[y], chunk);
             if constexpr (D == 64) {
               const uint2 z = *reinterpret_cast<const uint2*>(at + 8 * (g & 1));
@@ -611,7 +698,8 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
               const uint4 z = *reinterpret_cast<const uint4*>(at);
               w[y][0] = z.x; w[y][1] = z.y; w[y][W - 2] = z.z; w[y][W - 1] = z.w;
             }
-            s1[y] = *reinterpret_cast<const uint16_t*>(sk + F::vs + keys[y] * (D / 16) + (chunk >> 1) * 2);
+            if constexpr (VB == 0)
+              s1[y] = *reinterpret_cast<const uint16_t*>(sk + F::vs + keys[y] * (D / 16) + (chunk >> 1) * 2);
           } else {
             s1[y] = *reinterpret_cast<const uint16_t*>(sk + F::vs + keys[y] * 2);
             constexpr int CB = W * VB / 2;  // bytes of this lane's codes
@@ -649,7 +737,10 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
           uint32_t y[2][4];  // coordinates 0 to 3 of the first two keys, of the second two
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if constexpr (VB == 0) {
+            if constexpr (VB == kF8) {
+              f8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x5140), y[h][0], y[h][1]);
+              f8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x7362), y[h][2], y[h][3]);
+            } else if constexpr (VB == 0) {
               q8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x5140), y[h][0], y[h][1]);
               q8_pairs(__byte_perm(w[2 * h][z], w[2 * h + 1][z], 0x7362), y[h][2], y[h][3]);
 #pragma unroll
@@ -671,6 +762,15 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
 
     // ---- the warps' results, joined in their order ----
     float* mo = reinterpret_cast<float*>(sm);  // [NW][8 NT][OS]
+    if constexpr (VB == kF8) {
+      const float up = ex2((float)ve);
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[u][i][e] *= up;
+    }
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
 #pragma unroll
@@ -702,12 +802,12 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
     float* fin = reinterpret_cast<float*>(sm + F::fin);
     // four columns of a finished row: out, or (turbo values) to the transform
     auto finish = [&](int r, int c, const float (&y)[4]) {
-      if constexpr (VB == 0) store4(out_of(r) + 4 * c, y);
+      if constexpr (!kTurbo) store4(out_of(r) + 4 * c, y);
       else *reinterpret_cast<float4*>(fin + r * D + 4 * c) = make_float4(y[0], y[1], y[2], y[3]);
     };
     // out = diag(s) H of the finished rows, a row per warp, E coordinates per lane; folds 1 / lambda and 1 / sqrt(D)
     auto transform = [&]() {
-      if constexpr (VB > 0) {
+      if constexpr (kTurbo) {
         constexpr int E = D / 32;
         __syncthreads();
         for (int r = warp; r < rows; r += NW) {
@@ -862,6 +962,7 @@ cudaError_t launch_v(const Args& a, int vb, int sm_count, cudaStream_t s) {
     case 0: return launch<D, NT, 0>(a, sm_count, s);
     case 1: return launch<D, NT, 1>(a, sm_count, s);
     case 2: return launch<D, NT, 2>(a, sm_count, s);
+    case kF8: return launch<D, NT, kF8>(a, sm_count, s);
     default: return launch<D, NT, 3>(a, sm_count, s);
   }
 }

@@ -49,6 +49,8 @@
 // codes would want a score product, and its scores in tensor memory, for each block.
 #pragma once
 
+#include <cuda_fp8.h>
+
 #include "tq_batch.cuh"
 #include "tq_chunk.h"
 #include "tq_tc.cuh"
@@ -85,7 +87,8 @@ struct Shape {
   static constexpr int v = k + NB * kTileB;
   static constexpr int loc = v + NB * kTileB;          // long long [NL][BN]
   static constexpr int miss = loc + NL * BN * 8;       // uint32 [kMissRing][4]
-  static constexpr int rs = miss + kMissRing * 16;     // float [256]: row scales
+  static constexpr int words = miss + kMissRing * 16;  // uint32 [kMissRing][2][8]: f8_block words of a tile's K and V
+  static constexpr int rs = words + kMissRing * 64;    // float [256]: row scales
   static constexpr int items = rs + 256 * 4;           // Item [NI]
   static constexpr int tab = items + NI * 128;         // fp16 [8]: the V codebook
   static constexpr int bars = tab + 16;
@@ -106,12 +109,19 @@ struct Item {
   int kvh, seq, tok0, pos0, len, prefix;
   int row0, rows;  // of the sequence's rows
   int lo, hi;      // keys that some row sees
-  int tile, n;     // key tiles of this CTA
+  int tile, n;     // key tiles of this CTA, the first s_n of them sinks ahead of the windows: tile_of()
+  int s_lo, s_hi, s_tile, s_n;
   int two;         // two row tiles
   int first_cta, n_ctas, slot;  // CTAs that share the entry; this CTA's partial slot
   int counter;
 };
 static_assert(sizeof(Item) <= 128, "item");
+
+// Number of the CTA's tile j; the keys wanted from it.
+__device__ __forceinline__ int tile_of(const Item& it, int j) { return (j < it.s_n ? it.s_tile : it.tile) + j; }
+__device__ __forceinline__ int2 keys_of(const Item& it, int j) {
+  return j < it.s_n ? make_int2(it.s_lo, it.s_hi) : make_int2(it.lo, it.hi);
+}
 
 struct Bars {
   uint64_t k_full[3], k_free[3], v_full[3], v_free[3];
@@ -295,6 +305,19 @@ __device__ __forceinline__ uint32_t clamp_scale(uint32_t s2) {
                             *reinterpret_cast<const __half2*>(&nlim));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Four e4m3 codes to two fp16 pairs, exact.
+__device__ __forceinline__ void f8_pairs(uint32_t w, uint32_t& a, uint32_t& b) {
+  const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
+  const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  a = (uint32_t)x.x | (uint32_t)x.y << 16;
+  b = (uint32_t)y.x | (uint32_t)y.y << 16;
+}
+// The exponent of an f8_block word's scale, and the scale.
+__device__ __forceinline__ int f8_exponent(uint32_t w) { return (int)(w >> 23 & 255u) - 127; }
+__device__ __forceinline__ float f8_scale(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// The word of a block that is not there: the smallest scale, which moves no other block's, and no marks.
+constexpr uint32_t kF8None = (uint32_t)(kF8MinExp + 127) << 23;
+
 __device__ __forceinline__ bool not_finite(uint32_t s) { return (s & 0x7C00u) == 0x7C00u; }
 
 __device__ __forceinline__ void arrive_smem(uint64_t* bar, int lane) {
@@ -366,8 +389,12 @@ struct Items {
         it.kind = u == base ? 2 : 0;  // by the CTA that holds its first unit
       } else if (t0 < t1) {
         it.kind = 1;
-        it.tile = en.lo / Shape<D>::BN + (int)t0;
+        it.tile = en.lo / Shape<D>::BN + (int)t0 - en.s_tiles;
         it.n = (int)(t1 - t0);
+        it.s_lo = en.s_lo;
+        it.s_hi = en.s_hi;
+        it.s_tile = en.s_lo / Shape<D>::BN + (int)t0;
+        it.s_n = (int)max(0LL, min((long long)en.s_tiles, t1) - t0);
         it.first_cta = cta_of(base + kOverhead);
         it.n_ctas = cta_of(base + kOverhead + en.n_tiles - 1) - it.first_cta + 1;
         it.slot = t0 == 0 ? 1 : 0;
@@ -389,29 +416,34 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 // The two locator warps take half of a tile's rows each; lane's rows are BN / 2 * half + lane + 32 i.  page[i] is the
 // physical page of a row, read one tile ahead.
 template <int D>
-__device__ __forceinline__ void read_pages(const Args& a, const Item& it, int t, int half, int lane,
+__device__ __forceinline__ void read_pages(const Args& a, const Item& it, int tile, int half, int lane,
                                            int (&page)[Shape<D>::BN / 64]) {
   const DevBatch& b = a.c.b;
+  const int t = tile_of(it, tile);
+  const int2 keys = keys_of(it, tile);
 #pragma unroll
   for (int i = 0; i < Shape<D>::BN / 64; ++i) {
     const int j = t * Shape<D>::BN + Shape<D>::BN / 2 * half + 32 * i + lane;
     const int lp = (int)((uint32_t)j / (uint32_t)a.c.k.page_size);
     page[i] = b.block_table ? -1 : it.seq;
-    if (b.block_table && j >= it.lo && j < it.hi && lp < b.max_blocks)
+    if (b.block_table && j >= keys.x && j < keys.y && lp < b.max_blocks)
       page[i] = __ldg(b.block_table + (long long)it.seq * b.max_blocks + lp);
   }
 }
 
-template <int D>
-__device__ __forceinline__ void locate_tile(const Args& a, const Item& it, int t, int half, int lane,
-                                            const int (&page)[Shape<D>::BN / 64], long long* loc, uint32_t* miss) {
+template <int D, int VB>
+__device__ __forceinline__ void locate_tile(const Args& a, const Item& it, int tile, int half, int lane,
+                                            const int (&page)[Shape<D>::BN / 64], long long* loc, uint32_t* miss,
+                                            uint32_t* words) {
   constexpr int BN = Shape<D>::BN;
   const DevView &K = a.c.k, &V = a.c.v;
+  const int t = tile_of(it, tile);
+  const int2 keys = keys_of(it, tile);
   const long long first = (long long)a.c.layer * K.num_pages;
 #pragma unroll
   for (int i = 0; i < BN / 64; ++i) {
     const int at = BN / 2 * half + 32 * i + lane, j = t * BN + at;
-    const bool want = j >= it.lo && j < it.hi;
+    const bool want = j >= keys.x && j < keys.y;
     const bool on = want && page[i] >= 0 && page[i] < K.num_pages;
     const int off = j - (int)((uint32_t)j / (uint32_t)K.page_size) * K.page_size;
     const long long vec = on ? ((first + page[i]) * K.H + it.kvh) * K.page_size + off : -1;
@@ -431,8 +463,19 @@ __device__ __forceinline__ void locate_tile(const Args& a, const Item& it, int t
         prefetch_l2(pk + 128);
         if (V.pay_bytes > 128) prefetch_l2(pv + 128);
       }
-      prefetch_l2(K.header + vec * K.hdr_bytes);
-      prefetch_l2(V.header + vec * V.hdr_bytes);
+      if constexpr (VB != kF8) {
+        prefetch_l2(K.header + vec * K.hdr_bytes);
+        prefetch_l2(V.header + vec * V.hdr_bytes);
+      }
+    }
+    if constexpr (VB == kF8) {  // the words of the two blocks: lanes 0 and 16 K's, 1 and 17 V's
+      const uint32_t there = __ballot_sync(kFull, on) >> (lane & 16) & 0xFFFFu;
+      const long long some = __shfl_sync(kFull, vec, (lane & 16) + (there ? __ffs(there) - 1 : 0));
+      if ((lane & 14) == 0) {
+        const unsigned char* hdr = lane & 1 ? V.header : K.header;
+        words[8 * (lane & 1) + (BN / 2 * half + 32 * i + (lane & 16)) / 16] =
+            there ? __ldg(reinterpret_cast<const uint32_t*>(hdr) + some / kF8Block) : kF8None;
+      }
     }
   }
 }
@@ -477,14 +520,16 @@ struct Producer {
   static constexpr int RN = BN / 32, BK = D / 64;  // rows and 64-blocks per thread
   static_assert(kProdWarps / 2 * 8 == 32, "rows per pass");
 
+  static constexpr bool kBytes = VB == 0 || VB == kF8;  // V's codes are bytes
+
   struct RawK {
     uint4 w[RN][BK];
-    uint32_t k[RN][BK];               // K scales of the two 32-blocks of a 64-block
-    uint32_t v[RN][VB == 0 ? BK : 1];  // V scales, or the norm
+    uint32_t k[VB == kF8 ? 1 : RN][BK];               // K scales of the two 32-blocks of a 64-block
+    uint32_t v[VB == kF8 ? 1 : RN][VB == 0 ? BK : 1];  // V scales, or the norm
   };
   struct RawV {
-    uint32_t s[RN][VB == 0 ? BK : 1];  // scales, or the norm
-    uint4 w[VB == 0 ? RN : 1][BK];
+    uint32_t s[VB == kF8 ? 1 : RN][VB == 0 ? BK : 1];  // scales, or the norm
+    uint4 w[kBytes ? RN : 1][BK];
     uint32_t c[VB == 2 ? RN : 1][BK];                  // 16 codes of 2 bits
     uint16_t h[VB & 1 ? RN : 1][BK][VB == 3 ? 3 : 1];  // 16 codes of 1 or 3 bits
   };
@@ -498,6 +543,11 @@ struct Producer {
     const long long vec = loc[row_of(ptid, i)];
     const bool on = vec >= 0;
     const unsigned char* pk = K.payload + vec * D + 16 * c;
+    if constexpr (VB == kF8) {
+#pragma unroll
+      for (int b = 0; b < BK; ++b) r.w[i][b] = load16(pk + 64 * b, on);
+      return;
+    }
     const unsigned char* hk = K.header + vec * (D / 16);
     const unsigned char* hv = V.header + vec * (VB == 0 ? D / 16 : 2);
 #pragma unroll
@@ -517,21 +567,30 @@ struct Producer {
     const int c = ptid & 3;
     const long long vec = loc[row_of(ptid, i)];
     const bool on = vec >= 0;
-    const unsigned char* p = V.payload + vec * (VB == 0 ? D : D * VB / 8) + (VB == 0 ? 16 : 2 * VB) * c;
+    const unsigned char* p = V.payload + vec * (kBytes ? D : D * VB / 8) + (kBytes ? 16 : 2 * VB) * c;
     const unsigned char* hv = V.header + vec * (VB == 0 ? D / 16 : 2);
 #pragma unroll
     for (int b = 0; b < BK; ++b) {
-      if constexpr (VB == 0) {
-        r.w[i][b] = load16(p + 64 * b, on);
-        r.s[i][b] = load4(hv + 4 * b, on);
-      }
+      if constexpr (kBytes) r.w[i][b] = load16(p + 64 * b, on);
+      if constexpr (VB == 0) r.s[i][b] = load4(hv + 4 * b, on);
       if constexpr (VB == 2) r.c[i][b] = load4(p + 16 * b, on);
       if constexpr (VB == 1 || VB == 3) {
 #pragma unroll
         for (int k = 0; k < VB; ++k) r.h[i][b][k] = load2(p + 8 * VB * b + 2 * k, on);
       }
     }
-    if constexpr (VB != 0) r.s[i][0] = load2(hv, on);
+    if constexpr (!kBytes) r.s[i][0] = load2(hv, on);
+  }
+
+  // The same for 16 e4m3 codes.
+  static __device__ __forceinline__ void put_f8(unsigned char* tile, uint32_t c0, uint32_t c1, const uint4& w) {
+    uint4 h;
+    f8_pairs(w.x, h.x, h.y);
+    f8_pairs(w.y, h.z, h.w);
+    *reinterpret_cast<uint4*>(tile + c0) = h;
+    f8_pairs(w.z, h.x, h.y);
+    f8_pairs(w.w, h.z, h.w);
+    *reinterpret_cast<uint4*>(tile + c1) = h;
   }
 
   // Converts the 16 codes of a q8_0 unit and stores them as chunks 2 c, 2 c + 1 of 64-block b of a row; at: the
@@ -566,6 +625,10 @@ struct Producer {
     const uint32_t c0 = tile_at<BN>(row, 2 * c), c1 = tile_at<BN>(row, 2 * c + 1);
 #pragma unroll
     for (int b = 0; b < BK; ++b) {
+      if constexpr (VB == kF8) {
+        put_f8(tile + b * (128 * BN), c0, c1, r.w[i][b]);
+        continue;
+      }
       const uint32_t sk = scale_of(r.k[i][b], c);
       const uint32_t sv = VB == 0 ? scale_of(r.v[i][VB == 0 ? b : 0], c) : r.v[i][0];
       uint32_t s2 = clamp_scale(sk);
@@ -582,7 +645,9 @@ struct Producer {
     const uint32_t c0 = tile_at<BN>(row, 2 * c), c1 = tile_at<BN>(row, 2 * c + 1);
 #pragma unroll
     for (int b = 0; b < BK; ++b) {
-      if constexpr (VB == 0) {
+      if constexpr (VB == kF8) {
+        put_f8(tile + b * (128 * BN), c0, c1, r.w[i][b]);
+      } else if constexpr (VB == 0) {
         const uint32_t s = scale_of(r.s[i][b], c);
         put_q8(tile + b * (128 * BN), c0, c1, r.w[i][b], not_finite(s) ? 0u : clamp_scale(s));
       } else {
@@ -684,6 +749,7 @@ template <int D, int VB>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Args a) {
   using Sh = Shape<D>;
   constexpr int BN = Sh::BN, NB = Sh::NB, PH = Sh::PH;
+  constexpr bool kTurbo = VB > 0 && VB < kF8;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = tc::smem_addr(sm);
@@ -692,6 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   Item* items = reinterpret_cast<Item*>(sm + Sh::items);
   long long* loc = reinterpret_cast<long long*>(sm + Sh::loc);
   uint32_t* miss = reinterpret_cast<uint32_t*>(sm + Sh::miss);
+  uint32_t* words = reinterpret_cast<uint32_t*>(sm + Sh::words);
   float* rs = reinterpret_cast<float*>(sm + Sh::rs);
 
   if (warp == 0) {
@@ -722,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
     }
   }
-  if constexpr (VB > 0) {
+  if constexpr (kTurbo) {
     if (tid < 4) {  // byte tables of lambda * level: words 0, 1 the low bytes, 2, 3 the high ones
       uint32_t w = 0;
 #pragma unroll
@@ -765,14 +832,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         }
         const Item& it = items[is];
         if (!ok || it.kind == 0) break;
-        const int n = it.n, t0 = it.tile;
+        const int n = it.n;
         int page[BN / 64], next[BN / 64];
-        if (n > 0) read_pages<D>(a, it, t0, half, lane, page);
+        if (n > 0) read_pages<D>(a, it, 0, half, lane, page);
         for (int j = 0; j < n && ok; ++j, ++gt) {
           const int s = gt % NL;
-          if (j + 1 < n) read_pages<D>(a, it, t0 + j + 1, half, lane, next);
+          if (j + 1 < n) read_pages<D>(a, it, j + 1, half, lane, next);
           if (gt >= NL) wait_warp<100>(ok, &B->loc_free[s], gt / NL - 1);
-          locate_tile<D>(a, it, t0 + j, half, lane, page, loc + s * BN, miss + (gt % kMissRing) * 4);
+          locate_tile<D, VB>(a, it, j, half, lane, page, loc + s * BN, miss + (gt % kMissRing) * 4,
+                             words + (gt % kMissRing) * 16);
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&B->loc_full[s]);
 #pragma unroll
@@ -894,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       produce(raw, P::load_k, P::convert_k, B->k_full, B->k_free, Sh::k);
     } else {
       uint32_t tab[4] = {0u, 0u, 0u, 0u};
-      if constexpr (VB > 0) {
+      if constexpr (kTurbo) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) tab[i] = reinterpret_cast<const uint32_t*>(sm + Sh::tab)[i];
       }
@@ -943,11 +1011,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         continue;
       }
       int lo = 0, hi = 0x7FFFFFFF;  // rows that are not there see everything: they never need a mask
+      int s_lo = 0, s_hi = 0;       // and the sinks [s_lo, s_hi) among the keys before hi
       float sl = 1.f, slope = 0.f;
       if (valid) {
         hi = min(it.len, max(pos + 1, it.prefix));
         if (a.c.window) lo = max(lo, pos - a.c.window + 1);
-        if (a.c.first_keys) lo = max(lo, a.c.first_keys[tok]);
+        if (a.c.first_keys) s_lo = max(0, a.c.first_keys[tok]);
+        lo = max(lo, s_lo);
+        s_hi = min(sink_end(s_lo, a.c.sinks), hi);
         sl = fmaxf(a.scale * rs[rr], 1.2e-38f);
         if (a.c.slopes) slope = a.c.slopes[head] * kLog2e;
       }
@@ -959,6 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const bool any_valid = __any_sync(kFull, valid);  // a warp without rows only keeps the barriers
       float m = -INFINITY, l = 0.f;
       bool unset = true;  // (of the warp) a row that sees keys has no reference yet
+      int ve = kF8MinExp;  // (of the warp, f8_block) O is in units of 2^ve: no V scale so far is above
       int last = -1, last_phase = 0;  // barrier and phase of the last part's value product
       for (int i = 0; i < steps; ++i) {
         const int s = buffer(c0 + i), jt = first + stride * i;
@@ -966,12 +1038,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         tc::fence_after_sync();
 #pragma unroll 1
         for (int h = 0; h < PH; ++h) {
-          const int key0 = (it.tile + jt) * BN + h * HN;
+          const int key0 = tile_of(it, jt) * BN + h * HN;
           const uint32_t t_s = tmem + s * BN + h * HN + lanes;
           if (any_valid) {
             const uint2 mw = *reinterpret_cast<const uint2*>(miss + ((gt + jt) % kMissRing) * 4 + 2 * h);
             // steps that need more than a scale are changed in place, in tensor memory
-            const bool special = mods || key0 < all_lo || key0 + HN > all_hi || (mw.x | mw.y) != 0u;
+            uint32_t kw[4], vw[4], marks = 0;  // f8_block: the words of the part's blocks
+            if constexpr (VB == kF8) {
+              const uint32_t* w = words + ((gt + jt) % kMissRing) * 16 + 4 * h;
+              const uint4 x = *reinterpret_cast<const uint4*>(w), y = *reinterpret_cast<const uint4*>(w + 8);
+              kw[0] = x.x; kw[1] = x.y; kw[2] = x.z; kw[3] = x.w;
+              vw[0] = y.x; vw[1] = y.y; vw[2] = y.z; vw[3] = y.w;
+#pragma unroll
+              for (int b = 0; b < 4; ++b) marks |= (kw[b] | vw[b]) & 0xFFFFu;
+            }
+            const bool special = mods || key0 < all_lo || key0 + HN > all_hi || (mw.x | mw.y | marks) != 0u;
             if (special) {
               uint32_t xa[16];
               const bool capped = a.c.softcap > 0.f;
@@ -980,6 +1061,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               for (int c = 0; c < HN / 16; ++c) {
                 tc::tmem_ld16_nw(t_s + 16 * c, xa);
                 loaded(xa);
+                uint32_t poison = 0;
+                if constexpr (VB == kF8) {
+                  const uint32_t* w = words + ((gt + jt) % kMissRing) * 16 + 4 * h + c;
+                  poison = (w[0] | w[8]) & 0xFFFFu;
+                  if (mods) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) xa[e] = __float_as_uint(__uint_as_float(xa[e]) * f8_scale(w[0]));
+                  }
+                }
                 if (capped) {
 #pragma unroll
                   for (int e = 0; e < 16; ++e)
@@ -996,7 +1086,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 }
                 // visible keys of these 16 as a bit mask
                 const int p = min(max(lo - key0 - 16 * c, 0), 16), q = min(max(hi - key0 - 16 * c, 0), 16);
-                const uint32_t vis = ((1u << q) - 1u) & (0xFFFFFFFFu << p) & ~((c & 2 ? mw.y : mw.x) >> (16 * (c & 1)));
+                const int sp = min(max(s_lo - key0 - 16 * c, 0), 16), sq = min(max(s_hi - key0 - 16 * c, 0), 16);
+                const uint32_t vis = ((((1u << q) - 1u) & (0xFFFFFFFFu << p)) | (((1u << sq) - 1u) & (0xFFFFFFFFu << sp))) &
+                                     ~((c & 2 ? mw.y : mw.x) >> (16 * (c & 1)));
+                if (poison) {  // a key whose K or V is marked makes the rows that see it NaN
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) xa[e] = (poison >> e) & 1u ? 0x7FC00000u : xa[e];
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) xa[e] = (vis >> e) & 1u ? xa[e] : 0xFF800000u;
                 tmem_st16(t_s + 16 * c, xa);
@@ -1007,13 +1103,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // to more than kTop) the row's maximum, a new reference and the weights again: S is still there.
             const float f = mods ? 1.f : sl;  // scores to log2 units (special tiles are in them already where mods is set)
             bool raise = unset;
+            int ve_part = kF8MinExp;
+            if constexpr (VB == kF8) {
+              ve_part = max(max(f8_exponent(vw[0]), f8_exponent(vw[1])), max(f8_exponent(vw[2]), f8_exponent(vw[3])));
+              raise |= ve_part > ve;
+            }
             uint32_t pk[HN / 2];
             float sum;
 #pragma unroll 1
             for (;;) {
               uint32_t x[64];
               if (raise) {
-                float mx0 = -INFINITY, mx1 = -INFINITY;
+                float mx0 = -INFINITY, mx1 = -INFINITY, top = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < HN / 16; ++c) {
                   uint32_t y[16];
@@ -1024,11 +1125,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     mx0 = fmaxf(fmaxf(mx0, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
                     mx1 = fmaxf(fmaxf(mx1, __uint_as_float(y[e + 2])), __uint_as_float(y[e + 3]));
                   }
+                  if constexpr (VB == kF8) {  // (a block's scores at its scale; the part's so far in top)
+                    const float sk = mods ? 1.f : f8_scale(words[((gt + jt) % kMissRing) * 16 + 4 * h + c]);
+                    top = fmaxf(top, fmaxf(mx0, mx1) * sk);
+                    mx0 = mx1 = -INFINITY;
+                  }
                 }
+                if constexpr (VB == kF8) mx0 = top;
                 const float mn = fmaxf(m, fmaf(fmaxf(mx0, mx1), f, -kBias));
-                const float al = mn == -INFINITY ? 1.f : ex2(m - mn);
+                float al = mn == -INFINITY ? 1.f : ex2(m - mn);
                 m = mn;
                 l *= al;
+                if constexpr (VB == kF8) {
+                  if (ve_part > ve) {
+                    al *= ex2((float)(ve - ve_part));
+                    ve = ve_part;
+                  }
+                }
                 unset = __any_sync(kFull, live && m == -INFINITY);
                 if (last >= 0) {  // O, once the product of this warpgroup's last part is complete
                   wait_warp(ok, &B->pv_done[last], last_phase);
@@ -1046,6 +1159,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
               tmem_ld64(t_s, x);
               const float mu = m == -INFINITY ? 0.f : m;
+              if constexpr (VB == kF8) {
+                // Weights times their V block's scale over 2^ve; the sum takes that back.  (A scale below 2^-40 of 2^ve
+                // counts as that: its weights, below 2^15 2^-40, are 0 in fp16.)
+                sum = 0.f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  const float sh = (float)max(f8_exponent(vw[b]) - ve, -40), fb = mods ? 1.f : fmaxf(f * f8_scale(kw[b]), 1.2e-38f);
+                  const float2 f2 = make_float2(fb, fb), m2 = make_float2(sh - mu, sh - mu);
+                  float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll
+                  for (int e = 8 * b; e < 8 * b + 8; ++e) {
+                    float2 p = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2, m2);
+                    p.x = ex2(p.x);
+                    p.y = ex2(p.y);
+                    l2 = __fadd2_rn(l2, p);
+                    pk[e] = narrow(p.x, p.y, (const __half*)nullptr);
+                  }
+                  sum = fmaf(l2.x + l2.y, ex2(-sh), sum);
+                }
+              } else {
               const float2 f2 = make_float2(f, f), m2 = make_float2(-mu, -mu);
               float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -1057,6 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 pk[e] = narrow(p.x, p.y, (const __half*)nullptr);
               }
               sum = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+              }
               // (rows that are not there hold whatever shared memory had: they have no say, so that results do not vary)
               if (raise || !__any_sync(kFull, live && sum > kTop)) break;
               raise = true;
@@ -1087,7 +1221,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       // (a share's O: [D / 4][rows_cap] float4, so that the rows of a warp are consecutive)
       float4* po = reinterpret_cast<float4*>(a.part_o + my_slot * a.rows_cap * D) + r;
       float norm = a.inv_lam_v;  // folds 1 / lambda and the transform's 1 / sqrt(D)
-      if constexpr (VB > 0) norm *= inv_sqrt_dim<D>();
+      if constexpr (kTurbo) norm *= inv_sqrt_dim<D>();
+      if constexpr (VB == kF8) norm *= ex2((float)ve);
       if (mine) {
         if (whole) norm *= l == 0.f ? 0.f : __fdividef(1.f, l);
         if (!whole && valid) {
@@ -1106,7 +1241,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               po[((col >> 2) + 1) * a.rows_cap] = make_float4(y[4], y[5], y[6], y[7]);
             }
           };
-          if constexpr (VB == 0) {
+          if constexpr (!kTurbo) {
 #pragma unroll 1
             for (int c = 0; c < D / 32 && any_valid; ++c) {
               uint32_t o[32];
@@ -1249,6 +1384,7 @@ cudaError_t launch_d(const Args& a, int vb, int sm_count, cudaStream_t s) {
     case 0: return launch<D, 0>(a, sm_count, s);
     case 1: return launch<D, 1>(a, sm_count, s);
     case 2: return launch<D, 2>(a, sm_count, s);
+    case kF8: return launch<D, kF8>(a, sm_count, s);
     default: return launch<D, 3>(a, sm_count, s);
   }
 }

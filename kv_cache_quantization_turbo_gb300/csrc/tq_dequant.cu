@@ -4,9 +4,10 @@
 //   x~ = diag(s) H ( n c[idx]  +  rnorm sqrt(pi/2)/d S^T (2 sigma - 1) ),
 // the second term only for K formats with include_qjl (vector form of the
 // QJL estimate).  q8_0: q * delta per block of 32.  min-max: q * scale + zero
-// per group of 64 ("mac-code TurboQuant analysis", section 2.1).
+// per group of 64 ("mac-code TurboQuant analysis", section 2.1).  f8_block: code * 2^e.
 // One warp per (slot, head); lane l owns coordinates [E l, E l + E), E = d/32.
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "tq_device.cuh"
 
@@ -54,6 +55,14 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequant_kernel(DqArgs a) {
     const float delta = __half2float(reinterpret_cast<const __half*>(hdr)[(E * lane) / 32]);
 #pragma unroll
     for (int e = 0; e < E; ++e) dst[e] = (float)q[E * lane + e] * delta;
+    return;
+  }
+  if (V.format == TQ_FMT_F8_BLOCK) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(V.header)[vid / kF8Block];
+    const float scale = (w >> (vid % kF8Block)) & 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(w & 0xFFFF0000u);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      dst[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw(pay[E * lane + e], __NV_E4M3))) * scale;
     return;
   }
   const int nwords = V.pay_bytes / 4;

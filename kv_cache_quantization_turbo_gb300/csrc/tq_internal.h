@@ -31,7 +31,7 @@ struct DevView {
   int code_bits;    // bits per coordinate in the payload (turbo K: idx_bits + 1)
   int has_qjl;      // turbo K formats
   int pay_bytes;    // payload bytes per vector
-  int hdr_bytes;    // header bytes per vector
+  int hdr_bytes;    // header bytes per vector (f8_block: 0, a word per block of kF8Block vectors)
   unsigned char* payload;
   unsigned char* header;
 };
@@ -51,6 +51,9 @@ struct DevTables {
   const float* f16_scale;    // [3]: lambda per bit width, so that lambda * centroid is (nearly) an fp16 value
   uint32_t* status;          // device status word
 };
+
+// f8_block: tokens of a block, the range of its scale's exponent.
+constexpr int kF8Block = 16, kF8MinExp = -80, kF8MaxExp = 80;
 
 bool format_is_turbo(int f);
 bool format_has_qjl(int f);
@@ -157,6 +160,30 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, int dtype, int sm_count, cudaStream_t s);
 cudaError_t launch_read(const AppendArgs& a, int dtype, int sm_count, cudaStream_t s);
+// The same for f8_block views (both of them, where both are given).
+cudaError_t launch_append_f8(const AppendArgs& a, int dtype, int sm_count, cudaStream_t s);
+cudaError_t launch_read_f8(const AppendArgs& a, int dtype, int sm_count, cudaStream_t s);
+
+// Norms per head with the rotation (tq_norm.cu): rows[0] the queries, rows[1] the keys, n_heads 0 where there are none.
+struct NormRows {
+  const void* x;
+  void* out;               // forward: the result; gradient: dx
+  const void* dout;        // gradient
+  const void* weight;      // null: ones
+  float* dweight;          // gradient, may be null
+  long long x_stride, out_stride, dout_stride;
+  int n_heads;
+};
+struct NormArgs {
+  tq_rope_table rope;
+  NormRows rows[2];
+  const int32_t* positions;
+  float eps;
+  int n_tokens, weight_dtype;
+};
+cudaError_t launch_norm(const NormArgs& a, int dtype, int sm_count, cudaStream_t s);
+size_t norm_grad_workspace(int sm_count, int d, int n_heads);
+cudaError_t launch_norm_grad(const NormArgs& a, int dtype, void* workspace, int sm_count, cudaStream_t s);
 
 struct ChunkArgs {
   DevBatch b;
@@ -173,6 +200,7 @@ struct ChunkArgs {
   const float* slopes;
   const int32_t* first_keys;
   const int32_t* prefix_lens;
+  int sinks;  // 0 without a window
 };
 size_t chunk_workspace(int sm_count, int d, const tq_batch& b, int n_q_heads, int n_kv_heads);
 cudaError_t launch_chunk(const ChunkArgs& a, float lam_v, void* workspace, int sm_count, cudaStream_t s);

@@ -68,11 +68,11 @@ bool geometry(const tq_cache_view* v, Geometry* g) {
   if (!v || v->head_dim < 1 || v->n_kv_heads < 1 || v->page_size < 1 || v->num_pages < 1 || v->n_layers < 1)
     return false;
   const size_t pb = tq_payload_bytes((tq_format)v->format, v->head_dim, v->bits);
-  const size_t hb = tq_header_bytes((tq_format)v->format, v->head_dim, v->bits);
+  const size_t hb = tq_view_header_bytes(v);
   if (pb == 0 || hb == 0) return false;
   const size_t n = (size_t)v->n_layers * (size_t)v->num_pages * (size_t)v->n_kv_heads * (size_t)v->page_size;
   g->pay_bytes = n * pb;
-  g->hdr_bytes = n * hb;
+  g->hdr_bytes = hb;
   return true;
 }
 

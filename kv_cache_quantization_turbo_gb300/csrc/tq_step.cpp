@@ -1,5 +1,5 @@
 // Host side of the serving step: the rotation table, argument checks and the exported entry points of the rotary,
-// append, read and chunk-attention kernels (tq_rope.cu, tq_append.cu, tq_chunk.cu).
+// norm, append, read and chunk-attention kernels (tq_rope.cu, tq_norm.cu, tq_append.cu, tq_append_f8.cu, tq_chunk.cu).
 #include <cmath>
 
 #include "tq_internal.h"
@@ -32,6 +32,34 @@ bool table_ok(const tq_context* ctx, const tq_rope_table* t) {
          (t->layout == TQ_ROPE_HALF || t->layout == TQ_ROPE_INTERLEAVED);
 }
 
+bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// What the norm calls share; eps: a normal number, so that its square root has an inverse.
+bool norm_call_ok(const tq_context* ctx, const tq_rope_table* table, tq_dtype dtype, tq_dtype weight_dtype, float eps,
+                  int n_tokens, const int32_t* positions) {
+  return ctx && table && table_ok(ctx, table) && dtype_bytes(dtype) && dtype_bytes(weight_dtype) && eps >= 0x1p-126f &&
+         std::isfinite(eps) && n_tokens >= 0 && (positions || n_tokens == 0);
+}
+
+// Rows read from x and written to out (in place: the same stride).
+bool norm_rows_ok(const tq_context* ctx, const void* x, int64_t x_stride, const void* out, int64_t out_stride, int n_heads,
+                  tq_dtype dtype, int n_tokens) {
+  const int esz = dtype_bytes(dtype);
+  const int64_t row = (int64_t)n_heads * ctx->d;
+  return n_heads >= 1 && n_heads <= (1 << 20) && rows_ok(x, x_stride, row, esz, n_tokens) &&
+         rows_ok(out, out_stride, row, esz, n_tokens) && (x != out || n_tokens == 0 || x_stride == out_stride);
+}
+
+NormArgs norm_args(const tq_rope_table* table, int weight_dtype, float eps, int n_tokens, const int32_t* positions) {
+  NormArgs a{};
+  a.rope = *table;
+  a.positions = positions;
+  a.eps = eps;
+  a.n_tokens = n_tokens;
+  a.weight_dtype = weight_dtype;
+  return a;
+}
+
 // The sizes of a batch; the device pointers too when it is not empty.
 bool batch_ok(const tq_batch* b) {
   if (!b || b->n_seqs < 0 || b->n_tokens < 0 || b->max_tokens < 0 || b->max_ctx < 0) return false;
@@ -48,6 +76,8 @@ DevBatch dev_batch(const tq_batch* b) {
   return DevBatch{b->n_seqs, b->n_tokens, b->max_tokens, b->max_ctx, b->max_blocks, b->cu_tokens, b->seq_lens,
                   b->block_table};
 }
+
+bool is_f8(const DevView& v) { return v.format == TQ_FMT_F8_BLOCK; }
 
 bool stored_ok(const DevView& v) { return v.format == TQ_FMT_Q8_0 || (format_is_turbo(v.format) && !v.has_qjl); }
 
@@ -127,6 +157,54 @@ tq_status tq_rope(const tq_context* ctx, const tq_rope_table* table, const void*
                                  out_token_stride, ctx->sm_count, cuda_stream(stream)));
 }
 
+tq_status tq_norm_rope(const tq_context* ctx, const tq_rope_table* table, const tq_norm_rows* q, const tq_norm_rows* k,
+                       tq_dtype dtype, tq_dtype weight_dtype, float eps, int n_tokens, const int32_t* positions,
+                       tq_stream_t stream) {
+  if (!norm_call_ok(ctx, table, dtype, weight_dtype, eps, n_tokens, positions) || (!q && !k)) return TQ_ERR_INVALID_ARG;
+  NormArgs a = norm_args(table, weight_dtype, eps, n_tokens, positions);
+  for (int i = 0; i < 2; ++i) {
+    const tq_norm_rows* r = i ? k : q;
+    if (!r) continue;
+    if (!norm_rows_ok(ctx, r->x, r->x_token_stride, r->out, r->out_token_stride, r->n_heads, dtype, n_tokens))
+      return TQ_ERR_INVALID_ARG;
+    if (!aligned(r->weight, dtype_bytes(weight_dtype))) return TQ_ERR_INVALID_ARG;
+    a.rows[i] = NormRows{r->x, r->out, nullptr, r->weight, nullptr, r->x_token_stride, r->out_token_stride, 0, r->n_heads};
+  }
+  if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return TQ_OK;
+  return cuda_status(launch_norm(a, dtype, ctx->sm_count, cuda_stream(stream)));
+}
+
+size_t tq_norm_rope_grad_workspace_bytes(const tq_context* ctx, int n_tokens, int n_heads) {
+  if (!ctx || n_tokens < 0 || n_heads < 1 || n_heads > (1 << 21)) return 0;
+  return norm_grad_workspace(ctx->sm_count, ctx->d, n_heads);
+}
+
+tq_status tq_norm_rope_grad(const tq_context* ctx, const tq_rope_table* table, const tq_norm_grad_rows* q,
+                            const tq_norm_grad_rows* k, tq_dtype dtype, tq_dtype weight_dtype, float eps, int n_tokens,
+                            const int32_t* positions, void* workspace, size_t workspace_bytes, tq_stream_t stream) {
+  if (!norm_call_ok(ctx, table, dtype, weight_dtype, eps, n_tokens, positions) || (!q && !k)) return TQ_ERR_INVALID_ARG;
+  NormArgs a = norm_args(table, weight_dtype, eps, n_tokens, positions);
+  bool sums = false;
+  for (int i = 0; i < 2; ++i) {
+    const tq_norm_grad_rows* r = i ? k : q;
+    if (!r) continue;
+    if (!norm_rows_ok(ctx, r->x, r->x_token_stride, r->dx, r->dx_token_stride, r->n_heads, dtype, n_tokens) ||
+        !norm_rows_ok(ctx, r->dout, r->dout_token_stride, r->dx, r->dx_token_stride, r->n_heads, dtype, n_tokens))
+      return TQ_ERR_INVALID_ARG;
+    if (!aligned(r->weight, dtype_bytes(weight_dtype)) || !aligned(r->dweight, sizeof(float))) return TQ_ERR_INVALID_ARG;
+    a.rows[i] = NormRows{r->x, r->dx, r->dout, r->weight, r->dweight, r->x_token_stride, r->dx_token_stride,
+                         r->dout_token_stride, r->n_heads};
+    sums = sums || r->dweight;
+  }
+  if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
+  if (n_tokens == 0 && !sums) return TQ_OK;
+  if (!workspace || workspace_bytes < norm_grad_workspace(ctx->sm_count, ctx->d, a.rows[0].n_heads + a.rows[1].n_heads) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return TQ_ERR_WORKSPACE;
+  return cuda_status(launch_norm_grad(a, dtype, workspace, ctx->sm_count, cuda_stream(stream)));
+}
+
 tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void* k, int64_t k_token_stride,
                        const void* v, int64_t v_token_stride, tq_dtype dtype, const tq_rope_table* rope,
                        const int32_t* positions, const tq_cache_view* k_view, const tq_cache_view* v_view, int layer,
@@ -143,7 +221,8 @@ tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void*
   if (!rows_ok(k, k_token_stride, row, esz, batch->n_tokens) || !rows_ok(v, v_token_stride, row, esz, batch->n_tokens))
     return TQ_ERR_INVALID_ARG;
   if (!batch_fits(batch, a.k) || !on_device(ctx)) return TQ_ERR_INVALID_ARG;
-  if (a.k.format != TQ_FMT_Q8_0 || !stored_ok(a.v)) return TQ_ERR_UNSUPPORTED;
+  const bool f8 = is_f8(a.k) && is_f8(a.v);
+  if (!f8 && (a.k.format != TQ_FMT_Q8_0 || !stored_ok(a.v))) return TQ_ERR_UNSUPPORTED;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return TQ_OK;
   a.b = dev_batch(batch);
   a.tab = ctx->tables;
@@ -155,7 +234,8 @@ tq_status tq_append_kv(const tq_context* ctx, const tq_batch* batch, const void*
   a.positions = positions;
   a.has_rope = rope ? 1 : 0;
   if (rope) a.rope = *rope;
-  return cuda_status(launch_append(a, dtype, ctx->sm_count, cuda_stream(stream)));
+  return cuda_status(f8 ? launch_append_f8(a, dtype, ctx->sm_count, cuda_stream(stream))
+                        : launch_append(a, dtype, ctx->sm_count, cuda_stream(stream)));
 }
 
 tq_status tq_read_kv(const tq_context* ctx, const tq_batch* batch, const tq_cache_view* k_view, void* k_out,
@@ -176,14 +256,22 @@ tq_status tq_read_kv(const tq_context* ctx, const tq_batch* batch, const tq_cach
   if (k_view && v_view && (a.k.H != a.v.H || a.k.page_size != a.v.page_size || a.k.num_pages != a.v.num_pages))
     return TQ_ERR_INVALID_ARG;
   if (!on_device(ctx)) return TQ_ERR_INVALID_ARG;
-  if ((k_view && !stored_ok(a.k)) || (v_view && !stored_ok(a.v))) return TQ_ERR_UNSUPPORTED;
+  const bool k_f8 = k_view && is_f8(a.k), v_f8 = v_view && is_f8(a.v);
+  if ((k_view && !k_f8 && !stored_ok(a.k)) || (v_view && !v_f8 && !stored_ok(a.v))) return TQ_ERR_UNSUPPORTED;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return TQ_OK;
   a.b = dev_batch(batch);
   a.tab = ctx->tables;
   a.layer = layer;
-  a.k_out = k_out;
-  a.v_out = v_out;
-  return cuda_status(launch_read(a, dtype, ctx->sm_count, cuda_stream(stream)));
+  // (one launch, or one for each of two kinds of formats)
+  for (int f8 = 0; f8 < 2; ++f8) {
+    a.k_out = k_f8 == (f8 != 0) ? k_out : nullptr;
+    a.v_out = v_f8 == (f8 != 0) ? v_out : nullptr;
+    if (!a.k_out && !a.v_out) continue;
+    const cudaError_t e = f8 ? launch_read_f8(a, dtype, ctx->sm_count, cuda_stream(stream))
+                             : launch_read(a, dtype, ctx->sm_count, cuda_stream(stream));
+    if (e != cudaSuccess) return TQ_ERR_CUDA;
+  }
+  return TQ_OK;
 }
 
 size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, int n_q_heads, int n_kv_heads) {
@@ -191,6 +279,14 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
       n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads)
     return 0;
   return chunk_workspace(ctx->sm_count, ctx->d, *batch, n_q_heads, n_kv_heads);
+}
+
+size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int n_q_heads, const tq_cache_view* k_view,
+                              const tq_cache_view* v_view, const tq_score_mods* mods) {
+  DevView k{}, v{};
+  if (!make_dev_view(k_view, &k) || !make_dev_view(v_view, &v)) return 0;
+  (void)mods;
+  return tq_chunk_workspace_bytes(ctx, batch, n_q_heads, k.H);
 }
 
 tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const void* q, tq_dtype q_dtype,
@@ -210,9 +306,12 @@ tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const
   const int64_t row = (int64_t)n_q_heads * d;
   if (!rows_ok(q, q_token_stride, row, esz, batch->n_tokens) || !rows_ok(out, row, row, osz, batch->n_tokens))
     return TQ_ERR_INVALID_ARG;
-  if (mods && (!(mods->softcap >= 0.0f) || !std::isfinite(mods->softcap) || mods->window < 0)) return TQ_ERR_INVALID_ARG;
+  if (mods && (!(mods->softcap >= 0.0f) || !std::isfinite(mods->softcap) || mods->window < 0 ||
+               mods->sinks < 0))
+    return TQ_ERR_INVALID_ARG;
   if (!batch_fits(batch, a.k) || !on_device(ctx)) return TQ_ERR_INVALID_ARG;
-  if (a.k.format != TQ_FMT_Q8_0 || !stored_ok(a.v) || n_q_heads % a.k.H) return TQ_ERR_UNSUPPORTED;
+  const bool f8 = is_f8(a.k) && is_f8(a.v);
+  if ((!f8 && (a.k.format != TQ_FMT_Q8_0 || !stored_ok(a.v))) || n_q_heads % a.k.H) return TQ_ERR_UNSUPPORTED;
   // row numbers of a sequence and tile numbers are 32-bit in the kernels
   if ((int64_t)batch->max_tokens * (n_q_heads / a.k.H) >= (int64_t(1) << 30) || batch->max_ctx >= (1 << 30))
     return TQ_ERR_UNSUPPORTED;
@@ -237,8 +336,9 @@ tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const
     a.slopes = mods->slopes;
     a.first_keys = mods->first_keys;
     a.prefix_lens = mods->prefix_lens;
+    a.sinks = mods->window ? mods->sinks : 0;
   }
-  const float lam_v = a.v.format == TQ_FMT_Q8_0 ? 1.f : ctx->f16_scale_h[a.v.idx_bits - 1];
+  const float lam_v = a.v.format == TQ_FMT_Q8_0 || f8 ? 1.f : ctx->f16_scale_h[a.v.idx_bits - 1];
   return cuda_status(launch_chunk(a, lam_v, workspace, ctx->sm_count, cuda_stream(stream)));
 }
 

@@ -19,7 +19,7 @@ TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA, TQ
 FORMATS = {
     "turbo2": 0, "turbo3": 1, "turbo4": 2,
     "turbo2_mse": 3, "turbo3_mse": 4, "turbo4_mse": 5,
-    "q8_0": 6, "minmax": 7,
+    "q8_0": 6, "minmax": 7, "f8_block": 8,
 }
 
 if not os.path.exists(LIB_PATH):
@@ -62,7 +62,22 @@ class tq_batch(ctypes.Structure):
 class tq_score_mods(ctypes.Structure):
     _fields_ = [
         ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
-        ("first_keys", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+        ("first_keys", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p), ("sinks", ctypes.c_int32),
+    ]
+
+
+class tq_norm_rows(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+        ("out_token_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("n_heads", ctypes.c_int32),
+    ]
+
+
+class tq_norm_grad_rows(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64), ("dout", ctypes.c_void_p),
+        ("dout_token_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+        ("dx_token_stride", ctypes.c_int64), ("dweight", ctypes.c_void_p), ("n_heads", ctypes.c_int32),
     ]
 
 
@@ -80,6 +95,7 @@ _SIGS = {
     "tq_payload_bytes": (_SZ, [_I, _I, _I]),
     "tq_header_bytes": (_SZ, [_I, _I, _I]),
     "tq_vector_bytes": (_SZ, [_I, _I, _I]),
+    "tq_view_header_bytes": (_SZ, [_VP]),
     "tq_codebook_build": (_I, [_I, _I, _P, _P]),
     "tq_signs_generate": (_I, [_U32, _I, _P]),
     "tq_qjl_matrix_generate": (_I, [_U32, _I, _P]),
@@ -100,10 +116,16 @@ _SIGS = {
     "tq_prefill_attention": (_I, [_P, _P, _I, _I, _I, _VP, _VP, _I, _I, _P, _I, _I, _F, _P, _SZ, _P, _P]),
     "tq_rope_build": (_I, [ctypes.POINTER(tq_rope_params), ctypes.POINTER(tq_rope_table)]),
     "tq_rope": (_I, [_P, ctypes.POINTER(tq_rope_table), _P, _I, _I, _I, _I64, _P, _I, _P, _I64, _P]),
+    "tq_norm_rope": (_I, [_P, ctypes.POINTER(tq_rope_table), ctypes.POINTER(tq_norm_rows), ctypes.POINTER(tq_norm_rows),
+                          _I, _I, _F, _I, _P, _P]),
+    "tq_norm_rope_grad_workspace_bytes": (_SZ, [_P, _I, _I]),
+    "tq_norm_rope_grad": (_I, [_P, ctypes.POINTER(tq_rope_table), ctypes.POINTER(tq_norm_grad_rows),
+                               ctypes.POINTER(tq_norm_grad_rows), _I, _I, _F, _I, _P, _P, _SZ, _P]),
     "tq_append_kv": (_I, [_P, ctypes.POINTER(tq_batch), _P, _I64, _P, _I64, _I, ctypes.POINTER(tq_rope_table), _P,
                           _VP, _VP, _I, _P]),
     "tq_read_kv": (_I, [_P, ctypes.POINTER(tq_batch), _VP, _P, _VP, _P, _I, _I, _P]),
     "tq_chunk_workspace_bytes": (_SZ, [_P, ctypes.POINTER(tq_batch), _I, _I]),
+    "tq_chunk_workspace_for": (_SZ, [_P, ctypes.POINTER(tq_batch), _I, _VP, _VP, ctypes.POINTER(tq_score_mods)]),
     "tq_chunk_attention": (_I, [_P, ctypes.POINTER(tq_batch), _P, _I, _I64, _I, _VP, _VP, _I, _F,
                                 ctypes.POINTER(tq_score_mods), _P, _SZ, _P, _I, _P]),
     "tq_context_tables_hash": (_I, [_P, ctypes.POINTER(ctypes.c_uint64)]),
@@ -176,6 +198,12 @@ def tq_header_bytes(fmt, head_dim: int, bits: int = 0) -> int:
 
 def tq_vector_bytes(fmt, head_dim: int, bits: int = 0) -> int:
     return _lib.tq_vector_bytes(_fmt(fmt), head_dim, bits)
+
+
+def tq_view_header_bytes(view) -> int:
+    """Bytes of a whole view's header array."""
+    cv = view.c_view() if isinstance(view, CacheView) else view
+    return _lib.tq_view_header_bytes(ctypes.byref(cv))
 
 
 def tq_codebook_build(bits: int, head_dim: int):
@@ -272,11 +300,12 @@ def alloc_view(fmt, head_dim: int, n_kv_heads: int, page_size: int, num_pages: i
     import torch
 
     n = n_layers * num_pages * n_kv_heads * page_size
-    pb, hb = tq_payload_bytes(fmt, head_dim, bits), tq_header_bytes(fmt, head_dim, bits)
-    if pb == 0:
-        raise ValueError(f"unsupported view: {fmt} d={head_dim} bits={bits}")
+    pb = tq_payload_bytes(fmt, head_dim, bits)
+    hb = tq_view_header_bytes(tq_cache_view(_fmt(fmt), head_dim, n_kv_heads, page_size, num_pages, n_layers, bits))
+    if pb == 0 or hb == 0:
+        raise ValueError(f"unsupported view: {fmt} d={head_dim} bits={bits}, pages of {page_size} tokens")
     payload = torch.zeros(n * pb, dtype=torch.uint8, device=device)
-    header = torch.zeros(n * hb, dtype=torch.uint8, device=device)
+    header = torch.zeros(hb, dtype=torch.uint8, device=device)
     return CacheView(fmt if isinstance(fmt, str) else tq_format_name(fmt), head_dim, n_kv_heads, page_size,
                      num_pages, n_layers, payload, header, bits)
 
@@ -491,12 +520,14 @@ class Batch:
 @dataclass(frozen=True, eq=False)
 class ScoreMods:
     """Changes to the scores (tq_score_mods) and the device tensors they read: slopes float32 [n_q_heads],
-    first_keys int32 [n_tokens], prefix_lens int32 [n_seqs], each None for none; contents may change between calls."""
+    first_keys int32 [n_tokens], prefix_lens int32 [n_seqs], each None for none; contents may change between calls.
+    sinks: first tokens that the window does not hide."""
     softcap: float = 0.0
     window: int = 0
     slopes: object = None
     first_keys: object = None
     prefix_lens: object = None
+    sinks: int = 0
 
     def __post_init__(self):
         for t, want in ((self.slopes, "float32"), (self.first_keys, "int32"), (self.prefix_lens, "int32")):
@@ -504,7 +535,7 @@ class ScoreMods:
                 raise ValueError(f"a contiguous {want} tensor on the GPU is wanted: {t.dtype}, strides {t.stride()}, "
                                  f"{t.device}")
         object.__setattr__(self, "_c", tq_score_mods(self.softcap, self.window, _ptr(self.slopes),
-                                                     _ptr(self.first_keys), _ptr(self.prefix_lens)))
+                                                     _ptr(self.first_keys), _ptr(self.prefix_lens), self.sinks))
 
     def c_mods(self) -> tq_score_mods:
         return self._c
@@ -553,6 +584,70 @@ def tq_rope(ctx: int, table: tq_rope_table, x, positions, out, inverse: bool = F
                         _stream(stream))
 
 
+def _norm_parts(table, n: int, parts, weights) -> tuple[int, int]:
+    """(element type of the rows, of the weights) of a norm call's tensors: [tokens, heads, d] each, weights [d]."""
+    dtype = wtype = None
+    for part in parts:
+        shape = part[0].shape
+        for t in part:
+            if len(shape) != 3 or t.shape != shape or shape[0] != n or shape[-1] != table.head_dim:
+                raise ValueError(f"rows {tuple(shape)}, {tuple(t.shape)} for {n} tokens of {table.head_dim}")
+            if dtype is not None and t.dtype != dtype:
+                raise ValueError(f"rows of types {dtype} and {t.dtype}")
+            dtype = t.dtype
+    for w in weights:
+        if w is None:
+            continue
+        if w.shape != (table.head_dim,) or not w.is_contiguous() or not w.is_cuda or (wtype is not None and w.dtype != wtype):
+            raise ValueError(f"weights are contiguous [{table.head_dim}] tensors of one type on the GPU: {tuple(w.shape)}")
+        wtype = w.dtype
+    return _dtype(parts[0][0]), 0 if wtype is None else _dtype([w for w in weights if w is not None][0])
+
+
+def tq_norm_rope(ctx: int, table: tq_rope_table, q, q_out, q_weight, k, k_out, k_weight, eps: float, positions,
+                 stream=None) -> int:
+    """q, q_out [tokens, heads, d] and k, k_out [tokens, kv heads, d], all of one type (q_out may be q, k_out k; one pair may
+    be None); weights [d] or None for ones; positions int32 [tokens]."""
+    parts = [(x, o) for x, o in ((q, q_out), (k, k_out)) if x is not None]
+    if not parts or any(o is None for _, o in parts):
+        raise ValueError("queries or keys, and an output for each, are wanted")
+    n = parts[0][0].shape[0]
+    dtype, wtype = _norm_parts(table, n, parts, (q_weight, k_weight))
+
+    def rows(x, out, w):
+        return None if x is None else ctypes.byref(tq_norm_rows(
+            x.data_ptr(), _rows(x, x.shape), out.data_ptr(), _rows(out, x.shape), _ptr(w), x.shape[1]))
+    return _lib.tq_norm_rope(ctx, ctypes.byref(table), rows(q, q_out, q_weight), rows(k, k_out, k_weight), dtype, wtype, eps,
+                             n, _positions(positions, n), _stream(stream))
+
+
+def tq_norm_rope_grad_workspace_bytes(ctx: int, n_tokens: int, n_heads: int) -> int:
+    return _lib.tq_norm_rope_grad_workspace_bytes(ctx, n_tokens, n_heads)
+
+
+def tq_norm_rope_grad(ctx: int, table: tq_rope_table, q, dq_out, q_weight, dq, dq_weight, k, dk_out, k_weight, dk, dk_weight,
+                      eps: float, positions, workspace, workspace_bytes: int, stream=None) -> int:
+    """From the norm's inputs and its outputs' gradients dq_out, dk_out the inputs' gradients dq, dk (dq may be dq_out, dk
+    dk_out) and, where they are not None, the weights': dq_weight, dk_weight float32 [d]."""
+    parts = [p for p in ((q, dq_out, dq), (k, dk_out, dk)) if p[0] is not None]
+    if not parts or any(t is None for p in parts for t in p):
+        raise ValueError("queries or keys, and their gradients, are wanted")
+    n = parts[0][0].shape[0]
+    dtype, wtype = _norm_parts(table, n, parts, (q_weight, k_weight))
+    for t in (dq_weight, dk_weight):
+        if t is not None and (_short(t) != "float32" or t.shape != (table.head_dim,) or not t.is_contiguous()
+                              or not t.is_cuda):
+            raise ValueError(f"weight gradients are contiguous float32 [{table.head_dim}] tensors on the GPU")
+
+    def rows(x, dout, w, dx, dw):
+        return None if x is None else ctypes.byref(tq_norm_grad_rows(
+            x.data_ptr(), _rows(x, x.shape), dout.data_ptr(), _rows(dout, x.shape), _ptr(w), dx.data_ptr(),
+            _rows(dx, x.shape), _ptr(dw), x.shape[1]))
+    return _lib.tq_norm_rope_grad(ctx, ctypes.byref(table), rows(q, dq_out, q_weight, dq, dq_weight),
+                                  rows(k, dk_out, k_weight, dk, dk_weight), dtype, wtype, eps, n,
+                                  _positions(positions, n), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
 def tq_append_kv(ctx: int, batch: Batch, k, v, k_view, v_view, layer: int, rope: tq_rope_table | None = None,
                  positions=None, stream=None) -> int:
     """k, v: [n_tokens, H, d] tensors of one type (slices of a fused projection are fine)."""
@@ -583,6 +678,13 @@ def tq_read_kv(ctx: int, batch: Batch, k_view, k_out, v_view, v_out, layer: int,
 
 def tq_chunk_workspace_bytes(ctx: int, batch: Batch, n_q_heads: int, n_kv_heads: int) -> int:
     return _lib.tq_chunk_workspace_bytes(ctx, ctypes.byref(batch.c_batch()), n_q_heads, n_kv_heads)
+
+
+def tq_chunk_workspace_for(ctx: int, batch: Batch, n_q_heads: int, k_view, v_view, mods: ScoreMods | None = None) -> int:
+    """The workspace with which tq_chunk_attention runs these views and modifications fastest."""
+    ka, va = _view_arg(k_view), _view_arg(v_view)
+    return _lib.tq_chunk_workspace_for(ctx, ctypes.byref(batch.c_batch()), n_q_heads, ka[0], va[0],
+                                       None if mods is None else ctypes.byref(mods.c_mods()))
 
 
 def tq_chunk_attention(ctx: int, batch: Batch, q, k_view, v_view, layer: int, softmax_scale: float, workspace,
