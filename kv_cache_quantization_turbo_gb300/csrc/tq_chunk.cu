@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// The parts of the workspace, in order: head, entries, seq_base, counters, partial results.
+// The parts of the workspace, in order: head, entries, seq_base, counters, partial results; and the staged tiles, where a
+// call uses them.
 struct Layout {
   size_t entries, seq_base, counters, part_o, part_ml, bytes;
   long long max_entries;
@@ -235,13 +236,47 @@ Layout layout(int sm_count, int d, long long n_seqs, long long n_tokens, long lo
   return l;
 }
 
+// Staging f8_block tiles pays where each is used by some entries: converting one once costs about two conversions by the
+// entry that needs it, and the tile's way through the kernel is then shorter (tq_chunk_staged.cuh has both sides measured).
+// The batch's average decides, as far as the host knows it; documents (first_keys) are left to the other kernel, which
+// does not look at pages that no row sees.
+constexpr int kStagedEntries = 4;
+constexpr size_t kStagedMost = (size_t)8 << 30;
+
+struct StagedLayout {
+  size_t k, v, heads, bytes;  // from the workspace's start; bytes 0: not staged
+  int tiles;
+};
+
+StagedLayout staged_layout(size_t at, int d, const DevView& k, const tq_batch& b, int n_q_heads, bool documents) {
+  StagedLayout l{};
+  const long long G = n_q_heads / k.H, keys = ck::keys_per_tile(d);
+  if (k.format != TQ_FMT_F8_BLOCK || documents || b.n_seqs == 0) return l;
+  if ((long long)b.n_tokens * G < (long long)kStagedEntries * ck::rows_per_entry(d) * b.n_seqs) return l;
+  l.tiles = (int)((b.max_ctx + keys - 1) / keys);
+  const size_t n = (size_t)b.n_seqs * l.tiles * k.H;
+  if (n == 0 || n > kStagedMost / ck::tile_bytes(d)) return l;
+  l.k = at;
+  l.v = l.k + n * ck::tile_bytes(d);
+  l.heads = l.v + n * ck::tile_bytes(d);
+  l.bytes = l.heads + up(n * sizeof(ck::StagedHead));
+  return l;
+}
+
 }  // namespace
 
 size_t chunk_workspace(int sm_count, int d, const tq_batch& b, int n_q_heads, int n_kv_heads) {
   return layout(sm_count, d, b.n_seqs, b.n_tokens, b.max_tokens, n_q_heads, n_kv_heads).bytes;
 }
 
-cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, int sm_count, cudaStream_t s) {
+size_t chunk_workspace_most(int sm_count, const DevView& k, const tq_batch& b, int n_q_heads, bool documents) {
+  const size_t least = chunk_workspace(sm_count, k.d, b, n_q_heads, k.H);
+  const StagedLayout l = staged_layout(least, k.d, k, b, n_q_heads, documents);
+  return l.bytes ? l.bytes : least;
+}
+
+cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, size_t workspace_bytes, int sm_count,
+                         cudaStream_t s) {
   const Layout l = layout(sm_count, c.k.d, c.b.n_seqs, c.b.n_tokens, c.b.max_tokens, c.n_q_heads, c.k.H);
   if (l.max_entries * c.k.H * 2 >= (1LL << 31)) return cudaErrorInvalidValue;  // counter indices are 32-bit
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -277,6 +312,17 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, int s
     if (c.k.d == 64) return ck::launch_few64(a, (int)most, vb, sm_count, s);
     if (c.k.d == 128) return ck::launch_few128(a, (int)most, vb, sm_count, s);
     return ck::launch_few256(a, (int)most, vb, sm_count, s);
+  }
+  tq_batch b{};
+  b.n_seqs = c.b.n_seqs;
+  b.n_tokens = c.b.n_tokens;
+  b.max_ctx = c.b.max_ctx;
+  const StagedLayout t = staged_layout(l.bytes, c.k.d, c.k, b, c.n_q_heads, c.first_keys != nullptr);
+  if (t.bytes && workspace_bytes >= t.bytes) {
+    a.staged = ck::Staged{ws + t.k, ws + t.v, reinterpret_cast<ck::StagedHead*>(ws + t.heads), t.tiles};
+    if (c.k.d == 64) return ck::launch_staged64(a, sm_count, s);
+    if (c.k.d == 128) return ck::launch_staged128(a, sm_count, s);
+    return ck::launch_staged256(a, sm_count, s);
   }
   if (c.k.d == 64) return ck::launch_d64(a, vb, sm_count, s);
   if (c.k.d == 128) return ck::launch_d128(a, vb, sm_count, s);

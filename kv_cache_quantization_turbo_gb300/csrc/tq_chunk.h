@@ -29,6 +29,24 @@ struct PlanHead {
   int n_entries;
 };
 
+// f8_block tiles as operands, staged in the workspace (tq_chunk_staged.cuh): tile t of KV head h of sequence b is number
+// (b * tiles + t) * H + h of k, v (tile_bytes each, as the tensor core takes them) and heads.
+struct StagedHead {
+  float k_scale;      // of the tile's K operand; its V operand's is 2^v_exp
+  int v_exp;
+  uint32_t any;       // some bit of missing or marked is set
+  uint32_t pad;
+  uint32_t missing[4], marked[4];  // by key: its page is out of range; its K or V is marked
+  uint32_t pad2[4];
+};
+struct Staged {
+  unsigned char* k;
+  unsigned char* v;
+  StagedHead* heads;
+  int tiles;          // of a sequence
+};
+constexpr int tile_bytes(int d) { return keys_per_tile(d) * d * 2; }
+
 struct Args {
   ChunkArgs c;
   const PlanHead* plan;
@@ -39,11 +57,17 @@ struct Args {
   int rows_cap;
   float scale, q_sign;     // |softmax_scale| log2 e and its sign (0 for a scale of 0)
   float inv_lam_v;
+  Staged staged;           // launch_staged*
 };
 
 cudaError_t launch_d64(const Args& a, int vb, int sm_count, cudaStream_t s);
 cudaError_t launch_d128(const Args& a, int vb, int sm_count, cudaStream_t s);
 cudaError_t launch_d256(const Args& a, int vb, int sm_count, cudaStream_t s);
+
+// f8_block views whose tiles are staged first.
+cudaError_t launch_staged64(const Args& a, int sm_count, cudaStream_t s);
+cudaError_t launch_staged128(const Args& a, int sm_count, cudaStream_t s);
+cudaError_t launch_staged256(const Args& a, int sm_count, cudaStream_t s);
 
 // Entries of at most few_rows(d) rows (tq_chunk_few.cuh); their 2 sm_count CTAs use two partial results each.
 constexpr int few_rows(int d) { return d == 256 ? 8 : 16; }

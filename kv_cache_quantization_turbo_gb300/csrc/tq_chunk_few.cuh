@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
   const DevView &K = a.c.k, &V = a.c.v;
   const bool mods = a.c.softcap > 0.f || a.c.slopes != nullptr;
   // where the 16 keys of a slice, which begin at a multiple of 16, are consecutive vectors
-  const bool runs = !a.c.b.block_table || K.page_size % SK == 0;
+  const bool runs = VB == kF8 || !a.c.b.block_table || K.page_size % SK == 0;
   const uint32_t inv = 0xFFFFFFFFu / (uint32_t)K.page_size;
   uint32_t tab[4] = {0u, 0u, 0u, 0u};
   if constexpr (kTurbo) {

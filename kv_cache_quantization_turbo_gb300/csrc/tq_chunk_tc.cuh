@@ -49,8 +49,6 @@
 // codes would want a score product, and its scores in tensor memory, for each block.
 #pragma once
 
-#include <cuda_fp8.h>
-
 #include "tq_batch.cuh"
 #include "tq_chunk.h"
 #include "tq_tc.cuh"
@@ -129,6 +127,7 @@ struct Bars {
   // q_full is one per item slot: nothing makes the softmax warps wait for an issuer without a step in an item, and with one
   // barrier for all items they could complete a second phase before it has seen the first.  An item slot is written again
   // only once all have left the item.
+  uint64_t turn[2][4];  // (staged kernel) of softmax warp w % 4 of each warpgroup: its partner has done a step
   uint64_t drained[2], q_full[NI], item_full[NI], item_free[NI], loc_full[NL], loc_free[NL];
   uint32_t tmem;
 };
@@ -307,10 +306,10 @@ __device__ __forceinline__ uint32_t clamp_scale(uint32_t s2) {
 }
 // Four e4m3 codes to two fp16 pairs, exact.
 __device__ __forceinline__ void f8_pairs(uint32_t w, uint32_t& a, uint32_t& b) {
-  const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-  const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-  a = (uint32_t)x.x | (uint32_t)x.y << 16;
-  b = (uint32_t)y.x | (uint32_t)y.y << 16;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
 }
 // The exponent of an f8_block word's scale, and the scale.
 __device__ __forceinline__ int f8_exponent(uint32_t w) { return (int)(w >> 23 & 255u) - 127; }
@@ -745,6 +744,237 @@ __device__ __forceinline__ void store8(void* out, int dtype, long long at, const
   else store_row<8>(static_cast<__nv_bfloat16*>(out) + at, x);
 }
 
+// ---------------------------------------------------------------------------
+// the issuer of warpgroup w: its products, QK, PV, PV, QK, ... in order (D = 256: all)
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void issue_products(Bars* B, const Item* items, uint32_t sb, uint32_t tmem, int w, int lane,
+                                               bool& ok) {
+  using Sh = Shape<D>;
+  constexpr int BN = Sh::BN, NB = Sh::NB, PH = Sh::PH;
+  int icnt = 0, gt = 0;  // items and key tiles so far
+  // The whole warp runs the same code, one lane's predicate on the tensor instructions: descriptors and addresses
+  // then stay in uniform registers, where those instructions take them from.  (With one lane in a branch, every
+  // operand was moved there first, and issuing a product took longer than the product.)
+  const uint32_t one = lane == 0;
+  int c = 0;  // this warpgroup's steps so far
+  auto buffer = [&](int x) { return D == 256 ? x & 1 : w; };
+  auto phase = [&](int x) { return D == 256 ? x >> 1 : x; };
+  constexpr uint32_t id_qk = tc::idesc_f16_f32(128, BN);
+  constexpr uint32_t id_pv = tc::idesc_f16_f32(128, D) | (1u << 16);  // B (V) MN-major
+  const uint32_t hi = (uint32_t)(tc::desc_sw128(0) >> 32);  // the same for all operands
+  const uint32_t q_lo = (uint32_t)tc::desc_sw128(sb + Sh::q), k_lo = (uint32_t)tc::desc_sw128(sb + Sh::k);
+  const uint32_t v_lo = (uint32_t)tc::desc_sw128_mn(sb + Sh::v, BN * 128);
+  for (;; ++icnt) {
+    const int is = icnt % NI;
+    wait_warp(ok, &B->item_full[is], icnt / NI);
+    const int kind = uniform(items[is].kind), n = uniform(items[is].n), two = uniform(items[is].two);
+    if (!ok || kind == 0) break;
+    wait_warp(ok, &B->q_full[is], icnt / NI);
+    if (kind == 1) {
+      // own steps: every tile with two row tiles, else every other one; D = 256: all
+      const int first = two || D == 256 ? 0 : w, stride = two || D == 256 ? 1 : 2;
+      const int steps = (n - first + stride - 1) / stride;
+      const uint32_t dq = q_lo + (uint32_t)(two ? w * (Sh::kQTile >> 4) : 0);
+      const bool alone = !two;  // no other issuer uses the tile
+      auto qk = [&](int i) {
+        const int j = gt + first + stride * i, b = j % NB, s = buffer(c + i);
+        wait_warp(ok, &B->k_full[b], j / NB);
+        if (!ok) return;
+        // (no tcgen05 fence: K comes through shared memory, and the score buffer's last readers were seen by the
+        // value product that took their weights)
+        const uint32_t dk = k_lo + (uint32_t)(b * (Sh::kTileB >> 4));
+#pragma unroll
+        for (int kb = 0; kb < D / 64; ++kb)
+          mma4_ss(tmem + s * BN, dq + kb * (128 * 128 >> 4), dk + kb * (128 * BN >> 4), hi, id_qk, kb > 0, one);
+        commit(&B->s_done[s], one);
+        commit(&B->k_free[b], one);
+        if (alone) commit(&B->k_free[b], one);
+      };
+      auto pv = [&](int i) {
+        const int j = gt + first + stride * i, b = j % NB, s = buffer(c + i);
+        wait_warp(ok, &B->v_full[b], j / NB);
+#pragma unroll
+        for (int h = 0; h < PH; ++h) {
+          wait_warp(ok, &B->p_full[s * PH + h], phase(c + i));
+          if (!ok) return;
+          tc::fence_after_sync();
+          mma4_ts(tmem + Sh::tO + w * D, tmem + s * BN + h * (HN / 2),
+                  v_lo + (uint32_t)(b * (Sh::kTileB >> 4) + h * (HN * 128 >> 4)), hi, id_pv, i > 0 || h > 0, one);
+          commit(&B->pv_done[s * PH + h], one);
+        }
+        commit(&B->v_free[b], one);
+        if (alone) commit(&B->v_free[b], one);
+      };
+      // D = 256: one score buffer ahead; else a step's score product needs the buffer of the step before
+      constexpr int kAhead = D == 256 ? 1 : 0;
+      if (steps > 0) qk(0);
+      for (int i = 0; i < steps && ok; ++i) {
+        if (kAhead && i + 1 < steps) qk(i + 1);
+        pv(i);
+        if (!kAhead && i + 1 < steps) qk(i + 1);
+      }
+      c += steps;
+      gt += n;
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
+  }
+  commit(&B->drained[w], one);  // products still in flight end before the tensor memory is freed
+  tc::mbar_wait(&B->drained[w], 0u, 1 << 16);
+}
+
+// ---------------------------------------------------------------------------
+// the result of an item's rows: O / l where this warpgroup alone has the rows, else a partial result; the last of those that
+// share an entry joins them.  Row r of warpgroup wg; some: O holds something, in units of `unit`; m, l: its reference and sum.
+// ---------------------------------------------------------------------------
+template <int D, bool kTurbo>
+__device__ __forceinline__ void finish_rows(const Args& a, const Item& it, int wg, int r, bool valid, bool any_valid,
+                                            long long out_at, uint32_t t_o, bool some, float m, float l, float unit) {
+  const bool mine = D != 256 || wg == 0;  // this warpgroup holds rows
+  const int shares = D == 256 || it.two ? it.n_ctas : 2 * it.n_ctas;
+  const bool whole = shares == 1;
+  // partial slots: [CTA][start or end of its range][warpgroup], O and then m and l of each
+  auto slot_of = [&](int cta, int which, int w) { return ((long long)cta * 2 + which) * 2 + w; };
+  const long long my_slot = slot_of(blockIdx.x, it.slot, wg);
+  // (a share's O: [D / 4][rows_cap] float4, so that the rows of a warp are consecutive)
+  float4* po = reinterpret_cast<float4*>(a.part_o + my_slot * a.rows_cap * D) + r;
+  float norm = a.inv_lam_v * unit;  // folds 1 / lambda and the transform's 1 / sqrt(D)
+  if constexpr (kTurbo) norm *= inv_sqrt_dim<D>();
+  if (mine) {
+    if (whole) norm *= l == 0.f ? 0.f : __fdividef(1.f, l);
+    if (!whole && valid) {
+      float* ml = a.part_ml + my_slot * a.rows_cap * 2 + 2 * r;
+      ml[0] = m;
+      ml[1] = l;
+    }
+    if (some) {
+      // a row without any weight (l = 0) is zeros whatever its accumulator holds
+      const bool zero = l == 0.f;
+      auto emit = [&](int col, const float (&y)[8]) {  // eight columns of this thread's row
+        if (!valid) return;
+        if (whole) store8(a.c.out, a.c.out_dtype, out_at + col, y);
+        else {
+          po[(col >> 2) * a.rows_cap] = make_float4(y[0], y[1], y[2], y[3]);
+          po[((col >> 2) + 1) * a.rows_cap] = make_float4(y[4], y[5], y[6], y[7]);
+        }
+      };
+      if constexpr (!kTurbo) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32 && any_valid; ++c) {
+          uint32_t o[32];
+          tc::tmem_ld32_nw(t_o + 32 * c, o);
+          loaded(o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = zero ? 0.f : __uint_as_float(o[8 * k + e]) * norm;
+            emit(32 * c + 8 * k, y);
+          }
+        }
+      } else {
+        // diag(s) H: the transform of D = 64 n coordinates is one over the n blocks, taken while they are read
+        // (block p of the result: the blocks with signs (-1)^|p & k|), then one over 64 in registers
+#pragma unroll 1
+        for (int p = 0; p < D / 64 && any_valid; ++p) {
+          float z[64];
+#pragma unroll
+          for (int e = 0; e < 64; ++e) z[e] = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < D / 64; ++k) {
+            const float sgn = __popc(p & k) & 1 ? -1.f : 1.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t o[32];
+              tc::tmem_ld32_nw(t_o + 64 * k + 32 * c, o);
+              loaded(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) z[32 * c + e] = fmaf(sgn, __uint_as_float(o[e]), z[32 * c + e]);
+            }
+          }
+          thread_wht<64>(z);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              y[e] = zero ? 0.f : z[8 * k + e] * norm * (float)a.c.tab.signs[64 * p + 8 * k + e];
+            emit(64 * p + 8 * k, y);
+          }
+        }
+      }
+    } else if (whole && valid) {
+      const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < D / 8; ++c) store8(a.c.out, a.c.out_dtype, out_at + 8 * c, z);
+    }
+    if (!whole) {
+      // the last of the warpgroups that share the rows joins them, in the order of the key ranges
+      __threadfence();
+      tc::bar_sync(2 + wg, 128);
+      int done = 0;
+      if (r == 0) done = (int)atomicAdd(a.counters + it.counter + (it.two ? wg : 0), 1u) == shares - 1;
+      const bool join = tc::bar_sync_or(2 + wg, 128, done != 0);
+      if (join) {
+        __threadfence();
+        const int nrows = min(128, it.rows - (it.two ? 128 * wg : 0));
+        const int per = D == 256 || it.two ? 1 : 2;  // partial results per CTA
+#pragma unroll 1
+        for (int i = r; i < nrows * (D / 4); i += 128) {
+          const int jr = i % nrows, jc = i / nrows;
+          // (many loads in flight together; what a share without weight holds is not looked at)
+          auto share = [&](int p) {
+            const int q = min(p, shares - 1), ci = per == 2 ? q >> 1 : q;
+            return slot_of(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? q & 1 : wg) * a.rows_cap;
+          };
+          auto ml_of = [&](long long at) { return __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2) + jr); };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int p0 = 0; p0 < shares; p0 += 8) {
+            float2 ml[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ml[k] = ml_of(share(p0 + k));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].y != 0.f ? ml[k].x : -INFINITY);
+          }
+          if (top == -INFINITY) top = 0.f;
+          float acc[4] = {0.f, 0.f, 0.f, 0.f}, lt = 0.f;
+#pragma unroll 1
+          for (int p0 = 0; p0 < shares; p0 += 4) {
+            float2 ml[4];
+            float4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const long long at = share(p0 + k);
+              ml[k] = ml_of(at);
+              x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + (long long)jc * a.rows_cap + jr);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (p0 + k >= shares || ml[k].y == 0.f) continue;
+              const float w = ex2(ml[k].x - top);
+              lt = fmaf(w, ml[k].y, lt);
+              acc[0] = fmaf(w, x[k].x, acc[0]);
+              acc[1] = fmaf(w, x[k].y, acc[1]);
+              acc[2] = fmaf(w, x[k].z, acc[2]);
+              acc[3] = fmaf(w, x[k].w, acc[3]);
+            }
+          }
+          const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] *= inv;
+          const int jrow = it.row0 + (it.two ? 128 * wg : 0) + jr, jt = jrow / a.c.G;
+          const int jh = it.kvh * a.c.G + (jrow - jt * a.c.G);
+          const long long at = ((long long)(it.tok0 + jt) * a.c.n_q_heads + jh) * D + 4 * jc;
+          if (a.c.out_dtype == TQ_DTYPE_F32) store_row<4>(static_cast<float*>(a.c.out) + at, acc);
+          else if (a.c.out_dtype == TQ_DTYPE_F16) store_row<4>(static_cast<__half*>(a.c.out) + at, acc);
+          else store_row<4>(static_cast<__nv_bfloat16*>(a.c.out) + at, acc);
+        }
+      }
+    }
+  }
+}
+
 template <int D, int VB>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Args a) {
   using Sh = Shape<D>;
@@ -850,76 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (half && lane == 0) tc::mbar_arrive(&B->item_free[is]);
       }
     } else if (warp - kIssuer < Sh::kIssuers) {
-      // The whole warp runs the same code, one lane's predicate on the tensor instructions: descriptors and addresses
-      // then stay in uniform registers, where those instructions take them from.  (With one lane in a branch, every
-      // operand was moved there first, and issuing a product took longer than the product.)
-      const uint32_t one = lane == 0;
-      const int w = warp - kIssuer;  // this issuer's warpgroup
-      int c = 0;                     // its steps so far
-      auto buffer = [&](int x) { return D == 256 ? x & 1 : w; };
-      auto phase = [&](int x) { return D == 256 ? x >> 1 : x; };
-      constexpr uint32_t id_qk = tc::idesc_f16_f32(128, BN);
-      constexpr uint32_t id_pv = tc::idesc_f16_f32(128, D) | (1u << 16);  // B (V) MN-major
-      const uint32_t hi = (uint32_t)(tc::desc_sw128(0) >> 32);  // the same for all operands
-      const uint32_t q_lo = (uint32_t)tc::desc_sw128(sb + Sh::q), k_lo = (uint32_t)tc::desc_sw128(sb + Sh::k);
-      const uint32_t v_lo = (uint32_t)tc::desc_sw128_mn(sb + Sh::v, BN * 128);
-      for (;; ++icnt) {
-        const int is = icnt % NI;
-        wait_warp(ok, &B->item_full[is], icnt / NI);
-        const int kind = uniform(items[is].kind), n = uniform(items[is].n), two = uniform(items[is].two);
-        if (!ok || kind == 0) break;
-        wait_warp(ok, &B->q_full[is], icnt / NI);
-        if (kind == 1) {
-          // own steps: every tile with two row tiles, else every other one; D = 256: all
-          const int first = two || D == 256 ? 0 : w, stride = two || D == 256 ? 1 : 2;
-          const int steps = (n - first + stride - 1) / stride;
-          const uint32_t dq = q_lo + (uint32_t)(two ? w * (Sh::kQTile >> 4) : 0);
-          const bool alone = !two;  // no other issuer uses the tile
-          auto qk = [&](int i) {
-            const int j = gt + first + stride * i, b = j % NB, s = buffer(c + i);
-            wait_warp(ok, &B->k_full[b], j / NB);
-            if (!ok) return;
-            // (no tcgen05 fence: K comes through shared memory, and the score buffer's last readers were seen by the
-            // value product that took their weights)
-            const uint32_t dk = k_lo + (uint32_t)(b * (Sh::kTileB >> 4));
-#pragma unroll
-            for (int kb = 0; kb < D / 64; ++kb)
-              mma4_ss(tmem + s * BN, dq + kb * (128 * 128 >> 4), dk + kb * (128 * BN >> 4), hi, id_qk, kb > 0, one);
-            commit(&B->s_done[s], one);
-            commit(&B->k_free[b], one);
-            if (alone) commit(&B->k_free[b], one);
-          };
-          auto pv = [&](int i) {
-            const int j = gt + first + stride * i, b = j % NB, s = buffer(c + i);
-            wait_warp(ok, &B->v_full[b], j / NB);
-#pragma unroll
-            for (int h = 0; h < PH; ++h) {
-              wait_warp(ok, &B->p_full[s * PH + h], phase(c + i));
-              if (!ok) return;
-              tc::fence_after_sync();
-              mma4_ts(tmem + Sh::tO + w * D, tmem + s * BN + h * (HN / 2),
-                      v_lo + (uint32_t)(b * (Sh::kTileB >> 4) + h * (HN * 128 >> 4)), hi, id_pv, i > 0 || h > 0, one);
-              commit(&B->pv_done[s * PH + h], one);
-            }
-            commit(&B->v_free[b], one);
-            if (alone) commit(&B->v_free[b], one);
-          };
-          // D = 256: one score buffer ahead; else a step's score product needs the buffer of the step before
-          constexpr int kAhead = D == 256 ? 1 : 0;
-          if (steps > 0) qk(0);
-          for (int i = 0; i < steps && ok; ++i) {
-            if (kAhead && i + 1 < steps) qk(i + 1);
-            pv(i);
-            if (!kAhead && i + 1 < steps) qk(i + 1);
-          }
-          c += steps;
-          gt += n;
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
-      }
-      commit(&B->drained[w], one);  // products still in flight end before the tensor memory is freed
-      tc::mbar_wait(&B->drained[w], 0u, 1 << 16);
+      issue_products<D>(B, items, sb, tmem, warp - kIssuer, lane, ok);
     }
     __syncwarp();
   } else if (warp >= 8) {
@@ -1210,151 +1371,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       tc::fence_after_sync();
       c0 += steps;
       gt += it.n;
-      const bool mine = D != 256 || wg == 0;  // this warpgroup holds rows
-
-      // ---- the result: O / l where this warpgroup alone has the rows, else a partial result ----
-      const int shares = D == 256 || it.two ? it.n_ctas : 2 * it.n_ctas;
-      const bool whole = shares == 1;
-      // partial slots: [CTA][start or end of its range][warpgroup], O and then m and l of each
-      auto slot_of = [&](int cta, int which, int w) { return ((long long)cta * 2 + which) * 2 + w; };
-      const long long my_slot = slot_of(blockIdx.x, it.slot, wg);
-      // (a share's O: [D / 4][rows_cap] float4, so that the rows of a warp are consecutive)
-      float4* po = reinterpret_cast<float4*>(a.part_o + my_slot * a.rows_cap * D) + r;
-      float norm = a.inv_lam_v;  // folds 1 / lambda and the transform's 1 / sqrt(D)
-      if constexpr (kTurbo) norm *= inv_sqrt_dim<D>();
-      if constexpr (VB == kF8) norm *= ex2((float)ve);
-      if (mine) {
-        if (whole) norm *= l == 0.f ? 0.f : __fdividef(1.f, l);
-        if (!whole && valid) {
-          float* ml = a.part_ml + my_slot * a.rows_cap * 2 + 2 * r;
-          ml[0] = m;
-          ml[1] = l;
-        }
-        if (last >= 0) {
-          // a row without any weight (l = 0) is zeros whatever its accumulator holds
-          const bool zero = l == 0.f;
-          auto emit = [&](int col, const float (&y)[8]) {  // eight columns of this thread's row
-            if (!valid) return;
-            if (whole) store8(a.c.out, a.c.out_dtype, out_at + col, y);
-            else {
-              po[(col >> 2) * a.rows_cap] = make_float4(y[0], y[1], y[2], y[3]);
-              po[((col >> 2) + 1) * a.rows_cap] = make_float4(y[4], y[5], y[6], y[7]);
-            }
-          };
-          if constexpr (!kTurbo) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32 && any_valid; ++c) {
-              uint32_t o[32];
-              tc::tmem_ld32_nw(t_o + 32 * c, o);
-              loaded(o);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = zero ? 0.f : __uint_as_float(o[8 * k + e]) * norm;
-                emit(32 * c + 8 * k, y);
-              }
-            }
-          } else {
-            // diag(s) H: the transform of D = 64 n coordinates is one over the n blocks, taken while they are read
-            // (block p of the result: the blocks with signs (-1)^|p & k|), then one over 64 in registers
-#pragma unroll 1
-            for (int p = 0; p < D / 64 && any_valid; ++p) {
-              float z[64];
-#pragma unroll
-              for (int e = 0; e < 64; ++e) z[e] = 0.f;
-#pragma unroll 1
-              for (int k = 0; k < D / 64; ++k) {
-                const float sgn = __popc(p & k) & 1 ? -1.f : 1.f;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  uint32_t o[32];
-                  tc::tmem_ld32_nw(t_o + 64 * k + 32 * c, o);
-                  loaded(o);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) z[32 * c + e] = fmaf(sgn, __uint_as_float(o[e]), z[32 * c + e]);
-                }
-              }
-              thread_wht<64>(z);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  y[e] = zero ? 0.f : z[8 * k + e] * norm * (float)a.c.tab.signs[64 * p + 8 * k + e];
-                emit(64 * p + 8 * k, y);
-              }
-            }
-          }
-        } else if (whole && valid) {
-          const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          for (int c = 0; c < D / 8; ++c) store8(a.c.out, a.c.out_dtype, out_at + 8 * c, z);
-        }
-        if (!whole) {
-          // the last of the warpgroups that share the rows joins them, in the order of the key ranges
-          __threadfence();
-          tc::bar_sync(2 + wg, 128);
-          int done = 0;
-          if (r == 0) done = (int)atomicAdd(a.counters + it.counter + (it.two ? wg : 0), 1u) == shares - 1;
-          const bool join = tc::bar_sync_or(2 + wg, 128, done != 0);
-          if (join) {
-            __threadfence();
-            const int nrows = min(128, it.rows - (it.two ? 128 * wg : 0));
-            const int per = D == 256 || it.two ? 1 : 2;  // partial results per CTA
-#pragma unroll 1
-            for (int i = r; i < nrows * (D / 4); i += 128) {
-              const int jr = i % nrows, jc = i / nrows;
-              // (many loads in flight together; what a share without weight holds is not looked at)
-              auto share = [&](int p) {
-                const int q = min(p, shares - 1), ci = per == 2 ? q >> 1 : q;
-                return slot_of(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? q & 1 : wg) * a.rows_cap;
-              };
-              auto ml_of = [&](long long at) { return __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2) + jr); };
-              float top = -INFINITY;
-#pragma unroll 1
-              for (int p0 = 0; p0 < shares; p0 += 8) {
-                float2 ml[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) ml[k] = ml_of(share(p0 + k));
-#pragma unroll
-                for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].y != 0.f ? ml[k].x : -INFINITY);
-              }
-              if (top == -INFINITY) top = 0.f;
-              float acc[4] = {0.f, 0.f, 0.f, 0.f}, lt = 0.f;
-#pragma unroll 1
-              for (int p0 = 0; p0 < shares; p0 += 4) {
-                float2 ml[4];
-                float4 x[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const long long at = share(p0 + k);
-                  ml[k] = ml_of(at);
-                  x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + (long long)jc * a.rows_cap + jr);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (p0 + k >= shares || ml[k].y == 0.f) continue;
-                  const float w = ex2(ml[k].x - top);
-                  lt = fmaf(w, ml[k].y, lt);
-                  acc[0] = fmaf(w, x[k].x, acc[0]);
-                  acc[1] = fmaf(w, x[k].y, acc[1]);
-                  acc[2] = fmaf(w, x[k].z, acc[2]);
-                  acc[3] = fmaf(w, x[k].w, acc[3]);
-                }
-              }
-              const float inv = lt == 0.f ? 0.f : 1.f / lt;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[e] *= inv;
-              const int jrow = it.row0 + (it.two ? 128 * wg : 0) + jr, jt = jrow / a.c.G;
-              const int jh = it.kvh * a.c.G + (jrow - jt * a.c.G);
-              const long long at = ((long long)(it.tok0 + jt) * a.c.n_q_heads + jh) * D + 4 * jc;
-              if (a.c.out_dtype == TQ_DTYPE_F32) store_row<4>(static_cast<float*>(a.c.out) + at, acc);
-              else if (a.c.out_dtype == TQ_DTYPE_F16) store_row<4>(static_cast<__half*>(a.c.out) + at, acc);
-              else store_row<4>(static_cast<__nv_bfloat16*>(a.c.out) + at, acc);
-            }
-          }
-        }
-      }
+      finish_rows<D, kTurbo>(a, it, wg, r, valid, any_valid, out_at, t_o, last >= 0, m, l, VB == kF8 ? ex2((float)ve) : 1.f);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
     }

@@ -285,8 +285,9 @@ size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int 
                               const tq_cache_view* v_view, const tq_score_mods* mods) {
   DevView k{}, v{};
   if (!make_dev_view(k_view, &k) || !make_dev_view(v_view, &v)) return 0;
-  (void)mods;
-  return tq_chunk_workspace_bytes(ctx, batch, n_q_heads, k.H);
+  const size_t least = tq_chunk_workspace_bytes(ctx, batch, n_q_heads, k.H);
+  if (!least || k.d != ctx->d) return 0;
+  return chunk_workspace_most(ctx->sm_count, k, *batch, n_q_heads, mods && mods->first_keys);
 }
 
 tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const void* q, tq_dtype q_dtype,
@@ -339,7 +340,7 @@ tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const
     a.sinks = mods->window ? mods->sinks : 0;
   }
   const float lam_v = a.v.format == TQ_FMT_Q8_0 || f8 ? 1.f : ctx->f16_scale_h[a.v.idx_bits - 1];
-  return cuda_status(launch_chunk(a, lam_v, workspace, ctx->sm_count, cuda_stream(stream)));
+  return cuda_status(launch_chunk(a, lam_v, workspace, workspace_bytes, ctx->sm_count, cuda_stream(stream)));
 }
 
 }  // extern "C"

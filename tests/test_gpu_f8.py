@@ -703,3 +703,133 @@ def test_a_serving_loop(ctxs, d):  # noqa: F811
         c.append(new, lens, k, v)
         c.check_blocks()
         check(c, G, torch.float16, q=q, **mods)
+
+
+# ---------------------------------------------------------------------------
+# chunks whose key tiles are staged once for all their entries
+# ---------------------------------------------------------------------------
+
+STAGED = [  # G, new, lens, page: four entries (256 rows; 128 at 256) and more for a sequence
+    (2, [600], [600], 16),
+    (4, [300], [4000], 64),
+    (1, [1030, 1100], [1030, 2500], 48),
+    (8, [129, 0, 400], [1000, 0, 401], 256),
+    (7, [200], [32000], 16),
+]
+
+
+def staged_cache(ctx, d, G, new, lens, page, H=2, **kw):
+    """The cache, and that a call over it asks for the larger workspace."""
+    c = Cache(ctx, d, H, new, lens, page, padding=2, **kw)
+    least = tq.tq_chunk_workspace_bytes(ctx.h, c.batch, H * G, H)
+    assert tq.tq_chunk_workspace_for(ctx.h, c.batch, H * G, c.kv, c.vv) > least
+    return c
+
+
+def some(n):
+    return np.unique(np.concatenate([np.linspace(0, n - 1, 14).astype(int), [63 % n, 64 % n, 127 % n, 128 % n]]))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G,new,lens,page", STAGED)
+def test_staged_shapes(ctxs, d, G, new, lens, page):  # noqa: F811
+    """Both kernels, the one for the least workspace and the staged one, on the same call."""
+    c = staged_cache(ctxs[d], d, G, new, lens, page).fill(outliers=0.01)
+    for least in (False, True):
+        check(c, G, torch.float16, rows=some(sum(new)), least=least)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("mods", [dict(softcap=5.0), dict(window=1), dict(window=150), dict(bias=True), dict(prefix=[1500]),
+                                  dict(softcap=20.0, window=270, bias=True, prefix=[100]), dict(window=130, sinks=5),
+                                  dict(window=64, sinks=300, bias=True), dict(window=700, sinks=1)])
+def test_staged_score_modifications(ctxs, d, mods):  # noqa: F811
+    c = staged_cache(ctxs[d], d, 2, [600], [1500], 16).fill()
+    check(c, 2, torch.bfloat16, torch.float32, rows=some(600), **mods)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_staged_scales_marks_and_missing_pages(ctxs, d, dtype):  # noqa: F811
+    """Scales that jump by up to 2^16 and blocks of zeros; a marked K and a marked V vector; pages out of range, those behind
+    the window never looked at."""
+    def jumps(i, kind):
+        b = torch.div(i, 16, rounding_mode="floor")
+        return 2.0 ** -((b * 7 % 13).float()) if kind == 0 else torch.where(b % 5 == 3, 0.0, 2.0 ** (b * 11 % 17 - 8).float())
+    c = staged_cache(ctxs[d], d, 2, [520], [900], 16).fill(scale=jumps)
+    check(c, 2, DT[dtype], torch.float32, rows=some(520))
+    q = W.normal_tensor((522, 4, d), seed=3, device="cuda").to(DT[dtype])
+    clean = attend(c, q)
+    for view, key in ((c.kv, 500), (c.vv, 700)):
+        vec = c.vectors(0, [key])[0, 1]
+        view.header.view(torch.int32)[int(vec // 16)] |= 1 << int(vec % 16)
+    got = attend(c, q)
+    torch.cuda.synchronize()
+    pos = torch.as_tensor(c.pos)
+    assert torch.isnan(got[:520, 2:][pos >= 500]).all() and torch.equal(got[:520, :2], clean[:520, :2])
+    assert torch.equal(got[:520][pos < 500], clean[:520][pos < 500]) and status(c.ctx) == 0
+    c = staged_cache(ctxs[d], d, 2, [520], [900], 16).fill()
+    k, v = c.stored(0)
+    c.table = c.table.copy()
+    c.table[0, [2, 40]] = [-1, 10 ** 6]
+    c.set_batch([520], [900])
+    for kw, lost in ((dict(), [2, 40]), (dict(window=300), [40]), (dict(window=300, sinks=20), [40]),
+                     (dict(window=300, sinks=40), [2, 40])):
+        out = attend(c, q, mods_of(c, 4, **kw))
+        torch.cuda.synchronize()
+        assert status(c.ctx) == 2
+        missing = np.isin(np.arange(900) // 16, lost)
+        at = some(520)
+        want = S.chunk_attention(f64(q)[at], k, v, c.pos[at], 1 / math.sqrt(d), missing=missing, **kw)
+        _, tol = expected(f64(q)[at], k, v, c.pos[at], 1 / math.sqrt(d), True, DT[dtype], **kw)
+        assert (np.abs(f64(out)[at] - want) <= 2 * tol + rounding(out.dtype, want)).all(), kw
+
+
+def test_staged_repeats_streams_graphs_and_layers(ctxs):  # noqa: F811
+    d = 128
+    c = staged_cache(ctxs[d], d, 2, [700, 500], [2000, 900], 32, H=4, n_layers=3, layer=2).fill()
+    q = W.normal_tensor((c.n_tokens, 8, d), seed=1, device="cuda").half()
+    m = mods_of(c, 8, window=900, sinks=3)
+    want = [attend(c, q), attend(c, q, m)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(attend(c, q, m if i else None, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+    n = tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 8, c.kv, c.vv)
+    ws, out = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attend(c, q, m, stream=torch.cuda.current_stream(), ws=ws, out=out)
+        attend(c, q, None, stream=torch.cuda.current_stream(), ws=ws, out=out)  # the same workspace, one after the other
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:c.rows], want[0][:c.rows])
+    # lengths that break the bounds: zeros in their rows.  (The others' work is cut elsewhere then, so that their sums differ
+    # in the last bits: weights and values of order 1, a rounding of 2^-11 on each side and of the outputs.)
+    c.batch = c.batch_of([700, 500], [2000, 300], 2, max_ctx=2000)
+    out = attend(c, q, out=torch.full_like(q, 9.0))
+    torch.cuda.synchronize()
+    assert status(c.ctx) == 1 and not out[700:1200].any() and (out[1200:] == 9.0).all()
+    assert (out[:700].float() - want[0][:700].float()).abs().max() < 2.0 ** -9
+
+
+def test_staged_is_not_for_documents_or_too_large_batches(ctxs):  # noqa: F811
+    c = staged_cache(ctxs[64], 64, 2, [600], [600], 16).fill()
+    least = tq.tq_chunk_workspace_bytes(c.ctx.h, c.batch, 4, 2)
+    first = np.concatenate([c.pos - c.pos % 200, [0, 0]])
+    m = mods_of(c, 4, first=first)
+    assert tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 4, c.kv, c.vv, m) == least
+    check(c, 2, torch.float16, first=first, rows=some(600))
+    huge = tq.Batch(c.batch.cu_tokens, c.batch.seq_lens, torch.zeros((1, 1 << 24), dtype=torch.int32, device="cuda"), 600, 600,
+                    1 << 28)
+    assert tq.tq_chunk_workspace_for(c.ctx.h, huge, 4, c.kv, c.vv) == tq.tq_chunk_workspace_bytes(c.ctx.h, huge, 4, 2)
+    q8 = tq.alloc_view("q8_0", 64, 2, 16, 40)
+    assert tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 4, q8, q8) == least
