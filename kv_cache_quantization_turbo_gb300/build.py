@@ -20,7 +20,7 @@ SOURCES = ["tq_api.cpp", "tq_encode.cu", "tq_decode.cu", "tq_decode_mma64.cu", "
            "tq_decode_mma256.cu", "tq_decode_static.cu", "tq_dequant.cu", "tq_persist.cpp",
            "tq_prefill.cu", "tq_step.cpp", "tq_rope.cu", "tq_norm.cu", "tq_append.cu", "tq_append_f8.cu", "tq_chunk.cu",
            "tq_chunk64.cu", "tq_chunk128.cu", "tq_chunk256.cu", "tq_few64.cu",
-           "tq_few128.cu", "tq_few256.cu", "tq_staged64.cu", "tq_staged128.cu", "tq_staged256.cu"]
+           "tq_few128.cu", "tq_few256.cu", "tq_staged64.cu", "tq_staged128.cu"]
 
 
 def _nvcc() -> str:

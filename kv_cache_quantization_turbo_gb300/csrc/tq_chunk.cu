@@ -236,11 +236,12 @@ Layout layout(int sm_count, int d, long long n_seqs, long long n_tokens, long lo
   return l;
 }
 
-// Staging f8_block tiles pays where each is used by some entries: converting one once costs about two conversions by the
-// entry that needs it, and the tile's way through the kernel is then shorter (tq_chunk_staged.cuh has both sides measured).
-// The batch's average decides, as far as the host knows it; documents (first_keys) are left to the other kernel, which
-// does not look at pages that no row sees.
-constexpr int kStagedEntries = 4;
+// Staging f8_block tiles pays where enough entries use each.  8 KV heads of 128, 4 query heads each, us staged and not: one
+// sequence at 32K, 8 entries 306 and 323, 6 260 and 260, 4 227 and 213, 64 1515 and 2050; 8 sequences at 4K, 8 entries
+// each 326 and 349, 64 1205 and 1501; with a window of 1024, 16 entries of 64 tokens (8 uses of a tile) 282 and 284, 64 (14
+// uses) 804 and 888.  At head size 256 it never does.  The batch's average decides, as far as the host knows it; documents
+// (first_keys) are left to the other kernel, which does not look at pages that no row sees.
+constexpr int staged_uses(int d) { return d == 64 ? 6 : 8; }
 constexpr size_t kStagedMost = (size_t)8 << 30;
 
 struct StagedLayout {
@@ -248,11 +249,15 @@ struct StagedLayout {
   int tiles;
 };
 
-StagedLayout staged_layout(size_t at, int d, const DevView& k, const tq_batch& b, int n_q_heads, bool documents) {
+StagedLayout staged_layout(size_t at, int d, const DevView& k, const tq_batch& b, int n_q_heads, bool documents, int window) {
   StagedLayout l{};
   const long long G = n_q_heads / k.H, keys = ck::keys_per_tile(d);
-  if (k.format != TQ_FMT_F8_BLOCK || documents || b.n_seqs == 0) return l;
-  if ((long long)b.n_tokens * G < (long long)kStagedEntries * ck::rows_per_entry(d) * b.n_seqs) return l;
+  if (k.format != TQ_FMT_F8_BLOCK || d == 256 || documents || b.n_seqs == 0) return l;
+  // a sequence's tokens, its entries, the keys that one of them sees, the keys staged
+  const double tokens = (double)b.n_tokens / b.n_seqs, per = (double)ck::rows_per_entry(d) / G, entries = tokens / per;
+  const double seen = window && window < b.max_ctx ? window + per : b.max_ctx;
+  const double staged = window && window + tokens < b.max_ctx ? window + tokens : b.max_ctx;
+  if (!(entries * seen >= staged_uses(d) * staged)) return l;
   l.tiles = (int)((b.max_ctx + keys - 1) / keys);
   const size_t n = (size_t)b.n_seqs * l.tiles * k.H;
   if (n == 0 || n > kStagedMost / ck::tile_bytes(d)) return l;
@@ -269,9 +274,9 @@ size_t chunk_workspace(int sm_count, int d, const tq_batch& b, int n_q_heads, in
   return layout(sm_count, d, b.n_seqs, b.n_tokens, b.max_tokens, n_q_heads, n_kv_heads).bytes;
 }
 
-size_t chunk_workspace_most(int sm_count, const DevView& k, const tq_batch& b, int n_q_heads, bool documents) {
+size_t chunk_workspace_most(int sm_count, const DevView& k, const tq_batch& b, int n_q_heads, bool documents, int window) {
   const size_t least = chunk_workspace(sm_count, k.d, b, n_q_heads, k.H);
-  const StagedLayout l = staged_layout(least, k.d, k, b, n_q_heads, documents);
+  const StagedLayout l = staged_layout(least, k.d, k, b, n_q_heads, documents, window);
   return l.bytes ? l.bytes : least;
 }
 
@@ -317,12 +322,10 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, size_
   b.n_seqs = c.b.n_seqs;
   b.n_tokens = c.b.n_tokens;
   b.max_ctx = c.b.max_ctx;
-  const StagedLayout t = staged_layout(l.bytes, c.k.d, c.k, b, c.n_q_heads, c.first_keys != nullptr);
+  const StagedLayout t = staged_layout(l.bytes, c.k.d, c.k, b, c.n_q_heads, c.first_keys != nullptr, c.window);
   if (t.bytes && workspace_bytes >= t.bytes) {
     a.staged = ck::Staged{ws + t.k, ws + t.v, reinterpret_cast<ck::StagedHead*>(ws + t.heads), t.tiles};
-    if (c.k.d == 64) return ck::launch_staged64(a, sm_count, s);
-    if (c.k.d == 128) return ck::launch_staged128(a, sm_count, s);
-    return ck::launch_staged256(a, sm_count, s);
+    return c.k.d == 64 ? ck::launch_staged64(a, sm_count, s) : ck::launch_staged128(a, sm_count, s);
   }
   if (c.k.d == 64) return ck::launch_d64(a, vb, sm_count, s);
   if (c.k.d == 128) return ck::launch_d128(a, vb, sm_count, s);

@@ -67,7 +67,6 @@ cudaError_t launch_d256(const Args& a, int vb, int sm_count, cudaStream_t s);
 // f8_block views whose tiles are staged first.
 cudaError_t launch_staged64(const Args& a, int sm_count, cudaStream_t s);
 cudaError_t launch_staged128(const Args& a, int sm_count, cudaStream_t s);
-cudaError_t launch_staged256(const Args& a, int sm_count, cudaStream_t s);
 
 // Entries of at most few_rows(d) rows (tq_chunk_few.cuh); their 2 sm_count CTAs use two partial results each.
 constexpr int few_rows(int d) { return d == 256 ? 8 : 16; }

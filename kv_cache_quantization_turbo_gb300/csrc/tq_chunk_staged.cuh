@@ -195,7 +195,8 @@ __device__ __forceinline__ void modify(uint32_t (&x)[64], const ChunkArgs& c, co
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_constant__ Args a) {
   using Sh = Shape<D>;
-  constexpr int BN = Sh::BN, NB = Sh::NB, PH = Sh::PH;
+  static_assert(D <= 128, "at 256 the other kernel is faster for every batch");
+  constexpr int BN = Sh::BN, NB = Sh::NB, PH = 2;  // parts of a step
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = tc::smem_addr(sm);
@@ -292,8 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
     setmaxnreg_inc<kRegsSoftmax>();
     const int wg = warp >> 2, r = tid & 127;
     int c0 = 0, c1 = 0;  // this warpgroup's steps so far, the other's
-    auto buffer = [&](int x) { return D == 256 ? x & 1 : wg; };
-    auto phase = [&](int x) { return D == 256 ? x >> 1 : x; };
+    const int s = wg;  // its score buffer
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const bool mods = a.c.softcap > 0.f || a.c.slopes != nullptr;
     for (;; ++icnt) {
@@ -337,9 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
         if (a.c.slopes) me.slope = a.c.slopes[head] * kLog2e;
       }
       const int all_lo = __reduce_max_sync(kFull, me.lo), all_hi = __reduce_min_sync(kFull, me.hi);
-      const int first = it.two || D == 256 ? 0 : wg, stride = it.two || D == 256 ? 1 : 2;
-      const int steps = D == 256 && wg ? 0 : (it.n - first + stride - 1) / stride;
-      const uint32_t t_o = tmem + Sh::tO + (D == 256 ? 0 : wg * D) + lanes;
+      const int first = it.two ? 0 : wg, stride = it.two ? 1 : 2, steps = (it.n - first + stride - 1) / stride;
+      const uint32_t t_o = tmem + Sh::tO + wg * D + lanes;
       const bool live = valid && me.lo < me.hi;  // sees some key
       const bool any_valid = __any_sync(kFull, valid);  // a warp without rows only keeps the barriers
       float m = -INFINITY, l = 0.f;
@@ -358,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
       int next_tile = tile_at_step(0);
       uint4 next = steps > 0 ? head_of(next_tile) : make_uint4(0u, 0u, 0u, 0u);
       for (int i = 0; i < steps; ++i) {
-        const int s = buffer(c0 + i), tile = next_tile;
+        const int tile = next_tile;
         const uint4 hd = next;
         next_tile = tile_at_step(i + 1);
         if (i + 1 < steps) next = head_of(next_tile);
@@ -366,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
         const int v_exp = (int)hd.y, key0 = tile * BN;
         const float f = mods ? 1.f : fmaxf(me.sl * k_scale, 1.2e-38f);  // scores to log2 units
         const uint32_t t_s = tmem + s * BN + lanes;
-        wait_warp(ok, &B->s_done[s], phase(c0 + i));
+        wait_warp(ok, &B->s_done[s], c0 + i);
         tc::fence_after_sync();
         const bool special = mods || key0 < all_lo || key0 + BN > all_hi || hd.z;
         auto change = [&](uint32_t (&x)[64], int h) {
@@ -414,63 +413,49 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&B->p_full[s * PH + h]);
           last = s * PH + h;
-          last_phase = phase(c0 + i);
+          last_phase = c0 + i;
         };
         // The two softmax warps of an SM sub-partition take turns, step by step: then one's products run while the other has
         // the sub-partition to itself.  Left alone they fall into step, and the tensor core and the softmax take turns.
         auto pass_on = [&]() {
-          if (D != 256 && lane == 0) tc::mbar_arrive(&B->turn[1 - wg][warp & 3]);
+          if (lane == 0) tc::mbar_arrive(&B->turn[1 - wg][warp & 3]);
         };
         int todo = 0;  // parts before this one are published
         if (any_valid && !unset && v_exp <= ve) {
           uint32_t x0[64], pk[32];
           float2 u[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           tmem_ask64(t_s, x0);
-          if constexpr (PH == 2) {
-            uint32_t x1[64], qk[32];
-            float2 w[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            tmem_ask64(t_s + HN, x1);
-            arrived(x0);
-            arrived(x1);
-            if (special) {
-              change(x0, 0);
-              change(x1, 1);
-            }
-            if constexpr (D != 256) wait_warp(ok, &B->turn[wg][warp & 3], wg ? c1 + i : c1 + i - 1);
-            weights(x0, lower, pk, u);
-            weights(x0, upper, pk, u);
-            float sum = sum_of(u);
-            weights(x1, lower, qk, w);  // (while the first part's sum is looked at)
+          uint32_t x1[64], qk[32];
+          float2 w[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          tmem_ask64(t_s + HN, x1);
+          arrived(x0);
+          arrived(x1);
+          if (special) {
+            change(x0, 0);
+            change(x1, 1);
+          }
+          wait_warp(ok, &B->turn[wg][warp & 3], wg ? c1 + i : c1 + i - 1);
+          weights(x0, lower, pk, u);
+          weights(x0, upper, pk, u);
+          float sum = sum_of(u);
+          weights(x1, lower, qk, w);  // (while the first part's sum is looked at)
+          if (!too_large(sum)) {
+            l += sum;
+            store(0, pk);
+            weights(x1, upper, qk, w);  // (while the first part's weights are stored)
+            publish(0);
+            todo = 1;
+            sum = sum_of(w);
             if (!too_large(sum)) {
               l += sum;
-              store(0, pk);
-              weights(x1, upper, qk, w);  // (while the first part's weights are stored)
-              publish(0);
-              todo = 1;
-              sum = sum_of(w);
-              if (!too_large(sum)) {
-                l += sum;
-                store(1, qk);
-                pass_on();
-                publish(1);
-                todo = 2;
-              }
-            }
-          } else {
-            arrived(x0);
-            if (special) change(x0, 0);
-            weights(x0, lower, pk, u);
-            weights(x0, upper, pk, u);
-            const float sum = sum_of(u);
-            if (!too_large(sum)) {
-              l += sum;
-              store(0, pk);
-              publish(0);
-              todo = 1;
+              store(1, qk);
+              pass_on();
+              publish(1);
+              todo = 2;
             }
           }
         } else {
-          if constexpr (D != 256) wait_warp(ok, &B->turn[wg][warp & 3], wg ? c1 + i : c1 + i - 1);
+          wait_warp(ok, &B->turn[wg][warp & 3], wg ? c1 + i : c1 + i - 1);
         }
         // The reference is raised, and O and the sum with it, where it is unset, where V's scale rises, and where weights
         // against the reference so far turned out too large: their scores are still there.
@@ -521,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
       if (last >= 0) wait_warp(ok, &B->pv_done[last], last_phase);
       tc::fence_after_sync();
       c0 += steps;
-      c1 += D == 256 ? 0 : (it.n - (it.two ? 0 : 1 - wg) + stride - 1) / stride;
+      c1 += (it.n - (it.two ? 0 : 1 - wg) + stride - 1) / stride;
       gt += it.n;
       finish_rows<D, false>(a, it, wg, r, valid, any_valid, out_at, t_o, last >= 0, m, l, ex2((float)ve));
       __syncwarp();

@@ -824,6 +824,96 @@ __device__ __forceinline__ void issue_products(Bars* B, const Item* items, uint3
   tc::mbar_wait(&B->drained[w], 0u, 1 << 16);
 }
 
+// Partial slots: [CTA][start or end of its range][warpgroup], O and then m and l of each.
+__device__ __forceinline__ long long partial_slot(int cta, int which, int w) { return ((long long)cta * 2 + which) * 2 + w; }
+
+// The rows of an entry (row tile wg of two) from its shares, by 128 threads, r: their index.  Not inlined: what it holds in
+// registers would push out what the loop over the tiles keeps.
+template <int D>
+__device__ __noinline__ void join_rows(const Args& a, const Item& it, int wg, int r, int shares) {
+  const int nrows = min(128, it.rows - (it.two ? 128 * wg : 0));
+  const int per = D == 256 || it.two ? 1 : 2;  // partial results per CTA
+  // A thread keeps to one row: its shares' references and sums are looked at once, then kC columns of kS shares are
+  // loaded at a time.  (Row and column from a running index, so that every four columns began with the row's shares
+  // again, took 60 us of the 75 of 64 tokens that see 1024 keys.)
+  const int groups = 128 / nrows, jr = r % nrows, g = r / nrows;
+  if (g < groups) {
+    constexpr int kC = 4, kS = 4;
+    // (what a share without weight holds is not looked at)
+    auto share = [&](int p) {
+      const int q = min(p, shares - 1), ci = per == 2 ? q >> 1 : q;
+      return partial_slot(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? q & 1 : wg) * a.rows_cap;
+    };
+    auto ml_of = [&](long long at) { return __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2) + jr); };
+    float top = -INFINITY, lt = 0.f;
+#pragma unroll 1
+    for (int p0 = 0; p0 < shares; p0 += 8) {
+      float2 ml[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ml[k] = ml_of(share(p0 + k));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].y != 0.f ? ml[k].x : -INFINITY);
+    }
+    if (top == -INFINITY) top = 0.f;
+#pragma unroll 1
+    for (int p0 = 0; p0 < shares; p0 += 8) {
+      float2 ml[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ml[k] = ml_of(share(p0 + k));
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (p0 + k < shares && ml[k].y != 0.f) lt = fmaf(ex2(ml[k].x - top), ml[k].y, lt);
+    }
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+    const int jrow = it.row0 + (it.two ? 128 * wg : 0) + jr, jt = jrow / a.c.G;
+    const int jh = it.kvh * a.c.G + (jrow - jt * a.c.G);
+    const long long to = ((long long)(it.tok0 + jt) * a.c.n_q_heads + jh) * D;
+#pragma unroll 1
+    for (int c0 = g; c0 < D / 4; c0 += kC * groups) {
+      float acc[kC][4];
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+#pragma unroll 1
+      for (int p0 = 0; p0 < shares; p0 += kS) {
+        float2 ml[kS];
+        float4 x[kS][kC];
+#pragma unroll
+        for (int k = 0; k < kS; ++k) {
+          const long long at = share(p0 + k);
+          ml[k] = ml_of(at);
+          const float4* o = reinterpret_cast<const float4*>(a.part_o + at * D) + jr;
+#pragma unroll
+          for (int c = 0; c < kC; ++c) x[k][c] = __ldcg(o + (long long)min(c0 + c * groups, D / 4 - 1) * a.rows_cap);
+        }
+#pragma unroll
+        for (int k = 0; k < kS; ++k) {
+          if (p0 + k >= shares || ml[k].y == 0.f) continue;
+          const float w = ex2(ml[k].x - top);
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            acc[c][0] = fmaf(w, x[k][c].x, acc[c][0]);
+            acc[c][1] = fmaf(w, x[k][c].y, acc[c][1]);
+            acc[c][2] = fmaf(w, x[k][c].z, acc[c][2]);
+            acc[c][3] = fmaf(w, x[k][c].w, acc[c][3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        const int jc = c0 + c * groups;
+        if (jc >= D / 4) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[c][e] *= inv;
+        if (a.c.out_dtype == TQ_DTYPE_F32) store_row<4>(static_cast<float*>(a.c.out) + to + 4 * jc, acc[c]);
+        else if (a.c.out_dtype == TQ_DTYPE_F16) store_row<4>(static_cast<__half*>(a.c.out) + to + 4 * jc, acc[c]);
+        else store_row<4>(static_cast<__nv_bfloat16*>(a.c.out) + to + 4 * jc, acc[c]);
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // the result of an item's rows: O / l where this warpgroup alone has the rows, else a partial result; the last of those that
 // share an entry joins them.  Row r of warpgroup wg; some: O holds something, in units of `unit`; m, l: its reference and sum.
@@ -834,9 +924,7 @@ __device__ __forceinline__ void finish_rows(const Args& a, const Item& it, int w
   const bool mine = D != 256 || wg == 0;  // this warpgroup holds rows
   const int shares = D == 256 || it.two ? it.n_ctas : 2 * it.n_ctas;
   const bool whole = shares == 1;
-  // partial slots: [CTA][start or end of its range][warpgroup], O and then m and l of each
-  auto slot_of = [&](int cta, int which, int w) { return ((long long)cta * 2 + which) * 2 + w; };
-  const long long my_slot = slot_of(blockIdx.x, it.slot, wg);
+  const long long my_slot = partial_slot(blockIdx.x, it.slot, wg);
   // (a share's O: [D / 4][rows_cap] float4, so that the rows of a warp are consecutive)
   float4* po = reinterpret_cast<float4*>(a.part_o + my_slot * a.rows_cap * D) + r;
   float norm = a.inv_lam_v * unit;  // folds 1 / lambda and the transform's 1 / sqrt(D)
@@ -917,59 +1005,7 @@ __device__ __forceinline__ void finish_rows(const Args& a, const Item& it, int w
       const bool join = tc::bar_sync_or(2 + wg, 128, done != 0);
       if (join) {
         __threadfence();
-        const int nrows = min(128, it.rows - (it.two ? 128 * wg : 0));
-        const int per = D == 256 || it.two ? 1 : 2;  // partial results per CTA
-#pragma unroll 1
-        for (int i = r; i < nrows * (D / 4); i += 128) {
-          const int jr = i % nrows, jc = i / nrows;
-          // (many loads in flight together; what a share without weight holds is not looked at)
-          auto share = [&](int p) {
-            const int q = min(p, shares - 1), ci = per == 2 ? q >> 1 : q;
-            return slot_of(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? q & 1 : wg) * a.rows_cap;
-          };
-          auto ml_of = [&](long long at) { return __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2) + jr); };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int p0 = 0; p0 < shares; p0 += 8) {
-            float2 ml[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) ml[k] = ml_of(share(p0 + k));
-#pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].y != 0.f ? ml[k].x : -INFINITY);
-          }
-          if (top == -INFINITY) top = 0.f;
-          float acc[4] = {0.f, 0.f, 0.f, 0.f}, lt = 0.f;
-#pragma unroll 1
-          for (int p0 = 0; p0 < shares; p0 += 4) {
-            float2 ml[4];
-            float4 x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const long long at = share(p0 + k);
-              ml[k] = ml_of(at);
-              x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + (long long)jc * a.rows_cap + jr);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (p0 + k >= shares || ml[k].y == 0.f) continue;
-              const float w = ex2(ml[k].x - top);
-              lt = fmaf(w, ml[k].y, lt);
-              acc[0] = fmaf(w, x[k].x, acc[0]);
-              acc[1] = fmaf(w, x[k].y, acc[1]);
-              acc[2] = fmaf(w, x[k].z, acc[2]);
-              acc[3] = fmaf(w, x[k].w, acc[3]);
-            }
-          }
-          const float inv = lt == 0.f ? 0.f : 1.f / lt;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] *= inv;
-          const int jrow = it.row0 + (it.two ? 128 * wg : 0) + jr, jt = jrow / a.c.G;
-          const int jh = it.kvh * a.c.G + (jrow - jt * a.c.G);
-          const long long at = ((long long)(it.tok0 + jt) * a.c.n_q_heads + jh) * D + 4 * jc;
-          if (a.c.out_dtype == TQ_DTYPE_F32) store_row<4>(static_cast<float*>(a.c.out) + at, acc);
-          else if (a.c.out_dtype == TQ_DTYPE_F16) store_row<4>(static_cast<__half*>(a.c.out) + at, acc);
-          else store_row<4>(static_cast<__nv_bfloat16*>(a.c.out) + at, acc);
-        }
+        join_rows<D>(a, it, wg, r, shares);
       }
     }
   }

@@ -204,7 +204,7 @@ struct ChunkArgs {
 };
 size_t chunk_workspace(int sm_count, int d, const tq_batch& b, int n_q_heads, int n_kv_heads);
 // The workspace with which a call over these views is fastest; documents: it has first_keys.
-size_t chunk_workspace_most(int sm_count, const DevView& k, const tq_batch& b, int n_q_heads, bool documents);
+size_t chunk_workspace_most(int sm_count, const DevView& k, const tq_batch& b, int n_q_heads, bool documents, int window);
 cudaError_t launch_chunk(const ChunkArgs& a, float lam_v, void* workspace, size_t workspace_bytes, int sm_count,
                          cudaStream_t s);
 

@@ -287,7 +287,7 @@ size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int 
   if (!make_dev_view(k_view, &k) || !make_dev_view(v_view, &v)) return 0;
   const size_t least = tq_chunk_workspace_bytes(ctx, batch, n_q_heads, k.H);
   if (!least || k.d != ctx->d) return 0;
-  return chunk_workspace_most(ctx->sm_count, k, *batch, n_q_heads, mods && mods->first_keys);
+  return chunk_workspace_most(ctx->sm_count, k, *batch, n_q_heads, mods && mods->first_keys, mods ? mods->window : 0);
 }
 
 tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const void* q, tq_dtype q_dtype,

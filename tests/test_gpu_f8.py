@@ -709,20 +709,20 @@ def test_a_serving_loop(ctxs, d):  # noqa: F811
 # chunks whose key tiles are staged once for all their entries
 # ---------------------------------------------------------------------------
 
-STAGED = [  # G, new, lens, page: four entries (256 rows; 128 at 256) and more for a sequence
-    (2, [600], [600], 16),
-    (4, [300], [4000], 64),
-    (1, [1030, 1100], [1030, 2500], 48),
-    (8, [129, 0, 400], [1000, 0, 401], 256),
-    (7, [200], [32000], 16),
+STAGED = [  # G, new, lens, page: eight entries (of 256 rows) and more for a sequence
+    (4, [600], [600], 16),
+    (8, [300], [4000], 64),
+    (2, [1030, 1100], [1030, 2500], 48),
+    (8, [260, 0, 600], [1000, 0, 601], 256),
+    (7, [300], [32000], 16),
 ]
 
 
-def staged_cache(ctx, d, G, new, lens, page, H=2, **kw):
+def staged_cache(ctx, d, G, new, lens, page, H=2, mods=None, **kw):
     """The cache, and that a call over it asks for the larger workspace."""
     c = Cache(ctx, d, H, new, lens, page, padding=2, **kw)
     least = tq.tq_chunk_workspace_bytes(ctx.h, c.batch, H * G, H)
-    assert tq.tq_chunk_workspace_for(ctx.h, c.batch, H * G, c.kv, c.vv) > least
+    assert tq.tq_chunk_workspace_for(ctx.h, c.batch, H * G, c.kv, c.vv, mods) > least
     return c
 
 
@@ -730,7 +730,7 @@ def some(n):
     return np.unique(np.concatenate([np.linspace(0, n - 1, 14).astype(int), [63 % n, 64 % n, 127 % n, 128 % n]]))
 
 
-@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G,new,lens,page", STAGED)
 def test_staged_shapes(ctxs, d, G, new, lens, page):  # noqa: F811
     """Both kernels, the one for the least workspace and the staged one, on the same call."""
@@ -739,26 +739,27 @@ def test_staged_shapes(ctxs, d, G, new, lens, page):  # noqa: F811
         check(c, G, torch.float16, rows=some(sum(new)), least=least)
 
 
-@pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("mods", [dict(softcap=5.0), dict(window=1), dict(window=150), dict(bias=True), dict(prefix=[1500]),
-                                  dict(softcap=20.0, window=270, bias=True, prefix=[100]), dict(window=130, sinks=5),
-                                  dict(window=64, sinks=300, bias=True), dict(window=700, sinks=1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mods", [dict(softcap=5.0), dict(bias=True), dict(prefix=[2550]), dict(window=300),
+                                  dict(softcap=20.0, window=1000, bias=True, prefix=[1400]), dict(window=700, sinks=5),
+                                  dict(window=300, sinks=900, bias=True), dict(window=1000, sinks=130)])
 def test_staged_score_modifications(ctxs, d, mods):  # noqa: F811
-    c = staged_cache(ctxs[d], d, 2, [600], [1500], 16).fill()
-    check(c, 2, torch.bfloat16, torch.float32, rows=some(600), **mods)
+    window = tq.ScoreMods(window=mods.get("window", 0))
+    c = staged_cache(ctxs[d], d, 8, [1500], [2600], 16, H=1, mods=window).fill()
+    check(c, 8, torch.bfloat16, torch.float32, rows=some(1500), **mods)
 
 
 @pytest.mark.parametrize("dtype", list(DT))
-@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("d", [64, 128])
 def test_staged_scales_marks_and_missing_pages(ctxs, d, dtype):  # noqa: F811
     """Scales that jump by up to 2^16 and blocks of zeros; a marked K and a marked V vector; pages out of range, those behind
     the window never looked at."""
     def jumps(i, kind):
         b = torch.div(i, 16, rounding_mode="floor")
         return 2.0 ** -((b * 7 % 13).float()) if kind == 0 else torch.where(b % 5 == 3, 0.0, 2.0 ** (b * 11 % 17 - 8).float())
-    c = staged_cache(ctxs[d], d, 2, [520], [900], 16).fill(scale=jumps)
-    check(c, 2, DT[dtype], torch.float32, rows=some(520))
-    q = W.normal_tensor((522, 4, d), seed=3, device="cuda").to(DT[dtype])
+    c = staged_cache(ctxs[d], d, 4, [520], [900], 16).fill(scale=jumps)
+    check(c, 4, DT[dtype], torch.float32, rows=some(520))
+    q = W.normal_tensor((522, 8, d), seed=3, device="cuda").to(DT[dtype])
     clean = attend(c, q)
     for view, key in ((c.kv, 500), (c.vv, 700)):
         vec = c.vectors(0, [key])[0, 1]
@@ -766,20 +767,22 @@ def test_staged_scales_marks_and_missing_pages(ctxs, d, dtype):  # noqa: F811
     got = attend(c, q)
     torch.cuda.synchronize()
     pos = torch.as_tensor(c.pos)
-    assert torch.isnan(got[:520, 2:][pos >= 500]).all() and torch.equal(got[:520, :2], clean[:520, :2])
+    assert torch.isnan(got[:520, 4:][pos >= 500]).all() and torch.equal(got[:520, :4], clean[:520, :4])
     assert torch.equal(got[:520][pos < 500], clean[:520][pos < 500]) and status(c.ctx) == 0
-    c = staged_cache(ctxs[d], d, 2, [520], [900], 16).fill()
+    n, total = 1500, 2600
+    c = staged_cache(ctxs[d], d, 8, [n], [total], 16, H=1, mods=tq.ScoreMods(window=300)).fill()
+    q = W.normal_tensor((n + 2, 8, d), seed=3, device="cuda").to(DT[dtype])
     k, v = c.stored(0)
     c.table = c.table.copy()
-    c.table[0, [2, 40]] = [-1, 10 ** 6]
-    c.set_batch([520], [900])
-    for kw, lost in ((dict(), [2, 40]), (dict(window=300), [40]), (dict(window=300, sinks=20), [40]),
-                     (dict(window=300, sinks=40), [2, 40])):
-        out = attend(c, q, mods_of(c, 4, **kw))
+    c.table[0, [2, 100]] = [-1, 10 ** 6]
+    c.set_batch([n], [total])
+    for kw, lost in ((dict(), [2, 100]), (dict(window=300), [100]), (dict(window=300, sinks=20), [100]),
+                     (dict(window=300, sinks=40), [2, 100])):
+        out = attend(c, q, mods_of(c, 8, **kw))
         torch.cuda.synchronize()
         assert status(c.ctx) == 2
-        missing = np.isin(np.arange(900) // 16, lost)
-        at = some(520)
+        missing = np.isin(np.arange(total) // 16, lost)
+        at = some(n)
         want = S.chunk_attention(f64(q)[at], k, v, c.pos[at], 1 / math.sqrt(d), missing=missing, **kw)
         _, tol = expected(f64(q)[at], k, v, c.pos[at], 1 / math.sqrt(d), True, DT[dtype], **kw)
         assert (np.abs(f64(out)[at] - want) <= 2 * tol + rounding(out.dtype, want)).all(), kw
@@ -787,9 +790,10 @@ def test_staged_scales_marks_and_missing_pages(ctxs, d, dtype):  # noqa: F811
 
 def test_staged_repeats_streams_graphs_and_layers(ctxs):  # noqa: F811
     d = 128
-    c = staged_cache(ctxs[d], d, 2, [700, 500], [2000, 900], 32, H=4, n_layers=3, layer=2).fill()
+    c = staged_cache(ctxs[d], d, 4, [700, 500], [2000, 900], 32, H=2, n_layers=3, layer=2).fill()
     q = W.normal_tensor((c.n_tokens, 8, d), seed=1, device="cuda").half()
-    m = mods_of(c, 8, window=900, sinks=3)
+    m = mods_of(c, 8, window=1900, sinks=3)
+    assert tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 8, c.kv, c.vv, m) > tq.tq_chunk_workspace_bytes(c.ctx.h, c.batch, 8, 2)
     want = [attend(c, q), attend(c, q, m)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -822,14 +826,15 @@ def test_staged_repeats_streams_graphs_and_layers(ctxs):  # noqa: F811
 
 
 def test_staged_is_not_for_documents_or_too_large_batches(ctxs):  # noqa: F811
-    c = staged_cache(ctxs[64], 64, 2, [600], [600], 16).fill()
-    least = tq.tq_chunk_workspace_bytes(c.ctx.h, c.batch, 4, 2)
+    c = staged_cache(ctxs[64], 64, 4, [600], [600], 16).fill()
+    least = tq.tq_chunk_workspace_bytes(c.ctx.h, c.batch, 8, 2)
     first = np.concatenate([c.pos - c.pos % 200, [0, 0]])
-    m = mods_of(c, 4, first=first)
-    assert tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 4, c.kv, c.vv, m) == least
-    check(c, 2, torch.float16, first=first, rows=some(600))
+    m = mods_of(c, 8, first=first)
+    assert tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 8, c.kv, c.vv, m) == least
+    check(c, 4, torch.float16, first=first, rows=some(600))
+    assert tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 8, c.kv, c.vv, tq.ScoreMods(window=10)) == least
     huge = tq.Batch(c.batch.cu_tokens, c.batch.seq_lens, torch.zeros((1, 1 << 24), dtype=torch.int32, device="cuda"), 600, 600,
                     1 << 28)
-    assert tq.tq_chunk_workspace_for(c.ctx.h, huge, 4, c.kv, c.vv) == tq.tq_chunk_workspace_bytes(c.ctx.h, huge, 4, 2)
+    assert tq.tq_chunk_workspace_for(c.ctx.h, huge, 8, c.kv, c.vv) == tq.tq_chunk_workspace_bytes(c.ctx.h, huge, 8, 2)
     q8 = tq.alloc_view("q8_0", 64, 2, 16, 40)
-    assert tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 4, q8, q8) == least
+    assert tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 8, q8, q8) == least
