@@ -467,8 +467,8 @@ tq_status tq_norm_rope(const tq_context* ctx, const tq_rope_table* table, const 
  * The gradient of tq_norm_rope.  With g = dout rotated back (its transpose, attn_factor included) and x' = r x:
  *   dx_i = r (g_i weight[i] - x'_i sum_j(g_j weight[j] x'_j) / d),  dweight[i] = sum over tokens and heads of g_i x'_i.
  * x, dout and dx are of type dtype (dx may be dout with the same stride); dweight is device float [d], 4-byte aligned,
- * written and not added to, NULL where it is not wanted.  Sums are fp32, the last ones over partial results fp64, in an
- * order that depends on the sizes alone.  workspace: device, tq_norm_rope_grad_workspace_bytes() bytes, 256-byte aligned
+ * written and not added to, NULL where it is not wanted.  Sums are fp32 (the last ones, over partial results, with what
+ * each addition loses), in an order that depends on the sizes alone.  workspace: device, tq_norm_rope_grad_workspace_bytes() bytes, 256-byte aligned
  * (TQ_ERR_WORKSPACE); calls that may overlap need their own.  n_heads: the heads of q and k together.
  */
 typedef struct tq_norm_grad_rows {

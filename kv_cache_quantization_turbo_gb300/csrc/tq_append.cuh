@@ -20,9 +20,11 @@ struct Place {
   bool padding;  // behind the last sequence
 };
 
-// Row t's place, and its sequence in s.  Called by a whole warp.
-__device__ __forceinline__ Place find_row(const AppendArgs& a, const DevView& v, int t, int lane, bool report, SeqOf& s) {
+// Row t's place, its sequence's number (n_seqs behind the last one) and its data in s.  Called by a whole warp.
+__device__ __forceinline__ Place find_row(const AppendArgs& a, const DevView& v, int t, int lane, bool report, int& seq,
+                                          SeqOf& s) {
   Place p{-1, 0, true};
+  seq = a.b.n_seqs;
   if (t >= a.b.n_tokens) return p;
   // the sequence with cu[b] <= t < cu[b + 1]: 32 probes at a time of a shrinking range [lo, hi)
   int lo = 0, hi = a.b.n_seqs;
@@ -38,7 +40,9 @@ __device__ __forceinline__ Place find_row(const AppendArgs& a, const DevView& v,
     lo += step * k;
     hi = step == 1 ? lo : end;
   }
-  if (lo >= a.b.n_seqs || __ldg(a.b.cu + lo) > t) return p;
+  if (lo >= a.b.n_seqs) return p;
+  seq = lo;
+  if (__ldg(a.b.cu + lo) > t) return p;
   p.padding = false;
   s = seq_of(a.b, lo);
   if (!s.ok) {
@@ -53,7 +57,8 @@ __device__ __forceinline__ Place find_row(const AppendArgs& a, const DevView& v,
 
 __device__ __forceinline__ Place find_place(const AppendArgs& a, const DevView& v, int t, int lane, bool report) {
   SeqOf s;
-  return find_row(a, v, t, lane, report, s);
+  int seq;
+  return find_row(a, v, t, lane, report, seq, s);
 }
 
 // Angle p of a token's table, padded so that the lanes of a group read different banks.

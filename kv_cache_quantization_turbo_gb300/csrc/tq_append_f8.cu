@@ -16,12 +16,50 @@ namespace {
 constexpr int kF8Threads = 256, kF8Warps = kF8Threads / 32;
 constexpr uint32_t kTooLarge = 0x6BE00000u;  // 448 * 2^80 as fp32: what is above, infinities and NaN are marked
 
-// A block's part in the call: the slot of its first token (head 0), its first new row, the number of new tokens (0: the
-// CTA's row begins no block) and the offset of the first.
-struct Part {
+// As rope_at, with the bits of the angle that a float does not hold: the turn is off by 2^-32 then, and what is left is the
+// rounding of sincospi.  A key's code is decided by these, and so is nearly always that of the exact rotation.
+__device__ __forceinline__ float2 rope_finely(uint64_t turns, int pos, float m) {
+  const int top = (int)((turns * (uint64_t)(long long)pos) >> 32);
+  const float f = (float)top, d = (float)(top - (int)f) * (3.14159265f * 0x1p-31f);
+  float s, c;
+  sincospif(f * 0x1p-31f, &s, &c);
+  return make_float2(m * fmaf(-s, d, c), m * fmaf(c, d, s));
+}
+
+// A row's place (as Place has it) and the rows [first, end) of its sequence.
+struct Row {
   long long vec;
-  int row, n, off, pos;
+  int pos, first, end;
+  bool padding;
 };
+
+// The rows [t0, t0 + n) of a CTA, by all its warps.  Up to a row per warp each looks for its own; more rows are mostly of one
+// sequence: every warp looks for the first, whose followers then need a look at the block table each, by a lane, and the
+// warps share the rest.  (Two searches of a warp, one after the other, for 16 rows: 19 us where this takes 16, for 4096 tokens
+// of 8 heads of 128.)
+__device__ __forceinline__ void find_rows(const AppendArgs& a, const DevView& v, int t0, int n, int warp, int lane, bool report,
+                                          Row* rows) {
+  int seq, same = 0;
+  SeqOf s{};
+  auto put = [&](int k, const Place& p) { rows[k] = Row{p.vec, p.pos, s.first, s.first + s.n, p.padding}; };
+  if (n > kF8Warps) {
+    Place p = find_row(a, v, t0, lane, report && warp == 0, seq, s);
+    same = s.ok ? min(n, s.first + s.n - t0) : 1;
+    if (warp == 0 && lane < same) {
+      if (lane > 0) {
+        p.pos += lane;
+        p.vec = position_vector(a.b, v, a.layer, seq, p.pos);
+        if (p.vec < 0 && report) atomicOr(a.tab.status, kFlagBlockTable);
+      }
+      put(lane, p);
+    }
+  }
+  for (int k = same + warp; k < n; k += kF8Warps) {
+    s = SeqOf{};
+    const Place p = find_row(a, v, t0 + k, lane, report, seq, s);
+    if (lane == 0) put(k, p);
+  }
+}
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -40,7 +78,7 @@ template <class T, int D>
 __global__ void __launch_bounds__(kF8Threads, D == 256 ? 1 : 2) append_f8_kernel(const __grid_constant__ Launch L) {
   constexpr int LPV = D / kE, VPP = 32 / LPV, NP = kF8Block / VPP;  // lanes per vector, vectors per pass, passes
   constexpr int ANG = D / 2 + D / 8, W = kE * sizeof(T) / 16;
-  __shared__ Part part[kMaxTc];
+  __shared__ Row rows[kMaxTc];
   __shared__ __align__(16) float cs[kF8Block][ANG], sn[kF8Block][ANG];
   const AppendArgs& a = L.a;
   const bool is_v = blockIdx.y != 0;
@@ -49,30 +87,36 @@ __global__ void __launch_bounds__(kF8Threads, D == 256 ? 1 : 2) append_f8_kernel
   const int t0 = blockIdx.x * L.tc, H = V.H, n_tok = min(L.tc, a.b.n_tokens - t0);
   const long long stride = is_v ? a.v_stride : a.k_stride;
   const T* in = static_cast<const T*>(is_v ? a.xv : a.xk) + 16 * sub;
-  for (int k = warp; k < n_tok; k += kF8Warps) {
-    SeqOf s{};
-    const Place p = find_row(a, V, t0 + k, lane, !is_v, s);
-    if (lane == 0) {
-      const int off = p.pos % kF8Block;
-      Part q{p.vec - off, t0 + k, 0, off, p.pos};
-      if (p.vec >= 0 && (off == 0 || t0 + k == s.first)) q.n = min(kF8Block - off, s.first + s.n - (t0 + k));
-      part[k] = q;
-    }
+  // The rows are on their way to L2 while the first one's sequence is looked for.
+  constexpr int LINES = D * (int)sizeof(T) / 128;  // of a vector
+  for (int h = warp; h < H; h += kF8Warps) {
+    const T* row = static_cast<const T*>(is_v ? a.xv : a.xk) + (long long)t0 * stride + (long long)h * D;
+    for (int i = lane; i < n_tok * LINES; i += 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (long long)(i / LINES) * stride + i % LINES * (128 / (int)sizeof(T))));
   }
+  find_rows(a, V, t0, n_tok, warp, lane, !is_v, rows);
   __syncthreads();
   const tq_rope_table& R = a.rope;
   const int half = R.rotary_dim / 2;
   const bool turn = !is_v && a.has_rope;
-  for (int k = 0; k < n_tok; ++k) {
-    const Part q = part[k];
-    if (q.n == 0) continue;  // (the CTA's threads alike)
+  for (int k = 0; k < n_tok; ++k) {  // (the CTA's threads alike)
+    const Row r = rows[k];
+    struct {  // the slot of the block's first token (head 0), its first new row, the new tokens, the offset of the first
+      long long vec;
+      int row, n, off;
+    } q;
+    q.off = r.pos % kF8Block;
+    q.vec = r.vec - q.off;
+    q.row = t0 + k;
+    q.n = min(kF8Block - q.off, r.end - q.row);
+    if (r.vec < 0 || (q.off && q.row != r.first)) continue;  // no place, or no block begins here
     if (turn) {
       __syncthreads();  // the angles of the block before have been used
       for (int i = tid; i < q.n * half; i += kF8Threads) {
-        const int j = i / half, p = i - j * half;
-        const float2 f = rope_at(R.turns[p], a.positions ? __ldg(a.positions + q.row + j) : q.pos + j, R.attn_factor);
-        cs[j][angle_at(p)] = f.x;
-        sn[j][angle_at(p)] = f.y;
+        const int j = i / half, k = i - j * half;
+        const float2 f = rope_finely(R.turns[k], a.positions ? __ldg(a.positions + q.row + j) : r.pos + j, R.attn_factor);
+        cs[j][angle_at(k)] = f.x;
+        sn[j][angle_at(k)] = f.y;
       }
       __syncthreads();
     }
@@ -163,16 +207,13 @@ __global__ void __launch_bounds__(kF8Threads, D == 256 ? 1 : 2) append_f8_kernel
 template <class T, int D>
 __global__ void __launch_bounds__(kF8Threads) read_f8_kernel(const __grid_constant__ Launch L) {
   constexpr int LPV = D / kE, GROUPS = kF8Threads / LPV, NV = 4;
-  __shared__ Place place[kMaxTc];
+  __shared__ Row rows[kMaxTc];
   const bool is_v = L.a.k_out == nullptr || blockIdx.y != 0;
   const DevView& V = is_v ? L.a.v : L.a.k;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = tid % LPV;
   const int t0 = blockIdx.x * L.tc, H = V.H;
   const int n_tok = min(L.tc, L.a.b.n_tokens - t0), n_vec = n_tok * H;
-  for (int k = warp; k < n_tok; k += kF8Warps) {
-    const Place p = find_place(L.a, V, t0 + k, lane, blockIdx.y == 0);
-    if (lane == 0) place[k] = p;
-  }
+  find_rows(L.a, V, t0, n_tok, warp, lane, blockIdx.y == 0, rows);
   __syncthreads();
   T* out = static_cast<T*>(is_v ? L.a.v_out : L.a.k_out) + (long long)t0 * H * D + 16 * sub;
   for (int v0 = tid / LPV; v0 < n_vec; v0 += NV * GROUPS) {
@@ -182,7 +223,7 @@ __global__ void __launch_bounds__(kF8Threads) read_f8_kernel(const __grid_consta
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int v = v0 + u * GROUPS, t = v / H, h = v - t * H;
-      const Place p = v < n_vec ? place[t] : Place{-1, 0, true};
+      const Row p = v < n_vec ? rows[t] : Row{-1, 0, 0, 0, true};
       padding[u] = p.padding;
       c[u] = make_uint4(0u, 0u, 0u, 0u);
       w[u] = 0u;

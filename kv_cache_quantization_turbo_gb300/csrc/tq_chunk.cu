@@ -211,10 +211,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// The parts of the workspace, in order: head, entries, seq_base, counters, partial results; and the staged tiles, where a
-// call uses them.
+// The parts of the workspace, in order: head, entries, seq_base, counters, partial results, shared entries; and the staged
+// tiles, where a call uses them.
 struct Layout {
-  size_t entries, seq_base, counters, part_o, part_ml, bytes;
+  size_t entries, seq_base, counters, part_o, part_ml, shared, bytes;
   long long max_entries;
   int rows_cap;
 };
@@ -232,7 +232,8 @@ Layout layout(int sm_count, int d, long long n_seqs, long long n_tokens, long lo
   l.counters = l.seq_base + up((n_seqs + 1) * sizeof(int));
   l.part_o = l.counters + up(l.max_entries * n_kv_heads * 2 * sizeof(unsigned));
   l.part_ml = l.part_o + up((size_t)sm_count * 4 * l.rows_cap * d * sizeof(float));
-  l.bytes = l.part_ml + up((size_t)sm_count * 4 * l.rows_cap * 2 * sizeof(float));
+  l.shared = l.part_ml + up((size_t)sm_count * 4 * l.rows_cap * 2 * sizeof(float));
+  l.bytes = l.shared + up((size_t)sm_count * sizeof(ck::Shared));
   return l;
 }
 
@@ -295,7 +296,7 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, size_
   p.rows = ck::rows_per_entry(c.k.d);
   p.keys = ck::keys_per_tile(c.k.d);
   plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   Args a{};
   a.c = c;
@@ -304,6 +305,7 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, size_
   a.counters = p.counters;
   a.part_o = reinterpret_cast<float*>(ws + l.part_o);
   a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
+  a.shared = reinterpret_cast<ck::Shared*>(ws + l.shared);
   a.rows_cap = l.rows_cap;
   a.scale = (c.scale < 0.f ? -c.scale : c.scale) * 1.4426950408889634074f;
   a.q_sign = c.scale > 0.f ? 1.f : c.scale < 0.f ? -1.f : 0.f;
@@ -325,11 +327,14 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, size_
   const StagedLayout t = staged_layout(l.bytes, c.k.d, c.k, b, c.n_q_heads, c.first_keys != nullptr, c.window);
   if (t.bytes && workspace_bytes >= t.bytes) {
     a.staged = ck::Staged{ws + t.k, ws + t.v, reinterpret_cast<ck::StagedHead*>(ws + t.heads), t.tiles};
-    return c.k.d == 64 ? ck::launch_staged64(a, sm_count, s) : ck::launch_staged128(a, sm_count, s);
+    e = c.k.d == 64 ? ck::launch_staged64(a, sm_count, s) : ck::launch_staged128(a, sm_count, s);
+  } else {
+    e = c.k.d == 64 ? ck::launch_d64(a, vb, sm_count, s) : c.k.d == 128 ? ck::launch_d128(a, vb, sm_count, s)
+                                                                        : ck::launch_d256(a, vb, sm_count, s);
   }
-  if (c.k.d == 64) return ck::launch_d64(a, vb, sm_count, s);
-  if (c.k.d == 128) return ck::launch_d128(a, vb, sm_count, s);
-  return ck::launch_d256(a, vb, sm_count, s);
+  if (e != cudaSuccess) return e;
+  return c.k.d == 64 ? ck::launch_join64(a, sm_count, s) : c.k.d == 128 ? ck::launch_join128(a, sm_count, s)
+                                                                        : ck::launch_join256(a, sm_count, s);
 }
 
 }  // namespace tq

@@ -47,6 +47,11 @@ struct Staged {
 };
 constexpr int tile_bytes(int d) { return keys_per_tile(d) * d * 2; }
 
+// The entry that begins in a CTA's range and ends behind it: the CTAs that share it (0: there is none), its rows.
+struct Shared {
+  int n_ctas, kvh, tok0, row0, rows;
+};
+
 struct Args {
   ChunkArgs c;
   const PlanHead* plan;
@@ -54,6 +59,7 @@ struct Args {
   unsigned int* counters;  // [KV head][entry][row tile]: partial results so far
   float* part_o;           // [CTA][2][2][D / 4][rows_cap][4]
   float* part_ml;          // [CTA][2][2][rows_cap][2]: reference (log2 units), sum
+  Shared* shared;          // [CTA]
   int rows_cap;
   float scale, q_sign;     // |softmax_scale| log2 e and its sign (0 for a scale of 0)
   float inv_lam_v;
@@ -63,6 +69,10 @@ struct Args {
 cudaError_t launch_d64(const Args& a, int vb, int sm_count, cudaStream_t s);
 cudaError_t launch_d128(const Args& a, int vb, int sm_count, cudaStream_t s);
 cudaError_t launch_d256(const Args& a, int vb, int sm_count, cudaStream_t s);
+// After these or the staged ones: the rows that several CTAs share.
+cudaError_t launch_join64(const Args& a, int sm_count, cudaStream_t s);
+cudaError_t launch_join128(const Args& a, int sm_count, cudaStream_t s);
+cudaError_t launch_join256(const Args& a, int sm_count, cudaStream_t s);
 
 // f8_block views whose tiles are staged first.
 cudaError_t launch_staged64(const Args& a, int sm_count, cudaStream_t s);

@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
   tc::fence_after_sync();
   const uint32_t tmem = (uint32_t)uniform((int)B->tmem);
   pdl_wait();  // the staged tiles and the plan
+  pdl_launch_dependents();  // the join's start overlaps the last CTAs
   bool ok = true;
   int icnt = 0;  // items so far
   int gt = 0;    // key tiles so far
@@ -296,10 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
     const int s = wg;  // its score buffer
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const bool mods = a.c.softcap > 0.f || a.c.slopes != nullptr;
+    Shared shared{0, 0, 0, 0, 0};
     for (;; ++icnt) {
       const int is = icnt % NI;
       wait_warp(ok, &B->item_full[is], icnt / NI);
       const Item& it = items[is];
+      if (tid == 0) note_shared(it, shared);
       // A role that gave up leaves here: its partner's waits run out in their turn, and both meet no more barriers.
       if (tc::bar_sync_and(1, 256, ok && it.kind != 0) == false) break;  // (also: the last item's queries are not read any more)
       if (it.kind == 1) {
@@ -512,6 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
     }
+    if (tid == 0) a.shared[blockIdx.x] = shared;
   }
   if (!ok && lane == 0) atomicOr(a.c.tab.status, kFlagTimeout);
   tc::fence_before_sync();

@@ -827,96 +827,126 @@ __device__ __forceinline__ void issue_products(Bars* B, const Item* items, uint3
 // Partial slots: [CTA][start or end of its range][warpgroup], O and then m and l of each.
 __device__ __forceinline__ long long partial_slot(int cta, int which, int w) { return ((long long)cta * 2 + which) * 2 + w; }
 
-// The rows of an entry (row tile wg of two) from its shares, by 128 threads, r: their index.  Not inlined: what it holds in
-// registers would push out what the loop over the tiles keeps.
-template <int D>
-__device__ __noinline__ void join_rows(const Args& a, const Item& it, int wg, int r, int shares) {
-  const int nrows = min(128, it.rows - (it.two ? 128 * wg : 0));
-  const int per = D == 256 || it.two ? 1 : 2;  // partial results per CTA
-  // A thread keeps to one row: its shares' references and sums are looked at once, then kC columns of kS shares are
-  // loaded at a time.  (Row and column from a running index, so that every four columns began with the row's shares
-  // again, took 60 us of the 75 of 64 tokens that see 1024 keys.)
-  const int groups = 128 / nrows, jr = r % nrows, g = r / nrows;
-  if (g < groups) {
-    constexpr int kC = 4, kS = 4;
-    // (what a share without weight holds is not looked at)
-    auto share = [&](int p) {
-      const int q = min(p, shares - 1), ci = per == 2 ? q >> 1 : q;
-      return partial_slot(it.first_cta + ci, ci == 0 ? 1 : 0, per == 2 ? q & 1 : wg) * a.rows_cap;
-    };
-    auto ml_of = [&](long long at) { return __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2) + jr); };
-    float top = -INFINITY, lt = 0.f;
+// Four columns from 4 jc on of row `row` of a sequence.
+__device__ __forceinline__ void store4(const Args& a, int D, int kvh, int tok0, int row, int jc, const float (&y)[4]) {
+  const int t = row / a.c.G, head = kvh * a.c.G + (row - t * a.c.G);
+  const long long at = ((long long)(tok0 + t) * a.c.n_q_heads + head) * D + 4 * jc;
+  if (a.c.out_dtype == TQ_DTYPE_F32) store_row<4>(static_cast<float*>(a.c.out) + at, y);
+  else if (a.c.out_dtype == TQ_DTYPE_F16) store_row<4>(static_cast<__half*>(a.c.out) + at, y);
+  else store_row<4>(static_cast<__nv_bfloat16*>(a.c.out) + at, y);
+}
+
+// Partial results `shares` of one row, columns jc0, jc0 + step, ... (C of them) below D / 4, joined in the order of the shares;
+// share(p): slot of share p.  S shares' loads are in flight together; what a share without weight holds is not looked at.
+template <int D, int C, int S, class Share>
+__device__ __forceinline__ void join_columns(const Args& a, int shares, int row, int jc0, int step, Share share,
+                                             float (&acc)[C][4]) {
+  auto ml_of = [&](int p) {
+    return __ldcg(reinterpret_cast<const float2*>(a.part_ml + share(min(p, shares - 1)) * a.rows_cap * 2) + row);
+  };
+  float top = -INFINITY, lt = 0.f;
 #pragma unroll 1
-    for (int p0 = 0; p0 < shares; p0 += 8) {
-      float2 ml[8];
+  for (int p0 = 0; p0 < shares; p0 += 8) {
+    float2 ml[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ml[k] = ml_of(share(p0 + k));
+    for (int k = 0; k < 8; ++k) ml[k] = ml_of(p0 + k);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].y != 0.f ? ml[k].x : -INFINITY);
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].y != 0.f ? ml[k].x : -INFINITY);
+  }
+  if (top == -INFINITY) top = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+#pragma unroll 1
+  for (int p0 = 0; p0 < shares; p0 += S) {
+    float2 ml[S];
+    float4 x[S][C];
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if (p0 + k >= shares) break;  // (the block's threads alike)
+      ml[k] = ml_of(p0 + k);
+      const float4* o = reinterpret_cast<const float4*>(a.part_o + share(p0 + k) * a.rows_cap * D) + row;
+#pragma unroll
+      for (int c = 0; c < C; ++c) x[k][c] = __ldcg(o + (long long)min(jc0 + c * step, D / 4 - 1) * a.rows_cap);
     }
-    if (top == -INFINITY) top = 0.f;
-#pragma unroll 1
-    for (int p0 = 0; p0 < shares; p0 += 8) {
-      float2 ml[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ml[k] = ml_of(share(p0 + k));
+    for (int k = 0; k < S; ++k) {
+      if (p0 + k >= shares || ml[k].y == 0.f) continue;
+      const float w = ex2(ml[k].x - top);
+      lt = fmaf(w, ml[k].y, lt);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (p0 + k < shares && ml[k].y != 0.f) lt = fmaf(ex2(ml[k].x - top), ml[k].y, lt);
-    }
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
-    const int jrow = it.row0 + (it.two ? 128 * wg : 0) + jr, jt = jrow / a.c.G;
-    const int jh = it.kvh * a.c.G + (jrow - jt * a.c.G);
-    const long long to = ((long long)(it.tok0 + jt) * a.c.n_q_heads + jh) * D;
-#pragma unroll 1
-    for (int c0 = g; c0 < D / 4; c0 += kC * groups) {
-      float acc[kC][4];
-#pragma unroll
-      for (int c = 0; c < kC; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
-#pragma unroll 1
-      for (int p0 = 0; p0 < shares; p0 += kS) {
-        float2 ml[kS];
-        float4 x[kS][kC];
-#pragma unroll
-        for (int k = 0; k < kS; ++k) {
-          const long long at = share(p0 + k);
-          ml[k] = ml_of(at);
-          const float4* o = reinterpret_cast<const float4*>(a.part_o + at * D) + jr;
-#pragma unroll
-          for (int c = 0; c < kC; ++c) x[k][c] = __ldcg(o + (long long)min(c0 + c * groups, D / 4 - 1) * a.rows_cap);
-        }
-#pragma unroll
-        for (int k = 0; k < kS; ++k) {
-          if (p0 + k >= shares || ml[k].y == 0.f) continue;
-          const float w = ex2(ml[k].x - top);
-#pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            acc[c][0] = fmaf(w, x[k][c].x, acc[c][0]);
-            acc[c][1] = fmaf(w, x[k][c].y, acc[c][1]);
-            acc[c][2] = fmaf(w, x[k][c].z, acc[c][2]);
-            acc[c][3] = fmaf(w, x[k][c].w, acc[c][3]);
-          }
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const int jc = c0 + c * groups;
-        if (jc >= D / 4) break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[c][e] *= inv;
-        if (a.c.out_dtype == TQ_DTYPE_F32) store_row<4>(static_cast<float*>(a.c.out) + to + 4 * jc, acc[c]);
-        else if (a.c.out_dtype == TQ_DTYPE_F16) store_row<4>(static_cast<__half*>(a.c.out) + to + 4 * jc, acc[c]);
-        else store_row<4>(static_cast<__nv_bfloat16*>(a.c.out) + to + 4 * jc, acc[c]);
+      for (int c = 0; c < C; ++c) {
+        acc[c][0] = fmaf(w, x[k][c].x, acc[c][0]);
+        acc[c][1] = fmaf(w, x[k][c].y, acc[c][1]);
+        acc[c][2] = fmaf(w, x[k][c].z, acc[c][2]);
+        acc[c][3] = fmaf(w, x[k][c].w, acc[c][3]);
       }
     }
   }
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[c][e] *= inv;
+}
+
+// The rows of an entry that one CTA has, from its two warpgroups' results, by 128 threads, r: their index.  A thread keeps to
+// one row.  Not inlined: what it holds in registers would push out what the loop over the tiles keeps.
+template <int D>
+__device__ __noinline__ void join_pair(const Args& a, const Item& it, int r) {
+  const int groups = 128 / it.rows, row = r % it.rows, g = r / it.rows;
+  if (g >= groups) return;
+  constexpr int C = 8;
+#pragma unroll 1
+  for (int c0 = g; c0 < D / 4; c0 += C * groups) {
+    float acc[C][4];
+    join_columns<D, C, 2>(a, 2, row, c0, groups, [&](int p) { return partial_slot(blockIdx.x, it.slot, p); }, acc);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (c0 + c * groups < D / 4) store4(a, D, it.kvh, it.tok0, it.row0 + row, c0 + c * groups, acc[c]);
+  }
+}
+
+// Remembers an item whose entry begins in this CTA's range and ends behind it (the last one, if there is one).
+__device__ __forceinline__ void note_shared(const Item& it, Shared& s) {
+  if (it.kind == 1 && it.n_ctas > 1 && it.slot == 1) s = Shared{it.n_ctas, it.kvh, it.tok0, it.row0, it.rows};
+}
+
+// The rows of entries that several CTAs share: blocks (c, ...) those of the entry that begins in CTA c's range and ends behind
+// it, a row per thread and kJoinColumns groups of four columns per block.  (The last CTA to finish joined them itself, a
+// warpgroup alone: 54 us for 64 tokens of 32 heads of 128 that see 1024 keys, most of it in this.)
+constexpr int kJoinColumns = 4;
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a) {
+  constexpr int kBlocks = D / 4 / kJoinColumns;
+  pdl_wait();  // the shares
+  const Shared en = a.shared[blockIdx.x];
+  const bool two = D != 256 && en.rows > 128;
+  const int w = blockIdx.y / kBlocks, row = threadIdx.x, first = blockIdx.x;
+  if (en.n_ctas == 0 || (w == 1 && !two) || row >= min(128, en.rows - 128 * w)) return;
+  const int per = D == 256 || two ? 1 : 2;  // partial results per CTA
+  auto share = [&](int p) {
+    const int ci = per == 2 ? p >> 1 : p;
+    return partial_slot(first + ci, ci == 0 ? 1 : 0, per == 2 ? p & 1 : w);
+  };
+  const int jc0 = blockIdx.y % kBlocks * kJoinColumns;
+  float acc[kJoinColumns][4];
+  join_columns<D, kJoinColumns, 4>(a, per * en.n_ctas, row, jc0, 1, share, acc);
+#pragma unroll
+  for (int c = 0; c < kJoinColumns; ++c) store4(a, D, en.kvh, en.tok0, en.row0 + 128 * w + row, jc0 + c, acc[c]);
+}
+
+template <int D>
+cudaError_t launch_join(const Args& a, int sm_count, cudaStream_t s) {
+  const cudaError_t e = launch_pdl(join_kernel<D>, dim3((unsigned)sm_count, (D == 256 ? 1 : 2) * D / 4 / kJoinColumns),
+                                   dim3(128), 0, s, a);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 // ---------------------------------------------------------------------------
-// the result of an item's rows: O / l where this warpgroup alone has the rows, else a partial result; the last of those that
-// share an entry joins them.  Row r of warpgroup wg; some: O holds something, in units of `unit`; m, l: its reference and sum.
+// the result of an item's rows: O / l where this warpgroup alone has the rows, else a partial result, joined with the others
+// at once where they are this CTA's.  Row r of warpgroup wg; some: O holds something, in units of `unit`; m, l: its reference and sum.
 // ---------------------------------------------------------------------------
 template <int D, bool kTurbo>
 __device__ __forceinline__ void finish_rows(const Args& a, const Item& it, int wg, int r, bool valid, bool any_valid,
@@ -996,16 +1026,16 @@ __device__ __forceinline__ void finish_rows(const Args& a, const Item& it, int w
       const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       for (int c = 0; c < D / 8; ++c) store8(a.c.out, a.c.out_dtype, out_at + 8 * c, z);
     }
-    if (!whole) {
-      // the last of the warpgroups that share the rows joins them, in the order of the key ranges
+    if (!whole && it.n_ctas == 1) {
+      // the last of the two warpgroups joins them (what several CTAs share: join_kernel)
       __threadfence();
       tc::bar_sync(2 + wg, 128);
       int done = 0;
-      if (r == 0) done = (int)atomicAdd(a.counters + it.counter + (it.two ? wg : 0), 1u) == shares - 1;
+      if (r == 0) done = (int)atomicAdd(a.counters + it.counter, 1u) == 1;
       const bool join = tc::bar_sync_or(2 + wg, 128, done != 0);
       if (join) {
         __threadfence();
-        join_rows<D>(a, it, wg, r, shares);
+        join_pair<D>(a, it, r);
       }
     }
   }
@@ -1072,6 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   tc::fence_after_sync();
   const uint32_t tmem = (uint32_t)uniform((int)B->tmem);
   pdl_wait();  // the plan
+  pdl_launch_dependents();  // the join's start overlaps the last CTAs
   bool ok = true;
   int icnt = 0;  // items so far
   int gt = 0;    // key tiles so far
@@ -1175,10 +1206,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     auto phase = [&](int x) { return D == 256 ? x >> 1 : x; };
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const bool mods = a.c.softcap > 0.f || a.c.slopes != nullptr;
+    Shared shared{0, 0, 0, 0, 0};
     for (;; ++icnt) {
       const int is = icnt % NI;
       wait_warp(ok, &B->item_full[is], icnt / NI);
       const Item& it = items[is];
+      if (tid == 0) note_shared(it, shared);
       // A role that gave up leaves here: its partner's waits run out in their turn, and both meet no more barriers.
       if (tc::bar_sync_and(1, 256, ok && it.kind != 0) == false) break;  // (also: the last item's queries are not read any more)
       if (it.kind == 1) {
@@ -1411,6 +1444,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
     }
+    if (tid == 0) a.shared[blockIdx.x] = shared;
   }
   if (!ok && lane == 0) atomicOr(a.c.tab.status, kFlagTimeout);
   tc::fence_before_sync();

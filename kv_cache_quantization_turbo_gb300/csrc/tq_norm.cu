@@ -6,10 +6,13 @@
 // One pass over the data: 2 (gradient 3) elements moved per element, so HBM bounds it.  d / 16 lanes hold a vector, 8 pairs
 // of coordinates each, whose sums they share by shuffles; such a group walks over heads of one token with the angles and
 // the weight in registers, and asks for the next heads' words before it turns to the first ones.  Queries and keys are
-// heads of one launch.
+// heads of one launch.  4096 tokens of 32 + 8 heads of 128 in bf16: 20.5 us for 84 MB, where a plain copy of them takes 16.2
+// (2, 4 heads per group 25, 22; three CTAs per SM instead of two 23: the words in flight count, not the warps); the gradient
+// 34 us for 126 MB (4 heads per group 38, 16 41; twice or half the CTAs for the partial sums the same).
 //
 // The weight's gradient: a lane adds up its 16 coordinates over the rows of its group, the CTA's groups are joined in
-// shared memory and leave one row of partial sums, and a second kernel adds those rows in their order, in fp64.
+// shared memory and leave one row of partial sums, and a second kernel adds those rows in their order, with what each sum
+// loses carried along (fp64 sums, at this GPU's rate for them, took 21 us for 1210 rows of 128).
 #include <type_traits>
 
 #include "tq_batch.cuh"
@@ -19,7 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPairs = 8;            // of a lane
-constexpr int kGradHeads = 4;        // heads of a group
+constexpr int kHeads = 8;            // most heads of a group
 constexpr int kGradCtasPerSm = 8;
 constexpr int kJoin = 32;            // rows of partial sums that the second kernel adds side by side
 
@@ -68,8 +71,8 @@ __device__ __forceinline__ void fetch(const T* row, const At<MODE>& at, bool on,
     const uint4* q = MODE == kRuns ? reinterpret_cast<const uint4*>(row + at.b(0)) : p + W / 2;
 #pragma unroll
     for (int k = 0; k < W / 2; ++k) {
-      x.w[k] = p[k];
-      x.w[W / 2 + k] = q[k];
+      x.w[k] = __ldcs(p + k);
+      x.w[W / 2 + k] = __ldcs(q + k);
     }
   }
 }
@@ -224,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_kernel(const __grid_con
   __shared__ float joined[kThreads / 32][D];
   const int l = threadIdx.x % LPV, g = threadIdx.x / LPV, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x / L.ctas, c = blockIdx.x - split * L.ctas;
+  pdl_launch_dependents();  // the second kernel's start overlaps this one
   const bool of_k = split >= L.splits_q;
   const NormRows& R = L.n.rows[of_k];
   const int h0 = (of_k ? split - L.splits_q : split) * L.hpt, h1 = min(R.n_heads, h0 + L.hpt);
@@ -309,23 +313,34 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_kernel(const __grid_con
   }
 }
 
+// s += x; what the rounding of the sum leaves goes to lost (the two-sum of Knuth).
+__device__ __forceinline__ void add_exactly(float& s, float& lost, float x) {
+  const float t = __fadd_rn(s, x), v = __fsub_rn(t, s);
+  lost += __fadd_rn(__fsub_rn(s, __fsub_rn(t, v)), __fsub_rn(x, v));
+  s = t;
+}
+
 // The weight's gradient from the CTAs' rows: 32 coordinates of q's (y = 0) or k's weight.
 __global__ void __launch_bounds__(32 * kJoin) weight_kernel(const __grid_constant__ Launch L, int d) {
-  __shared__ double sums[kJoin][33];
+  __shared__ float2 sums[kJoin][33];
   pdl_wait();
   const bool of_k = blockIdx.y != 0;
   const NormRows& R = L.n.rows[of_k];
   if (!R.dweight) return;
   const int first = of_k ? L.splits_q * L.ctas : 0, end = of_k ? L.splits * L.ctas : L.splits_q * L.ctas;
   const int i = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;
-  double s = 0.0;
+  float s = 0.f, lost = 0.f;
 #pragma unroll 8
-  for (int c = first + y; c < end; c += kJoin) s += (double)L.part[(long long)c * d + i];
-  sums[y][threadIdx.x % 32] = s;
+  for (int c = first + y; c < end; c += kJoin) add_exactly(s, lost, L.part[(long long)c * d + i]);
+  sums[y][threadIdx.x % 32] = make_float2(s, lost);
   __syncthreads();
   if (y == 0) {
-    for (int k = 1; k < kJoin; ++k) s += sums[k][threadIdx.x];
-    R.dweight[i] = (float)s;
+    for (int k = 1; k < kJoin; ++k) {
+      const float2 x = sums[k][threadIdx.x];
+      add_exactly(s, lost, x.x);
+      lost += x.y;
+    }
+    R.dweight[i] = s + lost;
   }
 }
 
@@ -338,7 +353,7 @@ cudaError_t launch_forward(Launch& L, int sm_count, cudaStream_t s) {
   // As many heads per group, up to 8, as leave 512 threads on every SM (the angles then cost a few percent); a call that
   // cannot fill the GPU takes one head per group, the shortest chain.
   int hpt = 1;
-  while (hpt < 8 && (long long)n.n_tokens * (heads / (2 * hpt)) * (D / 16) >= (long long)sm_count * 512) hpt *= 2;
+  while (hpt < kHeads && (long long)n.n_tokens * (heads / (2 * hpt)) * (D / 16) >= (long long)sm_count * 512) hpt *= 2;
   L.hpt = hpt;
   L.splits_q = ceil_div(n.rows[0].n_heads, hpt);
   L.splits = L.splits_q + ceil_div(n.rows[1].n_heads, hpt);
@@ -353,7 +368,7 @@ cudaError_t launch_gradient(Launch& L, int sm_count, cudaStream_t s) {
   constexpr int GPC = kThreads / (D / 16);
   const NormArgs& n = L.n;
   int hpt = 1;
-  while (hpt < kGradHeads && hpt < n.rows[0].n_heads + n.rows[1].n_heads) hpt *= 2;
+  while (hpt < kHeads && hpt < n.rows[0].n_heads + n.rows[1].n_heads) hpt *= 2;
   L.hpt = hpt;
   L.splits_q = ceil_div(n.rows[0].n_heads, hpt);
   L.splits = L.splits_q + ceil_div(n.rows[1].n_heads, hpt);

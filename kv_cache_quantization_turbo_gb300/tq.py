@@ -584,39 +584,47 @@ def tq_rope(ctx: int, table: tq_rope_table, x, positions, out, inverse: bool = F
                         _stream(stream))
 
 
-def _norm_parts(table, n: int, parts, weights) -> tuple[int, int]:
-    """(element type of the rows, of the weights) of a norm call's tensors: [tokens, heads, d] each, weights [d]."""
-    dtype = wtype = None
-    for part in parts:
-        shape = part[0].shape
-        for t in part:
-            if len(shape) != 3 or t.shape != shape or shape[0] != n or shape[-1] != table.head_dim:
-                raise ValueError(f"rows {tuple(shape)}, {tuple(t.shape)} for {n} tokens of {table.head_dim}")
-            if dtype is not None and t.dtype != dtype:
-                raise ValueError(f"rows of types {dtype} and {t.dtype}")
-            dtype = t.dtype
-    for w in weights:
-        if w is None:
-            continue
-        if w.shape != (table.head_dim,) or not w.is_contiguous() or not w.is_cuda or (wtype is not None and w.dtype != wtype):
-            raise ValueError(f"weights are contiguous [{table.head_dim}] tensors of one type on the GPU: {tuple(w.shape)}")
-        wtype = w.dtype
-    return _dtype(parts[0][0]), 0 if wtype is None else _dtype([w for w in weights if w is not None][0])
+def _norm_check(x, other, d: int, n: int):
+    """The shape [n, heads, d] and type that the rows of a norm call share."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != d or other.shape != shape or other.dtype != x.dtype:
+        raise ValueError(f"rows {tuple(shape)} {x.dtype}, {tuple(other.shape)} {other.dtype} for {n} tokens of {d}")
+    return shape
+
+
+def _norm_weight(w, d: int):
+    if w is None:
+        return None
+    if w.shape != (d,) or not w.is_contiguous() or not w.is_cuda:
+        raise ValueError(f"weights are contiguous [{d}] tensors on the GPU: {tuple(w.shape)} on {w.device}")
+    return w.data_ptr()
+
+
+def _norm_types(q, q_weight, k, k_weight) -> tuple[int, int]:
+    """Element types of the rows and of the weights, the same for queries and keys."""
+    if q is not None and k is not None and q.dtype != k.dtype:
+        raise ValueError(f"rows of types {q.dtype} and {k.dtype}")
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError(f"weights of types {q_weight.dtype} and {k_weight.dtype}")
+    w = q_weight if q_weight is not None else k_weight
+    return _dtype(k if q is None else q), 0 if w is None else _dtype(w)
 
 
 def tq_norm_rope(ctx: int, table: tq_rope_table, q, q_out, q_weight, k, k_out, k_weight, eps: float, positions,
                  stream=None) -> int:
     """q, q_out [tokens, heads, d] and k, k_out [tokens, kv heads, d], all of one type (q_out may be q, k_out k; one pair may
     be None); weights [d] or None for ones; positions int32 [tokens]."""
-    parts = [(x, o) for x, o in ((q, q_out), (k, k_out)) if x is not None]
-    if not parts or any(o is None for _, o in parts):
+    if (q is None and k is None) or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("queries or keys, and an output for each, are wanted")
-    n = parts[0][0].shape[0]
-    dtype, wtype = _norm_parts(table, n, parts, (q_weight, k_weight))
+    n, d = (k if q is None else q).shape[0], table.head_dim
 
     def rows(x, out, w):
-        return None if x is None else ctypes.byref(tq_norm_rows(
-            x.data_ptr(), _rows(x, x.shape), out.data_ptr(), _rows(out, x.shape), _ptr(w), x.shape[1]))
+        if x is None:
+            return None
+        shape = _norm_check(x, out, d, n)
+        return ctypes.byref(tq_norm_rows(x.data_ptr(), _rows(x, shape), out.data_ptr(), _rows(out, shape),
+                                         _norm_weight(w, d), shape[1]))
+    dtype, wtype = _norm_types(q, q_weight, k, k_weight)
     return _lib.tq_norm_rope(ctx, ctypes.byref(table), rows(q, q_out, q_weight), rows(k, k_out, k_weight), dtype, wtype, eps,
                              n, _positions(positions, n), _stream(stream))
 
@@ -629,20 +637,20 @@ def tq_norm_rope_grad(ctx: int, table: tq_rope_table, q, dq_out, q_weight, dq, d
                       eps: float, positions, workspace, workspace_bytes: int, stream=None) -> int:
     """From the norm's inputs and its outputs' gradients dq_out, dk_out the inputs' gradients dq, dk (dq may be dq_out, dk
     dk_out) and, where they are not None, the weights': dq_weight, dk_weight float32 [d]."""
-    parts = [p for p in ((q, dq_out, dq), (k, dk_out, dk)) if p[0] is not None]
-    if not parts or any(t is None for p in parts for t in p):
+    if (q is None and k is None) or any((x is None) != (t is None) for x, *ts in ((q, dq_out, dq), (k, dk_out, dk)) for t in ts):
         raise ValueError("queries or keys, and their gradients, are wanted")
-    n = parts[0][0].shape[0]
-    dtype, wtype = _norm_parts(table, n, parts, (q_weight, k_weight))
-    for t in (dq_weight, dk_weight):
-        if t is not None and (_short(t) != "float32" or t.shape != (table.head_dim,) or not t.is_contiguous()
-                              or not t.is_cuda):
-            raise ValueError(f"weight gradients are contiguous float32 [{table.head_dim}] tensors on the GPU")
+    n, d = (k if q is None else q).shape[0], table.head_dim
 
     def rows(x, dout, w, dx, dw):
-        return None if x is None else ctypes.byref(tq_norm_grad_rows(
-            x.data_ptr(), _rows(x, x.shape), dout.data_ptr(), _rows(dout, x.shape), _ptr(w), dx.data_ptr(),
-            _rows(dx, x.shape), _ptr(dw), x.shape[1]))
+        if x is None:
+            return None
+        shape = _norm_check(x, dout, d, n)
+        _norm_check(x, dx, d, n)
+        if dw is not None and (_short(dw) != "float32" or dw.shape != (d,) or not dw.is_contiguous() or not dw.is_cuda):
+            raise ValueError(f"weight gradients are contiguous float32 [{d}] tensors on the GPU")
+        return ctypes.byref(tq_norm_grad_rows(x.data_ptr(), _rows(x, shape), dout.data_ptr(), _rows(dout, shape),
+                                              _norm_weight(w, d), dx.data_ptr(), _rows(dx, shape), _ptr(dw), shape[1]))
+    dtype, wtype = _norm_types(q, q_weight, k, k_weight)
     return _lib.tq_norm_rope_grad(ctx, ctypes.byref(table), rows(q, dq_out, q_weight, dq, dq_weight),
                                   rows(k, dk_out, k_weight, dk, dk_weight), dtype, wtype, eps, n,
                                   _positions(positions, n), _ptr(workspace), workspace_bytes, _stream(stream))

@@ -7,7 +7,7 @@ Tolerances, fixed before the first run.  All is fp32 until the result is rounded
   * gradient of x: g has the rotation's 6e-7, x' = r x 1e-6, their sum over d as above 1.2e-6: 4e-6 of what the terms of
     the formula add up to in magnitude, plus half a step;
   * gradient of the weight: terms as above (2e-6), a lane adds up at most 8 rows (5000 tokens) in a chain, a CTA 5 + 8 more,
-    each 2^-24 of the magnitudes so far; the rest is fp64: 4e-6 of the sum of magnitudes.
+    each 2^-24 of the magnitudes so far; the rest carries what it loses along: 4e-6 of the sum of magnitudes.
 """
 import ctypes
 
