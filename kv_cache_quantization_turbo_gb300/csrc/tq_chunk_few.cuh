@@ -291,24 +291,22 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
     constexpr int BN = Shape<D>::BN;
     // The keys of this CTA's tiles, in slices from j0 to end.  Sinks ahead of the windows take the numbers just before
     // the windows' first slice, base: they lie gap keys further ahead.
-    int j0, end, base, gap = 0, low = it.lo;
-    {
-      const int first = max((it.tile + it.s_n) * BN, it.lo) & ~(SK - 1);
-      end = min((it.tile + it.n) * BN, it.hi);
-      j0 = base = first;
-      if (it.s_n > 0) {
-        const int s0 = max(it.s_tile * BN, it.s_lo) & ~(SK - 1), s1 = min((it.s_tile + it.s_n) * BN, it.s_hi);
-        if (it.n == it.s_n) {  // sinks alone
-          j0 = base = s0;
-          end = s1;
-          low = it.s_lo;
-        } else {
-          j0 = first - ((s1 - s0 + SK - 1) & ~(SK - 1));
-          gap = j0 - s0;
-        }
+    int j0 = max(it.tile * BN, it.lo) & ~(SK - 1), end = min((it.tile + it.n) * BN, it.hi), low = it.lo;
+    int base = j0, gap = 0, s_lo = 0, s_hi = 0;
+    if (it.s_n > 0) {
+      s_lo = it.s_lo;
+      s_hi = it.s_hi;
+      const int s0 = max(it.s_tile * BN, s_lo) & ~(SK - 1), s1 = min((it.s_tile + it.s_n) * BN, s_hi);
+      if (it.n == it.s_n) {  // sinks alone
+        j0 = base = s0;
+        end = s1;
+        low = s_lo;
+      } else {
+        base = max((it.tile + it.s_n) * BN, low) & ~(SK - 1);
+        j0 = base - ((s1 - s0 + SK - 1) & ~(SK - 1));
+        gap = j0 - s0;
       }
     }
-    const int s_lo = it.s_lo, s_hi = it.s_hi;
     auto key_of = [&](int n0) { return n0 < base ? n0 - gap : n0; };   // first key of the slice with number n0
     auto low_of = [&](int n0) { return n0 < base ? s_lo : low; };      // the wanted keys of that slice: from here
     auto end_of = [&](int n0) { return n0 < base ? s_hi : end; };      // to here

@@ -108,7 +108,7 @@ struct Item {
   int row0, rows;  // of the sequence's rows
   int lo, hi;      // keys that some row sees
   int tile, n;     // key tiles of this CTA, the first s_n of them sinks ahead of the windows: tile_of()
-  int s_lo, s_hi, s_tile, s_n;
+  int s_n, s_lo, s_hi, s_tile;
   int two;         // two row tiles
   int first_cta, n_ctas, slot;  // CTAs that share the entry; this CTA's partial slot
   int counter;
@@ -388,12 +388,16 @@ struct Items {
         it.kind = u == base ? 2 : 0;  // by the CTA that holds its first unit
       } else if (t0 < t1) {
         it.kind = 1;
-        it.tile = en.lo / Shape<D>::BN + (int)t0 - en.s_tiles;
+        it.tile = en.lo / Shape<D>::BN + (int)t0;
         it.n = (int)(t1 - t0);
-        it.s_lo = en.s_lo;
-        it.s_hi = en.s_hi;
-        it.s_tile = en.s_lo / Shape<D>::BN + (int)t0;
-        it.s_n = (int)max(0LL, min((long long)en.s_tiles, t1) - t0);
+        it.s_n = 0;
+        if (en.s_tiles) {
+          it.tile -= en.s_tiles;
+          it.s_lo = en.s_lo;
+          it.s_hi = en.s_hi;
+          it.s_tile = en.s_lo / Shape<D>::BN + (int)t0;
+          it.s_n = max(0, min(en.s_tiles, (int)t1) - (int)t0);
+        }
         it.first_cta = cta_of(base + kOverhead);
         it.n_ctas = cta_of(base + kOverhead + en.n_tiles - 1) - it.first_cta + 1;
         it.slot = t0 == 0 ? 1 : 0;
@@ -1241,14 +1245,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         continue;
       }
       int lo = 0, hi = 0x7FFFFFFF;  // rows that are not there see everything: they never need a mask
-      int s_lo = 0, s_hi = 0;       // and the sinks [s_lo, s_hi) among the keys before hi
+      int s_lo = 0;                 // and the sinks from s_lo on
       float sl = 1.f, slope = 0.f;
       if (valid) {
         hi = min(it.len, max(pos + 1, it.prefix));
         if (a.c.window) lo = max(lo, pos - a.c.window + 1);
         if (a.c.first_keys) s_lo = max(0, a.c.first_keys[tok]);
         lo = max(lo, s_lo);
-        s_hi = min(sink_end(s_lo, a.c.sinks), hi);
         sl = fmaxf(a.scale * rs[rr], 1.2e-38f);
         if (a.c.slopes) slope = a.c.slopes[head] * kLog2e;
       }
@@ -1263,12 +1266,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       int ve = kF8MinExp;  // (of the warp, f8_block) O is in units of 2^ve: no V scale so far is above
       int last = -1, last_phase = 0;  // barrier and phase of the last part's value product
       for (int i = 0; i < steps; ++i) {
-        const int s = buffer(c0 + i), jt = first + stride * i;
+        const int s = buffer(c0 + i), jt = first + stride * i, tile0 = tile_of(it, jt) * BN;
         wait_warp(ok, &B->s_done[s], phase(c0 + i));
         tc::fence_after_sync();
 #pragma unroll 1
         for (int h = 0; h < PH; ++h) {
-          const int key0 = tile_of(it, jt) * BN + h * HN;
+          const int key0 = tile0 + h * HN;
           const uint32_t t_s = tmem + s * BN + h * HN + lanes;
           if (any_valid) {
             const uint2 mw = *reinterpret_cast<const uint2*>(miss + ((gt + jt) % kMissRing) * 4 + 2 * h);
@@ -1287,6 +1290,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               uint32_t xa[16];
               const bool capped = a.c.softcap > 0.f;
               const float2 cap = cap_factors(a.c.softcap);
+              const int s_hi = valid ? min(sink_end(s_lo, a.c.sinks), hi) : 0;
 #pragma unroll 1
               for (int c = 0; c < HN / 16; ++c) {
                 tc::tmem_ld16_nw(t_s + 16 * c, xa);

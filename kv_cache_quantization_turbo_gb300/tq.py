@@ -157,10 +157,10 @@ def _ptr(x) -> int | None:
     """Device/host address of a tensor, an ndarray, an int, or None."""
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
     if hasattr(x, "data_ptr"):
         return x.data_ptr()
+    if isinstance(x, int):
+        return x
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError(type(x))
