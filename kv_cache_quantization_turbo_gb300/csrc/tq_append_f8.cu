@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(kF8Threads, D == 256 ? 1 : 2) append_f8_kernel
   const int t0 = blockIdx.x * L.tc, H = V.H, n_tok = min(L.tc, a.b.n_tokens - t0);
   const long long stride = is_v ? a.v_stride : a.k_stride;
   const T* in = static_cast<const T*>(is_v ? a.xv : a.xk) + 16 * sub;
+  pdl_launch_dependents();  // the next kernel's start overlaps this one, as this one's the last
+  pdl_wait();
   // The rows are on their way to L2 while the first one's sequence is looked for.
   constexpr int LINES = D * (int)sizeof(T) / 128;  // of a vector
   for (int h = warp; h < H; h += kF8Warps) {
@@ -213,6 +215,8 @@ __global__ void __launch_bounds__(kF8Threads) read_f8_kernel(const __grid_consta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = tid % LPV;
   const int t0 = blockIdx.x * L.tc, H = V.H;
   const int n_tok = min(L.tc, L.a.b.n_tokens - t0), n_vec = n_tok * H;
+  pdl_launch_dependents();
+  pdl_wait();
   find_rows(L.a, V, t0, n_tok, warp, lane, blockIdx.y == 0, rows);
   __syncthreads();
   T* out = static_cast<T*>(is_v ? L.a.v_out : L.a.k_out) + (long long)t0 * H * D + 16 * sub;
@@ -253,16 +257,20 @@ __global__ void __launch_bounds__(kF8Threads) read_f8_kernel(const __grid_consta
 
 template <class T, int D>
 cudaError_t append_td(const AppendArgs& a, int sm_count, cudaStream_t s) {
-  return with_launch(a, sm_count, [&](const Launch& L, unsigned grid) {
-    append_f8_kernel<T, D><<<dim3(grid, 2), kF8Threads, 0, s>>>(L);
+  cudaError_t e = cudaSuccess;
+  const cudaError_t last = with_launch(a, sm_count, [&](const Launch& L, unsigned grid) {
+    e = launch_pdl(append_f8_kernel<T, D>, dim3(grid, 2), dim3(kF8Threads), 0, s, L);
   });
+  return e == cudaSuccess ? last : e;
 }
 
 template <class T, int D>
 cudaError_t read_td(const AppendArgs& a, int sm_count, cudaStream_t s) {
-  return with_launch(a, sm_count, [&](const Launch& L, unsigned grid) {
-    read_f8_kernel<T, D><<<dim3(grid, a.k_out && a.v_out ? 2 : 1), kF8Threads, 0, s>>>(L);
+  cudaError_t e = cudaSuccess;
+  const cudaError_t last = with_launch(a, sm_count, [&](const Launch& L, unsigned grid) {
+    e = launch_pdl(read_f8_kernel<T, D>, dim3(grid, a.k_out && a.v_out ? 2 : 1), dim3(kF8Threads), 0, s, L);
   });
+  return e == cudaSuccess ? last : e;
 }
 
 template <class T>

@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __shared__ Look look[kPlanThreads];
   const ChunkArgs& a = p.c;
   const int tid = threadIdx.x, G = a.G;
-  pdl_launch_dependents();  // the main kernel's start overlaps this one
+  pdl_wait();               // this kernel's start overlaps the one before
+  pdl_launch_dependents();  // and the main kernel's this one; not earlier: the staging kernel relies on all work before the call
   long long carry = 0, total;
   for (int b0 = 0; b0 < a.b.n_seqs; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -295,8 +296,8 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, size_
   p.max_entries = (int)l.max_entries;
   p.rows = ck::rows_per_entry(c.k.d);
   p.keys = ck::keys_per_tile(c.k.d);
-  plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   Args a{};
   a.c = c;

@@ -180,6 +180,8 @@ __device__ __forceinline__ void angles(const NormArgs& n, int l, int pos, bool o
 template <class T, int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) norm_kernel(const __grid_constant__ Launch L) {
   constexpr int LPV = D / 16, U = 8 / sizeof(T);  // heads in flight: as many as have the registers
+  pdl_launch_dependents();  // the next kernel's start overlaps this one, as this one's the last
+  pdl_wait();
   const long long group = ((long long)blockIdx.x * kThreads + threadIdx.x) / LPV;
   const int l = threadIdx.x % LPV, token = (int)(group / L.splits), split = (int)(group - (long long)token * L.splits);
   const bool of_k = split >= L.splits_q, on = token < L.n.n_tokens;
@@ -227,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_kernel(const __grid_con
   __shared__ float joined[kThreads / 32][D];
   const int l = threadIdx.x % LPV, g = threadIdx.x / LPV, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x / L.ctas, c = blockIdx.x - split * L.ctas;
-  pdl_launch_dependents();  // the second kernel's start overlaps this one
+  pdl_launch_dependents();
+  pdl_wait();
   const bool of_k = split >= L.splits_q;
   const NormRows& R = L.n.rows[of_k];
   const int h0 = (of_k ? split - L.splits_q : split) * L.hpt, h1 = min(R.n_heads, h0 + L.hpt);
@@ -323,6 +326,7 @@ __device__ __forceinline__ void add_exactly(float& s, float& lost, float x) {
 // The weight's gradient from the CTAs' rows: 32 coordinates of q's (y = 0) or k's weight.
 __global__ void __launch_bounds__(32 * kJoin) weight_kernel(const __grid_constant__ Launch L, int d) {
   __shared__ float2 sums[kJoin][33];
+  pdl_launch_dependents();
   pdl_wait();
   const bool of_k = blockIdx.y != 0;
   const NormRows& R = L.n.rows[of_k];
@@ -344,37 +348,41 @@ __global__ void __launch_bounds__(32 * kJoin) weight_kernel(const __grid_constan
   }
 }
 
+// As many heads per group, up to 8, as leave 512 threads on every SM (the angles then cost a few percent); a call that cannot
+// fill the GPU takes one head per group, the shortest chain.
+int heads_per_group(const NormArgs& n, int d, int sm_count) {
+  const int heads = n.rows[0].n_heads + n.rows[1].n_heads;
+  int hpt = 1;
+  while (hpt < kHeads && (long long)n.n_tokens * (heads / (2 * hpt)) * (d / 16) >= (long long)sm_count * 512) hpt *= 2;
+  return hpt;
+}
+
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 template <class T, int D, int MODE>
 cudaError_t launch_forward(Launch& L, int sm_count, cudaStream_t s) {
   const NormArgs& n = L.n;
-  const int heads = n.rows[0].n_heads + n.rows[1].n_heads;
-  // As many heads per group, up to 8, as leave 512 threads on every SM (the angles then cost a few percent); a call that
-  // cannot fill the GPU takes one head per group, the shortest chain.
-  int hpt = 1;
-  while (hpt < kHeads && (long long)n.n_tokens * (heads / (2 * hpt)) * (D / 16) >= (long long)sm_count * 512) hpt *= 2;
+  const int hpt = heads_per_group(n, D, sm_count);
   L.hpt = hpt;
   L.splits_q = ceil_div(n.rows[0].n_heads, hpt);
   L.splits = L.splits_q + ceil_div(n.rows[1].n_heads, hpt);
   const long long threads = (long long)n.n_tokens * L.splits * (D / 16), grid = (threads + kThreads - 1) / kThreads;
   if (grid >= (1LL << 31)) return cudaErrorInvalidValue;
-  norm_kernel<T, D, MODE><<<(unsigned)grid, kThreads, 0, s>>>(L);
-  return cudaGetLastError();
+  const cudaError_t e = launch_pdl(norm_kernel<T, D, MODE>, dim3((unsigned)grid), dim3(kThreads), 0, s, L);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 template <class T, int D, int MODE>
 cudaError_t launch_gradient(Launch& L, int sm_count, cudaStream_t s) {
   constexpr int GPC = kThreads / (D / 16);
   const NormArgs& n = L.n;
-  int hpt = 1;
-  while (hpt < kHeads && hpt < n.rows[0].n_heads + n.rows[1].n_heads) hpt *= 2;
-  L.hpt = hpt;
+  L.hpt = heads_per_group(n, D, sm_count);
+  const int hpt = L.hpt;
   L.splits_q = ceil_div(n.rows[0].n_heads, hpt);
   L.splits = L.splits_q + ceil_div(n.rows[1].n_heads, hpt);
   L.ctas = max(1, min(ceil_div(n.n_tokens, GPC), kGradCtasPerSm * sm_count / L.splits));
-  norm_grad_kernel<T, D, MODE><<<(unsigned)(L.splits * L.ctas), kThreads, 0, s>>>(L);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_pdl(norm_grad_kernel<T, D, MODE>, dim3((unsigned)(L.splits * L.ctas)), dim3(kThreads), 0, s, L);
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess || (!n.rows[0].dweight && !n.rows[1].dweight)) return e;
   e = launch_pdl(weight_kernel, dim3(D / 32, 2), dim3(32 * kJoin), 0, s, L, D);
   return e == cudaSuccess ? cudaGetLastError() : e;
