@@ -34,9 +34,8 @@ struct Row {
 };
 
 // The rows [t0, t0 + n) of a CTA, by all its warps.  Up to a row per warp each looks for its own; more rows are mostly of one
-// sequence: every warp looks for the first, whose followers then need a look at the block table each, by a lane, and the
-// warps share the rest.  (Two searches of a warp, one after the other, for 16 rows: 19 us where this takes 16, for 4096 tokens
-// of 8 heads of 128.)
+// sequence: every warp looks for the first, whose followers in its block lie behind it and in others need a look at the block
+// table each, by a lane; the warps share the rest.
 __device__ __forceinline__ void find_rows(const AppendArgs& a, const DevView& v, int t0, int n, int warp, int lane, bool report,
                                           Row* rows) {
   int seq, same = 0;
@@ -46,8 +45,11 @@ __device__ __forceinline__ void find_rows(const AppendArgs& a, const DevView& v,
     Place p = find_row(a, v, t0, lane, report && warp == 0, seq, s);
     same = s.ok ? min(n, s.first + s.n - t0) : 1;
     if (warp == 0 && lane < same) {
-      if (lane > 0) {
-        p.pos += lane;
+      const int first = p.pos;
+      p.pos += lane;
+      if (p.pos / kF8Block == first / kF8Block) {  // (a block lies in one page)
+        p.vec = p.vec < 0 ? -1 : p.vec + lane;
+      } else {
         p.vec = position_vector(a.b, v, a.layer, seq, p.pos);
         if (p.vec < 0 && report) atomicOr(a.tab.status, kFlagBlockTable);
       }
@@ -96,13 +98,28 @@ __global__ void __launch_bounds__(kF8Threads, D == 256 ? 1 : 2) append_f8_kernel
     for (int i = lane; i < n_tok * LINES; i += 32)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (long long)(i / LINES) * stride + i % LINES * (128 / (int)sizeof(T))));
   }
-  find_rows(a, V, t0, n_tok, warp, lane, !is_v, rows);
-  __syncthreads();
+  const bool many = n_tok > kF8Warps;
+  if (!many) {
+    find_rows(a, V, t0, n_tok, warp, lane, !is_v, rows);
+    __syncthreads();
+  }
   const tq_rope_table& R = a.rope;
   const int half = R.rotary_dim / 2;
   const bool turn = !is_v && a.has_rope;
-  for (int k = 0; k < n_tok; ++k) {  // (the CTA's threads alike)
-    const Row r = rows[k];
+  // Block by block (the CTA's threads alike).  Up to a row per warp the rows have been found side by side; of more, mostly of
+  // one sequence, every warp finds the first of a block itself (handed on through shared memory, with two searches of a warp
+  // one after the other: 20 us for 4096 tokens of 8 heads of 128, where this takes 16).
+  for (int k = 0; k < n_tok;) {
+    Row r;
+    if (many) {
+      SeqOf s{};
+      int seq;
+      const Place p = find_row(a, V, t0 + k, lane, !is_v && warp == 0, seq, s);
+      if (seq == a.b.n_seqs) break;
+      r = Row{p.vec, p.pos, s.first, s.first + s.n, p.padding || !s.ok};
+    } else {
+      r = rows[k];
+    }
     struct {  // the slot of the block's first token (head 0), its first new row, the new tokens, the offset of the first
       long long vec;
       int row, n, off;
@@ -111,6 +128,7 @@ __global__ void __launch_bounds__(kF8Threads, D == 256 ? 1 : 2) append_f8_kernel
     q.vec = r.vec - q.off;
     q.row = t0 + k;
     q.n = min(kF8Block - q.off, r.end - q.row);
+    k += many && !r.padding ? q.n : 1;
     if (r.vec < 0 || (q.off && q.row != r.first)) continue;  // no place, or no block begins here
     if (turn) {
       __syncthreads();  // the angles of the block before have been used

@@ -848,24 +848,9 @@ __device__ __forceinline__ void join_columns(const Args& a, int shares, int row,
   auto ml_of = [&](int p) {
     return __ldcg(reinterpret_cast<const float2*>(a.part_ml + share(min(p, shares - 1)) * a.rows_cap * 2) + row);
   };
-  float top = -INFINITY, lt = 0.f;
-#pragma unroll 1
-  for (int p0 = 0; p0 < shares; p0 += 8) {
-    float2 ml[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) ml[k] = ml_of(p0 + k);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].y != 0.f ? ml[k].x : -INFINITY);
-  }
-  if (top == -INFINITY) top = 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
-#pragma unroll 1
-  for (int p0 = 0; p0 < shares; p0 += S) {
-    float2 ml[S];
-    float4 x[S][C];
+  float2 ml[S];
+  float4 x[S][C];
+  auto ask = [&](int p0) {
 #pragma unroll
     for (int k = 0; k < S; ++k) {
       if (p0 + k >= shares) break;  // (the block's threads alike)
@@ -874,6 +859,27 @@ __device__ __forceinline__ void join_columns(const Args& a, int shares, int row,
 #pragma unroll
       for (int c = 0; c < C; ++c) x[k][c] = __ldcg(o + (long long)min(jc0 + c * step, D / 4 - 1) * a.rows_cap);
     }
+  };
+  ask(0);
+  float top = -INFINITY, lt = 0.f;
+#pragma unroll
+  for (int k = 0; k < S; ++k) top = fmaxf(top, k < shares && ml[k].y != 0.f ? ml[k].x : -INFINITY);
+#pragma unroll 1
+  for (int p0 = S; p0 < shares; p0 += 8) {
+    float2 z[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] = ml_of(p0 + k);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, z[k].y != 0.f ? z[k].x : -INFINITY);
+  }
+  if (top == -INFINITY) top = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+#pragma unroll 1
+  for (int p0 = 0; p0 < shares; p0 += S) {
+    if (p0) ask(p0);
 #pragma unroll
     for (int k = 0; k < S; ++k) {
       if (p0 + k >= shares || ml[k].y == 0.f) continue;
@@ -920,7 +926,7 @@ __device__ __forceinline__ void note_shared(const Item& it, Shared& s) {
 // The rows of entries that several CTAs share: blocks (c, ...) those of the entry that begins in CTA c's range and ends behind
 // it, a row per thread and kJoinColumns groups of four columns per block.  (The last CTA to finish joined them itself, a
 // warpgroup alone: 54 us for 64 tokens of 32 heads of 128 that see 1024 keys, most of it in this.)
-constexpr int kJoinColumns = 4;
+constexpr int kJoinColumns = 2;
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a) {
   constexpr int kBlocks = D / 4 / kJoinColumns;
