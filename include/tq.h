@@ -447,8 +447,8 @@ tq_status tq_rope(const tq_context* ctx, const tq_rope_table* table, const void*
  * keys: either may be NULL (not both), each has its own weight (device [d] of type weight_dtype, any alignment of an
  * element; NULL: ones), heads and strides; x and out are as in tq_rope (out may be x with the same stride; other overlaps
  * are not allowed, nor between the two).  eps > 0, 2^-126 at least.  A vector whose squares pass the range of fp32 is
- * normed all the same; one with a NaN or an infinity gives what the formula gives in fp32: NaN in those coordinates (with a
- * NaN, in all) and 0 in the others.  Errors as tq_rope.
+ * normed all the same; one with a NaN gives NaN in every coordinate, one with an infinity NaN in that coordinate and the
+ * one rotated with it and 0 in the others.  Errors as tq_rope.
  */
 typedef struct tq_norm_rows {
   const void* x;             /* element (t, h, i) at t * x_token_stride + h * d + i */
@@ -468,8 +468,9 @@ tq_status tq_norm_rope(const tq_context* ctx, const tq_rope_table* table, const 
  *   dx_i = r (g_i weight[i] - x'_i sum_j(g_j weight[j] x'_j) / d),  dweight[i] = sum over tokens and heads of g_i x'_i.
  * x, dout and dx are of type dtype (dx may be dout with the same stride); dweight is device float [d], 4-byte aligned,
  * written and not added to, NULL where it is not wanted.  Sums are fp32 (the last ones, over partial results, with what
- * each addition loses), in an order that depends on the sizes alone.  workspace: device, tq_norm_rope_grad_workspace_bytes() bytes, 256-byte aligned
- * (TQ_ERR_WORKSPACE); calls that may overlap need their own.  n_heads: the heads of q and k together.
+ * each addition loses), in an order that depends on the sizes alone.  workspace: device,
+ * tq_norm_rope_grad_workspace_bytes() bytes, 256-byte aligned (TQ_ERR_WORKSPACE); calls that may overlap need their own.
+ * n_heads: the heads of q and k together.
  */
 typedef struct tq_norm_grad_rows {
   const void* x;
@@ -516,8 +517,8 @@ typedef struct tq_batch {
  * NULL (to positions[t], device int32 [n_tokens], or where positions is NULL to the token's position in its sequence).
  * k / v element (t, h, i): k[t * k_token_stride + h * d + i], same type for both, 16-byte aligned, strides multiples
  * of 16 bytes and >= H d.  The rotated key is quantised from fp32 without a rounding in between.  K: Q8_0.  V: Q8_0
- * or turbo2/3/4_mse; or F8_BLOCK for both.  Others return TQ_ERR_UNSUPPORTED (turbo K: tq_rope, then tq_encode_kv).  Values in fp16
- * without a rotation give the bytes of tq_encode_kv for Q8_0.  A NaN element of a Q8_0 vector is stored as 0; an
+ * or turbo2/3/4_mse; or F8_BLOCK for both.  Others return TQ_ERR_UNSUPPORTED (turbo K: tq_rope, then tq_encode_kv).
+ * Values in fp16 without a rotation give the bytes of tq_encode_kv for Q8_0.  A NaN element of a Q8_0 vector is stored as 0; an
  * infinite one, or one so large that the fp16 scale overflows (a magnitude of 127 * 65520 or more), gives an infinite
  * scale and codes of 0, which read back as NaN in its block of 32.  A turbo vector with a NaN or an infinite element,
  * or whose norm passes fp16 (65520), reads back as NaN in every coordinate (tq_read_kv, tq_chunk_attention).  A token

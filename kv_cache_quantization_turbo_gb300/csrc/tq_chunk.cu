@@ -239,10 +239,12 @@ Layout layout(int sm_count, int d, long long n_seqs, long long n_tokens, long lo
 }
 
 // Staging f8_block tiles pays where enough entries use each.  8 KV heads of 128, 4 query heads each, us staged and not: one
-// sequence at 32K, 8 entries 306 and 323, 6 260 and 260, 4 227 and 213, 64 1515 and 2050; 8 sequences at 4K, 8 entries
-// each 326 and 349, 64 1205 and 1501; with a window of 1024, 16 entries of 64 tokens (8 uses of a tile) 282 and 284, 64 (14
-// uses) 804 and 888.  At head size 256 it never does.  The batch's average decides, as far as the host knows it; documents
-// (first_keys) are left to the other kernel, which does not look at pages that no row sees.
+// sequence at 32K, 4 entries 203 and 190, 6 244 and 251, 8 268 and 295, 16 443 and 557, 64 1515 and 2050; 8 sequences at 4K, 6
+// entries each 257 and 270, 8 293 and 325; with a window of 1024, 16 entries of 64 tokens (8 uses of a tile) 249 and 255, 8 (6
+// uses) 167 and 158.  Heads of 64, one sequence at 32K: 4 entries 138 and 148, 8 210 and 257; 8 sequences at 4K with the window,
+// 8 entries (6 uses) 126 and 123, 16 200 and 209.  Heads of 256: 16 entries 767 and 597, 64 2002 and 2055, so never there.  The
+// batch's average decides, as far as the host knows it; documents (first_keys) are left to the other kernel, which does not
+// look at pages that no row sees.
 constexpr int staged_uses(int d) { return d == 64 ? 6 : 8; }
 constexpr size_t kStagedMost = (size_t)8 << 30;
 
@@ -262,7 +264,7 @@ StagedLayout staged_layout(size_t at, int d, const DevView& k, const tq_batch& b
   if (!(entries * seen >= staged_uses(d) * staged)) return l;
   l.tiles = (int)((b.max_ctx + keys - 1) / keys);
   const size_t n = (size_t)b.n_seqs * l.tiles * k.H;
-  if (n == 0 || n > kStagedMost / ck::tile_bytes(d)) return l;
+  if (n == 0 || n > kStagedMost / ck::tile_bytes(d) || k.H > 65535 || b.n_seqs > 65535) return l;  // (the grid's y and z)
   l.k = at;
   l.v = l.k + n * ck::tile_bytes(d);
   l.heads = l.v + n * ck::tile_bytes(d);

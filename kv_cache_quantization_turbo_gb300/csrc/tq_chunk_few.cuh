@@ -17,7 +17,9 @@
 // copy bandwidth, at 64 % of the instruction slots (511 instructions per slice, of which 180 turn codes into fp16).  Keys as
 // the right operand, 8 of 16 rows idle, took 170 us; scales multiplied into K's fragments 149 us, and rounded K: an error of
 // 1.3e-3 instead of 3.6e-4.  Turbo values: more instructions (a lookup by byte permutes) for fewer bytes, 149 us for 48 such
-// sequences, bound by the instruction slots.  One token at 32K: 20 us after the plan, of which the range's 7 slices per
+// sequences, bound by the instruction slots.  f8_block: 364 instructions per slice (an instruction turns two codes into fp16;
+// a slice is a block, so that K's scale goes to its scores and V's, over the largest so far, to its weights), 140 us for
+// 0.82 GB, 5.8 TB/s.  One token at 32K: 20 us after the plan, of which the range's 7 slices per
 // warp take 9 (instruction slots), finding the range, the first copies and Q 5, the join of 38 shares 5.
 #pragma once
 

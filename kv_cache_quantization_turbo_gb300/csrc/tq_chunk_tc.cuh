@@ -4,7 +4,7 @@
 // entry is up to MT consecutive rows and the key tiles that any of them sees (the plan kernel lists them).  The tiles of
 // all entries of all KV heads form one line of work units, cut into equal ranges, one per CTA (one CTA per SM): a CTA
 // takes the end of one entry, whole entries, and the start of another.  Entries that several CTAs share are joined from
-// partial results by the last CTA that finishes, in a fixed order, so that results do not depend on timing.  With one
+// partial results by a second kernel, in a fixed order, so that results do not depend on timing.  With one
 // decode row the long axis is so split over the whole GPU; with a large chunk every SM works to the end.
 //
 // A tile is BN keys.  A step is one score product S = Q K^T (M 128, N BN, K D), its softmax and O += P V (M 128, N D,

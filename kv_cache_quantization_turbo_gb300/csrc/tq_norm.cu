@@ -6,9 +6,12 @@
 // One pass over the data: 2 (gradient 3) elements moved per element, so HBM bounds it.  d / 16 lanes hold a vector, 8 pairs
 // of coordinates each, whose sums they share by shuffles; such a group walks over heads of one token with the angles and
 // the weight in registers, and asks for the next heads' words before it turns to the first ones.  Queries and keys are
-// heads of one launch.  4096 tokens of 32 + 8 heads of 128 in bf16: 20.5 us for 84 MB, where a plain copy of them takes 16.2
-// (2, 4 heads per group 25, 22; three CTAs per SM instead of two 23: the words in flight count, not the warps); the gradient
-// 34 us for 126 MB (4 heads per group 38, 16 41; twice or half the CTAs for the partial sums the same).
+// heads of one launch.  4096 tokens of 32 + 8 heads of 128 in bf16: 17.7 us for 84 MB, where a plain copy of them takes 16.2
+// (4 heads per group 18.4; blocks of 256 threads 20.5, of 128 with four on an SM 19.4; two heads in flight and six blocks
+// 20.0); the gradient 33 us for 126 MB, of which the first kernel 29 (4 heads per group 38, 16 41; two heads in flight and
+// four blocks instead of four and three 34.8, one and four 43; twice or half the blocks for the partial sums the same).
+// What did not pay: two coordinates per instruction (the pairs' moves: 21.9 and 36.5), the next heads' lines asked into L2
+// at once (19.2 and 36).
 //
 // The weight's gradient: a lane adds up its 16 coordinates over the rows of its group, the CTA's groups are joined in
 // shared memory and leave one row of partial sums, and a second kernel adds those rows in their order, with what each sum
@@ -20,10 +23,10 @@
 namespace tq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPairs = 8;            // of a lane
 constexpr int kHeads = 8;            // most heads of a group
-constexpr int kGradCtasPerSm = 8;
+constexpr int kGradCtasPerSm = 16;
 constexpr int kJoin = 32;            // rows of partial sums that the second kernel adds side by side
 
 // How a lane's pairs lie: two runs of 8 (halves), one run of 16 (interleaved), or halves whose border no run meets.
@@ -178,7 +181,7 @@ __device__ __forceinline__ void angles(const NormArgs& n, int l, int pos, bool o
 }
 
 template <class T, int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 2) norm_kernel(const __grid_constant__ Launch L) {
+__global__ void __launch_bounds__(kThreads, MODE == kScattered ? 4 : 5) norm_kernel(const __grid_constant__ Launch L) {
   constexpr int LPV = D / 16, U = 8 / sizeof(T);  // heads in flight: as many as have the registers
   pdl_launch_dependents();  // the next kernel's start overlaps this one, as this one's the last
   pdl_wait();
@@ -224,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_kernel(const __grid_constant
 }
 
 template <class T, int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 2) norm_grad_kernel(const __grid_constant__ Launch L) {
-  constexpr int LPV = D / 16, GPC = kThreads / LPV, U = 4 / sizeof(T);
+__global__ void __launch_bounds__(kThreads, 3) norm_grad_kernel(const __grid_constant__ Launch L) {
+  constexpr int LPV = D / 16, GPC = kThreads / LPV, U = 8 / sizeof(T);
   __shared__ float joined[kThreads / 32][D];
   const int l = threadIdx.x % LPV, g = threadIdx.x / LPV, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x / L.ctas, c = blockIdx.x - split * L.ctas;
@@ -308,11 +311,11 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_kernel(const __grid_con
     }
   }
   __syncthreads();
-  if (threadIdx.x < D) {
+  for (int i = threadIdx.x; i < D; i += kThreads) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) s += joined[w][threadIdx.x];
-    L.part[(long long)blockIdx.x * D + threadIdx.x] = s;
+    for (int w = 0; w < kThreads / 32; ++w) s += joined[w][i];
+    L.part[(long long)blockIdx.x * D + i] = s;
   }
 }
 

@@ -838,3 +838,14 @@ def test_staged_is_not_for_documents_or_too_large_batches(ctxs):  # noqa: F811
     assert tq.tq_chunk_workspace_for(c.ctx.h, huge, 8, c.kv, c.vv) == tq.tq_chunk_workspace_bytes(c.ctx.h, huge, 8, 2)
     q8 = tq.alloc_view("q8_0", 64, 2, 16, 40)
     assert tq.tq_chunk_workspace_for(c.ctx.h, c.batch, 8, q8, q8) == least
+
+
+def test_staging_stays_within_a_grid(ctxs):  # noqa: F811
+    """65535 sequences of 64 tokens may be staged, one more is not (nothing runs: the sizes alone)."""
+    view = tq.alloc_view("f8_block", 64, 1, 16, 1)
+    tables = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (65537, 65536)]
+    table = torch.zeros((65536, 8), dtype=torch.int32, device="cuda")
+    for n, staged in ((65535, True), (65536, False)):
+        b = tq.Batch(tables[0][:n + 1], tables[1][:n], table[:n], 64 * n, 64, 128)
+        least = tq.tq_chunk_workspace_bytes(ctxs[64].h, b, 32, 1)
+        assert (tq.tq_chunk_workspace_for(ctxs[64].h, b, 32, view, view) > least) == staged
