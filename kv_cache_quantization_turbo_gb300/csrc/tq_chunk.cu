@@ -1,8 +1,8 @@
 // Plan and host side of the chunk attention (the attention itself: tq_chunk_tc.cuh).
 //
 // The sequences' lengths are on the device, so a one-block kernel lists the entries (up to rows_per_entry rows of a
-// sequence and the keys that any of them sees) and sums up their work.  It runs in a few microseconds for the sizes
-// that a step has, and clears the counters with which the main kernel joins partial results.
+// sequence and the keys that any of them sees), sums up their work and says whether they are cut between CTAs.  It runs in
+// a few microseconds for the sizes that a step has, and clears the counters with which the main kernel joins partial results.
 #include "tq_batch.cuh"
 #include "tq_chunk.h"
 
@@ -23,6 +23,7 @@ struct PlanArgs {
   int* seq_base;  // [n_seqs + 1]: entries of the sequences before
   unsigned int* counters;
   int max_entries, rows, keys;
+  int ctas;  // of the main kernel; 0: entries are cut
 };
 
 // What an entry's tokens see: the call's row and the position of its first token, their number, length and prefix of the
@@ -74,11 +75,20 @@ __device__ __noinline__ void zero_refused(const ChunkArgs& a, int b0, bool refus
   __syncthreads();  // before refused_of is written again
 }
 
+// How many work units more than an even share, `even`, the fullest CTA may have where entries are not cut: a cut costs a second
+// loading of queries, partial results and their join.  us cut and whole, by the even share and what the fullest has more: heads
+// of 256, q8_0, 13 and 7: 56 and 47, 17 and 7: 76 and 61, 6 and 4: 36 and 30, 40 and 20: 105 and 112, 4 and 14: 36 and 40; of 128,
+// 38 and 8: 170 and 159, 17 and 6: 93 and 86, 8 and 7: 61 and 66, 5 and 4: 42 and 42, 41 and 15: 144 and 162; of 64, 19 and 4: 78
+// and 71, 18 and 6: 71 and 67, 6 and 4: 33 and 34, 7 and 9: 38 and 47.  f8_block gains less at 64 (23 and 7: 87 and 89).
+__device__ __forceinline__ long long worth(int d, long long even) {
+  return d == 256 ? min(even, 10LL) : min(even / 2, d == 128 ? 8LL : 6LL);
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
   __shared__ long long warp_sums[kPlanThreads / 32];
   __shared__ int near_base[kNear];
   __shared__ uint32_t refused_of[kPlanThreads / 32];
-  __shared__ Look look[kPlanThreads];
+  __shared__ __align__(8) Look look[kPlanThreads];
   const ChunkArgs& a = p.c;
   const int tid = threadIdx.x, G = a.G;
   pdl_wait();               // this kernel's start overlaps the one before
@@ -207,7 +217,33 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     carry += total;
   }
   for (long long i = tid; i < (long long)E * a.k.H * 2; i += kPlanThreads) p.counters[i] = 0u;
-  if (tid == 0) *p.head = PlanHead{carry, E};
+  // Whether entries stay whole: where the fullest CTA then has little more than an even share, as far as that and the CTAs are
+  // known.  A CTA's load: from the first entry at or behind its range's start to the first at or behind its end.
+  int whole = 0;
+  if (p.ctas && E && E <= kPlanThreads) {
+    const long long T = carry, U = T * a.k.H;
+    const long long even = U / max(1LL, min((long long)p.ctas, U / ck::kMinUnits)), most = even + worth(a.k.d, even);
+    __syncthreads();  // the entries, and what was read of the look
+    long long* starts = reinterpret_cast<long long*>(look);
+    if (tid < E) starts[tid] = p.entries[tid].start;
+    __syncthreads();
+    auto first_at = [&](long long c) {  // where the first entry at or behind the start of CTA c's range begins
+      const long long u = U * c / p.ctas;
+      if (u >= U) return U;
+      const long long h = u / T, off = u - h * T;
+      int lo = 0, hi = E;  // the first entry with starts >= off
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (starts[mid] < off) lo = mid + 1;
+        else hi = mid;
+      }
+      return h * T + (lo < E ? starts[lo] : T);
+    };
+    bool long_one = false;
+    for (int c = tid; c < p.ctas; c += kPlanThreads) long_one = long_one || first_at(c + 1) - first_at(c) > most;
+    whole = !__syncthreads_or(long_one);
+  }
+  if (tid == 0) *p.head = PlanHead{carry, E, whole};
 }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
@@ -237,6 +273,7 @@ Layout layout(int sm_count, int d, long long n_seqs, long long n_tokens, long lo
   l.bytes = l.shared + up((size_t)sm_count * sizeof(ck::Shared));
   return l;
 }
+
 
 // Staging f8_block tiles pays where enough entries use each.  8 KV heads of 128, 4 query heads each, us staged and not: one
 // sequence at 32K, 4 entries 203 and 190, 6 244 and 251, 8 268 and 295, 16 443 and 557, 64 1515 and 2050; 8 sequences at 4K, 6
@@ -298,6 +335,9 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, size_
   p.max_entries = (int)l.max_entries;
   p.rows = ck::rows_per_entry(c.k.d);
   p.keys = ck::keys_per_tile(c.k.d);
+  const long long most = (long long)c.b.max_tokens * c.G;  // rows of an entry
+  const bool few = most <= ck::few_rows(c.k.d);
+  p.ctas = few ? 0 : sm_count;
   cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -317,8 +357,7 @@ cudaError_t launch_chunk(const ChunkArgs& c, float lam_v, void* workspace, size_
   // Entries of few rows.  48 sequences of 1K to 16K tokens, 8 KV heads of 128, 4 rows each: q8_0 128 us there and 253 in
   // the large kernel, turbo4 149 and 382; 16 rows: 152 and 275, turbo4 204 and 400; head size 64: 85 and 195; 256: 215 and
   // 330; 4 sequences of 500 tokens: 20 and 24.  At 256 a lane's registers hold 8 rows.
-  const long long most = (long long)c.b.max_tokens * c.G;  // rows of an entry
-  if (most <= ck::few_rows(c.k.d)) {
+  if (few) {
     if (c.k.d == 64) return ck::launch_few64(a, (int)most, vb, sm_count, s);
     if (c.k.d == 128) return ck::launch_few128(a, (int)most, vb, sm_count, s);
     return ck::launch_few256(a, (int)most, vb, sm_count, s);

@@ -8,6 +8,8 @@ namespace ck {
 
 // Work units of an entry besides its key tiles: loading its queries and storing its result takes about as long.
 constexpr int kOverhead = 2;
+// A CTA that takes part has at least as many, where entries are cut.
+constexpr int kMinUnits = 2;
 
 constexpr int rows_per_entry(int d) { return d == 256 ? 128 : 256; }
 constexpr int keys_per_tile(int d) { return d == 256 ? 64 : 128; }
@@ -27,6 +29,7 @@ struct Entry {
 struct PlanHead {
   long long units;  // of all entries of one KV head
   int n_entries;
+  int whole;        // entries are not cut: a CTA takes those that begin in its range
 };
 
 // f8_block tiles as operands, staged in the workspace (tq_chunk_staged.cuh): tile t of KV head h of sequence b is number

@@ -5,7 +5,8 @@
 // all entries of all KV heads form one line of work units, cut into equal ranges, one per CTA (one CTA per SM): a CTA
 // takes the end of one entry, whole entries, and the start of another.  Entries that several CTAs share are joined from
 // partial results by a second kernel, in a fixed order, so that results do not depend on timing.  With one
-// decode row the long axis is so split over the whole GPU; with a large chunk every SM works to the end.
+// decode row the long axis is so split over the whole GPU; with a large chunk every SM works to the end.  Where entries are so
+// many and so alike that ranges of whole ones are nearly even, the plan does not cut them.
 //
 // A tile is BN keys.  A step is one score product S = Q K^T (M 128, N BN, K D), its softmax and O += P V (M 128, N D,
 // K BN), the last two in parts of 64 keys.  Entries of more than 128 rows (D <= 128) have two row tiles, and steps
@@ -62,7 +63,6 @@ constexpr int kIssuer = 16, kLocator = 18, kLocWarps = 2;
 constexpr int NI = 3;       // items known ahead
 constexpr int NL = 6;       // tiles located ahead of the producers
 constexpr int kMissRing = 16;
-constexpr int kMinUnits = 2;
 constexpr float kBias = 4.0f;     // a fresh reference makes the row's largest weight 2^kBias
 constexpr float kTop = 32768.0f;  // the reference is raised where a tile's weights sum to more: each is below 65504
 constexpr float kLog2e = 1.4426950408889634074f;
@@ -336,7 +336,7 @@ __device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.
 template <int D>
 struct Items {
   long long T, U, nC, u, u1;
-  int n_entries, h, e;
+  int n_entries, h, e, whole;
 
   // A quotient of numbers >= 0; those of fewer than 32 bits, as good as always, are divided as such.
   static __device__ __forceinline__ long long div(long long x, long long y) {
@@ -352,7 +352,8 @@ struct Items {
     n_entries = head.n_entries;
     U = T * a.c.k.H;
     // every CTA that takes part has at least kMinUnits units (so no CTA inside an entry's range is without work)
-    nC = max(1LL, min((long long)gridDim.x, U / kMinUnits));
+    whole = head.whole;
+    nC = whole ? (long long)gridDim.x : max(1LL, min((long long)gridDim.x, U / kMinUnits));
     const long long c = blockIdx.x;
     u = c < nC ? div(U * c, nC) : 0;
     u1 = c < nC ? div(U * (c + 1), nC) : 0;
@@ -362,6 +363,11 @@ struct Items {
       const long long off = u - (long long)h * T;
       for (int step = 1 << 30; step > 0; step >>= 1)  // the last entry that starts at or before off
         if (e + step < n_entries && a.entries[e + step].start <= off) e += step;
+      if (whole && a.entries[e].start < off && ++e == n_entries) {
+        e = 0;
+        ++h;
+      }
+      if (whole) u = h < a.c.k.H ? (long long)h * T + a.entries[e].start : U;
     }
   }
 
@@ -383,7 +389,8 @@ struct Items {
       it.hi = en.hi;
       it.two = D != 256 && it.rows > 128;
       it.counter = (h * n_entries + e) * 2;
-      const long long t0 = max(0LL, u - base - kOverhead), t1 = min((long long)en.n_tiles, u1 - base - kOverhead);
+      const long long t0 = max(0LL, u - base - kOverhead);
+      const long long t1 = whole ? en.n_tiles : min((long long)en.n_tiles, u1 - base - kOverhead);
       if (en.n_tiles == 0) {
         it.kind = u == base ? 2 : 0;  // by the CTA that holds its first unit
       } else if (t0 < t1) {
@@ -398,8 +405,8 @@ struct Items {
           it.s_tile = en.s_lo / Shape<D>::BN + (int)t0;
           it.s_n = max(0, min(en.s_tiles, (int)t1) - (int)t0);
         }
-        it.first_cta = cta_of(base + kOverhead);
-        it.n_ctas = cta_of(base + kOverhead + en.n_tiles - 1) - it.first_cta + 1;
+        it.first_cta = whole ? (int)blockIdx.x : cta_of(base + kOverhead);
+        it.n_ctas = whole ? 1 : cta_of(base + kOverhead + en.n_tiles - 1) - it.first_cta + 1;
         it.slot = t0 == 0 ? 1 : 0;
       }
       u = base + en.n_tiles + kOverhead;

@@ -849,3 +849,16 @@ def test_staging_stays_within_a_grid(ctxs):  # noqa: F811
         b = tq.Batch(tables[0][:n + 1], tables[1][:n], table[:n], 64 * n, 64, 128)
         least = tq.tq_chunk_workspace_bytes(ctxs[64].h, b, 32, 1)
         assert (tq.tq_chunk_workspace_for(ctxs[64].h, b, 32, view, view) > least) == staged
+
+
+# Batches of many entries of like lengths, which the plan does not cut between blocks; and of more entries than it looks at.
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,new,H,G", [(48, 64, 8, 4), (47, 63, 7, 4), (152, 40, 2, 8), (600, 5, 1, 4)])
+def test_attend_many_like_entries(ctxs, d, n, new, H, G):  # noqa: F811
+    c = Cache(ctxs[d], d, H, [new] * n, [new + 7 * (b % 60) for b in range(n)], 16, padding=2).fill()
+    rows = some(n * new)
+    check(c, G, torch.float16, rows=rows, least=True, window=100, sinks=5)
+    # documents of 50 tokens, and one sequence in four that sees nothing
+    first = np.concatenate([np.where(c.seq % 4 == 3, 1 << 20, c.pos - c.pos % 50), [0, 0]])
+    out = check(c, G, torch.bfloat16, rows=rows, least=True, first=first)
+    assert not out[:c.rows][torch.from_numpy(c.seq[:c.rows] % 4 == 3).cuda()].any()
