@@ -18,7 +18,7 @@
 // the right operand, 8 of 16 rows idle, took 170 us; scales multiplied into K's fragments 149 us, and rounded K: an error of
 // 1.3e-3 instead of 3.6e-4.  Turbo values: more instructions (a lookup by byte permutes) for fewer bytes, 149 us for 48 such
 // sequences, bound by the instruction slots.  f8_block: 364 instructions per slice (an instruction turns two codes into fp16;
-// a slice is a block, so that K's scale goes to its scores and V's, over the largest so far, to its weights), 140 us for
+// a slice is a block, so that K's scale goes to its scores and V's to its weights: raised()), 141 us for
 // 0.82 GB, 5.8 TB/s.  One token at 32K: 20 us after the plan, of which the range's 7 slices per
 // warp take 9 (instruction slots), finding the range, the first copies and Q 5, the join of 38 shares 5.
 #pragma once
@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
     // Q's row g (and 8 + g) as fragments; everything else of this lane belongs to the rows 2 t, 2 t + 1 (and 8 more)
     uint32_t q[NT][D / 16][2];
     float f[NT][2], m[NT][2], mu[NT][2], l[NT][2];  // f: scores to log2 units; mu: m, or 0 where that is unset
+    float ve[NT][2];  // f8_block: O is in units of 2^ve, see raised()
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       const int r = g + 8 * u;
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
         f[u][e] = __shfl_sync(kFull, x, 8 * t + 4 * e);
         if (mods) f[u][e] = 1.f;  // (scores with modifications are in log2 units already)
         m[u][e] = -INFINITY;
-        mu[u][e] = l[u][e] = 0.f;
+        mu[u][e] = l[u][e] = ve[u][e] = 0.f;
       }
     }
     __syncthreads();  // the rows
@@ -500,7 +501,6 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
         for (int e = 0; e < 4; ++e) o[u][i][e] = 0.f;
 
     int st = 0;
-    int ve = kF8MinExp;  // f8_block: O is in units of 2^ve, no V scale so far is above
 #pragma unroll 1
     for (int num = j0 + SK * warp; num < end; num += STEP, st = st + 1 == NS ? 0 : st + 1) {
       const int key0 = key_of(num);
@@ -513,23 +513,12 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
       ahead = spot(ask);
       unsigned char* sk = ring + st * F::slice;
       uint32_t poison = 0;
-      float k_scale = 1.f, v_scale = 1.f;  // f8_block: the block's, V's over 2^ve
+      float k_scale = 1.f, v_exp = 0.f;  // f8_block: the block's, V's as an exponent
       if constexpr (VB == kF8) {
         const uint32_t kw = *reinterpret_cast<const uint32_t*>(sk + F::ks), vw = *reinterpret_cast<const uint32_t*>(sk + F::vs);
         poison = (kw | vw) & 0xFFFFu;
         k_scale = f8_scale(kw);
-        const int e = f8_exponent(vw);
-        if (e > ve) {  // (the warp's lanes alike)
-          const float down = ex2((float)(ve - e));
-          ve = e;
-#pragma unroll
-          for (int u = 0; u < NT; ++u)
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) o[u][i][z] *= down;
-        }
-        v_scale = ex2((float)(e - ve));
+        v_exp = (float)f8_exponent(vw);
       } else {
         __half* s = reinterpret_cast<__half*>(sk + sc_at);
         uint32_t big = 0;
@@ -641,6 +630,7 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
           fs[u][e] = VB == kF8 && !mods ? fmaxf(f[u][e] * k_scale, 1.2e-38f) : f[u][e];
           mx[u][e] = fmaxf(x[u][e], x[u][2 + e]) * fs[u][e];
           raise |= mx[u][e] - m[u][e] > kMaxExp;
+          if constexpr (VB == kF8) raise |= mx[u][e] + v_exp - (m[u][e] + ve[u][e]) > kMaxExp;
         }
       if (__any_sync(kFull, raise)) {
 #pragma unroll
@@ -651,11 +641,15 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
             float top = mx[u][e];
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-            const float mn = fmaxf(m[u][e], top - kBias);
-            al[e] = mn == -INFINITY ? 1.f : ex2(m[u][e] - mn);
-            m[u][e] = mn;
-            mu[u][e] = mn == -INFINITY ? 0.f : mn;
-            l[u][e] *= al[e];
+            if constexpr (VB == kF8) {
+              al[e] = raised(m[u][e], ve[u][e], l[u][e], top, top + v_exp);
+            } else {
+              const float mn = fmaxf(m[u][e], top - kBias);
+              al[e] = mn == -INFINITY ? 1.f : ex2(m[u][e] - mn);
+              m[u][e] = mn;
+              l[u][e] *= al[e];
+            }
+            mu[u][e] = m[u][e] == -INFINITY ? 0.f : m[u][e];
           }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
@@ -669,12 +663,17 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
         float w[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          w[e] = ex2(fmaf(x[u][e], fs[u][e], -mu[u][e]));
-          w[2 + e] = ex2(fmaf(x[u][2 + e], fs[u][e], -mu[u][e]));
-          l[u][e] += w[e] + w[2 + e];
           if constexpr (VB == kF8) {
-            w[e] *= v_scale;
-            w[2 + e] *= v_scale;
+            // weights times V's scale over 2^ve; the sum takes that back (a scale below 2^-40 of 2^ve counts as that: its
+            // weights, below 2^15 2^-40, are 0 in fp16)
+            const float sh = fmaxf(v_exp - ve[u][e], -40.f), at = sh - mu[u][e];
+            w[e] = ex2(fmaf(x[u][e], fs[u][e], at));
+            w[2 + e] = ex2(fmaf(x[u][2 + e], fs[u][e], at));
+            l[u][e] = fmaf(w[e] + w[2 + e], ex2(-sh), l[u][e]);
+          } else {
+            w[e] = ex2(fmaf(x[u][e], fs[u][e], -mu[u][e]));
+            w[2 + e] = ex2(fmaf(x[u][2 + e], fs[u][e], -mu[u][e]));
+            l[u][e] += w[e] + w[2 + e];
           }
         }
         p[u][0] = transpose8(narrow(w[0], w[1], (const __half*)nullptr));
@@ -763,13 +762,14 @@ __global__ void __launch_bounds__(Few<D, NT, VB>::NW * 32, 2) few_kernel(const _
     // ---- the warps' results, joined in their order ----
     float* mo = reinterpret_cast<float*>(sm);  // [NW][8 NT][OS]
     if constexpr (VB == kF8) {
-      const float up = ex2((float)ve);
 #pragma unroll
-      for (int u = 0; u < NT; ++u)
+      for (int u = 0; u < NT; ++u) {
+        const float up[2] = {ex2(ve[u][0]), ex2(ve[u][1])};
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[u][i][e] *= up;
+          for (int e = 0; e < 4; ++e) o[u][i][e] *= up[e & 1];
+      }
     }
 #pragma unroll
     for (int u = 0; u < NT; ++u) {

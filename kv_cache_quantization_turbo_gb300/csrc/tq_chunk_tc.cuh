@@ -317,6 +317,20 @@ __device__ __forceinline__ float f8_scale(uint32_t w) { return __uint_as_float(w
 // The word of a block that is not there: the smallest scale, which moves no other block's, and no marks.
 constexpr uint32_t kF8None = (uint32_t)(kF8MinExp + 127) << 23;
 
+// f8_block.  A row's output is a sum of weights times 2^(exponent of V's block) times codes, and its weights go to fp16 with
+// that power: s + exponent, s the score in log2 units, is what has to stay within fp16's range, for the keys that the row
+// sees.  So a row has two references, integers (powers of two then move between weights, sum and accumulator exactly): m of
+// its scores, for the sum l, and m + ve of s + exponent, for O, which is in units of 2^ve.  Raises them to kBias below
+// top and top_v, the largest s and s + exponent of the keys at hand (-INFINITY: none), with the sum; returns O's factor.
+__device__ __forceinline__ float raised(float& m, float& ve, float& l, float top, float top_v) {
+  const float mn = fmaxf(m, rintf(top) - kBias), mv = m + ve, mvn = fmaxf(mv, rintf(top_v) - kBias);
+  const float al = mvn == -INFINITY ? 1.f : ex2(mv - mvn);
+  l *= mn == -INFINITY ? 1.f : ex2(m - mn);
+  m = mn;
+  ve = mn == -INFINITY ? 0.f : mvn - mn;
+  return al;
+}
+
 __device__ __forceinline__ bool not_finite(uint32_t s) { return (s & 0x7C00u) == 0x7C00u; }
 
 __device__ __forceinline__ void arrive_smem(uint64_t* bar, int lane) {
@@ -974,7 +988,7 @@ __device__ __forceinline__ void finish_rows(const Args& a, const Item& it, int w
   const long long my_slot = partial_slot(blockIdx.x, it.slot, wg);
   // (a share's O: [D / 4][rows_cap] float4, so that the rows of a warp are consecutive)
   float4* po = reinterpret_cast<float4*>(a.part_o + my_slot * a.rows_cap * D) + r;
-  float norm = a.inv_lam_v * unit;  // folds 1 / lambda and the transform's 1 / sqrt(D)
+  float norm = a.inv_lam_v;  // folds 1 / lambda and the transform's 1 / sqrt(D)
   if constexpr (kTurbo) norm *= inv_sqrt_dim<D>();
   if (mine) {
     if (whole) norm *= l == 0.f ? 0.f : __fdividef(1.f, l);
@@ -1004,7 +1018,7 @@ __device__ __forceinline__ void finish_rows(const Args& a, const Item& it, int w
           for (int k = 0; k < 4; ++k) {
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = zero ? 0.f : __uint_as_float(o[8 * k + e]) * norm;
+            for (int e = 0; e < 8; ++e) y[e] = zero ? 0.f : __uint_as_float(o[8 * k + e]) * norm * unit;
             emit(32 * c + 8 * k, y);
           }
         }
@@ -1276,7 +1290,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const bool any_valid = __any_sync(kFull, valid);  // a warp without rows only keeps the barriers
       float m = -INFINITY, l = 0.f;
       bool unset = true;  // (of the warp) a row that sees keys has no reference yet
-      int ve = kF8MinExp;  // (of the warp, f8_block) O is in units of 2^ve: no V scale so far is above
+      float ve = 0.f;  // f8_block: O is in units of 2^ve, see raised()
       int last = -1, last_phase = 0;  // barrier and phase of the last part's value product
       for (int i = 0; i < steps; ++i) {
         const int s = buffer(c0 + i), jt = first + stride * i, tile0 = tile_of(it, jt) * BN;
@@ -1350,18 +1364,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // to more than kTop) the row's maximum, a new reference and the weights again: S is still there.
             const float f = mods ? 1.f : sl;  // scores to log2 units (special tiles are in them already where mods is set)
             bool raise = unset;
-            int ve_part = kF8MinExp;
-            if constexpr (VB == kF8) {
-              ve_part = max(max(f8_exponent(vw[0]), f8_exponent(vw[1])), max(f8_exponent(vw[2]), f8_exponent(vw[3])));
-              raise |= ve_part > ve;
-            }
             uint32_t pk[HN / 2];
-            float sum;
+            float sum, top_sum;
 #pragma unroll 1
             for (;;) {
               uint32_t x[64];
               if (raise) {
-                float mx0 = -INFINITY, mx1 = -INFINITY, top = -INFINITY;
+                float mx0 = -INFINITY, mx1 = -INFINITY, top = -INFINITY, top_v = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < HN / 16; ++c) {
                   uint32_t y[16];
@@ -1373,21 +1382,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     mx1 = fmaxf(fmaxf(mx1, __uint_as_float(y[e + 2])), __uint_as_float(y[e + 3]));
                   }
                   if constexpr (VB == kF8) {  // (a block's scores at its scale; the part's so far in top)
-                    const float sk = mods ? 1.f : f8_scale(words[((gt + jt) % kMissRing) * 16 + 4 * h + c]);
-                    top = fmaxf(top, fmaxf(mx0, mx1) * sk);
+                    const uint32_t* w = words + ((gt + jt) % kMissRing) * 16 + 4 * h + c;
+                    const float s1 = fmaxf(mx0, mx1) * (mods ? 1.f : fmaxf(f * f8_scale(w[0]), 1.2e-38f));
+                    top = fmaxf(top, s1);
+                    top_v = fmaxf(top_v, s1 + (float)f8_exponent(w[8]));
                     mx0 = mx1 = -INFINITY;
                   }
                 }
-                if constexpr (VB == kF8) mx0 = top;
-                const float mn = fmaxf(m, fmaf(fmaxf(mx0, mx1), f, -kBias));
-                float al = mn == -INFINITY ? 1.f : ex2(m - mn);
-                m = mn;
-                l *= al;
+                float al;
                 if constexpr (VB == kF8) {
-                  if (ve_part > ve) {
-                    al *= ex2((float)(ve - ve_part));
-                    ve = ve_part;
-                  }
+                  al = raised(m, ve, l, top, top_v);
+                } else {
+                  const float mn = fmaxf(m, fmaf(fmaxf(mx0, mx1), f, -kBias));
+                  al = mn == -INFINITY ? 1.f : ex2(m - mn);
+                  m = mn;
+                  l *= al;
                 }
                 unset = __any_sync(kFull, live && m == -INFINITY);
                 if (last >= 0) {  // O, once the product of this warpgroup's last part is complete
@@ -1409,10 +1418,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               if constexpr (VB == kF8) {
                 // Weights times their V block's scale over 2^ve; the sum takes that back.  (A scale below 2^-40 of 2^ve
                 // counts as that: its weights, below 2^15 2^-40, are 0 in fp16.)
-                sum = 0.f;
+                sum = top_sum = 0.f;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                  const float sh = (float)max(f8_exponent(vw[b]) - ve, -40), fb = mods ? 1.f : fmaxf(f * f8_scale(kw[b]), 1.2e-38f);
+                  const float sh = fmaxf((float)f8_exponent(vw[b]) - ve, -40.f);
+                  const float fb = mods ? 1.f : fmaxf(f * f8_scale(kw[b]), 1.2e-38f);
                   const float2 f2 = make_float2(fb, fb), m2 = make_float2(sh - mu, sh - mu);
                   float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -1424,7 +1434,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     pk[e] = narrow(p.x, p.y, (const __half*)nullptr);
                   }
                   sum = fmaf(l2.x + l2.y, ex2(-sh), sum);
+                  top_sum += l2.x + l2.y;
                 }
+                top_sum = fmaxf(top_sum, sum);
               } else {
               const float2 f2 = make_float2(f, f), m2 = make_float2(-mu, -mu);
               float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -1436,10 +1448,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 l2[e & 1] = __fadd2_rn(l2[e & 1], p);
                 pk[e] = narrow(p.x, p.y, (const __half*)nullptr);
               }
-              sum = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+              sum = top_sum = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
               }
               // (rows that are not there hold whatever shared memory had: they have no say, so that results do not vary)
-              if (raise || !__any_sync(kFull, live && sum > kTop)) break;
+              if (raise || !__any_sync(kFull, live && top_sum > kTop)) break;
               raise = true;
             }
             l += sum;
@@ -1457,7 +1469,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       tc::fence_after_sync();
       c0 += steps;
       gt += it.n;
-      finish_rows<D, kTurbo>(a, it, wg, r, valid, any_valid, out_at, t_o, last >= 0, m, l, VB == kF8 ? ex2((float)ve) : 1.f);
+      finish_rows<D, kTurbo>(a, it, wg, r, valid, any_valid, out_at, t_o, last >= 0, m, l, VB == kF8 ? ex2(ve) : 1.f);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
     }
