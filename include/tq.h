@@ -568,7 +568,8 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
 
 /*
  * The workspace with which tq_chunk_attention runs these views and modifications (may be NULL) fastest; never less than
- * tq_chunk_workspace_bytes(), with which every call runs.  0 for invalid arguments.
+ * tq_chunk_workspace_bytes(), with which every call runs.  0 for invalid arguments.  The size given to a call chooses the
+ * kernel, so its results agree with those of another size to rounding, not bit by bit.
  */
 size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int n_q_heads, const tq_cache_view* k_view,
                               const tq_cache_view* v_view, const tq_score_mods* mods);
@@ -593,8 +594,9 @@ size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int 
  *   tq_decode_attention, tq_prefill_attention).  F8_BLOCK codes are fp16 numbers: keys and values are not rounded, and a
  *   block's scale goes to its scores and weights.  A weight is rounded to fp16 with V's scale in it, relative to the row's
  *   largest such product: keys that the row does not see, or hardly weighs, take nothing from the others whatever their
- *   scale; a key whose product is below 2^-29 of the largest may count as 0.  Scores are fp32: beyond 2^22 in magnitude
- *   their steps pass what a weight can tell apart, and a row may come out as NaN from 2^28 on.
+ *   scale; a key whose product is below 2^-29 of the largest (2^-21 with the workspace of tq_chunk_workspace_for()) may
+ *   count as 0.  Scores are fp32: beyond 2^22 in magnitude their steps pass what a weight can tell apart, and a row may
+ *   come out as NaN from 2^28 on.
  *   workspace: device, tq_chunk_workspace_bytes() bytes, 256-byte aligned; calls that may overlap need their own.
  * max_tokens chooses the kernel: a batch of at most 16 rows (max_tokens * n_q_heads / n_kv_heads; 8 at head_dim 256)
  * per sequence and KV head takes one that is about twice as fast for them, so a decode step passes max_tokens = 1.

@@ -38,9 +38,9 @@ struct StagedHead {
   float k_scale;      // of the tile's K operand; its V operand's is 2^v_exp
   int v_exp;
   uint32_t any;       // some bit of missing or marked is set
-  uint32_t pad;
+  uint32_t wide;      // its blocks' scales lie too far apart for one: the operands are codes, without scales
   uint32_t missing[4], marked[4];  // by key: its page is out of range; its K or V is marked
-  uint32_t pad2[4];
+  signed char k_exps[8], v_exps[8];  // by block of 16 keys: the exponents of its scales
 };
 struct Staged {
   unsigned char* k;

@@ -1,12 +1,13 @@
 // Chunk attention over f8_block caches whose tiles many entries use, head sizes 64 and 128.
 //
 // A first kernel writes every key tile that some row sees once, as the tensor core takes it: fp16 values in swizzled operand
-// tiles, relative to the tile's largest scale (a power of two: exact, down to 2^-33 of the tile's largest value).  The main
-// kernel's tiles are then plain bulk copies by one thread, without producers, which in the kernel that converts for each
-// entry (tq_chunk_tc.cuh) share the instruction slots with the softmax.  Its registers go to the softmax instead: a row's
-// 128 scores are read from tensor memory at once, masks and score modifications happen in registers, and weights are written
-// only when their sum is known not to pass what fp16 holds, so that the scores are still there where it does.  Entries, ranges,
-// products, the running reference and the join of shared entries are those of tq_chunk_tc.cuh.
+// tiles, relative to the tile's largest scale where its blocks' scales lie within 2^8 of one another, else without scales,
+// which then go to scores and weights block by block; exact either way.  The main kernel's tiles are then plain bulk copies by
+// one thread, without producers, which in the kernel that converts for each entry (tq_chunk_tc.cuh) share the instruction
+// slots with the softmax.  Its registers go to the softmax instead: a row's 128 scores are read from tensor memory at once,
+// masks and score modifications happen in registers, and weights are written only when their sum is known not to pass what
+// fp16 holds, so that the scores are still there where it does.  Entries, ranges, products, the running references and the
+// join of shared entries are those of tq_chunk_tc.cuh.
 //
 // What bounds it.  Eight tensor instructions of M 128, N 128, K 16 take 584 cycles by themselves, for scores as for values, so a
 // tile of two row tiles (32 of them) 2.34 K cycles; it takes 3.1 to 3.3 K.  Scores and weights of a row tile share one buffer, so
@@ -32,6 +33,10 @@ namespace staged {
 // staging: a CTA per tile and KV head
 // ---------------------------------------------------------------------------
 constexpr int kStageThreads = 256;
+// Tiles whose blocks' scales differ by at most 2^kSpan have operands relative to the largest one, for keys and values; the
+// others' are the codes alone.  Weights of the former count by the tile's scale: a row's weights below 2^-29 of its largest
+// are 0 in fp16, which are then up to 2^(8 - 29) of it where a block's own scale is 2^-8 of its tile's.
+constexpr int kSpan = 8;
 
 // Orders this thread's accesses to global memory with those of asynchronous copies.
 __device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
@@ -64,9 +69,9 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
       loc[tid] = vec;
       const uint32_t m = __ballot_sync(kFull, want && !on), there = __ballot_sync(kFull, on) >> (lane & 16) & 0xFFFFu;
       const long long some = __shfl_sync(kFull, vec, (lane & 16) + (there ? __ffs(there) - 1 : 0));
-      if ((lane & 14) == 0) {  // lanes 0 and 16: K's words of two blocks, 1 and 17: V's
+      if ((lane & 14) == 0) {  // lanes 0 and 16: K's words of two blocks, 1 and 17: V's (0: no key of it is wanted)
         const unsigned char* hdr = lane & 1 ? V.header : K.header;
-        words[lane & 1][tid / 16] = there ? __ldg(reinterpret_cast<const uint32_t*>(hdr) + some / kF8Block) : kF8None;
+        words[lane & 1][tid / 16] = there ? __ldg(reinterpret_cast<const uint32_t*>(hdr) + some / kF8Block) : 0u;
       }
       __syncwarp();
       if (lane == 0) {
@@ -78,17 +83,23 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
       }
     }
     __syncthreads();
-    int top[2];
+    int top[2], least[2];  // exponents of K's scales, of V's
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       top[x] = kF8MinExp;
+      least[x] = kF8MaxExp;
 #pragma unroll
-      for (int i = 0; i < BN / 16; ++i) top[x] = max(top[x], f8_exponent(words[x][i]));
+      for (int i = 0; i < BN / 16; ++i) {
+        const uint32_t w = words[x][i];
+        top[x] = max(top[x], w ? f8_exponent(w) : kF8MinExp);
+        least[x] = min(least[x], w ? f8_exponent(w) : kF8MaxExp);
+      }
     }
+    const bool wide = top[0] - least[0] > kSpan || top[1] - least[1] > kSpan;
     const long long at = ((long long)b * a.staged.tiles + t) * K.H + h;
     const int row0 = tid / LPR, ch = tid % LPR;
-    // operands are values 2^-top 2^7: the largest, 448 2^7, is below fp16's end, and a code's last bit is above 2^-24 as long
-    // as its block's scale is above 2^-22 of the largest
+    // a code's last bit, 2^-9, is above fp16's 2^-24 kSpan further down
+    static_assert(kSpan <= 15, "exact operands");
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const unsigned char* pay = (x ? V.payload : K.payload) + 16 * ch;
@@ -101,9 +112,8 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
       }
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        const int row = p * RPP + row0, e = max(f8_exponent(words[x][row / 16]) - top[x], -40) + 7;
-        const __half f = __float2half_rn(ex2((float)max(e, -24)));
-        const uint32_t f2 = e < -24 ? 0u : (uint32_t)__half_as_ushort(f) * 0x10001u;
+        const int row = p * RPP + row0, e = wide ? 0 : max(f8_exponent(words[x][row / 16]) - top[x], -kSpan);
+        const uint32_t f2 = (uint32_t)(e + 15) << 10 | (uint32_t)(e + 15) << 26;  // 2^e
         uint32_t y[8];
         f8_pairs(w[p].x, y[0], y[1]);
         f8_pairs(w[p].y, y[2], y[3]);
@@ -117,13 +127,19 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
     }
     if (tid == 0) {
       StagedHead q{};
-      q.k_scale = ex2((float)(top[0] - 7));
-      q.v_exp = top[1] - 7;
+      q.k_scale = ex2((float)top[0]);
+      q.v_exp = top[1];
+      q.wide = wide;
 #pragma unroll
       for (int i = 0; i < BN / 32; ++i) {
         q.missing[i] = missing[i];
         q.marked[i] = marked[i];
         q.any |= missing[i] | marked[i];
+      }
+#pragma unroll
+      for (int i = 0; i < BN / 16; ++i) {
+        q.k_exps[i] = (signed char)f8_exponent(words[0][i]);
+        q.v_exps[i] = (signed char)f8_exponent(words[1][i]);
       }
       a.staged.heads[at] = q;
     }
@@ -358,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
       const bool any_valid = __any_sync(kFull, valid);  // a warp without rows only keeps the barriers
       float m = -INFINITY, l = 0.f;
       bool unset = true;  // (of the warp) a row that sees keys has no reference yet
-      int ve = kF8MinExp - 7;  // (of the warp) O is in units of 2^ve: no tile's V scale so far is above
+      float ve = 0.f;  // O is in units of 2^ve, see raised()
       int last = -1, last_phase = 0;  // barrier and phase of the last part's value product
       const int H = a.c.k.H, s_n = it.s_n, main_tile = it.tile, sink_tile = it.s_tile;
       const StagedHead* heads = a.staged.heads + (long long)it.seq * a.staged.tiles * H + it.kvh;
@@ -376,8 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
         const uint4 hd = next;
         next_tile = tile_at_step(i + 1);
         if (i + 1 < steps) next = head_of(next_tile);
-        const float k_scale = __uint_as_float(hd.x);
-        const int v_exp = (int)hd.y, key0 = tile * BN;
+        const bool wide = hd.w != 0;  // operands are codes, the blocks' scales in the head
+        const float k_scale = wide ? 1.f : __uint_as_float(hd.x), v_exp = (float)(int)hd.y;
+        const int key0 = tile * BN;
         const float f = mods ? 1.f : fmaxf(me.sl * k_scale, 1.2e-38f);  // scores to log2 units
         const uint32_t t_s = tmem + s * BN + lanes;
         wait_warp(ok, &B->s_done[s], c0 + i);
@@ -394,14 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
         };
         // Weights times 2^(v_exp - ve), in fp16; the sum takes that factor back.  (A scale below 2^-40 of 2^ve counts as that:
         // its weights, at most 2^15 2^-40, are 0 in fp16.)
-        float sh;
-        float2 f2 = make_float2(f, f), m2;
-        auto against = [&]() {
-          sh = (float)max(v_exp - ve, -40);
-          const float mu = sh - (m == -INFINITY ? 0.f : m);
-          m2 = make_float2(mu, mu);
-        };
-        against();
+        const float2 f2 = make_float2(f, f);
+        const float sh = fmaxf(v_exp - ve, -40.f), mu = sh - (m == -INFINITY ? 0.f : m);
+        const float2 m2 = make_float2(mu, mu);
+        // of 32 keys from half * 32 on
         auto weights = [&](const uint32_t (&y)[64], auto half, uint32_t (&pk)[32], float2 (&l2)[2]) {
           constexpr int k0 = half.value * 32;
 #pragma unroll
@@ -416,9 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
         };
         constexpr std::integral_constant<int, 0> lower{};
         constexpr std::integral_constant<int, 1> upper{};
-        auto sum_of = [&](const float2 (&l2)[2]) { return ((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y)) * ex2(-sh); };
+        auto sum_of = [&](const float2 (&l2)[2]) { return (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y); };
         // (rows that are not there hold whatever shared memory had: they have no say, so that results do not vary)
-        auto too_large = [&](float sum) { return __any_sync(kFull, live && sum > kTop); };
+        const float back = ex2(-sh), most = kTop * fminf(1.f, ex2(sh));
+        auto too_large = [&](float sum) { return __any_sync(kFull, live && sum > most); };
         auto store = [&](int h, const uint32_t (&pk)[32]) {  // over scores that have been read
           tc::tmem_st32(t_s + h * (HN / 2), pk);
         };
@@ -436,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
           if (lane == 0) tc::mbar_arrive(&B->turn[1 - wg][warp & 3]);
         };
         int todo = 0;  // parts before this one are published
-        if (any_valid && !unset && v_exp <= ve) {
+        if (any_valid && !unset && !wide) {
           uint32_t x0[64], pk[32];
           float2 u[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           tmem_ask64(t_s, x0);
@@ -455,14 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
           float sum = sum_of(u);
           weights(x1, lower, qk, w);  // (while the first part's sum is looked at)
           if (!too_large(sum)) {
-            l += sum;
+            l = fmaf(sum, back, l);
             store(0, pk);
             weights(x1, upper, qk, w);  // (while the first part's weights are stored)
             publish(0);
             todo = 1;
             sum = sum_of(w);
             if (!too_large(sum)) {
-              l += sum;
+              l = fmaf(sum, back, l);
               store(1, qk);
               pass_on();
               publish(1);
@@ -472,26 +486,39 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
         } else {
           wait_warp(ok, &B->turn[wg][warp & 3], wg ? c1 + i : c1 + i - 1);
         }
-        // The reference is raised, and O and the sum with it, where it is unset, where V's scale rises, and where weights
-        // against the reference so far turned out too large: their scores are still there.
+        // The references are raised, and O and the sum with them, where they are unset, and where weights against those so far
+        // turned out too large: their scores are still there.  Wide tiles come here, too: a block of 16 keys at a time.
         if (todo < PH) {
+          const StagedHead* q = heads + (long long)tile * H;
 #pragma unroll 1
           for (int h = todo; h < PH; ++h) {
             if (any_valid) {
               uint32_t x[64], pk[32];
               tmem_ld64(t_s + h * HN, x);
-              if (special) change(x, h);
-              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              float es[4] = {v_exp, v_exp, v_exp, v_exp};
+              if (wide) {
+                const uint32_t ke = *reinterpret_cast<const uint32_t*>(q->k_exps + 4 * h);
+                const uint32_t ev = *reinterpret_cast<const uint32_t*>(q->v_exps + 4 * h);
 #pragma unroll
-              for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[e]));
-              const float mn = fmaxf(m, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), f, -kBias));
-              float al = mn == -INFINITY ? 1.f : ex2(m - mn);
-              m = mn;
-              l *= al;
-              if (v_exp > ve) {
-                al *= ex2((float)(ve - v_exp));
-                ve = v_exp;
+                for (int b = 0; b < 4; ++b) {
+                  const float k_b = ex2((float)(signed char)(ke >> 8 * b & 255u));
+                  es[b] = (float)(signed char)(ev >> 8 * b & 255u);
+#pragma unroll
+                  for (int e = 16 * b; e < 16 * b + 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * k_b);
+                }
               }
+              if (special) change(x, h);
+              float top = -INFINITY, top_v = -INFINITY;
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 16 * b; e < 16 * b + 16; ++e) mx[e & 1] = fmaxf(mx[e & 1], __uint_as_float(x[e]));
+                const float s1 = fmaxf(mx[0], mx[1]) * f;
+                top = fmaxf(top, s1);
+                top_v = fmaxf(top_v, s1 + es[b]);
+              }
+              const float al = raised(m, ve, l, top, top_v);
               unset = __any_sync(kFull, live && m == -INFINITY);
               if (last >= 0) {  // O, once the product of this warpgroup's last part is complete
                 wait_warp(ok, &B->pv_done[last], last_phase);
@@ -506,11 +533,22 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
                   tmem_st16(t_o + 16 * c, o);
                 }
               }
-              against();
-              float2 u[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-              weights(x, lower, pk, u);
-              weights(x, upper, pk, u);
-              l += sum_of(u);
+              const float m1 = m == -INFINITY ? 0.f : m;
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const float shb = fmaxf(es[b] - ve, -40.f);
+                const float2 mb = make_float2(shb - m1, shb - m1);
+                float2 u = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 8 * b; e < 8 * b + 8; ++e) {
+                  float2 p = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2, mb);
+                  p.x = ex2(p.x);
+                  p.y = ex2(p.y);
+                  u = __fadd2_rn(u, p);
+                  pk[e] = narrow(p.x, p.y, (const __half*)nullptr);
+                }
+                l = fmaf(u.x + u.y, ex2(-shb), l);
+              }
               store(h, pk);
             }
             publish(h);
@@ -523,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) staged_kernel(const __grid_consta
       c0 += steps;
       c1 += (it.n - (it.two ? 0 : 1 - wg) + stride - 1) / stride;
       gt += it.n;
-      finish_rows<D, false>(a, it, wg, r, valid, any_valid, out_at, t_o, last >= 0, m, l, ex2((float)ve));
+      finish_rows<D, false>(a, it, wg, r, valid, any_valid, out_at, t_o, last >= 0, m, l, ex2(ve));
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&B->item_free[is]);
     }

@@ -21,7 +21,7 @@ from test_gpu_f8 import DT, S, W, ctxs, f64, rounding, status, tq  # noqa: F401 
 
 pytestmark = pytest.mark.gpu
 
-KERNELS = ["few", "many"]
+KERNELS = ["few", "many", "staged"]
 # query heads of the KV head, new tokens, context
 SIZES = {"few": (2, 3, 609), "many": (2, 100, 601), "staged": (8, 700, 1301)}
 
