@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const ChunkArgs& a = p.c;
   const int tid = threadIdx.x, G = a.G;
   pdl_wait();               // this kernel's start overlaps the one before
-  pdl_launch_dependents();  // and the main kernel's this one; not earlier: the staging kernel relies on all work before the call
+  pdl_launch_dependents();  // and the main kernel's this one
   long long carry = 0, total;
   for (int b0 = 0; b0 < a.b.n_seqs; b0 += kPlanThreads) {
     const int b = b0 + tid;

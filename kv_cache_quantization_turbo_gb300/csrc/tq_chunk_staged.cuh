@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
   const ChunkArgs& c = a.c;
   const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
   pdl_launch_dependents();
-  // (no wait here: the plan lets this kernel start only when all work before the call has ended, and it needs nothing of it)
+  pdl_wait();  // the plan, and with it what was written before this call
   const SeqOf s = seq_of(c.b, b);
   // the keys that some row sees: the sinks [0, s_hi) and [lo, len)
   const int lo = c.window ? max(0, s.len - s.n - c.window + 1) : 0, s_hi = min(c.sinks, lo);
@@ -145,7 +145,6 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const __grid_const
     }
     fence_async_global();  // the tiles, for the copies
   }
-  pdl_wait();  // the plan has ended, too, when this kernel has
 }
 
 // ---------------------------------------------------------------------------
