@@ -319,10 +319,11 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_kernel(const __grid_con
   }
 }
 
-// s += x; what the rounding of the sum leaves goes to lost (the two-sum of Knuth).
+// s += x; what the rounding of the sum leaves goes to lost (the two-sum of Knuth), nothing of a sum beyond fp32.
 __device__ __forceinline__ void add_exactly(float& s, float& lost, float x) {
   const float t = __fadd_rn(s, x), v = __fsub_rn(t, s);
-  lost += __fadd_rn(__fsub_rn(s, __fsub_rn(t, v)), __fsub_rn(x, v));
+  const float rest = __fadd_rn(__fsub_rn(s, __fsub_rn(t, v)), __fsub_rn(x, v));
+  if (isfinite(t)) lost += rest;
   s = t;
 }
 
