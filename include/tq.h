@@ -568,8 +568,10 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
 
 /*
  * The workspace with which tq_chunk_attention runs these views and modifications (may be NULL) fastest; never less than
- * tq_chunk_workspace_bytes(), with which every call runs.  0 for invalid arguments.  The size given to a call chooses the
- * kernel, so its results agree with those of another size to rounding, not bit by bit.
+ * tq_chunk_workspace_bytes(), with which every call runs.  0 for invalid arguments.  What it has more are keys and values as
+ * fp16 operands: 4 bytes for each coordinate of a key and its value, of n_seqs sequences of max_ctx (rounded up to 128)
+ * tokens each, 8 GiB at most (beyond, it is the least one).  The size given to a call chooses the kernel, so its results
+ * agree with those of another size to rounding, not bit by bit.
  */
 size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int n_q_heads, const tq_cache_view* k_view,
                               const tq_cache_view* v_view, const tq_score_mods* mods);

@@ -283,7 +283,7 @@ Layout layout(int sm_count, int d, long long n_seqs, long long n_tokens, long lo
 // batch's average decides, as far as the host knows it; documents (first_keys) are left to the other kernel, which does not
 // look at pages that no row sees.
 constexpr int staged_uses(int d) { return d == 64 ? 6 : 8; }
-constexpr size_t kStagedMost = (size_t)8 << 30;
+constexpr size_t kStagedMost = (size_t)8 << 30;  // bytes in all
 
 struct StagedLayout {
   size_t k, v, heads, bytes;  // from the workspace's start; bytes 0: not staged
@@ -301,7 +301,8 @@ StagedLayout staged_layout(size_t at, int d, const DevView& k, const tq_batch& b
   if (!(entries * seen >= staged_uses(d) * staged)) return l;
   l.tiles = (int)((b.max_ctx + keys - 1) / keys);
   const size_t n = (size_t)b.n_seqs * l.tiles * k.H;
-  if (n == 0 || n > kStagedMost / ck::tile_bytes(d) || k.H > 65535 || b.n_seqs > 65535) return l;  // (the grid's y and z)
+  const size_t most = (kStagedMost - 256) / (2 * ck::tile_bytes(d) + sizeof(ck::StagedHead));
+  if (n == 0 || n > most || k.H > 65535 || b.n_seqs > 65535) return l;  // (the grid's y and z)
   l.k = at;
   l.v = l.k + n * ck::tile_bytes(d);
   l.heads = l.v + n * ck::tile_bytes(d);
