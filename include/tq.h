@@ -556,8 +556,6 @@ typedef struct tq_score_mods {
   const int32_t* first_keys;   /* device int32 [n_tokens]: token t sees no key j < first_keys[t] (packed documents) */
   const int32_t* prefix_lens;  /* device int32 [n_seqs]: the keys j < prefix_lens[b] of sequence b are seen by all its
                                   tokens, before or after them (the window and first_keys still apply) */
-  int32_t sinks;               /* s > 0: the window hides no key j < f + s, f = first_keys[t] (0 without first_keys, and
-                                  where that is negative): the first tokens stay visible.  Without a window: no effect */
 } tq_score_mods;
 
 /*
@@ -615,6 +613,17 @@ tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const
                              const tq_cache_view* v_view, int layer, float softmax_scale, const tq_score_mods* mods,
                              void* workspace, size_t workspace_bytes, void* out, tq_dtype out_dtype,
                              tq_stream_t stream);
+
+/*
+ * The same with sinks, first tokens that stay visible: where sinks s > 0, the window of mods hides no key j < f + s,
+ * f = first_keys[t] (0 without first_keys, and where that is negative).  Without a window they change nothing.  (A call of
+ * its own, so that tq_score_mods keeps its size for programs that were built without them.)
+ */
+tq_status tq_chunk_attention_sinks(const tq_context* ctx, const tq_batch* batch, const void* q, tq_dtype q_dtype,
+                                   int64_t q_token_stride, int n_q_heads, const tq_cache_view* k_view,
+                                   const tq_cache_view* v_view, int layer, float softmax_scale, const tq_score_mods* mods,
+                                   int sinks, void* workspace, size_t workspace_bytes, void* out, tq_dtype out_dtype,
+                                   tq_stream_t stream);
 
 /* ---- dequantize (reconstruction; test and debugging path) ---- */
 

@@ -79,6 +79,10 @@ DevBatch dev_batch(const tq_batch* b) {
 
 bool is_f8(const DevView& v) { return v.format == TQ_FMT_F8_BLOCK; }
 
+bool mods_ok(const tq_score_mods* m) {
+  return !m || (m->softcap >= 0.0f && std::isfinite(m->softcap) && m->window >= 0);
+}
+
 bool stored_ok(const DevView& v) { return v.format == TQ_FMT_Q8_0 || (format_is_turbo(v.format) && !v.has_qjl); }
 
 }  // namespace
@@ -284,7 +288,7 @@ size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, in
 size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int n_q_heads, const tq_cache_view* k_view,
                               const tq_cache_view* v_view, const tq_score_mods* mods) {
   DevView k{}, v{};
-  if (!make_dev_view(k_view, &k) || !make_dev_view(v_view, &v)) return 0;
+  if (!make_dev_view(k_view, &k) || !make_dev_view(v_view, &v) || !mods_ok(mods)) return 0;
   const size_t least = tq_chunk_workspace_bytes(ctx, batch, n_q_heads, k.H);
   if (!least || k.d != ctx->d) return 0;
   return chunk_workspace_most(ctx->sm_count, k, *batch, n_q_heads, mods && mods->first_keys, mods ? mods->window : 0);
@@ -295,6 +299,15 @@ tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const
                              const tq_cache_view* v_view, int layer, float softmax_scale, const tq_score_mods* mods,
                              void* workspace, size_t workspace_bytes, void* out, tq_dtype out_dtype,
                              tq_stream_t stream) {
+  return tq_chunk_attention_sinks(ctx, batch, q, q_dtype, q_token_stride, n_q_heads, k_view, v_view, layer, softmax_scale,
+                                  mods, 0, workspace, workspace_bytes, out, out_dtype, stream);
+}
+
+tq_status tq_chunk_attention_sinks(const tq_context* ctx, const tq_batch* batch, const void* q, tq_dtype q_dtype,
+                                   int64_t q_token_stride, int n_q_heads, const tq_cache_view* k_view,
+                                   const tq_cache_view* v_view, int layer, float softmax_scale, const tq_score_mods* mods,
+                                   int sinks, void* workspace, size_t workspace_bytes, void* out, tq_dtype out_dtype,
+                                   tq_stream_t stream) {
   const int esz = dtype_bytes(q_dtype), osz = dtype_bytes(out_dtype);
   if (!ctx || !batch_ok(batch) || !esz || !osz || layer < 0 || n_q_heads < 1 || !std::isfinite(softmax_scale))
     return TQ_ERR_INVALID_ARG;
@@ -307,9 +320,7 @@ tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const
   const int64_t row = (int64_t)n_q_heads * d;
   if (!rows_ok(q, q_token_stride, row, esz, batch->n_tokens) || !rows_ok(out, row, row, osz, batch->n_tokens))
     return TQ_ERR_INVALID_ARG;
-  if (mods && (!(mods->softcap >= 0.0f) || !std::isfinite(mods->softcap) || mods->window < 0 ||
-               mods->sinks < 0))
-    return TQ_ERR_INVALID_ARG;
+  if (!mods_ok(mods) || sinks < 0) return TQ_ERR_INVALID_ARG;
   if (!batch_fits(batch, a.k) || !on_device(ctx)) return TQ_ERR_INVALID_ARG;
   const bool f8 = is_f8(a.k) && is_f8(a.v);
   if ((!f8 && (a.k.format != TQ_FMT_Q8_0 || !stored_ok(a.v))) || n_q_heads % a.k.H) return TQ_ERR_UNSUPPORTED;
@@ -337,7 +348,7 @@ tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const
     a.slopes = mods->slopes;
     a.first_keys = mods->first_keys;
     a.prefix_lens = mods->prefix_lens;
-    a.sinks = mods->window ? mods->sinks : 0;
+    a.sinks = mods->window ? sinks : 0;
   }
   const float lam_v = a.v.format == TQ_FMT_Q8_0 || f8 ? 1.f : ctx->f16_scale_h[a.v.idx_bits - 1];
   return cuda_status(launch_chunk(a, lam_v, workspace, workspace_bytes, ctx->sm_count, cuda_stream(stream)));

@@ -62,7 +62,7 @@ class tq_batch(ctypes.Structure):
 class tq_score_mods(ctypes.Structure):
     _fields_ = [
         ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
-        ("first_keys", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p), ("sinks", ctypes.c_int32),
+        ("first_keys", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
     ]
 
 
@@ -128,6 +128,8 @@ _SIGS = {
     "tq_chunk_workspace_for": (_SZ, [_P, ctypes.POINTER(tq_batch), _I, _VP, _VP, ctypes.POINTER(tq_score_mods)]),
     "tq_chunk_attention": (_I, [_P, ctypes.POINTER(tq_batch), _P, _I, _I64, _I, _VP, _VP, _I, _F,
                                 ctypes.POINTER(tq_score_mods), _P, _SZ, _P, _I, _P]),
+    "tq_chunk_attention_sinks": (_I, [_P, ctypes.POINTER(tq_batch), _P, _I, _I64, _I, _VP, _VP, _I, _F,
+                                      ctypes.POINTER(tq_score_mods), _I, _P, _SZ, _P, _I, _P]),
     "tq_context_tables_hash": (_I, [_P, ctypes.POINTER(ctypes.c_uint64)]),
     "tq_cache_save": (_I, [_P, _VP, _I, ctypes.c_char_p]),
     "tq_cache_file_info": (_I, [ctypes.c_char_p, _VP, ctypes.POINTER(ctypes.c_uint64)]),
@@ -521,7 +523,7 @@ class Batch:
 class ScoreMods:
     """Changes to the scores (tq_score_mods) and the device tensors they read: slopes float32 [n_q_heads],
     first_keys int32 [n_tokens], prefix_lens int32 [n_seqs], each None for none; contents may change between calls.
-    sinks: first tokens that the window does not hide."""
+    sinks: first tokens that the window does not hide (tq_chunk_attention_sinks)."""
     softcap: float = 0.0
     window: int = 0
     slopes: object = None
@@ -535,7 +537,7 @@ class ScoreMods:
                 raise ValueError(f"a contiguous {want} tensor on the GPU is wanted: {t.dtype}, strides {t.stride()}, "
                                  f"{t.device}")
         object.__setattr__(self, "_c", tq_score_mods(self.softcap, self.window, _ptr(self.slopes),
-                                                     _ptr(self.first_keys), _ptr(self.prefix_lens), self.sinks))
+                                                     _ptr(self.first_keys), _ptr(self.prefix_lens)))
 
     def c_mods(self) -> tq_score_mods:
         return self._c
@@ -708,7 +710,8 @@ def tq_chunk_attention(ctx: int, batch: Batch, q, k_view, v_view, layer: int, so
             if t is not None and t.numel() != n:
                 raise ValueError(f"{n} values are wanted: {tuple(t.shape)}")
     ka, va = _view_arg(k_view), _view_arg(v_view)
-    return _lib.tq_chunk_attention(ctx, ctypes.byref(batch.c_batch()), q.data_ptr(), _dtype(q), _rows(q, shape),
-                                   shape[1], ka[0], va[0], layer, softmax_scale,
-                                   None if mods is None else ctypes.byref(mods.c_mods()), _ptr(workspace),
-                                   workspace_bytes, _ptr(out), _dtype(out), _stream(stream))
+    return _lib.tq_chunk_attention_sinks(ctx, ctypes.byref(batch.c_batch()), q.data_ptr(), _dtype(q), _rows(q, shape),
+                                         shape[1], ka[0], va[0], layer, softmax_scale,
+                                         None if mods is None else ctypes.byref(mods.c_mods()),
+                                         0 if mods is None else mods.sinks, _ptr(workspace), workspace_bytes, _ptr(out),
+                                         _dtype(out), _stream(stream))
