@@ -592,8 +592,8 @@ size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int 
  *   Query head h reads KV head h / (n_q_heads / n_kv_heads); n_q_heads a multiple of n_kv_heads.
  *   K: Q8_0 with V: Q8_0 or turbo2/3/4_mse; or F8_BLOCK for both.  Others: TQ_ERR_UNSUPPORTED (turbo K:
  *   tq_decode_attention, tq_prefill_attention).  F8_BLOCK codes are fp16 numbers: keys and values are not rounded, and a
- *   block's scale goes to its scores and weights.  A weight is rounded to fp16 with V's scale in it, relative to the row's
- *   largest such product: keys that the row does not see, or hardly weighs, take nothing from the others whatever their
+ *   block's scale goes to its scores and weights.  A weight is rounded to fp16 (few rows: to 22 bits) with V's scale in it,
+ *   relative to the row's largest such product: keys that the row does not see, or hardly weighs, take nothing from the others whatever their
  *   scale; a key whose product is below 2^-29 of the largest (2^-21 with the workspace of tq_chunk_workspace_for()) may
  *   count as 0.  Scores are fp32: beyond 2^22 in magnitude their steps pass what a weight can tell apart, and a row may
  *   come out as NaN from 2^28 on.

@@ -237,3 +237,39 @@ def test_modified_scores_marks_and_missing_pages_over_scales_far_apart(ctxs, d, 
     missing = np.isin(np.arange(total) // 16, [3, 20])
     for kw in ({}, mods):
         check(c, G, q, kernel, scale, missing=missing, stored=stored, exps=exps, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("G,new", [(1, 1), (4, 1), (2, 3), (8, 2)])
+def test_weights_of_few_rows_are_not_rounded(ctxs, d, dtype, G, new):  # noqa: F811
+    """Kernel for few rows: weights have 22 bits.  Keys and queries of one coordinate have scores of one product, so a row of
+    few keys is off by 2^-22 (|s_j| + |s_max|) for the product with log2 e and the scales, 2^-22 |s_j| for what two fp16 numbers
+    leave of an fp32 query, 2^-21 of the weights (2^-22 for what two fp16 numbers leave of one, 2^-22 for the exponential),
+    2^-28 448 of the largest product of weight and scale for what of a small one is below fp16, and 2^-20 for its sums in
+    fp32 (16 additions at most).  The output is fp32."""
+    if new * G > (8 if d == 256 else 16):
+        pytest.skip("these are many rows")
+    for total in (16, 5, 37):
+        c = F.Cache(ctxs[d], d, 1, [new], [total], 16)
+        k, v = torch.zeros((total, 1, d), device="cuda"), W.normal_tensor((total, 1, d), seed=32 + total, device="cuda")
+        k[:, 0, 3] = W.normal_tensor((total, 1), seed=31, device="cuda")[:, 0]
+        c.append([total], [total], k, v, oracle=False)
+        q = torch.zeros((new, G, d), device="cuda")
+        q[:, :, 3] = 1 + 0.3 * W.normal_tensor((new, G), seed=9, device="cuda")
+        q = q.to(DT[dtype])
+        out = F.attend(c, q, None, torch.float32, scale=1.0)
+        torch.cuda.synchronize()
+        assert status(c.ctx) == 0
+        k, v = (y[:, 0] for y in c.stored(0))
+        exps = exponents(c, c.vv)
+        for t in range(new):
+            j = np.arange(int(c.pos[t]) + 1)
+            for h in range(G):
+                s = k[j] @ f64(q)[t, h]
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                want = w @ v[j]
+                e = 2.0 ** -22 * (2 * np.abs(s) + abs(s.max())) + 2.0 ** -21 + 2.0 ** -20
+                tol = (w * e) @ (np.abs(v[j]) + np.abs(want)) + len(j) * 2.0 ** -28 * 448 * (w * 2.0 ** exps[j]).max()
+                assert (np.abs(f64(out)[t, h] - want) <= tol).all(), (t, h, float((np.abs(f64(out)[t, h] - want) / tol).max()))
