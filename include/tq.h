@@ -565,11 +565,13 @@ typedef struct tq_score_mods {
 size_t tq_chunk_workspace_bytes(const tq_context* ctx, const tq_batch* batch, int n_q_heads, int n_kv_heads);
 
 /*
- * The workspace with which tq_chunk_attention runs these views and modifications (may be NULL) fastest; never less than
- * tq_chunk_workspace_bytes(), with which every call runs.  0 for invalid arguments.  What it has more are keys and values as
- * fp16 operands: 4 bytes for each coordinate of a key and its value, of n_seqs sequences of max_ctx (rounded up to 128)
- * tokens each, 8 GiB at most (beyond, it is the least one).  The size given to a call chooses the kernel, so its results
- * agree with those of another size to rounding, not bit by bit.
+ * The workspace with which tq_chunk_attention runs these views and modifications (may be NULL) fastest; never less
+ * than tq_chunk_workspace_bytes(), with which every call runs.  0 for invalid arguments.  What it has more are keys
+ * and values as fp16 operands: 4 bytes for each coordinate of a key and its value, of n_seqs sequences of max_ctx
+ * (rounded up to 128) tokens each, 8 GiB at most (beyond, it is the least one).  (Where most runs of 128 keys hold
+ * f8_block scales more than 2^8 apart, the least workspace is the faster one: 2.1 and 3.2 ms for 4096 tokens at 32K.)
+ * The size given to a call chooses the kernel, so its results agree with those of another size to rounding, not bit
+ * by bit.
  */
 size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int n_q_heads, const tq_cache_view* k_view,
                               const tq_cache_view* v_view, const tq_score_mods* mods);
@@ -592,21 +594,21 @@ size_t tq_chunk_workspace_for(const tq_context* ctx, const tq_batch* batch, int 
  *   Query head h reads KV head h / (n_q_heads / n_kv_heads); n_q_heads a multiple of n_kv_heads.
  *   K: Q8_0 with V: Q8_0 or turbo2/3/4_mse; or F8_BLOCK for both.  Others: TQ_ERR_UNSUPPORTED (turbo K:
  *   tq_decode_attention, tq_prefill_attention).  F8_BLOCK codes are fp16 numbers: keys and values are not rounded, and a
- *   block's scale goes to its scores and weights.  A weight is rounded to fp16 (few rows: to 22 bits) with V's scale in it,
- *   relative to the row's largest such product: keys that the row does not see, or hardly weighs, take nothing from the others whatever their
- *   scale; a key whose product is below 2^-29 of the largest (2^-21 with the workspace of tq_chunk_workspace_for()) may
- *   count as 0.  Scores are fp32: beyond 2^22 in magnitude their steps pass what a weight can tell apart, and a row may
- *   come out as NaN from 2^28 on.
+ *   block's scale goes to its scores and weights.  A weight is rounded to fp16 (few rows: to 22 bits) with V's scale in
+ *   it, relative to the row's largest such product: keys that the row does not see, or hardly weighs, take nothing from
+ *   the others whatever their scale; a key whose product is below 2^-29 of the largest (2^-21 with the workspace of
+ *   tq_chunk_workspace_for()) may count as 0.  Scores are fp32: beyond 2^22 in magnitude their steps pass what a weight
+ *   can tell apart, and a row may come out as NaN from 2^28 on.
  *   workspace: device, tq_chunk_workspace_bytes() bytes, 256-byte aligned; calls that may overlap need their own.
  * max_tokens chooses the kernel: a batch of at most 16 rows (max_tokens * n_q_heads / n_kv_heads; 8 at head_dim 256)
  * per sequence and KV head takes one that is about twice as fast for them, so a decode step passes max_tokens = 1.
  * The operands of the products are fp16: queries (scaled by a power of two per row, so that no type overflows), keys
  * and values as scale * code (turbo: norm * level), weights; the sums and the softmax are fp32.  Few rows: keys are
  * exact and fp32 queries have 22 bits.  Against fp64, N(0, 1) queries on a cache with 1 % of its channels 20 times
- * larger (2-norm of all outputs, the output's own rounding included: 2e-4 in fp16, 1.7e-3 in bf16): few rows 3.3e-4
- * to 4.5e-4, many 5e-4 to 2.0e-3 (fp16 out) and 1.9e-3 to 2.7e-3 (bf16 out).  Stored q8_0 scales above 511.5 (values
- * above 64960) are read as 511.5.  The result of a call does not depend on what else runs.  A block-table entry out
- * of range sets status bit 2, and its keys are left out.
+ * larger (2-norm of all outputs, the output's own rounding included: 2e-4 in fp16, 1.7e-3 in bf16): few rows 3.3e-4 to
+ * 4.5e-4 (F8_BLOCK: 2e-4), many 5e-4 to 2.0e-3 (fp16 out) and 1.9e-3 to 2.7e-3 (bf16 out).  Stored q8_0 scales above
+ * 511.5 (values above 64960) are read as 511.5.  The result of a call does not depend on what else runs.  A block-table
+ * entry out of range sets status bit 2, and its keys are left out.
  */
 tq_status tq_chunk_attention(const tq_context* ctx, const tq_batch* batch, const void* q, tq_dtype q_dtype,
                              int64_t q_token_stride, int n_q_heads, const tq_cache_view* k_view,

@@ -2,7 +2,9 @@
 //
 // The sequences' lengths are on the device, so a one-block kernel lists the entries (up to rows_per_entry rows of a
 // sequence and the keys that any of them sees), sums up their work and says whether they are cut between CTAs.  It runs in
-// a few microseconds for the sizes that a step has, and clears the counters with which the main kernel joins partial results.
+// a few microseconds for the sizes that a step has, and clears the counters with which the kernel for few rows finds the
+// last of an entry's CTAs, and the other kernels the last of a CTA's two warpgroups (what several CTAs share, join_kernel
+// joins).
 #include "tq_batch.cuh"
 #include "tq_chunk.h"
 
@@ -276,12 +278,13 @@ Layout layout(int sm_count, int d, long long n_seqs, long long n_tokens, long lo
 
 
 // Staging f8_block tiles pays where enough entries use each.  8 KV heads of 128, 4 query heads each, us staged and not: one
-// sequence at 32K, 4 entries 203 and 190, 6 244 and 251, 8 268 and 295, 16 443 and 557, 64 1515 and 2050; 8 sequences at 4K, 6
-// entries each 257 and 270, 8 293 and 325; with a window of 1024, 16 entries of 64 tokens (8 uses of a tile) 249 and 255, 8 (6
-// uses) 167 and 158.  Heads of 64, one sequence at 32K: 4 entries 138 and 148, 8 210 and 257; 8 sequences at 4K with the window,
-// 8 entries (6 uses) 126 and 123, 16 200 and 209.  Heads of 256: 16 entries 767 and 597, 64 2002 and 2055, so never there.  The
-// batch's average decides, as far as the host knows it; documents (first_keys) are left to the other kernel, which does not
-// look at pages that no row sees.
+// sequence at 32K, 4 entries 203 and 190, 6 244 and 251, 8 268 and 295, 16 443 and 557, 64 1515 and 2050; 8 sequences at 4K,
+// 6 entries each 257 and 270, 8 293 and 325; with a window of 1024, 16 entries of 64 tokens (8 uses of a tile) 249 and 255,
+// 8 (6 uses) 167 and 158.  Heads of 64, one sequence at 32K: 4 entries 138 and 148, 8 210 and 257; 8 sequences at 4K with
+// the window, 8 entries (6 uses) 126 and 123, 16 200 and 209.  Heads of 256: 16 entries 767 and 597, 64 2002 and 2055, so
+// never there.  The batch's average decides, as far as the host knows it (measured before rows had references of their own
+// for their weights' exponents, which took 1515 to 1555 and 2050 to 2130 us at 64 entries and leave the borders); documents
+// (first_keys) are left to the other kernel, which does not look at pages that no row sees.
 constexpr int staged_uses(int d) { return d == 64 ? 6 : 8; }
 constexpr size_t kStagedMost = (size_t)8 << 30;  // bytes in all
 

@@ -59,7 +59,7 @@ struct Args {
   ChunkArgs c;
   const PlanHead* plan;
   const Entry* entries;
-  unsigned int* counters;  // [KV head][entry][row tile]: partial results so far
+  unsigned int* counters;  // [KV head][entry][2]: partial results so far
   float* part_o;           // [CTA][2][2][D / 4][rows_cap][4]
   float* part_ml;          // [CTA][2][2][rows_cap][2]: reference (log2 units), sum
   Shared* shared;          // [CTA]

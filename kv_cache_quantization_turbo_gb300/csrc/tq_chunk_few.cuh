@@ -12,18 +12,18 @@
 //     accumulators with two 8 x 8 transposes.  A lane's columns are the same rows of Q in both products.  Over f8_block, whose
 //     codes are exact, what fp16 leaves of a weight has products of its own, too: an error of 2e-5 against the fp32 plain form
 //     instead of 3e-4, for 1 us of 140.  (Over q8_0 the same for weights and values, which are scale * code there, takes 179 us
-//     instead of 149, for the weights alone 155 with half of the error left: not done.)
+//     instead of 149 and leaves 2.0e-4 of 3.5e-4 against fp64, the output's rounding; for the weights alone 155: not done.)
 // The ranges, the join of entries that several CTAs share and the meaning of every mask are those of tq_chunk_tc.cuh;
 // weights are taken against a reference that is raised only when a weight would pass 2^15.
 //
-// What bounds it.  64 sequences of 1K to 16K tokens, 8 KV heads of 128, 4 rows: 147 us for 0.87 GB, 5.9 TB/s, 87 % of the
-// copy bandwidth, at 64 % of the instruction slots (511 instructions per slice, of which 180 turn codes into fp16).  Keys as
-// the right operand, 8 of 16 rows idle, took 170 us; scales multiplied into K's fragments 149 us, and rounded K: an error of
-// 1.3e-3 instead of 3.6e-4.  Turbo values: more instructions (a lookup by byte permutes) for fewer bytes, 149 us for 48 such
-// sequences, bound by the instruction slots.  f8_block: 364 instructions per slice (an instruction turns two codes into fp16;
-// a slice is a block, so that K's scale goes to its scores and V's to its weights: raised()), 141 us for
-// 0.82 GB, 5.8 TB/s.  One token at 32K: 20 us after the plan, of which the range's 7 slices per
-// warp take 9 (instruction slots), finding the range, the first copies and Q 5, the join of 38 shares 5.
+// What bounds it.  64 sequences of 1K to 16K tokens, 8 KV heads of 128, 4 rows: 147 us for 0.87 GB, 5.9 TB/s, 87 % of the copy
+// bandwidth, at 64 % of the instruction slots (511 instructions per slice, of which 180 turn codes into fp16).  Keys as the
+// right operand, 8 of 16 rows idle, took 170 us; scales multiplied into K's fragments 149 us, and rounded K: an error of 1.3e-3
+// instead of 3.6e-4.  Turbo values: more instructions (a lookup by byte permutes) for fewer bytes, 149 us for 48 such
+// sequences, bound by the instruction slots.  f8_block: 396 instructions per slice (an instruction turns two codes into fp16; a
+// slice is a block, so that K's scale goes to its scores and V's to its weights: raised()), 140 to 141 us for 0.82 GB, 5.8
+// TB/s, at 53 % of the instruction slots.  One token at 32K: 20 us after the plan, of which the range's 7 slices per warp take
+// 9 (instruction slots), finding the range, the first copies and Q 5, the join of 38 shares 5.
 #pragma once
 
 #include <type_traits>

@@ -9,16 +9,19 @@
 // fp16 holds, so that the scores are still there where it does.  Entries, ranges, products, the running references and the
 // join of shared entries are those of tq_chunk_tc.cuh.
 //
-// What bounds it.  Eight tensor instructions of M 128, N 128, K 16 take 584 cycles by themselves, for scores as for values, so a
-// tile of two row tiles (32 of them) 2.34 K cycles; it takes 3.1 to 3.3 K.  Scores and weights of a row tile share one buffer, so
-// its step is a chain: value products of the last tile's second half, score product, the scores' way to registers, weights (720
-// cycles for 128 keys by themselves, most of them the exponentials), stores.  The chains of the two row tiles do not fill each
-// other's gaps wholly, and the operands and copies of a tile, 256 KB, keep shared memory busy for 2 K cycles meanwhile.  4096
-// tokens at 32K, 32 query heads of 128 on 8 KV heads, bf16: 1.51 ms with staging (40 us) and join (15 us), 1.36 PFLOP/s; 2.05 ms in
-// the other kernel.  Steps on the way: without producers 1.74 ms; the two softmax warps of a sub-partition taking turns 1.65 (left
-// alone they fall into step); the check for a new reference by the scores' maximum before the turn 1.58, by the weights' sum, with
-// the weights in registers until it is known, 1.57; the join 1.53, its loads 1.51.  A version that kept the scores in registers
-// for that check spilled: 1.71.  Pairs of CTAs that share the operands (two thirds of the shared-memory traffic) are the way on.
+// What bounds it.  Eight tensor instructions of M 128, N 128, K 16 take 584 cycles by themselves, for scores as for values,
+// so a tile of two row tiles (32 of them) 2.34 K cycles; it takes 3.1 to 3.3 K.  Scores and weights of a row tile share one
+// buffer, so its step is a chain: value products of the last tile's second half, score product, the scores' way to
+// registers, weights (720 cycles for 128 keys by themselves, most of them the exponentials), stores.  The chains of the two
+// row tiles do not fill each other's gaps wholly, and the operands and copies of a tile, 256 KB, keep shared memory busy for
+// 2 K cycles meanwhile.  4096 tokens at 32K, 32 query heads of 128 on 8 KV heads, bf16: 1.55 ms with staging (42 us) and
+// join (15 us), 1.33 PFLOP/s; 2.13 ms in the other kernel.  Steps on the way: without producers 1.74 ms; the two softmax
+// warps of a sub-partition taking turns 1.65 (left alone they fall into step); the check for a new reference by the scores'
+// maximum before the turn 1.58, by the weights' sum, with the weights in registers until it is known, 1.57; the join 1.53,
+// its loads 1.51; with references of each row's own for its weights' exponents, instead of the warp's, 1.55.  Where every
+// other block of V has a scale 2^12 larger, so that every tile's scales are applied by block: 3.19 ms, 2.14 in the other
+// kernel.  A version that kept the scores in registers for that check spilled: 1.71.  Pairs of CTAs that share the operands
+// (two thirds of the shared-memory traffic) are the way on.
 #pragma once
 
 #include <type_traits>

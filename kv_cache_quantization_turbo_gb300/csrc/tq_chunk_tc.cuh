@@ -32,17 +32,18 @@
 // values carry lambda so that the codebook is nearly exact in fp16.  Rounding to fp16 (2^-11 relative at most per
 // operand) is what the tensor core's full rate asks for; sums are fp32.
 //
-// What bounds it.  Many rows: a tensor instruction of M 128, K 16 takes 65 cycles for any N up to 128 (measured alone), so
-// a tile of two row tiles (32 instructions) takes 2.1 K cycles; it takes 4.9 K.  A row tile's steps follow one another
+// What bounds it.  Many rows: a tensor instruction of M 128, K 16 takes 65 cycles for any N up to 128 (measured alone),
+// so a tile of two row tiles (32 instructions) takes 2.1 K cycles; it takes 4.9 K.  A row tile's steps follow one another
 // (its scores and weights share one buffer): score product 0.95 K, two softmax parts of 64 keys with 0.4 K around each,
-// value product 0.3 K.  The two row tiles' steps run side by side, so a tile takes as long as one of them, and most of that
-// is the softmax: a part takes 0.43 K cycles alone and 1.0 K beside the producers, which convert every tile again for each
-// entry and share the instruction slots of its SM sub-partition, as do the polls of barriers (5 K of 13.9 K instructions).
-// Without the softmax the loop runs at 1.56 ms, without softmax and conversion at 1.22 ms, with both at 2.03 ms for a
-// 4096-token chunk at 32K context, 32 query heads of 128 (1.02 PFLOP/s).  64-key score products with twice the buffers take
-// the same 65 cycles each for half the keys: 2.15 ms.  Few rows: a tile is 34.8 KB of cache, 1.5 K cycles of this GPU's
-// bandwidth; it takes 3.5 K, bound by the round of a tile through its two buffers.  Entries of up to 16 rows have a kernel
-// of their own (tq_chunk_few.cuh).
+// value product 0.3 K.  The two row tiles' steps run side by side, so a tile takes as long as one of them, and most of
+// that is the softmax: a part takes 0.43 K cycles alone and 1.0 K beside the producers, which convert every tile again
+// for each entry and share the instruction slots of its SM sub-partition, as do the polls of barriers (5 K of 13.9 K
+// instructions). Without the softmax the loop runs at 1.56 ms, without softmax and conversion at 1.22 ms, with both at
+// 2.04 ms for a 4096-token chunk at 32K context, 32 query heads of 128; the call takes 2.05 ms (1.00 PFLOP/s), 0.5 % more
+// since the join is a kernel of its own, which saves small batches most of their time (below, at join_kernel).  64-key
+// score products with twice the buffers take the same 65 cycles each for half the keys: 2.15 ms.  Few rows: a tile is
+// 34.8 KB of cache, 1.5 K cycles of this GPU's bandwidth; it takes 3.5 K, bound by the round of a tile through its two
+// buffers.  Entries of up to 16 rows have a kernel of their own (tq_chunk_few.cuh).
 //
 // Error against fp64 (2-norm of all outputs, N(0, 1) queries, 1 % of the channels 20 times larger): 512 tokens at 32K, fp16,
 // 2.0e-3; 4096 tokens, bf16, 2.7e-3, of which the output's type is 1.6e-3; without such channels 5e-4.  Nearly all of it is
@@ -149,7 +150,7 @@ __device__ __forceinline__ float ex2(float x) {
 // c (1 - 2 / (1 + 2^z)), whose difference keeps about 2.5e-7 of c and nothing of an s far below that: where |s / c| is
 // below 1/4 its series s (1 - y^2 / 3 + 2 y^4 / 15 - 17 y^6 / 315), y = z ln 2 / 2, is taken instead (62 y^8 / 2835 is
 // left out: 3.4e-7 relative at most).  So the error is 1e-6 relative for every c; a c that no score comes near leaves s.
-// (Eight chunks of up to 700 tokens, 256 wide, capped: 124 us without the series, 130 with it.)
+// (Eight chunks of up to 700 tokens, 256 wide, capped: 58.7 us without the series, 60.6 with it.)
 __device__ __forceinline__ float cap_score(float s, float c2, float i2) {
   constexpr float kY2 = 0.12011325347955035f;  // (ln 2 / 2)^2
   const float z = s * i2, w = z * z;

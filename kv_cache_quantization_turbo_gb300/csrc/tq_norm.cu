@@ -8,7 +8,7 @@
 // the weight in registers, and asks for the next heads' words before it turns to the first ones.  Queries and keys are
 // heads of one launch.  4096 tokens of 32 + 8 heads of 128 in bf16: 17.7 us for 84 MB, where a plain copy of them takes 16.2
 // (4 heads per group 18.4; blocks of 256 threads 20.5, of 128 with four on an SM 19.4; two heads in flight and six blocks
-// 20.0); the gradient 33 us for 126 MB, of which the first kernel 29 (4 heads per group 38, 16 41; two heads in flight and
+// 20.0); the gradient 33 us for 126 MB, of which the first kernel 28 (4 heads per group 38, 16 41; two heads in flight and
 // four blocks instead of four and three 34.8, one and four 43; twice or half the blocks for the partial sums the same).
 // What did not pay: two coordinates per instruction (the pairs' moves: 21.9 and 36.5), the next heads' lines asked into L2
 // at once (19.2 and 36).
